@@ -492,6 +492,145 @@ int moe_expert_backward(const uint16_t* dy, const uint16_t* x, int64_t tokens, i
                         void* const* stage_events, void* stream);
 
 /* ------------------------------------------------------------------------
+ * Operators on unquantized tensors around the expert layer.  Their element
+ * types are given by a dtype code: 0 float32, 1 bf16 (bit patterns), 2 fp16.
+ * `ld_*` is the distance of consecutive rows in elements (>= the row's
+ * width); rows need no more than their element's alignment.  Outputs do not
+ * overlap inputs.
+ * ---------------------------------------------------------------------- */
+
+/* ------------------------------------------------------------------------
+ * moe_router -- the experts of every token and their weights, in the form
+ * moe_permute and the expert layers take them.
+ *   key[t, e]  = fl32(logits[t, e] + bias[e])          (the choice)
+ *   topk_idx   = the topk experts with the largest keys, in descending order,
+ *                equal keys by ascending expert id.  An expert whose key is
+ *                -inf or NaN is never picked; what is left over has id -1
+ *                (not routed) and weight 0.
+ *   topk_prob  = scale * w, from the logits without the bias:
+ *     score 0 (softmax), renormalize 0: w_j = exp(l_j) / sum over all e
+ *     score 0,           renormalize 1: w_j = exp(l_j) / sum over the picks
+ *     score 1 (sigmoid), renormalize 0: w_j = s(l_j) = 1 / (1 + exp(-l_j))
+ *     score 1,           renormalize 1: w_j = s(l_j) / sum over the picks
+ * in binary32.  Logits of -inf mask an expert; a row that holds a NaN or
+ * +inf logit gets NaN weights (the ids stay valid).
+ *   logits     [tokens, ld_logits], dtype code; bias nullable float
+ *              [num_experts], finite or -inf (masks the expert)
+ *   topk_idx   out int32 [tokens, topk];  topk_prob out float [tokens, topk]
+ * Limits: 1 <= topk <= num_experts <= 1024; tokens * topk < 2^31; scale finite.
+ *
+ * moe_router_backward -- the logits' gradient from the weights' (dprob, e.g.
+ * moe_expert_backward's), with q = w above, dw = scale * dprob, S the picks:
+ *     score 0, renormalize 0: dl_e = [e in S] q_e dw_e - P_e sum_S q dw,
+ *                             P the softmax over all experts
+ *     score 0, renormalize 1: dl_j = q_j (dw_j - sum_S q dw), 0 outside S
+ *     score 1, renormalize 0: dl_j = dw_j s(l_j) (1 - s(l_j))
+ *     score 1, renormalize 1: dl_j = q_j (dw_j - sum_S q dw)(1 - s(l_j))
+ *   topk_idx   the forward's; ids outside [0, num_experts) are skipped, an id
+ *              twice in a row counts twice
+ *   dlogits    out [tokens, num_experts] in the logits' type, every element
+ *              written; rows with a NaN or +inf logit are NaN
+ * ---------------------------------------------------------------------- */
+int moe_router(const void* logits, int dtype, int64_t tokens, int32_t num_experts,
+               int64_t ld_logits, const float* bias, int32_t topk, int score, int renormalize,
+               float scale, int32_t* topk_idx, float* topk_prob, void* stream);
+int moe_router_backward(const void* logits, int dtype, int64_t tokens, int32_t num_experts,
+                        int64_t ld_logits, const int32_t* topk_idx, const float* dprob,
+                        int32_t topk, int score, int renormalize, float scale, void* dlogits,
+                        void* stream);
+
+/* ------------------------------------------------------------------------
+ * Tokens sorted by expert and back, unquantized, with the router weights
+ * applied, and the gradients of both.  The row layout and its arrays are
+ * moe_permute's (x = NULL computes them alone).
+ *   moe_sort_tokens     rows[dst_row[t, j]] = prob[t, j] * x[t]
+ *   moe_sort_tokens_backward
+ *                       dx[t] = sum_j prob[t, j] * drows[dst_row[t, j]]
+ *                       dprob[t, j] = sum_h drows[dst_row[t, j], h] x[t, h]
+ *   moe_unsort_tokens   y[t] = sum_j prob[t, j] * rows[dst_row[t, j]]
+ *   moe_unsort_tokens_backward
+ *                       drows[dst_row[t, j]] = prob[t, j] * dy[t]
+ *                       dprob[t, j] = sum_h rows[dst_row[t, j], h] dy[t, h]
+ * Products and sums in binary32 (j ascending), rounded once; every result is
+ * bitwise reproducible.  prob NULL: all ones, no multiplication.  dprob NULL:
+ * not computed (then x, or rows, may be NULL).  Entries with dst_row outside
+ * [0, rows_cap) move nothing, add nothing and get dprob 0.  The entries'
+ * dst_row are distinct (caller contract).
+ *   x, dy, y, dx   [tokens, ld] / [tokens, hidden] in the dtype code's type
+ *   rows, drows    in:  [rows_cap, ld_rows];  out: [rows_cap, hidden] -- the
+ *                  experts' rows, with zeros in the padding rows (row_src < 0
+ *                  and below expert_offsets[num_experts]); rows at or beyond
+ *                  that offset are not written
+ *   dst_row        int32 [tokens, topk];  row_src int32 [rows_cap]
+ *   expert_offsets int32 [num_experts + 1]
+ *   prob, dprob    float [tokens, topk]
+ * Limits: hidden >= 1; 1 <= topk; tokens * topk, rows_cap < 2^31.
+ * ---------------------------------------------------------------------- */
+int moe_sort_tokens(const void* x, int dtype, int64_t tokens, int64_t hidden, int64_t ld_x,
+                    const int32_t* dst_row, const float* prob, int32_t topk,
+                    const int32_t* row_src, const int32_t* expert_offsets, int32_t num_experts,
+                    int64_t rows_cap, void* rows, void* stream);
+int moe_sort_tokens_backward(const void* drows, int dtype, int64_t tokens, int64_t hidden,
+                             int64_t ld_rows, int64_t rows_cap, const int32_t* dst_row,
+                             const float* prob, int32_t topk, const void* x, int64_t ld_x,
+                             void* dx, float* dprob, void* stream);
+int moe_unsort_tokens(const void* rows, int dtype, int64_t tokens, int64_t hidden, int64_t ld_rows,
+                      int64_t rows_cap, const int32_t* dst_row, const float* prob, int32_t topk,
+                      void* y, void* stream);
+int moe_unsort_tokens_backward(const void* dy, int dtype, int64_t tokens, int64_t hidden,
+                               int64_t ld_dy, const int32_t* dst_row, const float* prob,
+                               int32_t topk, const int32_t* row_src,
+                               const int32_t* expert_offsets, int32_t num_experts,
+                               int64_t rows_cap, const void* rows, int64_t ld_rows, void* drows,
+                               float* dprob, void* stream);
+
+/* ------------------------------------------------------------------------
+ * nvfp4_matvec -- products of a few unquantized rows with one NVFP4 matrix
+ * (4-bit weights, 16-bit or 32-bit activations: a projection of new tokens):
+ *   out[t, i] = s_g * sum_k (q s_b)[i, k] * x[t, k]
+ * nvfp4_expert_matvec -- the same with the matrix of every entry's expert:
+ *   out[t, j, i] = s_g[e] * sum_k (q s_b)[e, i, k] * x[t, k]   e = topk_idx[t, j]
+ * (x_by_entry: x[t, j, k]); entries with an id outside [0, num_experts) get
+ * zeros.  An expert's weights are read once for up to 16 of its entries.
+ * Weights are exact in the matrix cores' operands and x is used as it is
+ * (binary32 x as the exact sum of three bf16 parts), sums are binary32:
+ * |out - exact| <= (k + 16) * 2^-24 * sum_k |w x| before the output's
+ * rounding.  Every result is bitwise reproducible.
+ *   x          [tokens, ld_x] (x_by_entry: [tokens * topk, ld_x]), dtype code
+ *   w          NVFP4 weights [n, k] / [num_experts, n, k]; layout 0, or 1
+ *              (nvfp4_pack_weights) where n % 32 == 0 and k % 128 == 0
+ *   out        [tokens, n] / [tokens, topk, n], out_dtype code
+ * Limits: k % 16 == 0, 16 <= k <= 16384; n >= 1; num_experts <= 1024; one
+ * matrix's codes below 2^31 bytes; nvfp4_matvec: tokens <= 65536;
+ * nvfp4_expert_matvec: tokens * topk <= 4096 (NVFP4_UNSUPPORTED beyond; the
+ * grouped GEMM is the operator for more).
+ *
+ * moe_expert_decode -- the expert layer for a few tokens (decoding) on
+ * unquantized activations:
+ *   h = W1[e] x[t];  D = silu(h[:inter]) * h[inter:] * topk_prob[t, j]
+ *   y[t] = sum_j W2[e] D
+ * with the products above, D kept to 2^-17 relative (the sum of two bf16
+ * parts) and the sum over j ascending in binary32, rounded once to y's type
+ * (x's).  The weights are moe_expert_forward's, in either layout.
+ *   workspace  moe_expert_decode_workspace_size() bytes, 16-byte aligned;
+ *              every word read is written before by the same call
+ * Limits: hidden % 16 == 0, inter % 16 == 0, both <= 16384 (% 128 with layout
+ * 1); 1 <= topk <= num_experts <= 1024; tokens * topk <= 4096.
+ * ---------------------------------------------------------------------- */
+int nvfp4_matvec(const void* x, int x_dtype, int64_t tokens, int64_t ld_x, const nvfp4_weights* w,
+                 int64_t n, int64_t k, int out_dtype, void* out, void* stream);
+int nvfp4_expert_matvec(const void* x, int x_dtype, int64_t tokens, int64_t ld_x, int x_by_entry,
+                        const int32_t* topk_idx, int32_t topk, const nvfp4_weights* w,
+                        int32_t num_experts, int64_t n, int64_t k, int out_dtype, void* out,
+                        void* stream);
+size_t moe_expert_decode_workspace_size(int64_t tokens, int64_t hidden, int64_t inter,
+                                        int32_t topk);
+int moe_expert_decode(const void* x, int x_dtype, int64_t tokens, int64_t hidden, int64_t inter,
+                      int64_t ld_x, const int32_t* topk_idx, const float* topk_prob, int32_t topk,
+                      int32_t num_experts, const nvfp4_weights* w1, const nvfp4_weights* w2,
+                      void* y, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * Profiling helpers: thin wrappers over hipEventCreate / hipEventRecord /
  * hipEventElapsedTime / hipEventDestroy so a caller without HIP headers can
  * time the stages of moe_expert_forward on its stream.  (These allocate a

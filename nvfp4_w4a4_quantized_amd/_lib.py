@@ -118,6 +118,35 @@ def _load(path):
     L.moe_expert_backward.argtypes = [_vp, _vp, _i64, _i64, _i64, _i32, _i32, _i64, _vp, _vp,
                                       _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                       C.c_size_t, C.POINTER(BackwardIntermediates), _vp, _vp]
+    L.moe_router.restype = C.c_int
+    L.moe_router.argtypes = [_vp, C.c_int, _i64, _i32, _i64, _vp, _i32, C.c_int, C.c_int,
+                             C.c_float, _vp, _vp, _vp]
+    L.moe_router_backward.restype = C.c_int
+    L.moe_router_backward.argtypes = [_vp, C.c_int, _i64, _i32, _i64, _vp, _vp, _i32, C.c_int,
+                                      C.c_int, C.c_float, _vp, _vp]
+    L.moe_sort_tokens.restype = C.c_int
+    L.moe_sort_tokens.argtypes = [_vp, C.c_int, _i64, _i64, _i64, _vp, _vp, _i32, _vp, _vp, _i32,
+                                  _i64, _vp, _vp]
+    L.moe_sort_tokens_backward.restype = C.c_int
+    L.moe_sort_tokens_backward.argtypes = [_vp, C.c_int, _i64, _i64, _i64, _i64, _vp, _vp, _i32,
+                                           _vp, _i64, _vp, _vp, _vp]
+    L.moe_unsort_tokens.restype = C.c_int
+    L.moe_unsort_tokens.argtypes = [_vp, C.c_int, _i64, _i64, _i64, _i64, _vp, _vp, _i32, _vp, _vp]
+    L.moe_unsort_tokens_backward.restype = C.c_int
+    L.moe_unsort_tokens_backward.argtypes = [_vp, C.c_int, _i64, _i64, _i64, _vp, _vp, _i32, _vp,
+                                             _vp, _i32, _i64, _vp, _i64, _vp, _vp, _vp]
+    L.nvfp4_matvec.restype = C.c_int
+    L.nvfp4_matvec.argtypes = [_vp, C.c_int, _i64, _i64, C.POINTER(Weights), _i64, _i64, C.c_int,
+                               _vp, _vp]
+    L.nvfp4_expert_matvec.restype = C.c_int
+    L.nvfp4_expert_matvec.argtypes = [_vp, C.c_int, _i64, _i64, C.c_int, _vp, _i32,
+                                      C.POINTER(Weights), _i32, _i64, _i64, C.c_int, _vp, _vp]
+    L.moe_expert_decode_workspace_size.restype = C.c_size_t
+    L.moe_expert_decode_workspace_size.argtypes = [_i64, _i64, _i64, _i32]
+    L.moe_expert_decode.restype = C.c_int
+    L.moe_expert_decode.argtypes = [_vp, C.c_int, _i64, _i64, _i64, _i64, _vp, _vp, _i32, _i32,
+                                    C.POINTER(Weights), C.POINTER(Weights), _vp, _vp, C.c_size_t,
+                                    _vp]
     L.nvfp4_event_create.restype = C.c_int
     L.nvfp4_event_create.argtypes = [C.POINTER(_vp)]
     L.nvfp4_event_record.restype = C.c_int

@@ -613,6 +613,264 @@ int nvfp4_pack_weights(const uint8_t* codes, const uint8_t* scales, int32_t num_
                                   packed_scales, static_cast<hipStream_t>(stream)));
 }
 
+// ---- operators on unquantized tensors ----
+
+static bool valid_dtype(int d) { return d >= 0 && d <= 2; }
+static size_t dtype_size(int d) { return d == 0 ? 4 : 2; }
+
+static int router_args_status(const void* logits, int dtype, int64_t tokens, int32_t num_experts,
+                              int64_t ld, int32_t topk, int score, int renormalize, float scale) {
+  if (!valid_dtype(dtype) || tokens < 0 || num_experts < 1 || num_experts > kMaxExperts ||
+      topk < 1 || topk > num_experts || ld < num_experts)
+    return NVFP4_INVALID_ARGUMENT;
+  if (score != 0 && score != 1) return NVFP4_INVALID_ARGUMENT;
+  if (renormalize != 0 && renormalize != 1) return NVFP4_INVALID_ARGUMENT;
+  if (!(scale - scale == 0.0f)) return NVFP4_INVALID_ARGUMENT;   // Inf or NaN
+  if (tokens > 0x7FFFFFFELL / topk) return NVFP4_INVALID_ARGUMENT;
+  if (tokens > 0 && !logits) return NVFP4_INVALID_ARGUMENT;
+  if (!aligned(logits, dtype_size(dtype))) return NVFP4_INVALID_ARGUMENT;
+  return NVFP4_OK;
+}
+
+int moe_router(const void* logits, int dtype, int64_t tokens, int32_t num_experts,
+               int64_t ld_logits, const float* bias, int32_t topk, int score, int renormalize,
+               float scale, int32_t* topk_idx, float* topk_prob, void* stream) {
+  const int st = router_args_status(logits, dtype, tokens, num_experts, ld_logits, topk, score,
+                                    renormalize, scale);
+  if (st != NVFP4_OK) return st;
+  if (tokens > 0 && (!topk_idx || !topk_prob)) return NVFP4_INVALID_ARGUMENT;
+  if (!aligned(bias, 4) || !aligned(topk_idx, 4) || !aligned(topk_prob, 4))
+    return NVFP4_INVALID_ARGUMENT;
+  RouterArgs a{logits, dtype, tokens, num_experts, ld_logits, bias,
+               topk,   score, renormalize, scale, topk_idx, topk_prob};
+  return hip_status(launch_router(a, static_cast<hipStream_t>(stream)));
+}
+
+int moe_router_backward(const void* logits, int dtype, int64_t tokens, int32_t num_experts,
+                        int64_t ld_logits, const int32_t* topk_idx, const float* dprob,
+                        int32_t topk, int score, int renormalize, float scale, void* dlogits,
+                        void* stream) {
+  const int st = router_args_status(logits, dtype, tokens, num_experts, ld_logits, topk, score,
+                                    renormalize, scale);
+  if (st != NVFP4_OK) return st;
+  if (tokens > 0 && (!topk_idx || !dprob || !dlogits)) return NVFP4_INVALID_ARGUMENT;
+  if (!aligned(topk_idx, 4) || !aligned(dprob, 4) || !aligned(dlogits, dtype_size(dtype)))
+    return NVFP4_INVALID_ARGUMENT;
+  RouterBackwardArgs a{logits, dtype, tokens, num_experts, ld_logits, topk_idx, dprob,
+                       topk,   score, renormalize, scale, dlogits};
+  return hip_status(launch_router_backward(a, static_cast<hipStream_t>(stream)));
+}
+
+// Checks shared by the four token movements: `tok` / `rows` are the token
+// and row tensors the call reads or writes (with their row distances).
+static int token_rows_status(int dtype, int64_t tokens, int64_t hidden, int32_t topk,
+                             int64_t rows_cap, const int32_t* dst_row, const float* prob,
+                             const float* dprob, const void* tok, int64_t ld_tok,
+                             const void* rows, int64_t ld_rows) {
+  if (!valid_dtype(dtype) || tokens < 0 || hidden < 1 || topk < 1 || rows_cap < 0 ||
+      rows_cap >= 0x7FFFFFFFLL || tokens > 0x7FFFFFFELL / topk)
+    return NVFP4_INVALID_ARGUMENT;
+  if (hidden > 0x7FFFFFFFLL) return NVFP4_UNSUPPORTED;
+  if (ld_tok < hidden || ld_rows < hidden) return NVFP4_INVALID_ARGUMENT;
+  if (tokens > 0 && (!tok || !dst_row)) return NVFP4_INVALID_ARGUMENT;
+  if (rows_cap > 0 && !rows) return NVFP4_INVALID_ARGUMENT;
+  const size_t es = dtype_size(dtype);
+  if (!aligned(tok, es) || !aligned(rows, es) || !aligned(dst_row, 4) || !aligned(prob, 4) ||
+      !aligned(dprob, 4))
+    return NVFP4_INVALID_ARGUMENT;
+  return NVFP4_OK;
+}
+
+static int spread_status(const int32_t* row_src, const int32_t* expert_offsets,
+                         int32_t num_experts, int64_t rows_cap) {
+  if (num_experts < 1 || num_experts > kMaxExperts || !expert_offsets ||
+      (rows_cap > 0 && !row_src) || !aligned(row_src, 4) || !aligned(expert_offsets, 4))
+    return NVFP4_INVALID_ARGUMENT;
+  return NVFP4_OK;
+}
+
+int moe_sort_tokens(const void* x, int dtype, int64_t tokens, int64_t hidden, int64_t ld_x,
+                    const int32_t* dst_row, const float* prob, int32_t topk,
+                    const int32_t* row_src, const int32_t* expert_offsets, int32_t num_experts,
+                    int64_t rows_cap, void* rows, void* stream) {
+  int st = token_rows_status(dtype, tokens, hidden, topk, rows_cap, dst_row, prob, nullptr, x,
+                             ld_x, rows, hidden);
+  if (st == NVFP4_OK) st = spread_status(row_src, expert_offsets, num_experts, rows_cap);
+  if (st != NVFP4_OK) return st;
+  TokenRowsArgs a{};
+  a.dtype = dtype; a.tokens = tokens; a.hidden = hidden; a.topk = topk; a.rows_cap = rows_cap;
+  a.dst_row = dst_row; a.prob = prob; a.tok = x; a.ld_tok = ld_x;
+  a.row_src = row_src; a.rows_end = expert_offsets + num_experts; a.rows_out = rows;
+  return hip_status(launch_spread(a, static_cast<hipStream_t>(stream)));
+}
+
+int moe_sort_tokens_backward(const void* drows, int dtype, int64_t tokens, int64_t hidden,
+                             int64_t ld_rows, int64_t rows_cap, const int32_t* dst_row,
+                             const float* prob, int32_t topk, const void* x, int64_t ld_x,
+                             void* dx, float* dprob, void* stream) {
+  const int st = token_rows_status(dtype, tokens, hidden, topk, rows_cap, dst_row, prob, dprob, dx,
+                                   hidden, drows, ld_rows);
+  if (st != NVFP4_OK) return st;
+  if (dprob && tokens > 0 && (!x || ld_x < hidden || !aligned(x, dtype_size(dtype))))
+    return NVFP4_INVALID_ARGUMENT;
+  TokenRowsArgs a{};
+  a.dtype = dtype; a.tokens = tokens; a.hidden = hidden; a.topk = topk; a.rows_cap = rows_cap;
+  a.dst_row = dst_row; a.prob = prob; a.dprob = dprob; a.given = x; a.ld_given = ld_x;
+  a.rows = drows; a.ld_rows = ld_rows; a.tok_out = dx;
+  return hip_status(launch_collect(a, static_cast<hipStream_t>(stream)));
+}
+
+int moe_unsort_tokens(const void* rows, int dtype, int64_t tokens, int64_t hidden, int64_t ld_rows,
+                      int64_t rows_cap, const int32_t* dst_row, const float* prob, int32_t topk,
+                      void* y, void* stream) {
+  const int st = token_rows_status(dtype, tokens, hidden, topk, rows_cap, dst_row, prob, nullptr,
+                                   y, hidden, rows, ld_rows);
+  if (st != NVFP4_OK) return st;
+  TokenRowsArgs a{};
+  a.dtype = dtype; a.tokens = tokens; a.hidden = hidden; a.topk = topk; a.rows_cap = rows_cap;
+  a.dst_row = dst_row; a.prob = prob; a.rows = rows; a.ld_rows = ld_rows; a.tok_out = y;
+  return hip_status(launch_collect(a, static_cast<hipStream_t>(stream)));
+}
+
+int moe_unsort_tokens_backward(const void* dy, int dtype, int64_t tokens, int64_t hidden,
+                               int64_t ld_dy, const int32_t* dst_row, const float* prob,
+                               int32_t topk, const int32_t* row_src,
+                               const int32_t* expert_offsets, int32_t num_experts,
+                               int64_t rows_cap, const void* rows, int64_t ld_rows, void* drows,
+                               float* dprob, void* stream) {
+  int st = token_rows_status(dtype, tokens, hidden, topk, rows_cap, dst_row, prob, dprob, dy,
+                             ld_dy, drows, hidden);
+  if (st == NVFP4_OK) st = spread_status(row_src, expert_offsets, num_experts, rows_cap);
+  if (st != NVFP4_OK) return st;
+  if (dprob && rows_cap > 0 && (!rows || ld_rows < hidden || !aligned(rows, dtype_size(dtype))))
+    return NVFP4_INVALID_ARGUMENT;
+  TokenRowsArgs a{};
+  a.dtype = dtype; a.tokens = tokens; a.hidden = hidden; a.topk = topk; a.rows_cap = rows_cap;
+  a.dst_row = dst_row; a.prob = prob; a.dprob = dprob; a.given = rows; a.ld_given = ld_rows;
+  a.tok = dy; a.ld_tok = ld_dy;
+  a.row_src = row_src; a.rows_end = expert_offsets + num_experts; a.rows_out = drows;
+  return hip_status(launch_spread(a, static_cast<hipStream_t>(stream)));
+}
+
+// Most entries (tokens * topk) of an expert call: their list lies in LDS.
+constexpr int64_t kMaxEntries = 4096;
+
+static int matvec_weights_status(const nvfp4_weights* w, int64_t n, int64_t k) {
+  if (!w || !w->codes || !w->scales || !w->gscale || (w->layout != 0 && w->layout != 1) ||
+      !aligned(w->gscale, 4))
+    return NVFP4_INVALID_ARGUMENT;
+  if (n < 1 || k < 16 || k % 16 != 0) return NVFP4_INVALID_ARGUMENT;
+  if (k > kMaxK || n > 0x7FFFFFFFLL / (k / 2)) return NVFP4_UNSUPPORTED;
+  if (w->layout == 1) {
+    if (n % 32 != 0 || k % 128 != 0) return NVFP4_UNSUPPORTED;
+    if (!aligned(w->codes, 16) || !aligned(w->scales, 4)) return NVFP4_INVALID_ARGUMENT;
+  }
+  return NVFP4_OK;
+}
+
+static MatvecArgs matvec_args(const void* x, int x_dtype, int64_t ld_x, int64_t tokens,
+                              const nvfp4_weights* w, int32_t groups, int64_t n, int64_t k) {
+  MatvecArgs a{};
+  a.x = x; a.x_dtype = x_dtype; a.ld_x = ld_x; a.tokens = tokens;
+  a.codes = w->codes; a.scales = w->scales; a.gscale = w->gscale; a.layout = w->layout;
+  a.num_groups = groups; a.n = n; a.k = k; a.topk = 1;
+  return a;
+}
+
+int nvfp4_matvec(const void* x, int x_dtype, int64_t tokens, int64_t ld_x, const nvfp4_weights* w,
+                 int64_t n, int64_t k, int out_dtype, void* out, void* stream) {
+  const int st = matvec_weights_status(w, n, k);
+  if (st != NVFP4_OK) return st;
+  if (!valid_dtype(x_dtype) || !valid_dtype(out_dtype) || tokens < 0 || ld_x < k)
+    return NVFP4_INVALID_ARGUMENT;
+  if (tokens > 65536) return NVFP4_UNSUPPORTED;
+  if (tokens > 0 && (!x || !out)) return NVFP4_INVALID_ARGUMENT;
+  if (!aligned(x, dtype_size(x_dtype)) || !aligned(out, dtype_size(out_dtype)))
+    return NVFP4_INVALID_ARGUMENT;
+  MatvecArgs a = matvec_args(x, x_dtype, ld_x, tokens, w, 1, n, k);
+  a.out = out; a.out_dtype = out_dtype;
+  return hip_status(launch_matvec(a, static_cast<hipStream_t>(stream)));
+}
+
+int nvfp4_expert_matvec(const void* x, int x_dtype, int64_t tokens, int64_t ld_x, int x_by_entry,
+                        const int32_t* topk_idx, int32_t topk, const nvfp4_weights* w,
+                        int32_t num_experts, int64_t n, int64_t k, int out_dtype, void* out,
+                        void* stream) {
+  const int st = matvec_weights_status(w, n, k);
+  if (st != NVFP4_OK) return st;
+  if (!valid_dtype(x_dtype) || !valid_dtype(out_dtype) || tokens < 0 || ld_x < k || topk < 1 ||
+      num_experts < 1 || num_experts > kMaxExperts || (x_by_entry != 0 && x_by_entry != 1))
+    return NVFP4_INVALID_ARGUMENT;
+  if (tokens > kMaxEntries / topk) return NVFP4_UNSUPPORTED;
+  if (tokens > 0 && (!x || !out || !topk_idx)) return NVFP4_INVALID_ARGUMENT;
+  if (!aligned(x, dtype_size(x_dtype)) || !aligned(out, dtype_size(out_dtype)) ||
+      !aligned(topk_idx, 4))
+    return NVFP4_INVALID_ARGUMENT;
+  MatvecArgs a = matvec_args(x, x_dtype, ld_x, tokens, w, num_experts, n, k);
+  a.x_by_entry = x_by_entry; a.topk_idx = topk_idx; a.topk = topk;
+  a.out = out; a.out_dtype = out_dtype;
+  return hip_status(launch_matvec(a, static_cast<hipStream_t>(stream)));
+}
+
+struct DecodeLayout {
+  uint16_t* d_hi; uint16_t* d_lo;   // FC2's input, two bf16 parts [entries, inter]
+  float* y_rows;                    // FC2's output [entries, hidden]
+  size_t bytes;
+};
+
+static DecodeLayout carve_decode(void* ws, int64_t entries, int64_t hidden, int64_t inter) {
+  Carver c(ws);
+  DecodeLayout L;
+  L.d_hi = c.take<uint16_t>((size_t)(entries * inter));
+  L.d_lo = c.take<uint16_t>((size_t)(entries * inter));
+  L.y_rows = c.take<float>((size_t)(entries * hidden));
+  L.bytes = c.used;
+  return L;
+}
+
+size_t moe_expert_decode_workspace_size(int64_t tokens, int64_t hidden, int64_t inter,
+                                        int32_t topk) {
+  if (tokens < 0 || topk < 1 || tokens > kMaxEntries / topk || hidden < 0 || inter < 0 ||
+      hidden > kMaxK || inter > kMaxK)
+    return 0;
+  return carve_decode(nullptr, tokens * topk, hidden, inter).bytes;
+}
+
+int moe_expert_decode(const void* x, int x_dtype, int64_t tokens, int64_t hidden, int64_t inter,
+                      int64_t ld_x, const int32_t* topk_idx, const float* topk_prob, int32_t topk,
+                      int32_t num_experts, const nvfp4_weights* w1, const nvfp4_weights* w2,
+                      void* y, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!valid_dtype(x_dtype) || tokens < 0 || ld_x < hidden || topk < 1 || num_experts < 1 ||
+      num_experts > kMaxExperts || topk > num_experts)
+    return NVFP4_INVALID_ARGUMENT;
+  if (hidden < 16 || hidden % 16 != 0 || inter < 16 || inter % 16 != 0 || hidden > kMaxK ||
+      inter > kMaxK)
+    return NVFP4_UNSUPPORTED;
+  int st = matvec_weights_status(w1, 2 * inter, hidden);
+  if (st == NVFP4_OK) st = matvec_weights_status(w2, hidden, inter);
+  if (st != NVFP4_OK) return st;
+  if (w1->layout == 1 && inter % 32 != 0) return NVFP4_UNSUPPORTED;
+  if (tokens > kMaxEntries / topk) return NVFP4_UNSUPPORTED;
+  if (tokens == 0) return NVFP4_OK;
+  if (!x || !y || !topk_idx || !topk_prob || !workspace) return NVFP4_INVALID_ARGUMENT;
+  if (!aligned(x, dtype_size(x_dtype)) || !aligned(y, dtype_size(x_dtype)) ||
+      !aligned(topk_idx, 4) || !aligned(topk_prob, 4) || !aligned(workspace, 16))
+    return NVFP4_INVALID_ARGUMENT;
+  const DecodeLayout L = carve_decode(workspace, tokens * topk, hidden, inter);
+  if (workspace_bytes < L.bytes) return NVFP4_WORKSPACE_TOO_SMALL;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  MatvecArgs f1 = matvec_args(x, x_dtype, ld_x, tokens, w1, num_experts, 2 * inter, hidden);
+  f1.topk_idx = topk_idx; f1.topk = topk; f1.prob = topk_prob;
+  f1.d_hi = L.d_hi; f1.d_lo = L.d_lo; f1.inter = inter;
+  if (launch_matvec(f1, s) != hipSuccess) return NVFP4_HIP_ERROR;
+  MatvecArgs f2 = matvec_args(L.d_hi, 1, inter, tokens, w2, num_experts, hidden, inter);
+  f2.x_lo = L.d_lo; f2.x_by_entry = 1; f2.topk_idx = topk_idx; f2.topk = topk;
+  f2.out = L.y_rows; f2.out_dtype = 0;
+  if (launch_matvec(f2, s) != hipSuccess) return NVFP4_HIP_ERROR;
+  return hip_status(launch_decode_combine(L.y_rows, topk_idx, tokens, topk, num_experts, hidden,
+                                          x_dtype, y, s));
+}
+
 int nvfp4_event_create(void** event) {
   if (!event) return NVFP4_INVALID_ARGUMENT;
   hipEvent_t ev;

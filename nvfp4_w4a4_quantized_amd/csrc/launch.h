@@ -194,4 +194,59 @@ hipError_t launch_combine(const void* y_rows, int y_rows_dtype, const int32_t* d
                           int64_t tokens, int32_t topk, int64_t hidden, uint16_t* y,
                           hipStream_t s);
 
+// ---- router.hip ----
+struct RouterArgs {
+  const void* logits; int dtype; int64_t tokens; int32_t num_experts; int64_t ld;
+  const float* bias;          // nullable [num_experts], added for the choice only
+  int32_t topk; int score; int renormalize; float scale;
+  int32_t* topk_idx; float* topk_prob;
+};
+struct RouterBackwardArgs {
+  const void* logits; int dtype; int64_t tokens; int32_t num_experts; int64_t ld;
+  const int32_t* topk_idx; const float* dprob;
+  int32_t topk; int score; int renormalize; float scale;
+  void* dlogits;              // [tokens, num_experts]
+};
+hipError_t launch_router(const RouterArgs& a, hipStream_t s);
+hipError_t launch_router_backward(const RouterBackwardArgs& a, hipStream_t s);
+
+// ---- tokens.hip ----
+// Tokens to rows (launch_spread) and rows to tokens (launch_collect); dtype
+// codes 0 binary32, 1 bf16, 2 fp16 for every tensor but prob and dprob.
+struct TokenRowsArgs {
+  int dtype;
+  int64_t tokens, hidden; int32_t topk; int64_t rows_cap;
+  const int32_t* dst_row;     // [tokens, topk]
+  const float* prob;          // nullable [tokens, topk]
+  float* dprob;               // nullable [tokens, topk]: the weights' gradient, from `given`
+  const void* given; int64_t ld_given;   // spread: rows; collect: tokens
+  // spread
+  const void* tok; int64_t ld_tok;
+  const int32_t* row_src; const int32_t* rows_end;   // padding rows: row_src < 0, below *rows_end
+  void* rows_out;             // [rows_cap, hidden]
+  // collect
+  const void* rows; int64_t ld_rows;
+  void* tok_out;              // [tokens, hidden]
+};
+hipError_t launch_spread(const TokenRowsArgs& a, hipStream_t s);
+hipError_t launch_collect(const TokenRowsArgs& a, hipStream_t s);
+
+// ---- matvec.hip ----
+struct MatvecArgs {
+  const void* x; int x_dtype; int64_t ld_x;   // 0 binary32, 1 bf16, 2 fp16
+  const uint16_t* x_lo;       // non-NULL: x is bf16 high parts, these the low parts
+  int x_by_entry;             // x has a row per entry, not per token
+  int64_t tokens;
+  const uint8_t* codes; const uint8_t* scales; const float* gscale; int layout;
+  int32_t num_groups; int64_t n, k;
+  const int32_t* topk_idx; int32_t topk;      // NULL, 1: one matrix for every row
+  void* out; int out_dtype;   // [rows, n]
+  // SwiGLU epilogue (n = 2 * inter): the two parts of D, [entries, inter]
+  uint16_t* d_hi; uint16_t* d_lo; int64_t inter; const float* prob;
+};
+hipError_t launch_matvec(const MatvecArgs& a, hipStream_t s);
+hipError_t launch_decode_combine(const float* y_rows, const int32_t* idx, int64_t tokens,
+                                 int32_t topk, int32_t num_experts, int64_t hidden, int y_dtype,
+                                 void* y, hipStream_t s);
+
 }  // namespace nvfp4

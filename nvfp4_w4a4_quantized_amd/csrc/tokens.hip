@@ -1,0 +1,282 @@
+// tokens.hip -- tokens sorted by expert and back, in the tensors' own type
+// (binary32, bf16 or fp16), with the router weights applied and the gradients
+// of both.  With r = dst_row[t, j] the row of entry (t, j):
+//   spread   rows[r] = w[t, j] tok[t]                (sort; unsort's gradient)
+//            dw[t, j] = sum_h tok[t, h] given[r, h]  (unsort's weight gradient)
+//   collect  tok[t] = sum_j w[t, j] rows[r]          (unsort; sort's gradient)
+//            dw[t, j] = sum_h rows[r, h] given[t, h] (sort's weight gradient)
+// Products and sums are binary32 (j ascending; a dot product's order is fixed
+// by the launch), rounded once to the tensors' type.  Entries with dst_row
+// outside [0, rows) move nothing and have a zero weight gradient.
+//
+// Bound: HBM.  A token's row is read once and its k rows written (or read)
+// once, so a workgroup takes a whole token: its threads hold 16-byte pieces
+// of the row and loop over the entries, all of whose loads are issued before
+// the first is used.  The weight gradient is taken on the way from the same
+// registers.
+#include "elem.h"
+#include "launch.h"
+
+namespace nvfp4 {
+
+namespace {
+
+constexpr int kBatch = 8;   // entries whose rows are in flight together
+
+// Sums of n <= kBatch values over the workgroup; every thread gets them all.
+__device__ __forceinline__ void block_sums(float (&v)[kBatch], int n, float* lds) {
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  const int waves = blockDim.x / kWave;
+#pragma unroll
+  for (int j = 0; j < kBatch; ++j) {
+    if (j < n) {
+      float s = __uint_as_float(wave_incl_scan_dpp(
+          __float_as_uint(v[j]), [](uint32_t a, uint32_t b) {
+            return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+          }));
+      v[j] = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(s), kWave - 1));
+    }
+  }
+  if (waves == 1) return;
+  __syncthreads();   // the previous batch's sums have been read
+  if (lane == 0) {
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) lds[wave * kBatch + j] = v[j];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kBatch; ++j) {
+    float s = lds[j];
+    for (int w = 1; w < waves; ++w) s += lds[w * kBatch + j];
+    v[j] = s;
+  }
+}
+
+// Row of entry (t, j), -1 if it has none.
+__device__ __forceinline__ int64_t entry_row(const TokenRowsArgs& a, int64_t t, int j) {
+  const int64_t i = t * a.topk + j;
+  const int64_t r = a.dst_row[i];
+  return r >= 0 && r < a.rows_cap ? r : -1;
+}
+
+}  // namespace
+
+// Spread: blocks [0, token_blocks) take tokens, the rest zero the padding
+// rows (row_src < 0) inside the experts' segments, `pad_rows` rows each.
+template <int DT, bool WEIGHTED, bool DOT>
+__global__ __launch_bounds__(256) void spread_kernel(TokenRowsArgs a, int64_t token_blocks,
+                                                     int pad_rows) {
+  typedef typename Elem<DT>::type T;
+  typedef Piece<DT> P;
+  __shared__ float sums[4 * kBatch];
+  T* rows = static_cast<T*>(a.rows_out);
+  if ((int64_t)blockIdx.x >= token_blocks) {
+    const int64_t end = *a.rows_end < a.rows_cap ? *a.rows_end : a.rows_cap;
+    const int64_t r0 = (int64_t)(blockIdx.x - token_blocks) * pad_rows;
+    const int64_t r1 = r0 + pad_rows < end ? r0 + pad_rows : end;
+    P zero;
+    zero.load_part(rows, 0);
+    for (int64_t b = r0; b < r1; b += kWave) {
+      // every wave takes the same ballot, so the workgroup clears each row together
+      const int64_t r = b + threadIdx.x % kWave;
+      const bool pad = r < r1 && a.row_src[r] < 0;
+      for (uint64_t m = __ballot(pad); m != 0; m &= m - 1) {
+        T* row = rows + (b + __builtin_ctzll(m)) * a.hidden;
+        for (int64_t c = (int64_t)threadIdx.x * P::kN; c < a.hidden; c += (int64_t)blockDim.x * P::kN) {
+          if (c + P::kN <= a.hidden) zero.store(row + c);
+          else zero.store_part(row + c, (int)(a.hidden - c));
+        }
+      }
+    }
+    return;
+  }
+  for (int64_t t = blockIdx.x; t < a.tokens; t += token_blocks) {
+    const T* tok = static_cast<const T*>(a.tok) + t * a.ld_tok;
+    for (int j0 = 0; j0 < a.topk; j0 += kBatch) {
+      const int n = a.topk - j0 < kBatch ? a.topk - j0 : kBatch;
+      int64_t row[kBatch];
+      float w[kBatch], dot[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        row[j] = j < n ? entry_row(a, t, j0 + j) : -1;
+        w[j] = WEIGHTED && row[j] >= 0 ? a.prob[t * a.topk + j0 + j] : 1.0f;
+        dot[j] = 0.0f;
+      }
+      for (int64_t c = (int64_t)threadIdx.x * P::kN; c < a.hidden; c += (int64_t)blockDim.x * P::kN) {
+        const bool whole = c + P::kN <= a.hidden;
+        const int part = (int)(a.hidden - c);
+        P x;
+        if (whole) x.load(tok + c);
+        else x.load_part(tok + c, part);
+        P g[DOT ? kBatch : 1];
+        if (DOT) {
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) {
+            if (row[j] < 0) continue;
+            const T* src = static_cast<const T*>(a.given) + row[j] * a.ld_given + c;
+            if (whole) g[DOT ? j : 0].load(src);
+            else g[DOT ? j : 0].load_part(src, part);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          if (row[j] < 0) continue;
+          P o = x;
+          if (WEIGHTED) {
+#pragma unroll
+            for (int i = 0; i < P::kN; ++i) o.set(i, x.get(i) * w[j]);
+          }
+          T* dst = rows + row[j] * a.hidden + c;
+          if (whole) o.store(dst);
+          else o.store_part(dst, part);
+          if (DOT) {
+#pragma unroll
+            for (int i = 0; i < P::kN; ++i) dot[j] += x.get(i) * g[DOT ? j : 0].get(i);
+          }
+        }
+      }
+      if (DOT) {
+        block_sums(dot, n, sums);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+          if ((int)threadIdx.x == j && j < n)
+            a.dprob[t * a.topk + j0 + j] = row[j] >= 0 ? dot[j] : 0.0f;
+      }
+    }
+  }
+}
+
+template <int DT, bool WEIGHTED, bool DOT>
+__global__ __launch_bounds__(256) void collect_kernel(TokenRowsArgs a) {
+  typedef typename Elem<DT>::type T;
+  typedef Piece<DT> P;
+  __shared__ float sums[4 * kBatch];
+  for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
+    T* out = static_cast<T*>(a.tok_out) + t * a.hidden;
+    const T* given = DOT ? static_cast<const T*>(a.given) + t * a.ld_given : nullptr;
+    // Columns outermost while one batch holds every entry; with more entries
+    // the dot products need the entries outermost, so the column's sum is
+    // then taken over the batches in an inner loop of its own.
+    for (int j0 = 0; j0 < (DOT ? a.topk : 1); j0 += kBatch) {
+      float dot[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) dot[j] = 0.0f;
+      for (int64_t c = (int64_t)threadIdx.x * P::kN; c < a.hidden; c += (int64_t)blockDim.x * P::kN) {
+        const bool whole = c + P::kN <= a.hidden;
+        const int part = (int)(a.hidden - c);
+        float sum[P::kN];
+#pragma unroll
+        for (int i = 0; i < P::kN; ++i) sum[i] = 0.0f;
+        P x;
+        if (DOT) {
+          if (whole) x.load(given + c);
+          else x.load_part(given + c, part);
+        }
+        // the first pass over the columns takes every entry into the sum,
+        // a later one (topk > kBatch) only its own entries' dot products
+        const int last = j0 == 0 ? a.topk : (j0 + kBatch < a.topk ? j0 + kBatch : a.topk);
+        for (int b = j0; b < last; b += kBatch) {
+          P p[kBatch];
+          int64_t row[kBatch];
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) {
+            row[j] = b + j < last ? entry_row(a, t, b + j) : -1;
+            if (row[j] < 0) continue;
+            const T* src = static_cast<const T*>(a.rows) + row[j] * a.ld_rows + c;
+            if (whole) p[j].load(src);
+            else p[j].load_part(src, part);
+          }
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) {
+            if (row[j] < 0) continue;
+            if (j0 == 0) {
+              const float w = WEIGHTED ? a.prob[t * a.topk + b + j] : 1.0f;
+#pragma unroll
+              for (int i = 0; i < P::kN; ++i)
+                sum[i] += WEIGHTED ? w * p[j].get(i) : p[j].get(i);
+            }
+            if (DOT && b == j0) {
+#pragma unroll
+              for (int i = 0; i < P::kN; ++i) dot[j] += x.get(i) * p[j].get(i);
+            }
+          }
+        }
+        if (j0 == 0) {
+          P o;
+#pragma unroll
+          for (int i = 0; i < P::kN; ++i) o.set(i, sum[i]);
+          if (whole) o.store(out + c);
+          else o.store_part(out + c, part);
+        }
+      }
+      if (DOT) {
+        const int n = a.topk - j0 < kBatch ? a.topk - j0 : kBatch;
+        block_sums(dot, n, sums);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+          if ((int)threadIdx.x == j && j < n)
+            a.dprob[t * a.topk + j0 + j] = entry_row(a, t, j0 + j) >= 0 ? dot[j] : 0.0f;
+      }
+    }
+  }
+}
+
+namespace {
+
+// Threads of a token's workgroup: one 16-byte piece each while four waves
+// reach, then more pieces per thread.
+int token_threads(int64_t hidden, int dtype) {
+  const int64_t pieces = (hidden * (dtype == 0 ? 4 : 2) + 15) / 16;
+  const int64_t t = (pieces + 63) / 64 * 64;
+  return (int)(t > 256 ? 256 : t);
+}
+// (blocks x threads stays far below 2^32; larger batches loop)
+int64_t token_grid(int64_t tokens) { return tokens < (1 << 22) ? tokens : (1 << 22); }
+
+}  // namespace
+
+#define NVFP4_TOKENS_CASE(D, LAUNCH)             \
+  case 4 * D: LAUNCH(D, false, false); break;    \
+  case 4 * D + 1: LAUNCH(D, false, true); break; \
+  case 4 * D + 2: LAUNCH(D, true, false); break; \
+  case 4 * D + 3: LAUNCH(D, true, true); break;
+
+hipError_t launch_spread(const TokenRowsArgs& a, hipStream_t s) {
+  const int threads = token_threads(a.hidden, a.dtype);
+  const int64_t tb = token_grid(a.tokens);
+  // Padding is looked for in every row: arrays with more rows than entries
+  // (align > 1) hold it throughout, 8 rows a block; others may hold some only
+  // where entries were dropped and the arrays cut to fit.  More than 2^21
+  // blocks take more rows each.
+  int64_t pad_rows = a.rows_cap > a.tokens * a.topk ? 8 : 512;
+  while (a.rows_cap / pad_rows >= 1 << 21) pad_rows *= 2;
+  const int64_t pad = (a.rows_cap + pad_rows - 1) / pad_rows;
+  if (tb + pad == 0) return hipSuccess;
+#define NVFP4_SPREAD(D, W, G) \
+  spread_kernel<D, W, G><<<(unsigned)(tb + pad), threads, 0, s>>>(a, tb, (int)pad_rows)
+  switch (a.dtype * 4 + (a.prob ? 2 : 0) + (a.dprob ? 1 : 0)) {
+    NVFP4_TOKENS_CASE(0, NVFP4_SPREAD)
+    NVFP4_TOKENS_CASE(1, NVFP4_SPREAD)
+    NVFP4_TOKENS_CASE(2, NVFP4_SPREAD)
+  }
+#undef NVFP4_SPREAD
+  return hipGetLastError();
+}
+
+hipError_t launch_collect(const TokenRowsArgs& a, hipStream_t s) {
+  if (a.tokens == 0) return hipSuccess;
+  const int threads = token_threads(a.hidden, a.dtype);
+  const unsigned blocks = (unsigned)token_grid(a.tokens);
+#define NVFP4_COLLECT(D, W, G) collect_kernel<D, W, G><<<blocks, threads, 0, s>>>(a)
+  switch (a.dtype * 4 + (a.prob ? 2 : 0) + (a.dprob ? 1 : 0)) {
+    NVFP4_TOKENS_CASE(0, NVFP4_COLLECT)
+    NVFP4_TOKENS_CASE(1, NVFP4_COLLECT)
+    NVFP4_TOKENS_CASE(2, NVFP4_COLLECT)
+  }
+#undef NVFP4_COLLECT
+  return hipGetLastError();
+}
+
+#undef NVFP4_TOKENS_CASE
+
+}  // namespace nvfp4

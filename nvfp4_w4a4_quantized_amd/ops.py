@@ -20,7 +20,10 @@ __all__ = ["nvfp4_quantize", "moe_rows_capacity", "moe_permute", "moe_permute_no
            "moe_expert_forward_workspace_size", "moe_expert_forward_single_pass",
            "moe_expert_forward_single_pass_workspace_size", "moe_expert_backward",
            "moe_expert_backward_workspace_size", "SINGLE_PASS_TILE", "NvFp4Weights",
-           "StageTimer", "BackwardTimer"]
+           "StageTimer", "BackwardTimer", "moe_router", "moe_router_backward",
+           "moe_sort_tokens", "moe_sort_tokens_backward", "moe_unsort_tokens",
+           "moe_unsort_tokens_backward", "nvfp4_matvec", "nvfp4_expert_matvec",
+           "moe_expert_decode", "moe_expert_decode_workspace_size"]
 
 SINGLE_PASS_TILE = 256   # intermediate columns per online-scale tile of the single-pass layer
 
@@ -496,3 +499,292 @@ def moe_expert_backward(dy, x, fc1_out, d, expert_offsets, row_src, row_prob, ds
     if debug:
         return out, inter_t
     return out
+
+
+# ---- operators on unquantized tensors --------------------------------------
+# Their tensors are float32, bfloat16 or float16; rows may be strided (a last
+# dimension of stride 1), outputs are contiguous.  Calls run on the current
+# stream of the operands' own device.
+
+_DTYPE_CODE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def _need_rows(t, name, width=None, dtype=None):
+    """A [rows, width] tensor of an element type, its last dimension dense.
+    Returns the distance of its rows in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise NvFp4Error(f"{name} must be a device tensor (got {t.device})")
+    have = t.dtype
+    if have not in _DTYPE_CODE or (dtype is not None and have != dtype):
+        raise TypeError(f"{name}: dtype {have}, expected "
+                        f"{dtype if dtype is not None else tuple(_DTYPE_CODE)}")
+    if t.dim() != 2 or (width is not None and t.shape[1] != width):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [rows, "
+                         f"{'width' if width is None else width}]")
+    n, w = t.shape
+    if w < 1:
+        raise ValueError(f"{name}: rows of no elements")
+    s0, s1 = t.stride()
+    ld = s0 if n > 1 else w
+    if n > 0 and ((s1 != 1 and w > 1) or ld < w):
+        raise ValueError(f"{name}: rows must be dense and must not overlap (strides {t.stride()})")
+    return ld
+
+
+def _need_shape(t, dtype, shape, name):
+    _need(t, (dtype,), name)
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _one_device(first, *others):
+    dev = first.device
+    for t in others:
+        if t is not None and t.device != dev:
+            raise NvFp4Error(f"operands on {dev} and {t.device}")
+    return dev
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _call(device, what, *args):
+    """The library call `what` on the device's current stream.  (A launch goes
+    to the current device; switching, and a Stream object for the handle, cost
+    as much as a small call, so neither is done without need.)"""
+    stream = torch._C._cuda_getCurrentRawStream(device.index)
+    if device.index == torch.cuda.current_device():
+        status = getattr(lib(), what)(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            status = getattr(lib(), what)(*args, stream)
+    if status:
+        check(status, what)
+
+
+def moe_router(logits, topk: int, bias=None, score: int = 0, renormalize: bool = True,
+               scale: float = 1.0):
+    """The top-k experts of every token and their weights, from router logits
+    [T, E] (float32, bf16 or fp16).  Returns (topk_idx int32 [T, k], topk_prob
+    float32 [T, k]), the arguments of moe_permute and the expert layers.
+    score 0: softmax over all experts, 1: sigmoid; renormalize: divided by the
+    picks' sum; scale multiplies the weights.  bias float32 [E] is added for
+    the choice alone.  Experts whose logit is -inf are never picked; a token
+    with fewer than k left gets ids -1 with weight 0."""
+    ld = _need_rows(logits, "logits")
+    T, E = logits.shape
+    if bias is not None:
+        _need_shape(bias, torch.float32, (E,), "bias")
+    dev = _one_device(logits, bias)
+    if not 1 <= topk <= E:
+        raise NvFp4Error(f"moe_router: topk {topk} of {E} experts")
+    idx = torch.empty((T, topk), dtype=torch.int32, device=dev)
+    prob = torch.empty((T, topk), dtype=torch.float32, device=dev)
+    _call(dev, "moe_router", _addr(logits), _DTYPE_CODE[logits.dtype], T, E, ld, _addr(bias), topk,
+          score, int(bool(renormalize)), scale, _addr(idx), _addr(prob))
+    return idx, prob
+
+
+def moe_router_backward(dprob, logits, topk_idx, score: int = 0, renormalize: bool = True,
+                        scale: float = 1.0):
+    """The logits' gradient [T, E] (their dtype) from the weights' gradient
+    dprob [T, k], with moe_router's logits, ids and choices."""
+    ld = _need_rows(logits, "logits")
+    T, E = logits.shape
+    _need(topk_idx, (torch.int32,), "topk_idx")
+    if topk_idx.dim() != 2 or topk_idx.shape[0] != T:
+        raise ValueError(f"topk_idx: shape {tuple(topk_idx.shape)}, expected [{T}, k]")
+    k = topk_idx.shape[1]
+    _need_shape(dprob, torch.float32, (T, k), "dprob")
+    dev = _one_device(logits, topk_idx, dprob)
+    out = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    _call(dev, "moe_router_backward", _addr(logits), _DTYPE_CODE[logits.dtype], T, E, ld,
+          _addr(topk_idx), _addr(dprob), k, score, int(bool(renormalize)), scale, _addr(out))
+    return out
+
+
+def _entries(dst_row, prob, tokens=None):
+    _need(dst_row, (torch.int32,), "dst_row")
+    if dst_row.dim() != 2 or (tokens is not None and dst_row.shape[0] != tokens):
+        raise ValueError(f"dst_row: shape {tuple(dst_row.shape)}, expected "
+                         f"[{'T' if tokens is None else tokens}, k]")
+    if prob is not None:
+        _need_shape(prob, torch.float32, dst_row.shape, "prob")
+    return dst_row.shape
+
+
+def _rows_out(out, cap, like, expert_offsets, row_src):
+    for t, n in ((expert_offsets, "expert_offsets"), (row_src, "row_src")):
+        _need(t, (torch.int32,), n)
+    if out is None:
+        return torch.empty((cap, like.shape[1]), dtype=like.dtype, device=like.device)
+    _need_shape(out, like.dtype, (cap, like.shape[1]), "out")
+    return out
+
+
+def moe_sort_tokens(x, dst_row, row_src, expert_offsets, prob=None, out=None):
+    """Tokens x [T, H] to routed rows [cap, H] in expert order, unquantized:
+    rows[dst_row[t, j]] = prob[t, j] * x[t] (prob None: copies), zeros in the
+    padding rows.  dst_row, row_src and expert_offsets are moe_permute's (its
+    `offsets`).  Rows at or beyond the last offset are not written."""
+    ld = _need_rows(x, "x")
+    T, k = _entries(dst_row, prob, x.shape[0])
+    rows = _rows_out(out, row_src.numel(), x, expert_offsets, row_src)
+    dev = _one_device(x, dst_row, prob, row_src, expert_offsets, rows)
+    _call(dev, "moe_sort_tokens", _addr(x), _DTYPE_CODE[x.dtype], T, x.shape[1], ld, _addr(dst_row),
+          _addr(prob), k, _addr(row_src), _addr(expert_offsets), expert_offsets.numel() - 1,
+          row_src.numel(), _addr(rows))
+    return rows
+
+
+def moe_sort_tokens_backward(drows, dst_row, x=None, prob=None):
+    """Gradients of moe_sort_tokens from that of its rows: dx [T, H] and, with
+    the forward's x given, dprob [T, k] (else None).  Returns (dx, dprob)."""
+    ld = _need_rows(drows, "drows")
+    T, k = _entries(dst_row, prob)
+    H = drows.shape[1]
+    ld_x = H
+    if x is not None:
+        ld_x = _need_rows(x, "x", H, drows.dtype)
+        if x.shape[0] != T:
+            raise ValueError(f"x: shape {tuple(x.shape)}, expected {(T, H)}")
+    dev = _one_device(drows, dst_row, prob, x)
+    dx = torch.empty((T, H), dtype=drows.dtype, device=dev)
+    dprob = torch.empty((T, k), dtype=torch.float32, device=dev) if x is not None else None
+    _call(dev, "moe_sort_tokens_backward", _addr(drows), _DTYPE_CODE[drows.dtype], T, H, ld,
+          drows.shape[0], _addr(dst_row), _addr(prob), k, _addr(x), ld_x, _addr(dx), _addr(dprob))
+    return dx, dprob
+
+
+def moe_unsort_tokens(rows, dst_row, prob=None):
+    """Routed rows [cap, H] back to tokens: y[t] = sum_j prob[t, j] *
+    rows[dst_row[t, j]] (prob None: plain sums), in the rows' dtype.  Entries
+    with dst_row < 0 add nothing."""
+    ld = _need_rows(rows, "rows")
+    T, k = _entries(dst_row, prob)
+    H = rows.shape[1]
+    dev = _one_device(rows, dst_row, prob)
+    y = torch.empty((T, H), dtype=rows.dtype, device=dev)
+    _call(dev, "moe_unsort_tokens", _addr(rows), _DTYPE_CODE[rows.dtype], T, H, ld, rows.shape[0],
+          _addr(dst_row), _addr(prob), k, _addr(y))
+    return y
+
+
+def moe_unsort_tokens_backward(dy, dst_row, row_src, expert_offsets, rows=None, prob=None,
+                               out=None):
+    """Gradients of moe_unsort_tokens from dy [T, H]: drows [cap, H] (zeros in
+    the padding rows, nothing written behind the last) and, with the forward's
+    rows given, dprob [T, k] (else None).  Returns (drows, dprob)."""
+    ld = _need_rows(dy, "dy")
+    T, k = _entries(dst_row, prob, dy.shape[0])
+    H, cap = dy.shape[1], row_src.numel()
+    drows = _rows_out(out, cap, dy, expert_offsets, row_src)
+    ld_rows = H
+    if rows is not None:
+        ld_rows = _need_rows(rows, "rows", H, dy.dtype)
+        if rows.shape[0] != cap:
+            raise ValueError(f"rows: shape {tuple(rows.shape)}, expected {(cap, H)}")
+    dev = _one_device(dy, dst_row, prob, row_src, expert_offsets, rows, drows)
+    dprob = torch.empty((T, k), dtype=torch.float32, device=dev) if rows is not None else None
+    _call(dev, "moe_unsort_tokens_backward", _addr(dy), _DTYPE_CODE[dy.dtype], T, H, ld,
+          _addr(dst_row), _addr(prob), k, _addr(row_src), _addr(expert_offsets),
+          expert_offsets.numel() - 1, cap, _addr(rows), ld_rows, _addr(drows), _addr(dprob))
+    return drows, dprob
+
+
+def _need_weights(w, name, groups=None, n=None, k=None):
+    """NVFP4 weights whose three tensors fit each other (and the given sizes)."""
+    if not isinstance(w, NvFp4Weights):
+        raise TypeError(f"{name} must be NvFp4Weights")
+    _need(w.codes, (torch.uint8,), f"{name}.codes")
+    if w.codes.dim() != 3:
+        raise ValueError(f"{name}.codes: shape {tuple(w.codes.shape)}, expected [G, N, K/2]")
+    G, N, kh = w.codes.shape
+    want = tuple(v if v is not None else h for v, h in ((groups, G), (n, N), (k, 2 * kh)))
+    if (G, N, 2 * kh) != want:
+        raise ValueError(f"{name}: [G, N, K] is {(G, N, 2 * kh)}, expected {want}")
+    _need_shape(w.scales, torch.uint8, (G, N, kh // 8), f"{name}.scales")
+    _need_shape(w.gscale, torch.float32, (G,), f"{name}.gscale")
+    return G, N, 2 * kh
+
+
+def _out_rows(out, shape, dtype, device):
+    if dtype not in _DTYPE_CODE:
+        raise TypeError(f"out_dtype {dtype} not in {tuple(_DTYPE_CODE)}")
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _need_shape(out, dtype, shape, "out")
+    return out
+
+
+def nvfp4_matvec(x, w: NvFp4Weights, out_dtype=None, out=None):
+    """x [T, K] (float32, bf16 or fp16) times one NVFP4 matrix (w: [1, N, K],
+    either layout): [T, N] in out_dtype (x's by default).  For the few rows of
+    new tokens: the weights are read once, as they are."""
+    _, N, K = _need_weights(w, "w", groups=1)
+    ld = _need_rows(x, "x", K)
+    T = x.shape[0]
+    dev = _one_device(x, w.codes, w.scales, w.gscale, out)
+    out = _out_rows(out, (T, N), out_dtype if out_dtype is not None else x.dtype, dev)
+    _call(dev, "nvfp4_matvec", _addr(x), _DTYPE_CODE[x.dtype], T, ld, C.byref(w.c_struct()), N, K,
+          _DTYPE_CODE[out.dtype], _addr(out))
+    return out
+
+
+def nvfp4_expert_matvec(x, topk_idx, w: NvFp4Weights, out_dtype=None, out=None):
+    """Every entry's row times its expert's NVFP4 matrix (w: [E, N, K]): x
+    [T, K], or [T, k, K] with a row per entry, topk_idx int32 [T, k] -> out
+    [T, k, N].  Entries with an id outside [0, E) give zeros."""
+    E, N, K = _need_weights(w, "w")
+    _need(topk_idx, (torch.int32,), "topk_idx")
+    if topk_idx.dim() != 2:
+        raise ValueError(f"topk_idx: shape {tuple(topk_idx.shape)}, expected [T, k]")
+    T, k = topk_idx.shape
+    by_entry = isinstance(x, torch.Tensor) and x.dim() == 3
+    if by_entry:
+        if not x.is_contiguous() or tuple(x.shape[:2]) != (T, k):
+            raise ValueError(f"x: shape {tuple(x.shape)}, expected contiguous {(T, k, K)}")
+        x = x.view(T * k, x.shape[2])
+    ld = _need_rows(x, "x", K)
+    if x.shape[0] != (T * k if by_entry else T):
+        raise ValueError(f"x: {x.shape[0]} rows for topk_idx {(T, k)}")
+    dev = _one_device(x, topk_idx, w.codes, w.scales, w.gscale, out)
+    out = _out_rows(out, (T, k, N), out_dtype if out_dtype is not None else x.dtype, dev)
+    _call(dev, "nvfp4_expert_matvec", _addr(x), _DTYPE_CODE[x.dtype], T, ld, int(by_entry),
+          _addr(topk_idx), k, C.byref(w.c_struct()), E, N, K, _DTYPE_CODE[out.dtype], _addr(out))
+    return out
+
+
+def moe_expert_decode_workspace_size(tokens, hidden, inter, topk) -> int:
+    return int(lib().moe_expert_decode_workspace_size(tokens, hidden, inter, topk))
+
+
+def moe_expert_decode(x, topk_idx, topk_prob, num_experts: int, inter: int, w1: NvFp4Weights,
+                      w2: NvFp4Weights, workspace=None, y=None):
+    """The expert layer for a few tokens on unquantized activations: FC1,
+    weighted SwiGLU, FC2 and the sum over a token's experts with
+    moe_expert_forward's weights.  x [T, H] float32, bf16 or fp16, T * k <=
+    4096; returns y [T, H] in x's dtype."""
+    ld = _need_rows(x, "x")
+    T, H = x.shape
+    _need(topk_idx, (torch.int32,), "topk_idx")
+    if topk_idx.dim() != 2 or topk_idx.shape[0] != T:
+        raise ValueError(f"topk_idx: shape {tuple(topk_idx.shape)}, expected [{T}, k]")
+    k = topk_idx.shape[1]
+    _need_shape(topk_prob, torch.float32, (T, k), "topk_prob")
+    _need_weights(w1, "w1", num_experts, 2 * inter, H)
+    _need_weights(w2, "w2", num_experts, H, inter)
+    dev = _one_device(x, topk_idx, topk_prob, w1.codes, w1.scales, w1.gscale, w2.codes, w2.scales,
+                      w2.gscale, workspace, y)
+    y = _out_rows(y, (T, H), x.dtype, dev)
+    if workspace is None:
+        workspace = torch.empty(max(moe_expert_decode_workspace_size(T, H, inter, k), 256),
+                                dtype=torch.uint8, device=dev)
+    _need(workspace, (torch.uint8,), "workspace")
+    _call(dev, "moe_expert_decode", _addr(x), _DTYPE_CODE[x.dtype], T, H, inter, ld, _addr(topk_idx),
+          _addr(topk_prob), k, num_experts, C.byref(w1.c_struct()), C.byref(w2.c_struct()), _addr(y),
+          _addr(workspace), workspace.numel())
+    return y

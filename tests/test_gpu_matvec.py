@@ -1,0 +1,207 @@
+"""nvfp4_matvec, nvfp4_expert_matvec and moe_expert_decode against binary64.
+
+Tolerances: the documented (k + 16) 2^-24 sum |w x| of a binary32 sum of
+exact products, plus the output type's half step.  The layer: errors of h
+carried through D = silu(g) u p (|silu'| <= 1.1, |silu| <= |g|), D's own
+roundings (2^-17 of its two parts, (|g| + 16) 2^-24 of the exponential) and
+FC2's sum."""
+import numpy as np
+import pytest
+import torch
+
+import operator_ref as R
+from gpu_util import say
+
+pytestmark = pytest.mark.gpu
+DTYPES = [torch.float32, torch.bfloat16, torch.float16]
+
+
+def held(codes, scales, gs, tiled):
+    from nvfp4_w4a4_quantized_amd.ops import NvFp4Weights
+    w = NvFp4Weights(codes.cuda(), scales.cuda(), gs.cuda())
+    if tiled:
+        w = w.packed()
+        c, s = R.tile_weights(codes, scales)
+        assert torch.equal(w.codes.cpu(), c) and torch.equal(w.scales.cpu(), s)
+    return w
+
+
+def check(got, ref, mag, k, what):
+    bad = R.outside(got, ref, (k + 16) * 2.0 ** -24 * mag)
+    assert not bool(bad.any()), f"{what}: {int(bad.sum())} of {bad.numel()} outside"
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,n,k,tiled", [
+    (1, 1, 16, False), (1, 5, 48, False), (3, 33, 112, False), (17, 100, 144, False),
+    (1, 32, 128, True), (2, 96, 256, True), (16, 64, 1024, True), (33, 160, 640, True),
+    (5, 1001, 2064, False), (64, 257, 1040, False), (65, 48, 16384, False), (1, 64, 16384, True),
+    (130, 64, 384, True), (1, 5120, 2048, True)])
+def test_matvec(T, n, k, tiled, dtype):
+    from nvfp4_w4a4_quantized_amd import ops
+    rng = np.random.default_rng(T + n + k)
+    codes, scales, gs = R.make_weights(rng, 1, n, k)
+    w = held(codes, scales, gs, tiled)
+    x = torch.from_numpy(rng.standard_normal((T, k)).astype(np.float32)).to(dtype)
+    m = R.decode(codes, scales, gs)[0]
+    ref, mag = x.double() @ m.t(), x.double().abs() @ m.abs().t()
+    for out in {dtype, torch.float32}:
+        say("matvec", T, n, k, tiled, dtype, out)
+        check(ops.nvfp4_matvec(x.cuda(), w, out_dtype=out), ref, mag, k, f"{dtype} -> {out}")
+
+
+def test_matvec_every_code_and_scale_is_exact():
+    """x = one-hot rows: out is the weight itself, every code with every
+    finite E4M3 byte (outer scale 1, binary32 out)."""
+    from nvfp4_w4a4_quantized_amd import ops
+    from nvfp4_w4a4_quantized_amd.ops import NvFp4Weights
+    n, k = 127, 16
+    codes = np.zeros((1, n, k // 2), np.uint8)
+    codes[:] = [(2 * j) | ((2 * j + 1) << 4) for j in range(8)]
+    scales = np.arange(127, dtype=np.uint8).reshape(1, n, 1)
+    gs = torch.ones(1)
+    codes, scales = torch.from_numpy(codes), torch.from_numpy(scales)
+    w = held(codes, scales, gs, False)
+    ref = R.decode(codes, scales, gs)[0].t()
+    for dtype in DTYPES:
+        y = ops.nvfp4_matvec(torch.eye(k, dtype=dtype, device="cuda"), w, out_dtype=torch.float32)
+        assert torch.equal(y.cpu().double(), ref)
+
+
+def test_matvec_binary32_keeps_all_bits():
+    """A binary32 x is used whole: one-hot rows with 24-bit values."""
+    from nvfp4_w4a4_quantized_amd import ops
+    rng = np.random.default_rng(3)
+    codes, scales, _ = R.make_weights(rng, 1, 40, 64)
+    gs = torch.ones(1)
+    w = held(codes, scales, gs, False)
+    v = torch.from_numpy(rng.standard_normal(64).astype(np.float32))
+    y = ops.nvfp4_matvec(torch.diag(v).cuda(), w)
+    ref = (R.decode(codes, scales, gs)[0] * v.double()).t()
+    assert bool(((y.cpu().double() - ref).abs() <= 2.0 ** -24 * 1.0001 * 3 * ref.abs()).all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_matvec_strided_x(dtype):
+    from nvfp4_w4a4_quantized_amd import ops
+    rng = np.random.default_rng(5)
+    codes, scales, gs = R.make_weights(rng, 1, 70, 208)
+    w = held(codes, scales, gs, False)
+    big = torch.full((9, 240), float("nan"), dtype=dtype, device="cuda")
+    xs = big[:, 5:213]
+    xs.copy_(torch.from_numpy(rng.standard_normal((9, 208)).astype(np.float32)))
+    out = torch.empty((9, 70), dtype=torch.float32, device="cuda")
+    y = ops.nvfp4_matvec(xs, w, out_dtype=torch.float32, out=out)
+    assert y is out and torch.equal(y, ops.nvfp4_matvec(xs.contiguous(), w, out_dtype=torch.float32))
+
+
+def make_ids(rng, T, k, E, kind):
+    if kind == "one":
+        ids = np.full((T, k), -1, np.int32)
+        ids[:, 0] = E - 1                   # one expert holds every entry
+    else:
+        ids = np.stack([rng.choice(E, k, replace=False) for _ in range(T)]).astype(np.int32)
+        if kind == "dropped":
+            gone = rng.random((T, k)) < 0.3
+            ids[gone] = rng.choice([-1, E, -1000, 1 << 30], int(gone.sum()))
+            ids[T // 2] = -1
+    return torch.from_numpy(ids.reshape(T, k))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,k,E,n,K,tiled,kind", [
+    (1, 1, 1, 16, 16, False, "plain"), (1, 8, 128, 64, 256, True, "plain"),
+    (4, 3, 5, 50, 80, False, "dropped"), (37, 4, 60, 101, 336, False, "dropped"),
+    (40, 1, 7, 32, 128, True, "one"), (64, 8, 16, 96, 384, True, "dropped"),
+    (512, 8, 8, 32, 128, True, "plain"), (4096, 1, 3, 17, 32, False, "plain"),
+    (2, 2, 1024, 16, 48, False, "plain")])
+def test_expert_matvec(T, k, E, n, K, tiled, kind, dtype):
+    from nvfp4_w4a4_quantized_amd import ops
+    rng = np.random.default_rng(T + n + K)
+    codes, scales, gs = R.make_weights(rng, E, n, K)
+    w = held(codes, scales, gs, tiled)
+    m = R.decode(codes, scales, gs)
+    ids = make_ids(rng, T, k, E, kind)
+    for by_entry in (False, True):
+        shape = (T, k, K) if by_entry else (T, K)
+        x = torch.from_numpy(rng.standard_normal(shape).astype(np.float32)).to(dtype)
+        ref, mag = R.expert_products(x, ids, m, by_entry)
+        say("expert_matvec", T, k, E, n, K, tiled, kind, dtype, by_entry)
+        out = torch.full((T, k, n), 3.0, dtype=dtype, device="cuda")
+        y = ops.nvfp4_expert_matvec(x.cuda(), ids.cuda(), w, out=out)
+        assert y is out
+        check(y, ref, mag, K, f"by_entry={by_entry}")
+        assert bool((y.cpu()[(ids < 0) | (ids >= E)] == 0).all())
+
+
+def decode_ref(x, ids, prob, m1, m2):
+    """y, and how far a result may be from it before its rounding."""
+    I = m2.shape[2]
+    H = m1.shape[2]
+    h, hm = R.expert_products(x, ids, m1)
+    g, u = h[..., :I], h[..., I:]
+    p = prob.double().unsqueeze(-1)
+    sig = torch.exp(R.log_sigmoid(g))
+    ok = ((ids >= 0) & (ids < m1.shape[0])).unsqueeze(-1)
+    d = torch.where(ok, g * sig * u * p, torch.zeros_like(h[..., :I]))
+    eg, eu = ((H + 16) * 2.0 ** -24 * hm[..., :I], (H + 16) * 2.0 ** -24 * hm[..., I:])
+    ed = torch.where(ok, (1.1 * eg * (u.abs() + eu) + (g * sig).abs() * eu) * p.abs()
+                     + d.abs() * (2.0 ** -17 + (g.abs() + 16) * 2.0 ** -24), torch.zeros_like(d))
+    y, ym = R.expert_products(d, ids, m2, True)
+    _, ey = R.expert_products(ed, ids, m2, True)
+    lim = ey.sum(1) + (I + 32 + ids.shape[1]) * 2.0 ** -24 * ym.sum(1)
+    return y.sum(1), lim
+
+
+DECODE = [(1, 1, 1, 16, 16, False, "plain"), (1, 8, 128, 256, 128, True, "plain"),
+          (3, 2, 4, 48, 80, False, "dropped"), (16, 4, 8, 256, 128, True, "dropped"),
+          (37, 4, 20, 272, 112, False, "dropped"), (40, 1, 7, 128, 128, True, "one"),
+          (128, 8, 16, 256, 256, True, "plain"), (512, 8, 12, 64, 48, False, "plain")]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,k,E,H,I,tiled,kind", DECODE)
+def test_expert_decode(T, k, E, H, I, tiled, kind, dtype):
+    from nvfp4_w4a4_quantized_amd import ops
+    rng = np.random.default_rng(T + H + I)
+    w1, w2 = R.make_weights(rng, E, 2 * I, H, std=0.1), R.make_weights(rng, E, H, I, std=0.1)
+    ids = make_ids(rng, T, k, E, kind)
+    prob = torch.from_numpy(rng.random((T, k)).astype(np.float32))
+    prob[(ids < 0) | (ids >= E)] = float("nan")       # of no entry: must not matter
+    x = torch.from_numpy(rng.standard_normal((T, H)).astype(np.float32)).to(dtype)
+    ref, lim = decode_ref(x, ids, torch.nan_to_num(prob), R.decode(*w1), R.decode(*w2))
+    say("expert_decode", T, k, E, H, I, tiled, kind, dtype)
+    a, b = held(*w1, tiled), held(*w2, tiled)
+    # the workspace's old contents must not matter
+    ws = torch.full((ops.moe_expert_decode_workspace_size(T, H, I, k),), 255, dtype=torch.uint8,
+                    device="cuda")
+    y = ops.moe_expert_decode(x.cuda(), ids.cuda(), prob.cuda(), E, I, a, b, workspace=ws)
+    assert y.dtype == dtype
+    bad = R.outside(y, ref, lim)
+    assert not bool(bad.any()), f"{int(bad.sum())} of {bad.numel()} outside"
+    assert torch.equal(y, ops.moe_expert_decode(x.cuda(), ids.cuda(), prob.cuda(), E, I, a, b))
+
+
+def test_infinite_activations_stay_in_their_row():
+    from nvfp4_w4a4_quantized_amd import ops
+    rng = np.random.default_rng(10)
+    w = held(*R.make_weights(rng, 1, 64, 256), True)
+    x = torch.from_numpy(rng.standard_normal((6, 256)).astype(np.float32)).bfloat16().cuda()
+    clean = ops.nvfp4_matvec(x, w)
+    x[2, 5] = float("inf")
+    x[4, 100] = float("nan")
+    y = ops.nvfp4_matvec(x, w)
+    for t in (0, 1, 3, 5):
+        assert torch.equal(y[t], clean[t])
+    assert not bool(torch.isfinite(y[2]).any()) and bool(torch.isnan(y[4]).all())
+
+
+def test_no_tokens():
+    from nvfp4_w4a4_quantized_amd import ops
+    rng = np.random.default_rng(11)
+    w1, w2 = held(*R.make_weights(rng, 4, 256, 128), True), held(*R.make_weights(rng, 4, 128, 128), True)
+    x = torch.empty((0, 128), dtype=torch.bfloat16, device="cuda")
+    ids = torch.empty((0, 2), dtype=torch.int32, device="cuda")
+    prob = torch.empty((0, 2), dtype=torch.float32, device="cuda")
+    assert ops.moe_expert_decode(x, ids, prob, 4, 128, w1, w2).shape == (0, 128)
+    assert ops.nvfp4_expert_matvec(x, ids, w1).shape == (0, 2, 256)
