@@ -46,8 +46,18 @@ struct Piece {
   typedef typename Elem<DT>::type T;
   static constexpr int kN = 16 / (int)sizeof(T);
   T v[kN];
+  typedef u32x4_t any16_t __attribute__((aligned(2)));   // 16 bytes at an element's alignment
   __device__ __forceinline__ void load(const T* p) { __builtin_memcpy(v, p, 16); }
-  __device__ __forceinline__ void store(T* p) const { __builtin_memcpy(p, v, 16); }
+  // read once, and written for a later kernel: past the caches' replacement order
+  __device__ __forceinline__ void load_once(const T* p) {
+    const u32x4_t w = __builtin_nontemporal_load(reinterpret_cast<const any16_t*>(p));
+    __builtin_memcpy(v, &w, 16);
+  }
+  __device__ __forceinline__ void store(T* p) const {
+    u32x4_t w;
+    __builtin_memcpy(&w, v, 16);
+    __builtin_nontemporal_store(w, reinterpret_cast<any16_t*>(p));
+  }
   // the first n elements (n < kN): a row's last, partial piece
   __device__ __forceinline__ void load_part(const T* p, int n) {
 #pragma unroll

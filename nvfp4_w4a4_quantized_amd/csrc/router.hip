@@ -36,62 +36,88 @@ constexpr int kRouterThreads = 256;
 constexpr float kNegInf = -__builtin_huge_valf();
 
 template <int N>
-__device__ __forceinline__ uint32_t row_rotate(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x120 + N, 0xf, 0xf, false);   // row_ror:N
+__device__ __forceinline__ int row_rotate(int v) {
+  return __builtin_amdgcn_mov_dpp(v, 0x120 + N, 0xf, 0xf, true);   // row_ror:N
 }
 
 // Reduction over a token's L lanes (16: one DPP row; 64: the wave), the
 // result in every lane.  All lanes of the wave are active.
 template <int L, class Op>
-__device__ __forceinline__ uint32_t group_reduce_bits(uint32_t v, Op op) {
+__device__ __forceinline__ int group_reduce(int v, Op op) {
   v = op(v, row_rotate<8>(v));
   v = op(v, row_rotate<4>(v));
   v = op(v, row_rotate<2>(v));
   v = op(v, row_rotate<1>(v));
   if (L == 64) {
-    const uint32_t a = (uint32_t)__builtin_amdgcn_readlane((int)v, 0);
-    const uint32_t b = (uint32_t)__builtin_amdgcn_readlane((int)v, 16);
-    const uint32_t c = (uint32_t)__builtin_amdgcn_readlane((int)v, 32);
-    const uint32_t d = (uint32_t)__builtin_amdgcn_readlane((int)v, 48);
+    const int a = __builtin_amdgcn_readlane(v, 0), b = __builtin_amdgcn_readlane(v, 16);
+    const int c = __builtin_amdgcn_readlane(v, 32), d = __builtin_amdgcn_readlane(v, 48);
     v = op(op(a, b), op(c, d));
   }
   return v;
 }
 template <int L>
-__device__ __forceinline__ float group_max(float v) {
-  return __uint_as_float(group_reduce_bits<L>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
-    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
-  }));
+__device__ __forceinline__ int group_max_int(int v) {
+  return group_reduce<L>(v, [](int a, int b) { return a > b ? a : b; });
+}
+template <int L>
+__device__ __forceinline__ int group_min_int(int v) {
+  return group_reduce<L>(v, [](int a, int b) { return a < b ? a : b; });
 }
 template <int L>
 __device__ __forceinline__ float group_sum(float v) {
-  return __uint_as_float(group_reduce_bits<L>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
-    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  return __int_as_float(group_reduce<L>(__float_as_int(v), [](int a, int b) {
+    return __float_as_int(__int_as_float(a) + __int_as_float(b));
   }));
 }
+
+// A binary32 value as an integer of the same order (both zeros alike, NaN
+// below everything), and back: integer maxima need no canonicalisation.
+constexpr int kKeyNan = (int)0x80000000;
+constexpr int kKeyNegInf = (int)0x807FFFFF;
+__device__ __forceinline__ int key_of(float f) {
+  const int b = __float_as_int(f + 0.0f);
+  const int k = b ^ ((b >> 31) & 0x7FFFFFFF);
+  return f == f ? k : kKeyNan;
+}
+__device__ __forceinline__ float value_of(int k) {
+  return __int_as_float(k ^ ((k >> 31) & 0x7FFFFFFF));
+}
 template <int L>
-__device__ __forceinline__ uint32_t group_min_u32(uint32_t v) {
-  return group_reduce_bits<L>(v, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
+__device__ __forceinline__ float group_max(float v) {
+  return value_of(group_max_int<L>(key_of(v)));
 }
 
+// e^x for x <= 0, within (|x| + 2) 2^-24 relative (the argument's product is
+// rounded once; results below 2^-126 flush to zero).
+__device__ __forceinline__ float exp_neg(float x) {
+  return __builtin_amdgcn_exp2f(x * 1.44269504088896340736f);
+}
 __device__ __forceinline__ float log_sigmoid(float z) {
   return fminf(z, 0.0f) - log1pf(expf(-fabsf(z)));
 }
 __device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + expf(-z)); }
 
-// V consecutive logits from element e0 of a row of `experts`; -inf past it.
+// V consecutive logits from element e0 of a row of `experts`, -inf past it,
+// in 16-byte pieces: whole pieces are one load each, and the element loop is
+// skipped where no lane holds a partial one (any width that is a multiple of
+// a piece).
 template <int DT, int V>
 __device__ __forceinline__ void load_logits(float (&v)[V], const void* row, int e0, int experts) {
-  typedef typename Elem<DT>::type T;
-  const T* p = static_cast<const T*>(row);
-  if (e0 + V <= experts) {
-    T raw[V];
-    __builtin_memcpy(raw, p + e0, sizeof(raw));
+  typedef Piece<DT> P;
+  constexpr int N = P::kN < V ? P::kN : V;
+  const typename P::T* p = static_cast<const typename P::T*>(row);
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = Elem<DT>::to_float(raw[i]);
-  } else {
+  for (int c = 0; c < V; c += N) {
+    const int left = experts - (e0 + c);
+    typename P::T raw[N];
+    if (left >= N) {
+      __builtin_memcpy(raw, p + e0 + c, sizeof(raw));
+    } else if (left > 0) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = e0 + i < experts ? Elem<DT>::to_float(p[e0 + i]) : kNegInf;
+      for (int i = 0; i < N; ++i) raw[i] = i < left ? p[e0 + c + i] : (typename P::T)0;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[c + i] = i < left ? Elem<DT>::to_float(raw[i]) : kNegInf;
   }
 }
 
@@ -114,7 +140,24 @@ __device__ __forceinline__ void pick_softmax(const float* vals, int topk, int la
   m = group_max<L>(m);
   float s = 0.0f;
   if (m > kNegInf)
-    for (int j = lane; j < topk; j += L) s += expf(vals[j] - m);
+    for (int j = lane; j < topk; j += L) s += exp_neg(vals[j] - m);
+  *mx = m;
+  *sum = group_sum<L>(s);
+}
+
+// exp(v - max) of a whole row, their sum; zeros for a row of -inf alone.
+template <int L, int V>
+__device__ __forceinline__ void row_softmax(const float (&v)[V], float (&p)[V], float* mx, float* sum) {
+  float m = kNegInf;
+#pragma unroll
+  for (int i = 0; i < V; ++i) m = fmaxf(m, v[i]);
+  m = group_max<L>(m);
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    p[i] = m > kNegInf ? exp_neg(v[i] - m) : 0.0f;
+    s += p[i];
+  }
   *mx = m;
   *sum = group_sum<L>(s);
 }
@@ -149,50 +192,50 @@ __global__ __launch_bounds__(kRouterThreads) void router_kernel(RouterArgs a) {
     for (int i = 0; i < V; ++i) bad = bad || !(v[i] < __builtin_huge_valf());
     float mx = 0.0f, sum = 0.0f;
     if (a.score == 0 && !a.renormalize) {
-      mx = kNegInf;
-#pragma unroll
-      for (int i = 0; i < V; ++i) mx = fmaxf(mx, v[i]);
-      mx = group_max<L>(mx);
-      if (mx > kNegInf) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) sum += expf(v[i] - mx);
-      }
-      sum = group_sum<L>(sum);
+      float p[V];
+      row_softmax<L, V>(v, p, &mx, &sum);
     }
     if (a.bias) {
 #pragma unroll
       for (int i = 0; i < V; ++i)
         if (e0 + i < a.num_experts) v[i] += a.bias[e0 + i];
     }
+    int key[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = v[i] == v[i] ? v[i] : kNegInf;
-    for (int j = 0; j < a.topk; ++j) {
-      float m = v[0];
+    for (int i = 0; i < V; ++i) key[i] = key_of(v[i]);
+    for (int j = 0, at = 0; j < a.topk; ++j, at = at + 1 == L ? 0 : at + 1) {
+      int m = key[0];
 #pragma unroll
-      for (int i = 1; i < V; ++i) m = fmaxf(m, v[i]);
-      m = group_max<L>(m);
-      uint32_t cand = 0x7FFFFFFFu;
+      for (int i = 1; i < V; ++i) m = m > key[i] ? m : key[i];
+      m = group_max_int<L>(m);
+      int cand = 0x7FFFFFFF;
 #pragma unroll
-      for (int i = V - 1; i >= 0; --i) cand = v[i] == m ? (uint32_t)(e0 + i) : cand;
-      const uint32_t e = group_min_u32<L>(cand);
+      for (int i = V - 1; i >= 0; --i) cand = key[i] == m ? e0 + i : cand;
+      const int e = group_min_int<L>(cand);
+      const int in = e - e0;
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[i] = (uint32_t)(e0 + i) == e ? kNegInf : v[i];
-      if (lane == j % L) pick[j] = m > kNegInf ? (int32_t)e : -1;
+      for (int i = 0; i < V; ++i) key[i] = in == i ? kKeyNan : key[i];
+      if (lane == at) {
+        pick[j] = m > kKeyNegInf ? e : -1;
+        vals[j] = value_of(m);
+      }
     }
     wave_lds_fence();
-    for (int j = lane; j < a.topk; j += L) {
-      const int e = pick[j];
-      float z = e >= 0 ? logit_at<DT>(row, e) : kNegInf;
-      vals[j] = e >= 0 && a.score == 1 && a.renormalize ? log_sigmoid(z) : z;
+    if (a.bias || (a.score == 1 && a.renormalize)) {
+      for (int j = lane; j < a.topk; j += L) {
+        const int e = pick[j];
+        const float z = e < 0 ? kNegInf : (a.bias ? logit_at<DT>(row, e) : vals[j]);
+        vals[j] = e >= 0 && a.score == 1 && a.renormalize ? log_sigmoid(z) : z;
+      }
+      wave_lds_fence();
     }
-    wave_lds_fence();
     if (a.renormalize) pick_softmax<L>(vals, a.topk, lane, &mx, &sum);
-    const bool any_bad = group_max<L>(bad ? 1.0f : 0.0f) > 0.0f;
+    const bool any_bad = group_max_int<L>(bad ? 1 : 0) != 0;
     for (int j = lane; j < a.topk; j += L) {
       const int e = pick[j];
       float w = 0.0f;
       if (e >= 0)
-        w = a.score == 1 && !a.renormalize ? sigmoid(vals[j]) : expf(vals[j] - mx) / sum;
+        w = a.score == 1 && !a.renormalize ? sigmoid(vals[j]) : exp_neg(vals[j] - mx) / sum;
       if (any_bad) w = __builtin_nanf("");
       if (live) {
         a.topk_idx[t * a.topk + j] = e;
@@ -225,7 +268,7 @@ __global__ __launch_bounds__(kRouterThreads) void router_backward_kernel(RouterB
     bool bad = false;
 #pragma unroll
     for (int i = 0; i < V; ++i) bad = bad || !(v[i] < __builtin_huge_valf());
-    const bool any_bad = group_max<L>(bad ? 1.0f : 0.0f) > 0.0f;
+    const bool any_bad = group_max_int<L>(bad ? 1 : 0) != 0;
     for (int j = lane; j < a.topk; j += L) {
       int e = a.topk_idx[tt * a.topk + j];
       if (e < 0 || e >= a.num_experts) e = -1;
@@ -235,17 +278,9 @@ __global__ __launch_bounds__(kRouterThreads) void router_backward_kernel(RouterB
     }
     wave_lds_fence();
     float mx = 0.0f, sum = 1.0f;
+    float p[V];
     if (full) {
-      mx = kNegInf;
-#pragma unroll
-      for (int i = 0; i < V; ++i) mx = fmaxf(mx, v[i]);
-      mx = group_max<L>(mx);
-      sum = 0.0f;
-      if (mx > kNegInf) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) sum += expf(v[i] - mx);
-      }
-      sum = group_sum<L>(sum);
+      row_softmax<L, V>(v, p, &mx, &sum);
     } else if (a.renormalize) {
       pick_softmax<L>(vals, a.topk, lane, &mx, &sum);
     }
@@ -256,7 +291,7 @@ __global__ __launch_bounds__(kRouterThreads) void router_backward_kernel(RouterB
     if (some && (full || a.renormalize)) {
       for (int j = lane; j < a.topk; j += L)
         if (pick[j] >= 0)
-          mean += expf(vals[j] - mx) * inv * (a.dprob[tt * a.topk + j] * a.scale);
+          mean += exp_neg(vals[j] - mx) * inv * (a.dprob[tt * a.topk + j] * a.scale);
     }
     mean = group_sum<L>(mean);
     for (int j = lane; j < a.topk; j += L) {
@@ -266,9 +301,9 @@ __global__ __launch_bounds__(kRouterThreads) void router_backward_kernel(RouterB
         const float dw = a.dprob[tt * a.topk + j] * a.scale;
         const float z = vals[j];
         if (full) {
-          d = expf(z - mx) * inv * dw;
+          d = exp_neg(z - mx) * inv * dw;
         } else if (a.renormalize) {
-          d = expf(z - mx) * inv * (dw - mean);
+          d = exp_neg(z - mx) * inv * (dw - mean);
           // vals holds log s(l) there; 1 - s(l) = s(-l)
           if (a.score == 1) d *= sigmoid(-logit_at<DT>(row, e));
         } else {
@@ -281,7 +316,7 @@ __global__ __launch_bounds__(kRouterThreads) void router_backward_kernel(RouterB
     float dz[V];
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      dz[i] = full && some ? -(expf(v[i] - mx) * inv) * mean : 0.0f;
+      dz[i] = full ? -(p[i] * inv) * mean : 0.0f;
     for (int j = 0; j < a.topk; ++j) {
       const int at = pick[j] - e0;
       const float d = vals[j];
@@ -292,16 +327,21 @@ __global__ __launch_bounds__(kRouterThreads) void router_backward_kernel(RouterB
     }
     if (live) {
       T* out = static_cast<T*>(a.dlogits) + t * a.num_experts;
-      T raw[V];
+      constexpr int N = Piece<DT>::kN < V ? Piece<DT>::kN : V;
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        raw[i] = Elem<DT>::from_float(any_bad ? __builtin_nanf("") : dz[i]);
-      if (e0 + V <= a.num_experts) {
-        __builtin_memcpy(out + e0, raw, sizeof(raw));
-      } else {
+      for (int c = 0; c < V; c += N) {
+        T raw[N];
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (e0 + i < a.num_experts) out[e0 + i] = raw[i];
+        for (int i = 0; i < N; ++i)
+          raw[i] = Elem<DT>::from_float(any_bad ? __builtin_nanf("") : dz[c + i]);
+        const int left = a.num_experts - (e0 + c);
+        if (left >= N) {
+          __builtin_memcpy(out + e0 + c, raw, sizeof(raw));
+        } else if (left > 0) {
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            if (i < left) out[e0 + c + i] = raw[i];
+        }
       }
     }
     wave_lds_fence();

@@ -1,11 +1,13 @@
 """moe_router and its gradient against their binary64 definitions.
 
-Tolerances: a weight is a quotient of binary32 exponentials.  With R the
-largest |l - max| among the terms that count, the argument's rounding and
-the exponential's own error move one by at most (R + 4) 2^-24 relative (R
-capped at 104: beyond it the term is zero), the n-term sum by n 2^-24, the
-quotient and the scale by 2 2^-24: together (2 R + n + 16) 2^-24, with room
-for the sum's terms.  log s(l) carries one more rounding of its magnitude,
+Tolerances: a weight is a quotient of binary32 exponentials.  With r the
+largest |l - max| among the terms that count, the two roundings of the
+argument, that of log2 e and the exponential's own error move a term by at
+most (2.5 r + 4) 2^-24 relative (r capped at 104: beyond it the term is
+zero), the n-term sum by n 2^-24, the quotient and the scale by 2 2^-24:
+together below (2 R + n + 16) 2^-24 with R = r + max |l| >= 1.5 r.  A weight
+below the normal range may be flushed to zero, 2^-126 off; the gradient
+multiplies that error by at most |dw| + sum q |dw| <= 2 max |dw|.  log s(l) carries one more rounding of its magnitude,
 which R covers.  The gradient multiplies two such values with binary32
 differences of dw, so its error is below twice that, relative to
 q (|dw| + sum q |dw|); the result's type adds its half step."""
@@ -83,6 +85,7 @@ def test_router_matches_the_definition(T, E, k, kind, dtype):
                 lim += R.softmax_rows(logits.double()) * (q * dw).sum(1, keepdim=True)
             err = (dz.cpu().double() - refd).abs()
             lim = 2 * tol * lim + R.STEP[dtype] * refd.abs() * 1.0001 + R.TINY[dtype] * 1.0001
+            lim += 2 * float(dw.max()) * 2.0 ** -126       # flushed weights (see above)
             assert bool((err <= lim).all()), float((err - lim).max())
 
 
