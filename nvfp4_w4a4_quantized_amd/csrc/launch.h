@@ -241,6 +241,7 @@ struct MatvecArgs {
   int32_t num_groups; int64_t n, k;
   const int32_t* topk_idx; int32_t topk;      // NULL, 1: one matrix for every row
   void* out; int out_dtype;   // [rows, n]
+  int skip_unrouted;          // entries of no expert are left unwritten (else zeros)
   // SwiGLU epilogue (n = 2 * inter): the two parts of D, [entries, inter]
   uint16_t* d_hi; uint16_t* d_lo; int64_t inter; const float* prob;
 };

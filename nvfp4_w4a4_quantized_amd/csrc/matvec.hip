@@ -141,6 +141,26 @@ __device__ __forceinline__ uint4 load_u128(const uint8_t* p) {
   return v;
 }
 
+// The entries whose expert is e (e == num_groups: of no expert) into `list`,
+// their number into *found; true if an entry before `slot` is among them.
+// `id` is topk_idx[threadIdx.x], loaded by the caller ahead of other work.
+__device__ __forceinline__ bool collect_entries(const MatvecArgs& a, int e, int id, int entries,
+                                                int slot, uint16_t* list, int* found) {
+  if (threadIdx.x == 0) *found = 0;
+  __syncthreads();
+  bool earlier = false;
+  for (int i = threadIdx.x; i < entries; i += blockDim.x) {
+    if (i != (int)threadIdx.x) id = a.topk_idx[i];
+    const int of = id >= 0 && id < a.num_groups ? id : a.num_groups;
+    if (of == e) {
+      earlier = earlier || i < slot;
+      // (a column's place does not change its result, so any order will do)
+      list[atomicAdd(found, 1)] = (uint16_t)i;
+    }
+  }
+  return __syncthreads_or(earlier);
+}
+
 // Stores the values of rows [row, row + 4) of one column (those below n).
 __device__ __forceinline__ void store4(const MatvecArgs& a, int64_t out_row, int64_t row, f32x4_t v) {
   const int64_t at = out_row * a.n + row;
@@ -151,6 +171,13 @@ __device__ __forceinline__ void store4(const MatvecArgs& a, int64_t out_row, int
     else if (a.out_dtype == 1) static_cast<uint16_t*>(a.out)[at + i] = Elem<1>::from_float(v[i]);
     else static_cast<_Float16*>(a.out)[at + i] = (_Float16)v[i];
   }
+}
+
+// Zero results for the listed entries' rows [row, row + count).
+__device__ __forceinline__ void store_zeros(const MatvecArgs& a, const uint16_t* list, int m,
+                                            int64_t row, int count) {
+  for (int i = threadIdx.x; i < m * (count / 4); i += blockDim.x)
+    store4(a, list[i / (count / 4)], row + 4 * (i % (count / 4)), (f32x4_t){0.f, 0.f, 0.f, 0.f});
 }
 
 // The layer's D of one entry: silu(g) u p, as its two bf16 parts.
@@ -187,48 +214,47 @@ __global__ __launch_bounds__(512) void matvec_kernel(MatvecArgs a) {
   uint16_t* list = reinterpret_cast<uint16_t*>(lds + waves * RT * kWave * sizeof(f32x4_t));
   __shared__ int found;
   int e = 0, m = (int)a.tokens, first = 0;
+  const int entries = EXPERT ? (int)a.tokens * a.topk : 0, slot = blockIdx.y;
+  const bool by_entry = EXPERT && entries <= a.num_groups;
+  int id = -1;
   if (EXPERT) {
-    const int entries = (int)a.tokens * a.topk;
-    const bool by_entry = entries <= a.num_groups;
-    const int slot = blockIdx.y;
+    if ((int)threadIdx.x < entries) id = a.topk_idx[threadIdx.x];
     e = by_entry ? a.topk_idx[slot] : slot;
     if (e < 0 || e >= a.num_groups) {
-      if (SWIGLU) return;
-      // entries of no expert: zero results
-      for (int i = by_entry ? slot : 0; i < (by_entry ? slot + 1 : entries); ++i) {
-        const int id = a.topk_idx[i];
-        if ((id < 0 || id >= a.num_groups) && threadIdx.x < 4)
-          store4(a, i, row0 + 4 * threadIdx.x, (f32x4_t){0.f, 0.f, 0.f, 0.f});
-      }
-      return;
+      if (SWIGLU || a.skip_unrouted) return;
+      e = a.num_groups;
     }
-    if (threadIdx.x == 0) found = 0;
-    __syncthreads();
-    bool earlier = false;
-    for (int i = threadIdx.x; i < entries; i += blockDim.x) {
-      if (a.topk_idx[i] == e) {
-        earlier = earlier || (by_entry && i < slot);
-        // (a column's place does not change its result, so any order will do)
-        list[atomicAdd(&found, 1)] = (uint16_t)i;
-      }
-    }
-    if (__syncthreads_or(earlier)) return;
-    m = found;
-    if (m == 0) return;
-  } else {
-    first = blockIdx.y * kTile;
-    m = m < first + kTile ? m : first + kTile;
   }
+  const int64_t cstep = a.layout == 0 ? kStage / 2 : 2048, sstep = a.layout == 0 ? kStage / 16 : 256;
+  const int stages = (int)(a.k / kStage);
   LanePlace place[RT];
+  uint4 wc[RT];        // the wave's first stage, on its way while the entries are listed
+  uint32_t ws[RT];
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
     // rows past the last read the last one (and are not stored)
     int64_t row = row0 + r + (SWIGLU ? rt * a.inter : 0);
     if (!SWIGLU && row >= a.n) row = a.n - 1;
-    place[rt] = lane_place(a, e, row, q);
+    place[rt] = lane_place(a, EXPERT && e == a.num_groups ? 0 : e, row, q);
+    const int st = wave < stages ? wave : 0;
+    if (stages > 0) {
+      wc[rt] = load_u128(place[rt].codes + st * cstep);
+      ws[rt] = load_u16(place[rt].scales + st * sstep);
+    }
   }
-  const int64_t cstep = a.layout == 0 ? kStage / 2 : 2048, sstep = a.layout == 0 ? kStage / 16 : 256;
-  const int stages = (int)(a.k / kStage);
+  if (EXPERT) {
+    const bool earlier = collect_entries(a, e, id, entries, by_entry ? slot : 0, list, &found);
+    if (earlier) return;
+    m = found;
+    if (m == 0) return;
+    if (e == a.num_groups) {
+      store_zeros(a, list, m, row0, kTile);
+      return;
+    }
+  } else {
+    first = blockIdx.y * kTile;
+    m = m < first + kTile ? m : first + kTile;
+  }
   const int xsize = XT == 0 ? 4 : 2;
   const float sg = a.gscale[e];
   for (int c0 = first; c0 < m; c0 += kTile) {
@@ -245,9 +271,11 @@ __global__ __launch_bounds__(512) void matvec_kernel(MatvecArgs a) {
     for (int st = wave; st < stages; st += waves) {
       const XStage<XT> x = load_x<XT>(xp + (int64_t)st * kStage * xsize, XT == kPair ? xl + st * kStage * 2 : nullptr);
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-        stage_product<XT>(acc[rt], load_u128(place[rt].codes + st * cstep),
-                          load_u16(place[rt].scales + st * sstep), x);
+      for (int rt = 0; rt < RT; ++rt) {
+        const bool had = c0 == first && st == wave;
+        stage_product<XT>(acc[rt], had ? wc[rt] : load_u128(place[rt].codes + st * cstep),
+                          had ? ws[rt] : load_u16(place[rt].scales + st * sstep), x);
+      }
     }
     // the k behind the last whole stage (row-major weights only): a multiple
     // of 16, so a lane has none, half or all of its 32
@@ -300,7 +328,254 @@ __global__ __launch_bounds__(512) void matvec_kernel(MatvecArgs a) {
   }
 }
 
+// ---- more columns: x staged in LDS --------------------------------------
+//
+// From a handful of columns on, a wave's own reads of x cost more than its
+// weights (a 16-column operand is 4 KiB a stage beside 1.1 KiB of weights).
+// Here a workgroup's four waves take 32 rows each (16 gate and 16 up rows
+// with SwiGLU) and share 16 NC columns of x, brought into LDS once per
+// workgroup as the parts' bf16 / fp16 values, two stages at a time, double
+// buffered.  A column's stage is 16 pieces of 8 elements, piece p in slot
+// p ^ (column % 16): the 16 lanes that read one piece of 16 columns meet 16
+// different slots, so neither side has bank conflicts.  Each wave keeps four
+// stages of its weights in flight in registers.
+//
+// The last stage of a k that is no multiple of 128 (row-major weights):
+// lanes take the window [min(k0, k - 32), + 32) instead of [k0, + 32), and x
+// is zero wherever the window leaves [k0, k), so the loads need no branch.
+
 namespace {
+
+constexpr int kRowWaves = 4;
+constexpr int kDepth = 4;              // stages of weights in flight
+constexpr int kWide = 2;               // 16-row tiles of a wave
+
+template <int XT>
+constexpr int x_stages() { return XT == 0 ? 1 : 2; }
+
+// Where a wave's weights of one stage lie.
+struct WStage {
+  uint4 c[kWide];
+  uint32_t s[kWide];
+};
+
+// 8 elements of a column on their way to LDS.
+template <int XT>
+struct XPiece {
+  uint4 w[XT == 0 || XT == kPair ? 2 : 1];
+};
+
+template <int XT>
+__device__ __forceinline__ XPiece<XT> load_piece(const char* p, const char* p_lo) {
+  XPiece<XT> v;
+  __builtin_memcpy(&v.w[0], p, XT == 0 ? 32 : 16);
+  if (XT == kPair) __builtin_memcpy(&v.w[XT == kPair ? 1 : 0], p_lo, 16);
+  return v;
+}
+
+template <int XT>
+__device__ __forceinline__ uint4 piece_part(const XPiece<XT>& v, int part) {
+  if (XT != 0) return v.w[XT == kPair ? part : 0];
+  XStage<0> x;
+  x.w[0] = v.w[0];
+  x.w[1] = v.w[XT == 0 ? 1 : 0];
+  return x_operand<0>(x, 0, part);
+}
+
+}  // namespace
+
+template <int XT, int NC, bool SWIGLU, bool EXPERT>
+__global__ __launch_bounds__(kRowWaves* kWave) void matvec_rows_kernel(MatvecArgs a) {
+  constexpr int kCols = NC * kTile, kParts = parts_of(XT), XS = x_stages<XT>();
+  constexpr int kColBytes = kStage * 2;                   // one part of a column's stage
+  constexpr int kPlane = kCols * kColBytes;
+  constexpr int kBuffer = XS * kParts * kPlane;
+  constexpr int kThreads = kRowWaves * kWave;
+  constexpr int kOwn = XS * NC * 16 * 16 / kThreads;      // pieces a thread brings per buffer
+  extern __shared__ __align__(16) char lds[];
+  uint16_t* list = reinterpret_cast<uint16_t*>(lds + 2 * kBuffer);
+  __shared__ int found;
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  const int r = lane % kTile, q = lane / kTile;
+  int e = 0, m = (int)a.tokens, first = 0;
+  // first row of the wave: of the output, or of the gate half
+  const int64_t row0 = ((int64_t)blockIdx.x * kRowWaves + wave) * (SWIGLU ? kTile : kWide * kTile);
+  const int64_t rows = SWIGLU ? a.inter : a.n;
+  if (EXPERT) {
+    const int entries = (int)a.tokens * a.topk;
+    e = blockIdx.y;
+    if (e == a.num_groups && (SWIGLU || a.skip_unrouted)) return;
+    const int id = (int)threadIdx.x < entries ? a.topk_idx[threadIdx.x] : -1;
+    collect_entries(a, e, id, entries, 0, list, &found);
+    m = found;
+    if (m == 0) return;
+    if (e == a.num_groups) {   // entries of no expert
+      store_zeros(a, list, m, row0 - wave * kWide * kTile, kRowWaves * kWide * kTile);
+      return;
+    }
+  } else {
+    first = blockIdx.y * kCols;
+    m = m < first + kCols ? m : first + kCols;
+  }
+  const uint8_t* wc[kWide];
+  const uint8_t* ws[kWide];
+#pragma unroll
+  for (int rt = 0; rt < kWide; ++rt) {
+    // rows past the last read the last one (and are not stored)
+    int64_t row = row0 + r + (SWIGLU ? 0 : rt * kTile);
+    if (row >= rows) row = rows - 1;
+    const LanePlace p = lane_place(a, e, row + (SWIGLU ? rt * a.inter : 0), a.layout == 0 ? 0 : q);
+    wc[rt] = p.codes;
+    ws[rt] = p.scales;
+  }
+  const int k = (int)a.k, stages = (k + kStage - 1) / kStage;
+  auto load_w = [&](int st) {
+    WStage w;
+    st = st < stages ? st : stages - 1;
+    int co, so;
+    if (a.layout == 0) {
+      const int k0 = st * kStage + 32 * q;
+      const int at = k0 < k - 32 ? k0 : k - 32;
+      co = at / 2;
+      so = at / 16;
+    } else {
+      co = st * 2048;
+      so = st * 256;
+    }
+#pragma unroll
+    for (int rt = 0; rt < kWide; ++rt) {
+      w.c[rt] = load_u128(wc[rt] + co);
+      w.s[rt] = load_u16(ws[rt] + so);
+    }
+    return w;
+  };
+  const float sg = a.gscale[e];
+  constexpr int xsize = XT == 0 ? 4 : 2;
+  // a thread brings piece `slot ^ column` of columns own_col, own_col + 16, ...
+  const int own_col = threadIdx.x / 16, slot = threadIdx.x % 16;
+  const int piece = slot ^ own_col;                       // (kThreads / 16 == 16 columns)
+  const int pq = piece / 4, ps = piece % 4;
+  char* own_lds = lds + own_col * kColBytes + slot * 16;
+  for (int c0 = first; c0 < m; c0 += kCols) {
+    const char* xp[NC];
+    const char* xl[NC];
+#pragma unroll
+    for (int b = 0; b < NC; ++b) {
+      // columns past the last repeat it (and are not stored)
+      const int ci = c0 + b * 16 + own_col < m ? c0 + b * 16 + own_col : m - 1;
+      const int entry = EXPERT ? list[ci] : ci;
+      const int64_t xrow = EXPERT && !a.x_by_entry ? entry / a.topk : entry;
+      xp[b] = static_cast<const char*>(a.x) + xrow * a.ld_x * xsize;
+      xl[b] = XT == kPair ? reinterpret_cast<const char*>(a.x_lo) + xrow * a.ld_x * 2 : nullptr;
+    }
+    XPiece<XT> xr[kOwn];
+    auto load_xs = [&](int st0) {
+#pragma unroll
+      for (int i = 0; i < kOwn; ++i) {
+        int st = st0 + i / NC;
+        st = st < stages ? st : stages - 1;
+        const int k0 = st * kStage + 32 * pq;
+        const int at = (k0 < k - 32 ? k0 : k - 32) + 8 * ps;
+        xr[i] = load_piece<XT>(xp[i % NC] + (int64_t)at * xsize,
+                               XT == kPair ? xl[i % NC] + (int64_t)at * 2 : nullptr);
+        if (at < k0 || at >= k) xr[i] = XPiece<XT>{};
+      }
+    };
+    auto store_xs = [&](int buf) {
+#pragma unroll
+      for (int i = 0; i < kOwn; ++i)
+#pragma unroll
+        for (int p = 0; p < kParts; ++p)
+          *reinterpret_cast<uint4*>(own_lds + buf * kBuffer + ((i / NC) * kParts + p) * kPlane +
+                                    (i % NC) * 16 * kColBytes) = piece_part<XT>(xr[i], p);
+    };
+    f32x4_t acc[kWide][NC];
+#pragma unroll
+    for (int rt = 0; rt < kWide; ++rt)
+#pragma unroll
+      for (int b = 0; b < NC; ++b) acc[rt][b] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+    load_xs(0);
+    WStage w[kDepth];
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) w[d] = load_w(d);
+    if (c0 != first) __syncthreads();                     // the last columns' buffers have been read
+    store_xs(0);
+    __syncthreads();
+    for (int st0 = 0; st0 < stages; st0 += kDepth) {
+#pragma unroll
+      for (int d = 0; d < kDepth; ++d) {
+        const int st = st0 + d, buf = (d / XS) % 2;
+        if (d % XS == 0) load_xs(st + XS);
+        if (st < stages) {
+          half2_t s2[kWide];
+#pragma unroll
+          for (int rt = 0; rt < kWide; ++rt) s2[rt] = e4m3x2_to_half2(w[d].s[rt]);
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            uint4 xo[kParts][NC];
+#pragma unroll
+            for (int p = 0; p < kParts; ++p)
+#pragma unroll
+              for (int b = 0; b < NC; ++b)
+                xo[p][b] = *reinterpret_cast<const uint4*>(
+                    lds + buf * kBuffer + ((d % XS) * kParts + p) * kPlane +
+                    (b * 16 + r) * kColBytes + ((4 * q + s) ^ r) * 16);
+#pragma unroll
+            for (int rt = 0; rt < kWide; ++rt) {
+              const uint32_t cw[4] = {w[d].c[rt].x, w[d].c[rt].y, w[d].c[rt].z, w[d].c[rt].w};
+              if (XT == 2) {
+                const _Float16 h = s2[rt][s / 2];
+                const half8_t wa = decode8(cw[s], (half2_t){h, h});
+#pragma unroll
+                for (int b = 0; b < NC; ++b) {
+                  half8_t xb;
+                  __builtin_memcpy(&xb, &xo[0][b], 16);
+                  acc[rt][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wa, xb, acc[rt][b], 0, 0, 0);
+                }
+              } else {
+                const bf16x8_t wa = decode8_bf16(cw[s], (float)s2[rt][s / 2]);
+#pragma unroll
+                for (int p = 0; p < kParts; ++p)
+#pragma unroll
+                  for (int b = 0; b < NC; ++b) {
+                    bf16x8_t xb;
+                    __builtin_memcpy(&xb, &xo[p][b], 16);
+                    acc[rt][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wa, xb, acc[rt][b], 0, 0, 0);
+                  }
+              }
+            }
+          }
+        }
+        w[d] = load_w(st + kDepth);
+        if (d % XS == XS - 1) {
+          store_xs(1 - buf);
+          __syncthreads();
+        }
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < NC; ++b) {
+      const int ci = c0 + b * 16 + r;
+      if (ci >= m) continue;
+      const int entry = EXPERT ? list[ci] : ci;
+      if (SWIGLU) {
+        if (row0 < rows)
+          store_d4(a, entry, row0 + 4 * q, acc[0][b] * sg, acc[1][b] * sg, a.prob[entry]);
+      } else {
+#pragma unroll
+        for (int rt = 0; rt < kWide; ++rt)
+          store4(a, entry, row0 + rt * kTile + 4 * q, acc[rt][b] * sg);
+      }
+    }
+  }
+}
+
+namespace {
+
+#ifndef FEW
+#define FEW 4
+#endif
+constexpr int kFewColumns = FEW;
 
 int matvec_waves(int64_t k) {
   const int64_t stages = (k + kStage - 1) / kStage;
@@ -309,34 +584,53 @@ int matvec_waves(int64_t k) {
 
 }  // namespace
 
+template <int XT, bool SWIGLU, bool EXPERT>
+static void launch_matvec_one(const MatvecArgs& a, hipStream_t s) {
+  const int64_t entries = a.tokens * a.topk;
+  // columns a matrix meets, on average over the matrices that meet any
+  const int64_t cols = EXPERT ? (entries + a.num_groups - 1) / a.num_groups : a.tokens;
+  const size_t list = EXPERT ? (size_t)entries * 2 : 0;
+  if (cols > kFewColumns && a.k >= 32) {
+    const int64_t per = kRowWaves * kTile * (SWIGLU ? 1 : kWide);
+    const int64_t rows = SWIGLU ? a.inter : a.n;
+#define NVFP4_MATVEC_ROWS(NC)                                                                   \
+  matvec_rows_kernel<XT, NC, SWIGLU, EXPERT>                                                    \
+      <<<dim3((unsigned)((rows + per - 1) / per),                                               \
+              (unsigned)(EXPERT ? a.num_groups + 1 : (a.tokens + 16 * NC - 1) / (16 * NC))),    \
+         kRowWaves * kWave,                                                                     \
+         2 * x_stages<XT>() * parts_of(XT) * NC * kTile * kStage * 2 + list, s>>>(a)
+    // the entries of an expert scatter about their mean: room for twice as many
+    if ((EXPERT ? 2 * cols : cols) <= 16) NVFP4_MATVEC_ROWS(1);
+    else if (EXPERT || cols <= 32) NVFP4_MATVEC_ROWS(2);
+    else NVFP4_MATVEC_ROWS(4);
+#undef NVFP4_MATVEC_ROWS
+    return;
+  }
+  const int waves = matvec_waves(a.k);
+  const int64_t tiles = SWIGLU ? a.inter / kTile : (a.n + kTile - 1) / kTile;
+  const int64_t slots = !EXPERT ? (a.tokens + kTile - 1) / kTile
+                                : (entries <= a.num_groups ? entries : a.num_groups + 1);
+  matvec_kernel<XT, SWIGLU, EXPERT>
+      <<<dim3((unsigned)tiles, (unsigned)slots), waves * kWave,
+         (size_t)waves * (SWIGLU ? 2 : 1) * kWave * sizeof(f32x4_t) + list, s>>>(a);
+}
+
 hipError_t launch_matvec(const MatvecArgs& a, hipStream_t s) {
   if (a.tokens == 0) return hipSuccess;
   const bool swiglu = a.d_hi != nullptr, expert = a.topk_idx != nullptr;
-  const int waves = matvec_waves(a.k);
-  const int64_t entries = a.tokens * a.topk;
-  const int64_t tiles = swiglu ? a.inter / kTile : (a.n + kTile - 1) / kTile;
-  const int64_t slots = !expert ? (a.tokens + kTile - 1) / kTile
-                                : (entries <= a.num_groups ? entries : a.num_groups + 1);
-  const size_t lds = (size_t)waves * (swiglu ? 2 : 1) * kWave * sizeof(f32x4_t) +
-                     (expert ? (size_t)entries * 2 : 0);
-  const dim3 grid((unsigned)tiles, (unsigned)slots);
-#define NVFP4_MATVEC(XT, SW, EX) \
-  matvec_kernel<XT, SW, EX><<<grid, waves * kWave, lds, s>>>(a)
-  if (swiglu) {
-    if (a.x_dtype == 0) NVFP4_MATVEC(0, true, true);
-    else if (a.x_dtype == 1) NVFP4_MATVEC(1, true, true);
-    else NVFP4_MATVEC(2, true, true);
-  } else if (expert) {
-    if (a.x_lo) NVFP4_MATVEC(kPair, false, true);
-    else if (a.x_dtype == 0) NVFP4_MATVEC(0, false, true);
-    else if (a.x_dtype == 1) NVFP4_MATVEC(1, false, true);
-    else NVFP4_MATVEC(2, false, true);
-  } else {
-    if (a.x_dtype == 0) NVFP4_MATVEC(0, false, false);
-    else if (a.x_dtype == 1) NVFP4_MATVEC(1, false, false);
-    else NVFP4_MATVEC(2, false, false);
+  const int xt = a.x_lo ? kPair : a.x_dtype;
+  switch (xt * 4 + (swiglu ? 2 : 0) + (expert ? 1 : 0)) {
+    case 0: launch_matvec_one<0, false, false>(a, s); break;
+    case 1: launch_matvec_one<0, false, true>(a, s); break;
+    case 3: launch_matvec_one<0, true, true>(a, s); break;
+    case 4: launch_matvec_one<1, false, false>(a, s); break;
+    case 5: launch_matvec_one<1, false, true>(a, s); break;
+    case 7: launch_matvec_one<1, true, true>(a, s); break;
+    case 8: launch_matvec_one<2, false, false>(a, s); break;
+    case 9: launch_matvec_one<2, false, true>(a, s); break;
+    case 11: launch_matvec_one<2, true, true>(a, s); break;
+    default: launch_matvec_one<kPair, false, true>(a, s); break;
   }
-#undef NVFP4_MATVEC
   return hipGetLastError();
 }
 
