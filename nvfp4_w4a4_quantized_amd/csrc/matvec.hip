@@ -85,24 +85,31 @@ __device__ __forceinline__ bf16x8_t decode8_bf16(uint32_t c, float sb) {
   return r;
 }
 
+// Two E4M3 bytes (bits 0-7 and 8-15) as binary32, exactly: the hardware
+// conversion reads the OCP format, subnormals included (the NaN byte 0x7F is
+// no scale).
+__device__ __forceinline__ f32x2_t block_scales(uint32_t s) {
+  return __builtin_amdgcn_cvt_pk_f32_fp8((int)s, false);
+}
+
 // One stage of one 16-row tile: c = the lane's 32 codes, sb = its two E4M3
 // bytes (the second block's in bits 8-15).
 template <int XT>
 __device__ __forceinline__ void stage_product(f32x4_t& acc, const uint4& c, uint32_t sb,
                                               const XStage<XT>& x) {
   const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
-  const half2_t s2 = e4m3x2_to_half2(sb);
+  const f32x2_t s2 = block_scales(sb);
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
     if (XT == 2) {
-      const _Float16 h = s2[s / 2];
+      const _Float16 h = (_Float16)s2[s / 2];
       const half8_t a = decode8(cw[s], (half2_t){h, h});
       const uint4 xo = x_operand<XT>(x, s, 0);
       half8_t b;
       __builtin_memcpy(&b, &xo, 16);
       acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, acc, 0, 0, 0);
     } else {
-      const bf16x8_t a = decode8_bf16(cw[s], (float)s2[s / 2]);
+      const bf16x8_t a = decode8_bf16(cw[s], s2[s / 2]);
 #pragma unroll
       for (int p = 0; p < parts_of(XT); ++p) {
         const uint4 xo = x_operand<XT>(x, s, p);
@@ -143,19 +150,35 @@ __device__ __forceinline__ uint4 load_u128(const uint8_t* p) {
 
 // The entries whose expert is e (e == num_groups: of no expert) into `list`,
 // their number into *found; true if an entry before `slot` is among them.
-// `id` is topk_idx[threadIdx.x], loaded by the caller ahead of other work.
-__device__ __forceinline__ bool collect_entries(const MatvecArgs& a, int e, int id, int entries,
-                                                int slot, uint16_t* list, int* found) {
+// `ids` holds topk_idx[threadIdx.x + i * blockDim.x], loaded by the caller
+// ahead of other work; more entries are read in rounds of as many loads.
+constexpr int kIds = 8;
+__device__ __forceinline__ void load_ids(const MatvecArgs& a, int at, int entries, int (&ids)[kIds]) {
+#pragma unroll
+  for (int i = 0; i < kIds; ++i) {
+    const int j = at + i * (int)blockDim.x;
+    // (no load where no thread of the workgroup has an entry left)
+    if (at - (int)threadIdx.x + i * (int)blockDim.x < entries)
+      ids[i] = a.topk_idx[j < entries ? j : 0];
+  }
+}
+__device__ __forceinline__ bool collect_entries(const MatvecArgs& a, int e, int (&ids)[kIds],
+                                                int entries, int slot, uint16_t* list, int* found) {
   if (threadIdx.x == 0) *found = 0;
   __syncthreads();
   bool earlier = false;
-  for (int i = threadIdx.x; i < entries; i += blockDim.x) {
-    if (i != (int)threadIdx.x) id = a.topk_idx[i];
-    const int of = id >= 0 && id < a.num_groups ? id : a.num_groups;
-    if (of == e) {
-      earlier = earlier || i < slot;
-      // (a column's place does not change its result, so any order will do)
-      list[atomicAdd(found, 1)] = (uint16_t)i;
+  for (int at = threadIdx.x; at - (int)threadIdx.x < entries; at += kIds * blockDim.x) {
+    if (at >= kIds * (int)blockDim.x) load_ids(a, at, entries, ids);
+#pragma unroll
+    for (int i = 0; i < kIds; ++i) {
+      const int j = at + i * (int)blockDim.x;
+      if (j - (int)threadIdx.x >= entries) break;   // (the whole workgroup's)
+      const int of = ids[i] >= 0 && ids[i] < a.num_groups ? ids[i] : a.num_groups;
+      if (j < entries && of == e) {
+        earlier = earlier || j < slot;
+        // (a column's place does not change its result, so any order will do)
+        list[atomicAdd(found, 1)] = (uint16_t)j;
+      }
     }
   }
   return __syncthreads_or(earlier);
@@ -216,9 +239,9 @@ __global__ __launch_bounds__(512) void matvec_kernel(MatvecArgs a) {
   int e = 0, m = (int)a.tokens, first = 0;
   const int entries = EXPERT ? (int)a.tokens * a.topk : 0, slot = blockIdx.y;
   const bool by_entry = EXPERT && entries <= a.num_groups;
-  int id = -1;
+  int ids[kIds];
   if (EXPERT) {
-    if ((int)threadIdx.x < entries) id = a.topk_idx[threadIdx.x];
+    load_ids(a, threadIdx.x, entries, ids);
     e = by_entry ? a.topk_idx[slot] : slot;
     if (e < 0 || e >= a.num_groups) {
       if (SWIGLU || a.skip_unrouted) return;
@@ -243,7 +266,7 @@ __global__ __launch_bounds__(512) void matvec_kernel(MatvecArgs a) {
     }
   }
   if (EXPERT) {
-    const bool earlier = collect_entries(a, e, id, entries, by_entry ? slot : 0, list, &found);
+    const bool earlier = collect_entries(a, e, ids, entries, by_entry ? slot : 0, list, &found);
     if (earlier) return;
     m = found;
     if (m == 0) return;
@@ -332,13 +355,15 @@ __global__ __launch_bounds__(512) void matvec_kernel(MatvecArgs a) {
 //
 // From a handful of columns on, a wave's own reads of x cost more than its
 // weights (a 16-column operand is 4 KiB a stage beside 1.1 KiB of weights).
-// Here a workgroup's four waves take 32 rows each (16 gate and 16 up rows
-// with SwiGLU) and share 16 NC columns of x, brought into LDS once per
-// workgroup as the parts' bf16 / fp16 values, two stages at a time, double
-// buffered.  A column's stage is 16 pieces of 8 elements, piece p in slot
-// p ^ (column % 16): the 16 lanes that read one piece of 16 columns meet 16
-// different slots, so neither side has bank conflicts.  Each wave keeps four
-// stages of its weights in flight in registers.
+// Here the waves of a workgroup take 32 rows each (16 gate and 16 up rows
+// with SwiGLU) in two groups of four, the groups taking the stages in turn,
+// and share 16 NC columns of x, brought into LDS once per workgroup as the
+// parts' bf16 / fp16 values, double buffered.  A column's stage is 16 pieces
+// of 8 elements, piece p in slot p ^ (column % 16): the 16 lanes that read one
+// piece of 16 columns meet 16 different slots, so neither side has bank
+// conflicts.  Each wave keeps kDepth stages of its weights in flight in
+// registers; loads past the last stage are out of the buffer's range and
+// cost nothing.
 //
 // The last stage of a k that is no multiple of 128 (row-major weights):
 // lanes take the window [min(k0, k - 32), + 32) instead of [k0, + 32), and x
@@ -346,148 +371,188 @@ __global__ __launch_bounds__(512) void matvec_kernel(MatvecArgs a) {
 
 namespace {
 
-constexpr int kRowWaves = 4;
-constexpr int kDepth = 4;              // stages of weights in flight
+constexpr int kRowWaves = 4;           // waves of a group: 4 x 32 rows
 constexpr int kWide = 2;               // 16-row tiles of a wave
+#ifndef DEPTH
+#define DEPTH 2
+#endif
+#ifndef ETURNS
+#define ETURNS 1
+#endif
+#ifndef EWAVES
+#define EWAVES 1
+#endif
 
-template <int XT>
-constexpr int x_stages() { return XT == 0 ? 1 : 2; }
+template <int XT, int NC, bool EXPERT>
+struct RowsShape {
+  // groups of waves, taking the stages in turn
+  static constexpr int kGroups = EXPERT ? 1 : 2;
+  static constexpr int kThreads = kGroups * kRowWaves * kWave;
+  static constexpr int kDepth = EXPERT ? DEPTH : 4;   // stages of weights a wave has in flight
+  // stages of a group in one LDS buffer, and the buffer's size
+  static constexpr int kTurns = EXPERT ? ETURNS : (parts_of(XT) * NC <= 2 ? 2 : 1);
+  static constexpr int kBuffer = kTurns * kGroups * parts_of(XT) * NC * kTile * kStage * 2;
+};
 
-// Where a wave's weights of one stage lie.
+// A wave's weights of one stage.
 struct WStage {
-  uint4 c[kWide];
+  u32x4_t c[kWide];
   uint32_t s[kWide];
 };
 
 // 8 elements of a column on their way to LDS.
 template <int XT>
 struct XPiece {
-  uint4 w[XT == 0 || XT == kPair ? 2 : 1];
+  u32x4_t w[XT == 0 || XT == kPair ? 2 : 1];
 };
 
 template <int XT>
-__device__ __forceinline__ XPiece<XT> load_piece(const char* p, const char* p_lo) {
-  XPiece<XT> v;
-  __builtin_memcpy(&v.w[0], p, XT == 0 ? 32 : 16);
-  if (XT == kPair) __builtin_memcpy(&v.w[XT == kPair ? 1 : 0], p_lo, 16);
-  return v;
-}
-
-template <int XT>
 __device__ __forceinline__ uint4 piece_part(const XPiece<XT>& v, int part) {
-  if (XT != 0) return v.w[XT == kPair ? part : 0];
+  constexpr int kLast = XT == 0 || XT == kPair ? 1 : 0;
+  const u32x4_t& a = v.w[XT == kPair && part == 1 ? kLast : 0];
+  if (XT != 0) return make_uint4(a[0], a[1], a[2], a[3]);
+  const u32x4_t& b = v.w[kLast];
   XStage<0> x;
-  x.w[0] = v.w[0];
-  x.w[1] = v.w[XT == 0 ? 1 : 0];
+  x.w[0] = make_uint4(a[0], a[1], a[2], a[3]);
+  x.w[1] = make_uint4(b[0], b[1], b[2], b[3]);
   return x_operand<0>(x, 0, part);
 }
 
 }  // namespace
 
 template <int XT, int NC, bool SWIGLU, bool EXPERT>
-__global__ __launch_bounds__(kRowWaves* kWave) void matvec_rows_kernel(MatvecArgs a) {
-  constexpr int kCols = NC * kTile, kParts = parts_of(XT), XS = x_stages<XT>();
+__global__ __launch_bounds__((EXPERT ? 1 : 2) * kRowWaves * kWave, EXPERT ? EWAVES : 1) void
+matvec_rows_kernel(MatvecArgs a) {
+  typedef RowsShape<XT, NC, EXPERT> Shape;
+  constexpr int kGroups = Shape::kGroups, kTurns = Shape::kTurns, kDepth = Shape::kDepth;
+  constexpr int kThreads = Shape::kThreads, kLines = kThreads / 16;
+  constexpr int kCols = NC * kTile, kParts = parts_of(XT);
+  constexpr int XS = kTurns * kGroups;                    // stages of a buffer
   constexpr int kColBytes = kStage * 2;                   // one part of a column's stage
   constexpr int kPlane = kCols * kColBytes;
-  constexpr int kBuffer = XS * kParts * kPlane;
-  constexpr int kThreads = kRowWaves * kWave;
-  constexpr int kOwn = XS * NC * 16 * 16 / kThreads;      // pieces a thread brings per buffer
+  constexpr int kBuffer = Shape::kBuffer;
+  constexpr int kOwn = XS * NC * 256 / kThreads;          // pieces a thread brings per buffer
+  constexpr int xsize = XT == 0 ? 4 : 2;
+  static_assert(kDepth % kTurns == 0 && (kDepth / kTurns) % 2 == 0, "buffers alternate in the loop");
   extern __shared__ __align__(16) char lds[];
   uint16_t* list = reinterpret_cast<uint16_t*>(lds + 2 * kBuffer);
   __shared__ int found;
-  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  const int lane = threadIdx.x % kWave, wid = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int wave = wid % kRowWaves, group = kGroups == 1 ? 0 : wid / kRowWaves;
   const int r = lane % kTile, q = lane / kTile;
   int e = 0, m = (int)a.tokens, first = 0;
   // first row of the wave: of the output, or of the gate half
   const int64_t row0 = ((int64_t)blockIdx.x * kRowWaves + wave) * (SWIGLU ? kTile : kWide * kTile);
   const int64_t rows = SWIGLU ? a.inter : a.n;
+  int ids[kIds];
+  const int entries = EXPERT ? (int)a.tokens * a.topk : 0;
   if (EXPERT) {
-    const int entries = (int)a.tokens * a.topk;
     e = blockIdx.y;
     if (e == a.num_groups && (SWIGLU || a.skip_unrouted)) return;
-    const int id = (int)threadIdx.x < entries ? a.topk_idx[threadIdx.x] : -1;
-    collect_entries(a, e, id, entries, 0, list, &found);
+    load_ids(a, threadIdx.x, entries, ids);
+  } else {
+    first = blockIdx.y * kCols;
+    m = m < first + kCols ? m : first + kCols;
+  }
+  const int em = EXPERT && e == a.num_groups ? 0 : e;     // a matrix whose addresses are valid
+  const int k = (int)a.k, stages = (k + kStage - 1) / kStage;
+  const bool ragged = k % kStage != 0;                    // the last stage is a partial one
+  const int64_t matrix = a.n * (a.k / 2);                 // bytes of its codes, below 2^31
+  const __amdgpu_buffer_rsrc_t codes = buffer_rsrc(a.codes + em * matrix, (uint32_t)matrix);
+  const uint8_t* scales = a.scales + em * (matrix / 8);
+  uint32_t wc[kWide], ws[kWide], wc_last[kWide], ws_last[kWide];
+#pragma unroll
+  for (int rt = 0; rt < kWide; ++rt) {
+    // rows past the last read the last one (and are not stored)
+    int64_t row = row0 + r + (SWIGLU ? 0 : rt * kTile);
+    if (row >= rows) row = rows - 1;
+    row += SWIGLU ? rt * a.inter : 0;
+    const LanePlace p = lane_place(a, em, row, q);
+    wc[rt] = (uint32_t)(p.codes - (a.codes + em * matrix));
+    ws[rt] = (uint32_t)(p.scales - scales);
+    const int k0 = (stages - 1) * kStage + 32 * q, at = k0 < k - 32 ? k0 : k - 32;
+    wc_last[rt] = (uint32_t)(row * (k / 2) + at / 2);
+    ws_last[rt] = (uint32_t)(row * (k / 16) + at / 16);
+  }
+  const int cstep = a.layout == 0 ? kStage / 2 : 2048, sstep = a.layout == 0 ? kStage / 16 : 256;
+  // the wave's turn-th stage
+  auto load_w = [&](int turn) {
+    WStage w;
+    const int st = turn * kGroups + group;
+    const bool none = st >= stages, last = ragged && st >= stages - 1;
+    const int at = none ? stages - 1 : st;
+#pragma unroll
+    for (int rt = 0; rt < kWide; ++rt) {
+      w.c[rt] = __builtin_amdgcn_raw_buffer_load_b128(
+          codes, none ? kNone : (last ? wc_last[rt] : wc[rt]), last ? 0 : at * cstep, 0);
+      w.s[rt] = load_u16(scales + (last ? 0 : at * sstep) + (last ? ws_last[rt] : ws[rt]));
+    }
+    return w;
+  };
+  const float sg = a.gscale[em];
+  // the first weights are on their way while the entries are listed
+  WStage w[kDepth];
+#pragma unroll
+  for (int d = 0; d < kDepth; ++d) w[d] = load_w(d);
+  if (EXPERT) {
+    collect_entries(a, e, ids, entries, 0, list, &found);
     m = found;
     if (m == 0) return;
     if (e == a.num_groups) {   // entries of no expert
       store_zeros(a, list, m, row0 - wave * kWide * kTile, kRowWaves * kWide * kTile);
       return;
     }
-  } else {
-    first = blockIdx.y * kCols;
-    m = m < first + kCols ? m : first + kCols;
   }
-  const uint8_t* wc[kWide];
-  const uint8_t* ws[kWide];
-#pragma unroll
-  for (int rt = 0; rt < kWide; ++rt) {
-    // rows past the last read the last one (and are not stored)
-    int64_t row = row0 + r + (SWIGLU ? 0 : rt * kTile);
-    if (row >= rows) row = rows - 1;
-    const LanePlace p = lane_place(a, e, row + (SWIGLU ? rt * a.inter : 0), a.layout == 0 ? 0 : q);
-    wc[rt] = p.codes;
-    ws[rt] = p.scales;
-  }
-  const int k = (int)a.k, stages = (k + kStage - 1) / kStage;
-  auto load_w = [&](int st) {
-    WStage w;
-    st = st < stages ? st : stages - 1;
-    int co, so;
-    if (a.layout == 0) {
-      const int k0 = st * kStage + 32 * q;
-      const int at = k0 < k - 32 ? k0 : k - 32;
-      co = at / 2;
-      so = at / 16;
-    } else {
-      co = st * 2048;
-      so = st * 256;
-    }
-#pragma unroll
-    for (int rt = 0; rt < kWide; ++rt) {
-      w.c[rt] = load_u128(wc[rt] + co);
-      w.s[rt] = load_u16(ws[rt] + so);
-    }
-    return w;
-  };
-  const float sg = a.gscale[e];
-  constexpr int xsize = XT == 0 ? 4 : 2;
-  // a thread brings piece `slot ^ column` of columns own_col, own_col + 16, ...
-  const int own_col = threadIdx.x / 16, slot = threadIdx.x % 16;
-  const int piece = slot ^ own_col;                       // (kThreads / 16 == 16 columns)
-  const int pq = piece / 4, ps = piece % 4;
-  char* own_lds = lds + own_col * kColBytes + slot * 16;
+  // A thread brings slot threadIdx.x % 16 of every kLines-th line, a line being
+  // a column's stage (line = stage * kCols + column; a wave's four lines are of
+  // one stage).  Columns past the last and stages past the last are out of the
+  // buffer's range: zeros, and no traffic.
+  const int64_t xrows = EXPERT && a.x_by_entry ? entries : a.tokens;
+  const uint32_t xbytes = (uint32_t)(((xrows - 1) * a.ld_x + a.k) * xsize);   // below 2^31
+  const __amdgpu_buffer_rsrc_t xres = buffer_rsrc(a.x, xbytes);
+  const __amdgpu_buffer_rsrc_t xlow = buffer_rsrc(XT == kPair ? a.x_lo : a.x, xbytes);
+  const int slot = threadIdx.x % 16, own = threadIdx.x / 16;
+  const int piece = slot ^ (own % 16);
+  const int turns = (stages + kGroups - 1) / kGroups;
   for (int c0 = first; c0 < m; c0 += kCols) {
-    const char* xp[NC];
-    const char* xl[NC];
+    uint32_t xo[kOwn], xo_last[kOwn];
 #pragma unroll
-    for (int b = 0; b < NC; ++b) {
-      // columns past the last repeat it (and are not stored)
-      const int ci = c0 + b * 16 + own_col < m ? c0 + b * 16 + own_col : m - 1;
-      const int entry = EXPERT ? list[ci] : ci;
-      const int64_t xrow = EXPERT && !a.x_by_entry ? entry / a.topk : entry;
-      xp[b] = static_cast<const char*>(a.x) + xrow * a.ld_x * xsize;
-      xl[b] = XT == kPair ? reinterpret_cast<const char*>(a.x_lo) + xrow * a.ld_x * 2 : nullptr;
+    for (int i = 0; i < kOwn; ++i) {
+      const int col = c0 + (i * kLines + own) % kCols;
+      uint32_t at = kNone;
+      if (col < m) {
+        const int entry = EXPERT ? list[col] : col;
+        const int64_t xrow = EXPERT && !a.x_by_entry ? entry / a.topk : entry;
+        at = (uint32_t)(xrow * a.ld_x * xsize);
+      }
+      xo[i] = at + 8 * piece * xsize;
+      // the window of the last, partial stage (see above)
+      const int k0 = (stages - 1) * kStage + 32 * (piece / 4);
+      const int kw = (k0 < k - 32 ? k0 : k - 32) + 8 * (piece % 4);
+      xo_last[i] = kw >= k0 && kw < k ? at + kw * xsize : kNone;
     }
     XPiece<XT> xr[kOwn];
     auto load_xs = [&](int st0) {
 #pragma unroll
       for (int i = 0; i < kOwn; ++i) {
-        int st = st0 + i / NC;
-        st = st < stages ? st : stages - 1;
-        const int k0 = st * kStage + 32 * pq;
-        const int at = (k0 < k - 32 ? k0 : k - 32) + 8 * ps;
-        xr[i] = load_piece<XT>(xp[i % NC] + (int64_t)at * xsize,
-                               XT == kPair ? xl[i % NC] + (int64_t)at * 2 : nullptr);
-        if (at < k0 || at >= k) xr[i] = XPiece<XT>{};
+        const int st = st0 + (i * kLines + wid * 4) / kCols;
+        const bool none = st >= stages, last = ragged && st == stages - 1;
+        const uint32_t lo = none ? kNone : (last ? xo_last[i] : xo[i]);
+        const int un = none || last ? 0 : st * kStage * xsize;
+        xr[i].w[0] = __builtin_amdgcn_raw_buffer_load_b128(xres, lo, un, 0);
+        if (XT == 0) xr[i].w[XT == 0 ? 1 : 0] = __builtin_amdgcn_raw_buffer_load_b128(xres, lo + 16, un, 0);
+        if (XT == kPair) xr[i].w[XT == kPair ? 1 : 0] = __builtin_amdgcn_raw_buffer_load_b128(xlow, lo, un, 0);
       }
     };
     auto store_xs = [&](int buf) {
 #pragma unroll
-      for (int i = 0; i < kOwn; ++i)
+      for (int i = 0; i < kOwn; ++i) {
+        const int line = i * kLines + own;
 #pragma unroll
         for (int p = 0; p < kParts; ++p)
-          *reinterpret_cast<uint4*>(own_lds + buf * kBuffer + ((i / NC) * kParts + p) * kPlane +
-                                    (i % NC) * 16 * kColBytes) = piece_part<XT>(xr[i], p);
+          *reinterpret_cast<uint4*>(lds + buf * kBuffer + ((line / kCols) * kParts + p) * kPlane +
+                                    (line % kCols) * kColBytes + slot * 16) = piece_part<XT>(xr[i], p);
+      }
     };
     f32x4_t acc[kWide][NC];
 #pragma unroll
@@ -495,76 +560,91 @@ __global__ __launch_bounds__(kRowWaves* kWave) void matvec_rows_kernel(MatvecArg
 #pragma unroll
       for (int b = 0; b < NC; ++b) acc[rt][b] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
     load_xs(0);
-    WStage w[kDepth];
+    if (c0 != first) {
 #pragma unroll
-    for (int d = 0; d < kDepth; ++d) w[d] = load_w(d);
-    if (c0 != first) __syncthreads();                     // the last columns' buffers have been read
+      for (int d = 0; d < kDepth; ++d) w[d] = load_w(d);
+      __syncthreads();                                    // the last columns' sums have been read
+    }
     store_xs(0);
     __syncthreads();
-    for (int st0 = 0; st0 < stages; st0 += kDepth) {
+    for (int t0 = 0; t0 < turns; t0 += kDepth) {
 #pragma unroll
       for (int d = 0; d < kDepth; ++d) {
-        const int st = st0 + d, buf = (d / XS) % 2;
-        if (d % XS == 0) load_xs(st + XS);
-        if (st < stages) {
-          half2_t s2[kWide];
+        const int turn = t0 + d, buf = (d / kTurns) % 2;
+        if (d % kTurns == 0) load_xs((turn + kTurns) * kGroups);
+        if (turn * kGroups + group < stages) {
+          const char* xb0 = lds + buf * kBuffer + ((d % kTurns) * kGroups + group) * kParts * kPlane;
+          f32x2_t s2[kWide];
 #pragma unroll
-          for (int rt = 0; rt < kWide; ++rt) s2[rt] = e4m3x2_to_half2(w[d].s[rt]);
+          for (int rt = 0; rt < kWide; ++rt) s2[rt] = block_scales(w[d].s[rt]);
 #pragma unroll
           for (int s = 0; s < 4; ++s) {
-            uint4 xo[kParts][NC];
+            uint4 xv[kParts][NC];
 #pragma unroll
             for (int p = 0; p < kParts; ++p)
 #pragma unroll
               for (int b = 0; b < NC; ++b)
-                xo[p][b] = *reinterpret_cast<const uint4*>(
-                    lds + buf * kBuffer + ((d % XS) * kParts + p) * kPlane +
-                    (b * 16 + r) * kColBytes + ((4 * q + s) ^ r) * 16);
+                xv[p][b] = *reinterpret_cast<const uint4*>(
+                    xb0 + p * kPlane + (b * 16 + r) * kColBytes + ((4 * q + s) ^ r) * 16);
 #pragma unroll
             for (int rt = 0; rt < kWide; ++rt) {
-              const uint32_t cw[4] = {w[d].c[rt].x, w[d].c[rt].y, w[d].c[rt].z, w[d].c[rt].w};
               if (XT == 2) {
-                const _Float16 h = s2[rt][s / 2];
-                const half8_t wa = decode8(cw[s], (half2_t){h, h});
+                const _Float16 h = (_Float16)s2[rt][s / 2];
+                const half8_t wa = decode8(w[d].c[rt][s], (half2_t){h, h});
 #pragma unroll
                 for (int b = 0; b < NC; ++b) {
                   half8_t xb;
-                  __builtin_memcpy(&xb, &xo[0][b], 16);
+                  __builtin_memcpy(&xb, &xv[0][b], 16);
                   acc[rt][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wa, xb, acc[rt][b], 0, 0, 0);
                 }
               } else {
-                const bf16x8_t wa = decode8_bf16(cw[s], (float)s2[rt][s / 2]);
+                const bf16x8_t wa = decode8_bf16(w[d].c[rt][s], s2[rt][s / 2]);
 #pragma unroll
                 for (int p = 0; p < kParts; ++p)
 #pragma unroll
                   for (int b = 0; b < NC; ++b) {
                     bf16x8_t xb;
-                    __builtin_memcpy(&xb, &xo[p][b], 16);
+                    __builtin_memcpy(&xb, &xv[p][b], 16);
                     acc[rt][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wa, xb, acc[rt][b], 0, 0, 0);
                   }
               }
             }
           }
         }
-        w[d] = load_w(st + kDepth);
-        if (d % XS == XS - 1) {
+        w[d] = load_w(turn + kDepth);
+        if (d % kTurns == kTurns - 1) {
           store_xs(1 - buf);
           __syncthreads();
         }
       }
     }
+    // the second group's sums join the first's (the buffers are free now)
+    f32x4_t* red = reinterpret_cast<f32x4_t*>(lds);
+    if (kGroups == 2 && group == 1) {
+#pragma unroll
+      for (int rt = 0; rt < kWide; ++rt)
+#pragma unroll
+        for (int b = 0; b < NC; ++b) red[((wave * kWide + rt) * NC + b) * kWave + lane] = acc[rt][b];
+    }
+    if (kGroups == 2) {
+      __syncthreads();
+      if (group == 1) continue;
+    }
 #pragma unroll
     for (int b = 0; b < NC; ++b) {
+#pragma unroll
+      for (int rt = 0; rt < kWide; ++rt) {
+        if (kGroups == 2) acc[rt][b] += red[((wave * kWide + rt) * NC + b) * kWave + lane];
+        acc[rt][b] *= sg;
+      }
       const int ci = c0 + b * 16 + r;
       if (ci >= m) continue;
       const int entry = EXPERT ? list[ci] : ci;
       if (SWIGLU) {
-        if (row0 < rows)
-          store_d4(a, entry, row0 + 4 * q, acc[0][b] * sg, acc[1][b] * sg, a.prob[entry]);
+        if (row0 < rows) store_d4(a, entry, row0 + 4 * q, acc[0][b], acc[1][b], a.prob[entry]);
       } else {
 #pragma unroll
-        for (int rt = 0; rt < kWide; ++rt)
-          store4(a, entry, row0 + rt * kTile + 4 * q, acc[rt][b] * sg);
+        for (int rt = 0; rt < kWide; ++rt) store4(a, entry, row0 + rt * kTile + 4 * q, acc[rt][b]);
       }
     }
   }
@@ -584,26 +664,30 @@ int matvec_waves(int64_t k) {
 
 }  // namespace
 
+template <int XT, int NC, bool SWIGLU, bool EXPERT>
+static void launch_rows(const MatvecArgs& a, size_t list, hipStream_t s) {
+  const int64_t per = kRowWaves * kTile * (SWIGLU ? 1 : kWide);
+  const int64_t rows = SWIGLU ? a.inter : a.n, cols = NC * kTile;
+  const dim3 grid((unsigned)((rows + per - 1) / per),
+                  (unsigned)(EXPERT ? a.num_groups + 1 : (a.tokens + cols - 1) / cols));
+  matvec_rows_kernel<XT, NC, SWIGLU, EXPERT>
+      <<<grid, RowsShape<XT, NC, EXPERT>::kThreads, 2 * RowsShape<XT, NC, EXPERT>::kBuffer + list, s>>>(a);
+}
+
 template <int XT, bool SWIGLU, bool EXPERT>
 static void launch_matvec_one(const MatvecArgs& a, hipStream_t s) {
   const int64_t entries = a.tokens * a.topk;
   // columns a matrix meets, on average over the matrices that meet any
   const int64_t cols = EXPERT ? (entries + a.num_groups - 1) / a.num_groups : a.tokens;
   const size_t list = EXPERT ? (size_t)entries * 2 : 0;
-  if (cols > kFewColumns && a.k >= 32) {
-    const int64_t per = kRowWaves * kTile * (SWIGLU ? 1 : kWide);
-    const int64_t rows = SWIGLU ? a.inter : a.n;
-#define NVFP4_MATVEC_ROWS(NC)                                                                   \
-  matvec_rows_kernel<XT, NC, SWIGLU, EXPERT>                                                    \
-      <<<dim3((unsigned)((rows + per - 1) / per),                                               \
-              (unsigned)(EXPERT ? a.num_groups + 1 : (a.tokens + 16 * NC - 1) / (16 * NC))),    \
-         kRowWaves * kWave,                                                                     \
-         2 * x_stages<XT>() * parts_of(XT) * NC * kTile * kStage * 2 + list, s>>>(a)
+  const int64_t xrows = EXPERT && a.x_by_entry ? entries : a.tokens;
+  const int64_t xbytes = ((xrows - 1) * a.ld_x + a.k) * (XT == 0 ? 4 : 2);
+  if (cols > kFewColumns && a.k >= 32 && xbytes < kNone) {
     // the entries of an expert scatter about their mean: room for twice as many
-    if ((EXPERT ? 2 * cols : cols) <= 16) NVFP4_MATVEC_ROWS(1);
-    else if (EXPERT || cols <= 32) NVFP4_MATVEC_ROWS(2);
-    else NVFP4_MATVEC_ROWS(4);
-#undef NVFP4_MATVEC_ROWS
+    const int64_t room = EXPERT ? 2 * cols : cols;
+    if (room <= 16) launch_rows<XT, 1, SWIGLU, EXPERT>(a, list, s);
+    else if (EXPERT || XT == 0 || room <= 32) launch_rows<XT, 2, SWIGLU, EXPERT>(a, list, s);
+    else launch_rows<XT, EXPERT || XT == 0 ? 2 : 4, SWIGLU, EXPERT>(a, list, s);
     return;
   }
   const int waves = matvec_waves(a.k);
