@@ -865,6 +865,10 @@ int moe_expert_decode(const void* x, int x_dtype, int64_t tokens, int64_t hidden
   if (launch_matvec(f1, s) != hipSuccess) return NVFP4_HIP_ERROR;
   MatvecArgs f2 = matvec_args(L.d_hi, 1, inter, tokens, w2, num_experts, hidden, inter);
   f2.x_lo = L.d_lo; f2.x_by_entry = 1; f2.topk_idx = topk_idx; f2.topk = topk;
+  if (decode_down_fits(tokens)) {
+    f2.out = y; f2.out_dtype = x_dtype;
+    return hip_status(launch_decode_down(f2, s));
+  }
   f2.out = L.y_rows; f2.out_dtype = 0; f2.skip_unrouted = 1;
   if (launch_matvec(f2, s) != hipSuccess) return NVFP4_HIP_ERROR;
   return hip_status(launch_decode_combine(L.y_rows, topk_idx, tokens, topk, num_experts, hidden,

@@ -246,6 +246,10 @@ struct MatvecArgs {
   uint16_t* d_hi; uint16_t* d_lo; int64_t inter; const float* prob;
 };
 hipError_t launch_matvec(const MatvecArgs& a, hipStream_t s);
+// FC2 and the sum over a token's experts in one launch, for a few tokens (a.x
+// and a.x_lo the two parts of D, a.out the tokens' rows).
+bool decode_down_fits(int64_t tokens);
+hipError_t launch_decode_down(const MatvecArgs& a, hipStream_t s);
 hipError_t launch_decode_combine(const float* y_rows, const int32_t* idx, int64_t tokens,
                                  int32_t topk, int32_t num_experts, int64_t hidden, int y_dtype,
                                  void* y, hipStream_t s);

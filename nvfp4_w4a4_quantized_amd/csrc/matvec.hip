@@ -221,6 +221,101 @@ __device__ __forceinline__ void store_d4(const MatvecArgs& a, int64_t entry, int
 
 }  // namespace
 
+// The n-th set bit of a mask (n below its population).
+__device__ __forceinline__ int nth_bit(uint64_t mask, int n) {
+  for (int i = 0; i < n; ++i) mask &= mask - 1;
+  return __builtin_ctzll(mask);
+}
+
+// The entries of expert e, found by every wave on its own (one ballot per 64
+// ids, no LDS and no barrier).  *entry is that of column c0 + r, or some other
+// entry of e where the column is past the last; returns their number, or 0 if
+// an entry before `slot` is among them.
+__device__ __forceinline__ int find_entries(const MatvecArgs& a, int e, int entries, int slot, int c0,
+                                            int r, int* entry) {
+  const int lane = threadIdx.x % kWave;
+  int m = 0;
+  for (int base = 0; base < entries; base += kWave) {
+    const int i = base + lane;
+    const int id = a.topk_idx[i < entries ? i : 0];
+    const uint64_t mask = __ballot(i < entries && id == e);
+    if (mask == 0) continue;
+    if (base + __builtin_ctzll(mask) < slot) return 0;
+    const int n = __popcll(mask), want = c0 + r - m;
+    if (m == 0) *entry = base + __builtin_ctzll(mask);
+    if (want > 0 && want < n) *entry = base + nth_bit(mask, want);
+    if (want == 0) *entry = base + __builtin_ctzll(mask);
+    m += n;
+  }
+  return m;
+}
+
+// acc += the products of stages st, st + step, ... of the lane's rows, two
+// stages in flight.  With k no multiple of 128 (row-major weights) the stage
+// behind the last whole one, a multiple of 16, is taken too: a lane has none,
+// half or all of its 32 elements there.
+template <int XT, int RT>
+__device__ __forceinline__ void stage_loop(const MatvecArgs& a, f32x4_t (&acc)[RT],
+                                           const LanePlace (&place)[RT], const char* xp,
+                                           const char* xl, int q, int st, int step) {
+  constexpr int xsize = XT == 0 ? 4 : 2;
+  const int64_t cstep = a.layout == 0 ? kStage / 2 : 2048, sstep = a.layout == 0 ? kStage / 16 : 256;
+  const int stages = (int)(a.k / kStage);
+  for (; st < stages; st += 2 * step) {
+    const int st2 = st + step < stages ? st + step : st;
+    uint4 c[2][RT];
+    uint32_t sb[2][RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      c[0][rt] = load_u128(place[rt].codes + st * cstep);
+      sb[0][rt] = load_u16(place[rt].scales + st * sstep);
+    }
+    const XStage<XT> x0 = load_x<XT>(xp + (int64_t)st * kStage * xsize, xl + st * kStage * 2);
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      c[1][rt] = load_u128(place[rt].codes + st2 * cstep);
+      sb[1][rt] = load_u16(place[rt].scales + st2 * sstep);
+    }
+    const XStage<XT> x1 = load_x<XT>(xp + (int64_t)st2 * kStage * xsize, xl + st2 * kStage * 2);
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) stage_product<XT>(acc[rt], c[0][rt], sb[0][rt], x0);
+    if (st2 != st) {
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) stage_product<XT>(acc[rt], c[1][rt], sb[1][rt], x1);
+    }
+  }
+  if (a.k % kStage != 0 && st % step == stages % step) {
+    const int left = (int)(a.k - (int64_t)stages * kStage) - 32 * q;
+    XStage<XT> x = {};
+    uint4 c[RT] = {};
+    uint32_t sb[RT] = {};
+    if (left >= 16) {
+      xp += (int64_t)stages * kStage * xsize;
+      xl += stages * kStage * 2;
+      if (left >= 32) {
+        x = load_x<XT>(xp, xl);
+      } else {
+        __builtin_memcpy(&x.w[0], xp, 16 * xsize);
+        if (XT == kPair) __builtin_memcpy(&x.w[4 % (sizeof(x.w) / 16)], xl, 32);
+      }
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        const uint8_t* pc = place[rt].codes + stages * cstep;
+        const uint8_t* ps = place[rt].scales + stages * sstep;
+        if (left >= 32) {
+          c[rt] = load_u128(pc);
+          sb[rt] = load_u16(ps);
+        } else {
+          __builtin_memcpy(&c[rt], pc, 8);
+          sb[rt] = *ps;
+        }
+      }
+    }
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) stage_product<XT>(acc[rt], c[rt], sb[rt], x);
+  }
+}
+
 // Grid: x = 16-row tiles of the output, y = slots (EXPERT) or chunks of 16
 // columns.  A slot is an entry when there are no more entries than experts
 // (the first entry of an expert does the work of all of its entries), else an
@@ -229,109 +324,55 @@ template <int XT, bool SWIGLU, bool EXPERT>
 __global__ __launch_bounds__(512) void matvec_kernel(MatvecArgs a) {
   constexpr int RT = SWIGLU ? 2 : 1;
   extern __shared__ char lds[];
-  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int waves = blockDim.x / kWave;
   const int r = lane % kTile, q = lane / kTile;
   const int64_t row0 = (int64_t)blockIdx.x * kTile;
   f32x4_t* red = reinterpret_cast<f32x4_t*>(lds);
-  uint16_t* list = reinterpret_cast<uint16_t*>(lds + waves * RT * kWave * sizeof(f32x4_t));
-  __shared__ int found;
-  int e = 0, m = (int)a.tokens, first = 0;
   const int entries = EXPERT ? (int)a.tokens * a.topk : 0, slot = blockIdx.y;
   const bool by_entry = EXPERT && entries <= a.num_groups;
-  int ids[kIds];
+  int e = 0, m = (int)a.tokens, first = 0, entry = 0;
   if (EXPERT) {
-    load_ids(a, threadIdx.x, entries, ids);
     e = by_entry ? a.topk_idx[slot] : slot;
     if (e < 0 || e >= a.num_groups) {
+      // entries of no expert: zero results, this one's or all of them
       if (SWIGLU || a.skip_unrouted) return;
-      e = a.num_groups;
+      for (int i = by_entry ? slot : threadIdx.x; i < (by_entry ? slot + 1 : entries); i += blockDim.x) {
+        const int id = a.topk_idx[i];
+        if ((id >= 0 && id < a.num_groups) || (by_entry && threadIdx.x != 0)) continue;
+        for (int c = 0; c < kTile; c += 4) store4(a, i, row0 + c, (f32x4_t){0.f, 0.f, 0.f, 0.f});
+      }
+      return;
     }
+    m = find_entries(a, e, entries, by_entry ? slot : 0, 0, r, &entry);
+    if (m == 0) return;
+  } else {
+    first = blockIdx.y * kTile;
+    m = m < first + kTile ? m : first + kTile;
   }
-  const int64_t cstep = a.layout == 0 ? kStage / 2 : 2048, sstep = a.layout == 0 ? kStage / 16 : 256;
-  const int stages = (int)(a.k / kStage);
   LanePlace place[RT];
-  uint4 wc[RT];        // the wave's first stage, on its way while the entries are listed
-  uint32_t ws[RT];
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
     // rows past the last read the last one (and are not stored)
     int64_t row = row0 + r + (SWIGLU ? rt * a.inter : 0);
     if (!SWIGLU && row >= a.n) row = a.n - 1;
-    place[rt] = lane_place(a, EXPERT && e == a.num_groups ? 0 : e, row, q);
-    const int st = wave < stages ? wave : 0;
-    if (stages > 0) {
-      wc[rt] = load_u128(place[rt].codes + st * cstep);
-      ws[rt] = load_u16(place[rt].scales + st * sstep);
-    }
+    place[rt] = lane_place(a, e, row, q);
   }
-  if (EXPERT) {
-    const bool earlier = collect_entries(a, e, ids, entries, by_entry ? slot : 0, list, &found);
-    if (earlier) return;
-    m = found;
-    if (m == 0) return;
-    if (e == a.num_groups) {
-      store_zeros(a, list, m, row0, kTile);
-      return;
-    }
-  } else {
-    first = blockIdx.y * kTile;
-    m = m < first + kTile ? m : first + kTile;
-  }
-  const int xsize = XT == 0 ? 4 : 2;
+  constexpr int xsize = XT == 0 ? 4 : 2;
   const float sg = a.gscale[e];
   for (int c0 = first; c0 < m; c0 += kTile) {
-    // columns past the last repeat it (and are not stored)
-    const int ci = c0 + r < m ? c0 + r : m - 1;
-    const int entry = EXPERT ? list[ci] : ci;
+    // columns past the last read another's row (and are not stored)
+    if (!EXPERT) entry = c0 + r < m ? c0 + r : m - 1;
+    else if (c0 != 0) find_entries(a, e, entries, 0, c0, r, &entry);
     const int64_t xrow = EXPERT && !a.x_by_entry ? entry / a.topk : entry;
     const char* xp = static_cast<const char*>(a.x) + (xrow * a.ld_x + 32 * q) * xsize;
     const char* xl = XT == kPair ? reinterpret_cast<const char*>(a.x_lo) + (xrow * a.ld_x + 32 * q) * 2
                                  : nullptr;
+    const float p = SWIGLU ? a.prob[entry] : 1.0f;
     f32x4_t acc[RT];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) acc[rt] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
-    for (int st = wave; st < stages; st += waves) {
-      const XStage<XT> x = load_x<XT>(xp + (int64_t)st * kStage * xsize, XT == kPair ? xl + st * kStage * 2 : nullptr);
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        const bool had = c0 == first && st == wave;
-        stage_product<XT>(acc[rt], had ? wc[rt] : load_u128(place[rt].codes + st * cstep),
-                          had ? ws[rt] : load_u16(place[rt].scales + st * sstep), x);
-      }
-    }
-    // the k behind the last whole stage (row-major weights only): a multiple
-    // of 16, so a lane has none, half or all of its 32
-    const int left = (int)(a.k - (int64_t)stages * kStage) - 32 * q;
-    if (a.k % kStage != 0 && wave == stages % waves) {
-      XStage<XT> x = {};
-      uint4 c[RT] = {};
-      uint32_t sb[RT] = {};
-      const int64_t xo = (int64_t)stages * kStage * xsize;
-      if (left >= 16) {
-        const int bytes = left >= 32 ? 32 : 16;
-        if (bytes == 32) {
-          x = load_x<XT>(xp + xo, XT == kPair ? xl + stages * kStage * 2 : nullptr);
-        } else {
-          __builtin_memcpy(&x.w[0], xp + xo, 16 * xsize);
-          if (XT == kPair) __builtin_memcpy(&x.w[4 % (sizeof(x.w) / 16)], xl + stages * kStage * 2, 32);
-        }
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-          const uint8_t* pc = place[rt].codes + stages * cstep;
-          const uint8_t* ps = place[rt].scales + stages * sstep;
-          if (bytes == 32) {
-            c[rt] = load_u128(pc);
-            sb[rt] = load_u16(ps);
-          } else {
-            __builtin_memcpy(&c[rt], pc, 8);
-            sb[rt] = *ps;
-          }
-        }
-      }
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) stage_product<XT>(acc[rt], c[rt], sb[rt], x);
-    }
+    stage_loop<XT, RT>(a, acc, place, xp, xl, q, wave, waves);
     if (c0 != first) __syncthreads();   // the last chunk's sums have been read
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) red[(wave * RT + rt) * kWave + lane] = acc[rt];
@@ -344,10 +385,45 @@ __global__ __launch_bounds__(512) void matvec_kernel(MatvecArgs a) {
         acc[rt] = s * sg;
       }
       if (c0 + r < m) {
-        if (SWIGLU) store_d4(a, entry, row0 + 4 * q, acc[0], acc[RT - 1], a.prob[entry]);
+        if (SWIGLU) store_d4(a, entry, row0 + 4 * q, acc[0], acc[RT - 1], p);
         else store4(a, entry, row0 + 4 * q, acc[0]);
       }
     }
+  }
+}
+
+// The layer's FC2 and the sum over a token's experts in one: grid x = 16-row
+// tiles, y = tokens; `parts` waves share the stages of one of the token's
+// entries, the workgroup's wave sets take the entries in turn, and the waves'
+// sums (each times its expert's outer scale) are added in LDS in wave order.
+// All 16 columns of a product are the same row; the first is used.
+__global__ __launch_bounds__(1024) void decode_down_kernel(MatvecArgs a, int parts) {
+  extern __shared__ char lds[];
+  const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int waves = blockDim.x / kWave, sets = waves / parts;
+  const int r = lane % kTile, q = lane / kTile;
+  const int64_t row0 = (int64_t)blockIdx.x * kTile, t = blockIdx.y;
+  f32x4_t* red = reinterpret_cast<f32x4_t*>(lds);
+  f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
+  for (int j = wave / parts; j < a.topk; j += sets) {
+    const int64_t entry = t * a.topk + j;
+    const int e = a.topk_idx[entry];
+    if (e < 0 || e >= a.num_groups) continue;
+    const float sg = a.gscale[e];
+    const int64_t row = row0 + r;
+    const LanePlace place[1] = {lane_place(a, e, row < a.n ? row : a.n - 1, q)};
+    const int64_t at = (entry * a.ld_x + 32 * q) * 2;
+    f32x4_t acc[1] = {(f32x4_t){0.f, 0.f, 0.f, 0.f}};
+    stage_loop<kPair, 1>(a, acc, place, static_cast<const char*>(a.x) + at,
+                         reinterpret_cast<const char*>(a.x_lo) + at, q, wave % parts, parts);
+    sum += acc[0] * sg;
+  }
+  if (r == 0) red[wave * 4 + q] = sum;
+  __syncthreads();
+  if (threadIdx.x < 4) {
+    sum = red[threadIdx.x];
+    for (int w = 1; w < waves; ++w) sum += red[w * 4 + threadIdx.x];
+    store4(a, t, row0 + 4 * threadIdx.x, sum);
   }
 }
 
@@ -659,7 +735,8 @@ constexpr int kFewColumns = FEW;
 
 int matvec_waves(int64_t k) {
   const int64_t stages = (k + kStage - 1) / kStage;
-  return (int)(stages < 8 ? stages : 8);
+  // two stages a wave: one round of loads
+  return (int)(stages < 2 ? 1 : (stages < 16 ? (stages + 1) / 2 : 8));
 }
 
 }  // namespace
@@ -696,7 +773,7 @@ static void launch_matvec_one(const MatvecArgs& a, hipStream_t s) {
                                 : (entries <= a.num_groups ? entries : a.num_groups + 1);
   matvec_kernel<XT, SWIGLU, EXPERT>
       <<<dim3((unsigned)tiles, (unsigned)slots), waves * kWave,
-         (size_t)waves * (SWIGLU ? 2 : 1) * kWave * sizeof(f32x4_t) + list, s>>>(a);
+         (size_t)waves * (SWIGLU ? 2 : 1) * kWave * sizeof(f32x4_t), s>>>(a);
 }
 
 hipError_t launch_matvec(const MatvecArgs& a, hipStream_t s) {
@@ -715,6 +792,23 @@ hipError_t launch_matvec(const MatvecArgs& a, hipStream_t s) {
     case 11: launch_matvec_one<2, true, true>(a, s); break;
     default: launch_matvec_one<kPair, false, true>(a, s); break;
   }
+  return hipGetLastError();
+}
+
+#ifndef FUSE
+#define FUSE 2
+#endif
+bool decode_down_fits(int64_t tokens) { return tokens <= FUSE; }
+
+hipError_t launch_decode_down(const MatvecArgs& a, hipStream_t s) {
+  if (a.tokens == 0) return hipSuccess;
+  const int64_t stages = (a.k + kStage - 1) / kStage;
+  const int sets = a.topk < 16 ? a.topk : 16;
+  int parts = 16 / sets;
+  if (parts > (stages + 1) / 2) parts = (int)((stages + 1) / 2);
+  const int waves = sets * parts;
+  decode_down_kernel<<<dim3((unsigned)((a.n + kTile - 1) / kTile), (unsigned)a.tokens), waves * kWave,
+                       (size_t)waves * 4 * sizeof(f32x4_t), s>>>(a, parts);
   return hipGetLastError();
 }
 
