@@ -242,12 +242,13 @@ struct MatvecArgs {
   const int32_t* topk_idx; int32_t topk;      // NULL, 1: one matrix for every row
   void* out; int out_dtype;   // [rows, n]
   int skip_unrouted;          // entries of no expert are left unwritten (else zeros)
-  // SwiGLU epilogue (n = 2 * inter): the two parts of D, [entries, inter]
-  uint16_t* d_hi; uint16_t* d_lo; int64_t inter; const float* prob;
+  // SwiGLU epilogue (n = 2 * inter): D [entries, inter], binary32 (binary32 x)
+  // or its two bf16 parts
+  void* d; uint16_t* d_lo; int64_t inter; const float* prob;
 };
 hipError_t launch_matvec(const MatvecArgs& a, hipStream_t s);
 // FC2 and the sum over a token's experts in one launch, for a few tokens (a.x
-// and a.x_lo the two parts of D, a.out the tokens' rows).
+// and a.x_lo the layer's D, a.out the tokens' rows).
 bool decode_down_fits(int64_t tokens);
 hipError_t launch_decode_down(const MatvecArgs& a, hipStream_t s);
 hipError_t launch_decode_combine(const float* y_rows, const int32_t* idx, int64_t tokens,

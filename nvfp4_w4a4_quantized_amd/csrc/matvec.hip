@@ -9,9 +9,10 @@
 // cores in the type of x; products are exact in the binary32 accumulator and
 // s_g multiplies the sum.  binary32 x is split into three bf16 parts by
 // truncation (8 + 8 + 8 significant bits, an exact sum) and takes three
-// products.  The layer's intermediate D is kept as the sum of two bf16 parts,
-// high = bf16(D) and low = bf16(D - high), within 2^-17 of the binary32 D, so
-// FC2 adds no rounding that shows in a 16-bit result.
+// products.  The layer's intermediate D is kept in binary32 for binary32 x;
+// for 16-bit x as the sum of two bf16 parts, high = bf16(D) and low =
+// bf16(D - high), within 2^-17 of the binary32 D: FC2 takes two products
+// instead of three and adds no rounding that shows in a 16-bit result.
 //
 // Mapping: a wave multiplies 16 weight rows (32 with SwiGLU: 16 gate and the
 // 16 up rows) with 16 columns, a column being a row of x: v_mfma 16x16x32
@@ -149,9 +150,9 @@ __device__ __forceinline__ uint4 load_u128(const uint8_t* p) {
 }
 
 // The entries whose expert is e (e == num_groups: of no expert) into `list`,
-// their number into *found; true if an entry before `slot` is among them.
-// `ids` holds topk_idx[threadIdx.x + i * blockDim.x], loaded by the caller
-// ahead of other work; more entries are read in rounds of as many loads.
+// their number into *found.  `ids` holds topk_idx[threadIdx.x + i *
+// blockDim.x], loaded by the caller ahead of other work; more entries are
+// read in rounds of as many loads.
 constexpr int kIds = 8;
 __device__ __forceinline__ void load_ids(const MatvecArgs& a, int at, int entries, int (&ids)[kIds]) {
 #pragma unroll
@@ -162,11 +163,10 @@ __device__ __forceinline__ void load_ids(const MatvecArgs& a, int at, int entrie
       ids[i] = a.topk_idx[j < entries ? j : 0];
   }
 }
-__device__ __forceinline__ bool collect_entries(const MatvecArgs& a, int e, int (&ids)[kIds],
-                                                int entries, int slot, uint16_t* list, int* found) {
+__device__ __forceinline__ void collect_entries(const MatvecArgs& a, int e, int (&ids)[kIds],
+                                                int entries, uint16_t* list, int* found) {
   if (threadIdx.x == 0) *found = 0;
   __syncthreads();
-  bool earlier = false;
   for (int at = threadIdx.x; at - (int)threadIdx.x < entries; at += kIds * blockDim.x) {
     if (at >= kIds * (int)blockDim.x) load_ids(a, at, entries, ids);
 #pragma unroll
@@ -174,14 +174,11 @@ __device__ __forceinline__ bool collect_entries(const MatvecArgs& a, int e, int 
       const int j = at + i * (int)blockDim.x;
       if (j - (int)threadIdx.x >= entries) break;   // (the whole workgroup's)
       const int of = ids[i] >= 0 && ids[i] < a.num_groups ? ids[i] : a.num_groups;
-      if (j < entries && of == e) {
-        earlier = earlier || j < slot;
-        // (a column's place does not change its result, so any order will do)
-        list[atomicAdd(found, 1)] = (uint16_t)j;
-      }
+      // (a column's place does not change its result, so any order will do)
+      if (j < entries && of == e) list[atomicAdd(found, 1)] = (uint16_t)j;
     }
   }
-  return __syncthreads_or(earlier);
+  __syncthreads();
 }
 
 // Stores the values of rows [row, row + 4) of one column (those below n).
@@ -203,19 +200,27 @@ __device__ __forceinline__ void store_zeros(const MatvecArgs& a, const uint16_t*
     store4(a, list[i / (count / 4)], row + 4 * (i % (count / 4)), (f32x4_t){0.f, 0.f, 0.f, 0.f});
 }
 
-// The layer's D of one entry: silu(g) u p, as its two bf16 parts.
+// The layer's D of one entry, silu(g) u p: binary32 for binary32 x, else its
+// two bf16 parts.
+template <int XT>
 __device__ __forceinline__ void store_d4(const MatvecArgs& a, int64_t entry, int64_t col, f32x4_t g,
                                          f32x4_t u, float p) {
+  f32x4_t d;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) d[i] = g[i] / (1.0f + expf(-g[i])) * u[i] * p;
+  if (XT == 0) {
+    __builtin_memcpy(static_cast<float*>(a.d) + entry * a.inter + col, &d, 16);
+    return;
+  }
   uint16_t hi[4], lo[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float d = g[i] / (1.0f + expf(-g[i])) * u[i] * p;
-    hi[i] = Elem<1>::from_float(d);
+    hi[i] = Elem<1>::from_float(d[i]);
     const float h = Elem<1>::to_float(hi[i]);
     // an infinite D keeps a zero low part (inf - inf would be NaN)
-    lo[i] = Elem<1>::from_float(fabsf(h) < __builtin_huge_valf() ? d - h : 0.0f);
+    lo[i] = Elem<1>::from_float(fabsf(h) < __builtin_huge_valf() ? d[i] - h : 0.0f);
   }
-  __builtin_memcpy(a.d_hi + entry * a.inter + col, hi, 8);
+  __builtin_memcpy(static_cast<uint16_t*>(a.d) + entry * a.inter + col, hi, 8);
   __builtin_memcpy(a.d_lo + entry * a.inter + col, lo, 8);
 }
 
@@ -385,7 +390,7 @@ __global__ __launch_bounds__(512) void matvec_kernel(MatvecArgs a) {
         acc[rt] = s * sg;
       }
       if (c0 + r < m) {
-        if (SWIGLU) store_d4(a, entry, row0 + 4 * q, acc[0], acc[RT - 1], p);
+        if (SWIGLU) store_d4<XT>(a, entry, row0 + 4 * q, acc[0], acc[RT - 1], p);
         else store4(a, entry, row0 + 4 * q, acc[0]);
       }
     }
@@ -397,6 +402,7 @@ __global__ __launch_bounds__(512) void matvec_kernel(MatvecArgs a) {
 // entries, the workgroup's wave sets take the entries in turn, and the waves'
 // sums (each times its expert's outer scale) are added in LDS in wave order.
 // All 16 columns of a product are the same row; the first is used.
+template <int XT>
 __global__ __launch_bounds__(1024) void decode_down_kernel(MatvecArgs a, int parts) {
   extern __shared__ char lds[];
   const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -412,10 +418,11 @@ __global__ __launch_bounds__(1024) void decode_down_kernel(MatvecArgs a, int par
     const float sg = a.gscale[e];
     const int64_t row = row0 + r;
     const LanePlace place[1] = {lane_place(a, e, row < a.n ? row : a.n - 1, q)};
-    const int64_t at = (entry * a.ld_x + 32 * q) * 2;
+    const int64_t at = (entry * a.ld_x + 32 * q) * (XT == 0 ? 4 : 2);
     f32x4_t acc[1] = {(f32x4_t){0.f, 0.f, 0.f, 0.f}};
-    stage_loop<kPair, 1>(a, acc, place, static_cast<const char*>(a.x) + at,
-                         reinterpret_cast<const char*>(a.x_lo) + at, q, wave % parts, parts);
+    stage_loop<XT, 1>(a, acc, place, static_cast<const char*>(a.x) + at,
+                      XT == kPair ? reinterpret_cast<const char*>(a.x_lo) + at : nullptr, q,
+                      wave % parts, parts);
     sum += acc[0] * sg;
   }
   if (r == 0) red[wave * 4 + q] = sum;
@@ -447,28 +454,16 @@ __global__ __launch_bounds__(1024) void decode_down_kernel(MatvecArgs a, int par
 
 namespace {
 
-constexpr int kRowWaves = 4;           // waves of a group: 4 x 32 rows
 constexpr int kWide = 2;               // 16-row tiles of a wave
-#ifndef DEPTH
-#define DEPTH 2
-#endif
-#ifndef ETURNS
-#define ETURNS 1
-#endif
-#ifndef EWAVES
-#define EWAVES 1
-#endif
-
-template <int XT, int NC, bool EXPERT>
+// The workgroup's shape: waves of a group (32 rows each), and groups, taking
+// the stages in turn.
+template <int XT, int NC, int ROW_WAVES, int GROUPS>
 struct RowsShape {
-  // groups of waves, taking the stages in turn
-  static constexpr int kGroups = EXPERT ? 1 : 2;
-  static constexpr int kThreads = kGroups * kRowWaves * kWave;
-  static constexpr int kDepth = EXPERT ? DEPTH : 4;   // stages of weights a wave has in flight
-  // stages of a group in one LDS buffer, and the buffer's size
-  static constexpr int kTurns = EXPERT ? ETURNS : (parts_of(XT) * NC <= 2 ? 2 : 1);
-  static constexpr int kBuffer = kTurns * kGroups * parts_of(XT) * NC * kTile * kStage * 2;
+  static constexpr int kThreads = GROUPS * ROW_WAVES * kWave;
+  // an LDS buffer: one stage of every group
+  static constexpr int kBuffer = GROUPS * parts_of(XT) * NC * kTile * kStage * 2;
 };
+constexpr int kDepth = 2;              // stages of weights and of x on their way
 
 // A wave's weights of one stage.
 struct WStage {
@@ -481,6 +476,13 @@ template <int XT>
 struct XPiece {
   u32x4_t w[XT == 0 || XT == kPair ? 2 : 1];
 };
+
+// Where piece 4q + s of a column's stage lies, before the exclusive or with
+// the column.  A 16-byte LDS read serves lanes 0-3, 12-15, 20-23 and 24-27 of
+// each half wave together; with the quarters in this order those lanes, eight
+// columns of quarter q and the eight others of q + 1, meet different banks
+// (in the plain order they met in pairs, 4 extra cycles a read).
+__device__ __forceinline__ int slot_of(int q, int s) { return 4 * ((q >> 1) ^ (q & 1 ? 3 : 0)) + s; }
 
 template <int XT>
 __device__ __forceinline__ uint4 piece_part(const XPiece<XT>& v, int part) {
@@ -496,23 +498,25 @@ __device__ __forceinline__ uint4 piece_part(const XPiece<XT>& v, int part) {
 
 }  // namespace
 
-template <int XT, int NC, bool SWIGLU, bool EXPERT>
-__global__ __launch_bounds__((EXPERT ? 1 : 2) * kRowWaves * kWave, EXPERT ? EWAVES : 1) void
-matvec_rows_kernel(MatvecArgs a) {
-  typedef RowsShape<XT, NC, EXPERT> Shape;
-  constexpr int kGroups = Shape::kGroups, kTurns = Shape::kTurns, kDepth = Shape::kDepth;
+template <int XT, int NC, int ROW_WAVES, int GROUPS, bool SWIGLU, bool EXPERT>
+__global__ __launch_bounds__(ROW_WAVES* GROUPS* kWave) void matvec_rows_kernel(MatvecArgs a) {
+  typedef RowsShape<XT, NC, ROW_WAVES, GROUPS> Shape;
+  constexpr int kRowWaves = ROW_WAVES, kGroups = GROUPS, kSets = kDepth;
   constexpr int kThreads = Shape::kThreads, kLines = kThreads / 16;
   constexpr int kCols = NC * kTile, kParts = parts_of(XT);
-  constexpr int XS = kTurns * kGroups;                    // stages of a buffer
+  constexpr int XS = kGroups;                             // stages of a buffer
   constexpr int kColBytes = kStage * 2;                   // one part of a column's stage
   constexpr int kPlane = kCols * kColBytes;
   constexpr int kBuffer = Shape::kBuffer;
   constexpr int kOwn = XS * NC * 256 / kThreads;          // pieces a thread brings per buffer
   constexpr int xsize = XT == 0 ? 4 : 2;
-  static_assert(kDepth % kTurns == 0 && (kDepth / kTurns) % 2 == 0, "buffers alternate in the loop");
+  static_assert(kDepth % 2 == 0 && kDepth % kSets == 0, "buffers and sets turn in the loop");
+  // No static LDS in this kernel: the dynamic part would begin behind it, and
+  // at an address that is no multiple of 16 the buffers' 16-byte accesses run
+  // at half their rate (the layer of 256 tokens took 240 us instead of 110).
   extern __shared__ __align__(16) char lds[];
-  uint16_t* list = reinterpret_cast<uint16_t*>(lds + 2 * kBuffer);
-  __shared__ int found;
+  int* found = reinterpret_cast<int*>(lds + 2 * kBuffer);
+  uint16_t* list = reinterpret_cast<uint16_t*>(found + 1);
   const int lane = threadIdx.x % kWave, wid = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int wave = wid % kRowWaves, group = kGroups == 1 ? 0 : wid / kRowWaves;
   const int r = lane % kTile, q = lane / kTile;
@@ -554,9 +558,10 @@ matvec_rows_kernel(MatvecArgs a) {
   // the wave's turn-th stage
   auto load_w = [&](int turn) {
     WStage w;
-    const int st = turn * kGroups + group;
-    const bool none = st >= stages, last = ragged && st >= stages - 1;
-    const int at = none ? stages - 1 : st;
+    const int i = turn * kGroups + group;
+    const bool none = i >= stages;
+    const int at = none ? 0 : i;
+    const bool last = ragged && at == stages - 1;
 #pragma unroll
     for (int rt = 0; rt < kWide; ++rt) {
       w.c[rt] = __builtin_amdgcn_raw_buffer_load_b128(
@@ -571,8 +576,8 @@ matvec_rows_kernel(MatvecArgs a) {
 #pragma unroll
   for (int d = 0; d < kDepth; ++d) w[d] = load_w(d);
   if (EXPERT) {
-    collect_entries(a, e, ids, entries, 0, list, &found);
-    m = found;
+    collect_entries(a, e, ids, entries, list, found);
+    m = *found;
     if (m == 0) return;
     if (e == a.num_groups) {   // entries of no expert
       store_zeros(a, list, m, row0 - wave * kWide * kTile, kRowWaves * kWide * kTile);
@@ -588,7 +593,8 @@ matvec_rows_kernel(MatvecArgs a) {
   const __amdgpu_buffer_rsrc_t xres = buffer_rsrc(a.x, xbytes);
   const __amdgpu_buffer_rsrc_t xlow = buffer_rsrc(XT == kPair ? a.x_lo : a.x, xbytes);
   const int slot = threadIdx.x % 16, own = threadIdx.x / 16;
-  const int piece = slot ^ (own % 16);
+  const int pi = slot ^ (own % 16), pm = pi / 4;
+  const int piece = 4 * ((((pm ^ (pm >> 1)) & 1) << 1) | (pm >> 1)) + pi % 4;   // slot_of's inverse
   const int turns = (stages + kGroups - 1) / kGroups;
   for (int c0 = first; c0 < m; c0 += kCols) {
     uint32_t xo[kOwn], xo_last[kOwn];
@@ -607,27 +613,30 @@ matvec_rows_kernel(MatvecArgs a) {
       const int kw = (k0 < k - 32 ? k0 : k - 32) + 8 * (piece % 4);
       xo_last[i] = kw >= k0 && kw < k ? at + kw * xsize : kNone;
     }
-    XPiece<XT> xr[kOwn];
-    auto load_xs = [&](int st0) {
+    // pieces of the next buffers (see kSets)
+    XPiece<XT> xr[kSets][kOwn];
+    auto load_xs = [&](int set, int st0) {
 #pragma unroll
       for (int i = 0; i < kOwn; ++i) {
-        const int st = st0 + (i * kLines + wid * 4) / kCols;
-        const bool none = st >= stages, last = ragged && st == stages - 1;
+        const int nth = st0 + (i * kLines + wid * 4) / kCols;
+        const bool none = nth >= stages;
+        const int st = none ? 0 : nth;
+        const bool last = ragged && st == stages - 1;
         const uint32_t lo = none ? kNone : (last ? xo_last[i] : xo[i]);
         const int un = none || last ? 0 : st * kStage * xsize;
-        xr[i].w[0] = __builtin_amdgcn_raw_buffer_load_b128(xres, lo, un, 0);
-        if (XT == 0) xr[i].w[XT == 0 ? 1 : 0] = __builtin_amdgcn_raw_buffer_load_b128(xres, lo + 16, un, 0);
-        if (XT == kPair) xr[i].w[XT == kPair ? 1 : 0] = __builtin_amdgcn_raw_buffer_load_b128(xlow, lo, un, 0);
+        xr[set][i].w[0] = __builtin_amdgcn_raw_buffer_load_b128(xres, lo, un, 0);
+        if (XT == 0) xr[set][i].w[XT == 0 ? 1 : 0] = __builtin_amdgcn_raw_buffer_load_b128(xres, lo + 16, un, 0);
+        if (XT == kPair) xr[set][i].w[XT == kPair ? 1 : 0] = __builtin_amdgcn_raw_buffer_load_b128(xlow, lo, un, 0);
       }
     };
-    auto store_xs = [&](int buf) {
+    auto store_xs = [&](int set, int buf) {
 #pragma unroll
       for (int i = 0; i < kOwn; ++i) {
         const int line = i * kLines + own;
 #pragma unroll
         for (int p = 0; p < kParts; ++p)
           *reinterpret_cast<uint4*>(lds + buf * kBuffer + ((line / kCols) * kParts + p) * kPlane +
-                                    (line % kCols) * kColBytes + slot * 16) = piece_part<XT>(xr[i], p);
+                                    (line % kCols) * kColBytes + slot * 16) = piece_part<XT>(xr[set][i], p);
       }
     };
     f32x4_t acc[kWide][NC];
@@ -635,21 +644,22 @@ matvec_rows_kernel(MatvecArgs a) {
     for (int rt = 0; rt < kWide; ++rt)
 #pragma unroll
       for (int b = 0; b < NC; ++b) acc[rt][b] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
-    load_xs(0);
+#pragma unroll
+    for (int i = 0; i < kSets; ++i) load_xs(i, i * XS);
     if (c0 != first) {
 #pragma unroll
       for (int d = 0; d < kDepth; ++d) w[d] = load_w(d);
       __syncthreads();                                    // the last columns' sums have been read
     }
-    store_xs(0);
+    store_xs(0, 0);
     __syncthreads();
     for (int t0 = 0; t0 < turns; t0 += kDepth) {
 #pragma unroll
       for (int d = 0; d < kDepth; ++d) {
-        const int turn = t0 + d, buf = (d / kTurns) % 2;
-        if (d % kTurns == 0) load_xs((turn + kTurns) * kGroups);
-        if (turn * kGroups + group < stages) {
-          const char* xb0 = lds + buf * kBuffer + ((d % kTurns) * kGroups + group) * kParts * kPlane;
+        const int turn = t0 + d, buf = d % 2;
+        load_xs(d % kSets, (turn + kSets) * kGroups);
+        {   // (past the last stage both operands are zero)
+          const char* xb0 = lds + buf * kBuffer + group * kParts * kPlane;
           f32x2_t s2[kWide];
 #pragma unroll
           for (int rt = 0; rt < kWide; ++rt) s2[rt] = block_scales(w[d].s[rt]);
@@ -661,7 +671,7 @@ matvec_rows_kernel(MatvecArgs a) {
 #pragma unroll
               for (int b = 0; b < NC; ++b)
                 xv[p][b] = *reinterpret_cast<const uint4*>(
-                    xb0 + p * kPlane + (b * 16 + r) * kColBytes + ((4 * q + s) ^ r) * 16);
+                    xb0 + p * kPlane + (b * 16 + r) * kColBytes + (slot_of(q, s) ^ r) * 16);
 #pragma unroll
             for (int rt = 0; rt < kWide; ++rt) {
               if (XT == 2) {
@@ -688,10 +698,8 @@ matvec_rows_kernel(MatvecArgs a) {
           }
         }
         w[d] = load_w(turn + kDepth);
-        if (d % kTurns == kTurns - 1) {
-          store_xs(1 - buf);
-          __syncthreads();
-        }
+        store_xs((d + 1) % kSets, 1 - buf);
+        __syncthreads();
       }
     }
     // the second group's sums join the first's (the buffers are free now)
@@ -717,7 +725,7 @@ matvec_rows_kernel(MatvecArgs a) {
       if (ci >= m) continue;
       const int entry = EXPERT ? list[ci] : ci;
       if (SWIGLU) {
-        if (row0 < rows) store_d4(a, entry, row0 + 4 * q, acc[0][b], acc[1][b], a.prob[entry]);
+        if (row0 < rows) store_d4<XT>(a, entry, row0 + 4 * q, acc[0][b], acc[1][b], a.prob[entry]);
       } else {
 #pragma unroll
         for (int rt = 0; rt < kWide; ++rt) store4(a, entry, row0 + rt * kTile + 4 * q, acc[rt][b]);
@@ -728,10 +736,28 @@ matvec_rows_kernel(MatvecArgs a) {
 
 namespace {
 
-#ifndef FEW
-#define FEW 4
-#endif
-constexpr int kFewColumns = FEW;
+// Whether the kernel with x in LDS is the faster one.  It reads the weights at
+// a higher rate and does not pay for more columns, but needs many workgroups.
+// Measured (GPU time, bf16, tiled; direct kernel / LDS kernel), one matrix:
+//   k 2048: n 6144, 16 rows 7.9 / 9.0 us, 64 rows 16.9 / 16.2; n 8192, 16 rows
+//   8.4 / 9.4, 32 rows 12.7 / 11.5; n 12288, 8 rows 8.6 / 9.5, 16 rows 10.7 /
+//   9.5; n 24576, 1 row 10.0 / 12.1, 8 rows 12.9 / 12.2;
+//   k 8192: n 32768, 1 row 46.3 / 36.9.
+// Experts (the layer's two products and the sum; top-8 of 128, hidden 2048,
+// intermediate 768): 4 tokens 36.9 / 48.6 us, 8 tokens 64.2 / 59.0, 64 tokens
+// 195 / 82; top-4 of 16, hidden 1024, intermediate 512: 32 tokens 17.1 / 19.9,
+// 128 tokens 42.1 / 36.4; top-2 of 8, 2048 and 768: 64 tokens 29.6 / 29.4.
+bool rows_kernel_pays(const MatvecArgs& a, bool expert, bool swiglu) {
+  if (!expert) {
+    const int64_t t = a.tokens;
+    return a.n >= (t <= 2 ? 32768 : (t <= 8 ? 24576 : (t <= 16 ? 10240 : (t <= 32 ? 8192 : 6144))));
+  }
+  // 128-row blocks of the experts met, and the columns each meets on average
+  const int64_t entries = a.tokens * a.topk;
+  const int64_t hit = entries < a.num_groups ? entries : a.num_groups;
+  const int64_t blocks = hit * (((swiglu ? 2 * a.inter : a.n) + 127) / 128);
+  return blocks * (4 + entries / hit) >= 2688;
+}
 
 int matvec_waves(int64_t k) {
   const int64_t stages = (k + kStage - 1) / kStage;
@@ -741,30 +767,36 @@ int matvec_waves(int64_t k) {
 
 }  // namespace
 
-template <int XT, int NC, bool SWIGLU, bool EXPERT>
+template <int XT, int NC, int ROW_WAVES, int GROUPS, bool SWIGLU, bool EXPERT>
 static void launch_rows(const MatvecArgs& a, size_t list, hipStream_t s) {
-  const int64_t per = kRowWaves * kTile * (SWIGLU ? 1 : kWide);
+  typedef RowsShape<XT, NC, ROW_WAVES, GROUPS> Shape;
+  const int64_t per = ROW_WAVES * kTile * (SWIGLU ? 1 : kWide);
   const int64_t rows = SWIGLU ? a.inter : a.n, cols = NC * kTile;
   const dim3 grid((unsigned)((rows + per - 1) / per),
                   (unsigned)(EXPERT ? a.num_groups + 1 : (a.tokens + cols - 1) / cols));
-  matvec_rows_kernel<XT, NC, SWIGLU, EXPERT>
-      <<<grid, RowsShape<XT, NC, EXPERT>::kThreads, 2 * RowsShape<XT, NC, EXPERT>::kBuffer + list, s>>>(a);
+  matvec_rows_kernel<XT, NC, ROW_WAVES, GROUPS, SWIGLU, EXPERT>
+      <<<grid, Shape::kThreads, 2 * Shape::kBuffer + list, s>>>(a);
 }
 
 template <int XT, bool SWIGLU, bool EXPERT>
 static void launch_matvec_one(const MatvecArgs& a, hipStream_t s) {
   const int64_t entries = a.tokens * a.topk;
-  // columns a matrix meets, on average over the matrices that meet any
-  const int64_t cols = EXPERT ? (entries + a.num_groups - 1) / a.num_groups : a.tokens;
-  const size_t list = EXPERT ? (size_t)entries * 2 : 0;
   const int64_t xrows = EXPERT && a.x_by_entry ? entries : a.tokens;
   const int64_t xbytes = ((xrows - 1) * a.ld_x + a.k) * (XT == 0 ? 4 : 2);
-  if (cols > kFewColumns && a.k >= 32 && xbytes < kNone) {
-    // the entries of an expert scatter about their mean: room for twice as many
-    const int64_t room = EXPERT ? 2 * cols : cols;
-    if (room <= 16) launch_rows<XT, 1, SWIGLU, EXPERT>(a, list, s);
-    else if (EXPERT || XT == 0 || room <= 32) launch_rows<XT, 2, SWIGLU, EXPERT>(a, list, s);
-    else launch_rows<XT, EXPERT || XT == 0 ? 2 : 4, SWIGLU, EXPERT>(a, list, s);
+  if (a.k >= 32 && xbytes < kNone && rows_kernel_pays(a, EXPERT, SWIGLU)) {
+    if constexpr (EXPERT) {
+      // the entries of an expert scatter about their mean: room for twice as many
+      const size_t list = 4 + (size_t)entries * 2;   // their number and the entries
+      if (2 * entries <= 16 * a.num_groups) launch_rows<XT, 1, 4, 1, SWIGLU, true>(a, list, s);
+      else launch_rows<XT, 2, 4, 1, SWIGLU, true>(a, list, s);
+    } else {
+      if (a.tokens <= 16) launch_rows<XT, 1, 2, 2, false, false>(a, 0, s);
+      else if (XT == 0 || a.tokens <= 32) launch_rows<XT, 2, 2, 2, false, false>(a, 0, s);
+      // x is read once per workgroup: with 64 columns 128 rows each while that
+      // leaves a workgroup for every CU
+      else if (a.n >= 128 * 256) launch_rows<XT, XT == 0 ? 2 : 4, 4, 2, false, false>(a, 0, s);
+      else launch_rows<XT, XT == 0 ? 2 : 4, 2, 2, false, false>(a, 0, s);
+    }
     return;
   }
   const int waves = matvec_waves(a.k);
@@ -778,7 +810,7 @@ static void launch_matvec_one(const MatvecArgs& a, hipStream_t s) {
 
 hipError_t launch_matvec(const MatvecArgs& a, hipStream_t s) {
   if (a.tokens == 0) return hipSuccess;
-  const bool swiglu = a.d_hi != nullptr, expert = a.topk_idx != nullptr;
+  const bool swiglu = a.d != nullptr, expert = a.topk_idx != nullptr;
   const int xt = a.x_lo ? kPair : a.x_dtype;
   switch (xt * 4 + (swiglu ? 2 : 0) + (expert ? 1 : 0)) {
     case 0: launch_matvec_one<0, false, false>(a, s); break;
@@ -795,10 +827,11 @@ hipError_t launch_matvec(const MatvecArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-#ifndef FUSE
-#define FUSE 2
-#endif
-bool decode_down_fits(int64_t tokens) { return tokens <= FUSE; }
+// Measured (the whole layer, separate / fused sum): top-8 of 128, hidden 2048,
+// intermediate 768: 1 token 18.2 / 16.2 us, 4 tokens 36.9 / 33.7, 8 tokens
+// 64.2 / 64.6; top-4 of 16, hidden 1024, intermediate 512: 4 tokens 13.4 / 11.1,
+// 8 tokens 14.4 / 12.9, 16 tokens 15.2 / 16.8; top-2 of 8: 8 tokens 16.5 / 18.2.
+bool decode_down_fits(int64_t tokens) { return tokens <= 4; }
 
 hipError_t launch_decode_down(const MatvecArgs& a, hipStream_t s) {
   if (a.tokens == 0) return hipSuccess;
@@ -807,8 +840,10 @@ hipError_t launch_decode_down(const MatvecArgs& a, hipStream_t s) {
   int parts = 16 / sets;
   if (parts > (stages + 1) / 2) parts = (int)((stages + 1) / 2);
   const int waves = sets * parts;
-  decode_down_kernel<<<dim3((unsigned)((a.n + kTile - 1) / kTile), (unsigned)a.tokens), waves * kWave,
-                       (size_t)waves * 4 * sizeof(f32x4_t), s>>>(a, parts);
+  const dim3 grid((unsigned)((a.n + kTile - 1) / kTile), (unsigned)a.tokens);
+  const size_t lds = (size_t)waves * 4 * sizeof(f32x4_t);
+  if (a.x_lo) decode_down_kernel<kPair><<<grid, waves * kWave, lds, s>>>(a, parts);
+  else decode_down_kernel<0><<<grid, waves * kWave, lds, s>>>(a, parts);
   return hipGetLastError();
 }
 

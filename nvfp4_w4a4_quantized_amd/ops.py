@@ -533,33 +533,37 @@ def _need_rows(t, name, width=None, dtype=None):
     return ld
 
 
-def _need_shape(t, dtype, shape, name):
+def _dense(t, dtype, shape, dev, name):
+    """A contiguous tensor of this dtype and shape on device number dev.  (The
+    checks of a small call take as long as its kernel: one test where all is
+    well, the reasons only where it is not.)"""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev
+            and t.shape == shape and t.is_contiguous()):
+        return
     _need(t, (dtype,), name)
-    if t.shape != shape:
+    if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    raise NvFp4Error(f"{name} is on {t.device}, the call's first operand on cuda:{dev}")
 
 
-def _one_device(first, *others):
-    dev = first.device
-    for t in others:
-        if t is not None and t.device != dev:
-            raise NvFp4Error(f"operands on {dev} and {t.device}")
-    return dev
+def _same_device(t, dev, name):
+    if t.get_device() != dev:
+        raise NvFp4Error(f"{name} is on {t.device}, the call's first operand on cuda:{dev}")
 
 
 def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _call(device, what, *args):
-    """The library call `what` on the device's current stream.  (A launch goes
-    to the current device; switching, and a Stream object for the handle, cost
-    as much as a small call, so neither is done without need.)"""
-    stream = torch._C._cuda_getCurrentRawStream(device.index)
-    if device.index == torch.cuda.current_device():
+def _call(dev, what, *args):
+    """The library call `what` on device number dev's current stream.  (A
+    launch goes to the current device; switching, and a Stream object for the
+    handle, cost as much as a small call, so neither is done without need.)"""
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    if dev == torch.cuda.current_device():
         status = getattr(lib(), what)(*args, stream)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(dev):
             status = getattr(lib(), what)(*args, stream)
     if status:
         check(status, what)
@@ -576,15 +580,15 @@ def moe_router(logits, topk: int, bias=None, score: int = 0, renormalize: bool =
     with fewer than k left gets ids -1 with weight 0."""
     ld = _need_rows(logits, "logits")
     T, E = logits.shape
+    dev = logits.get_device()
     if bias is not None:
-        _need_shape(bias, torch.float32, (E,), "bias")
-    dev = _one_device(logits, bias)
+        _dense(bias, torch.float32, (E,), dev, "bias")
     if not 1 <= topk <= E:
         raise NvFp4Error(f"moe_router: topk {topk} of {E} experts")
-    idx = torch.empty((T, topk), dtype=torch.int32, device=dev)
-    prob = torch.empty((T, topk), dtype=torch.float32, device=dev)
-    _call(dev, "moe_router", _addr(logits), _DTYPE_CODE[logits.dtype], T, E, ld, _addr(bias), topk,
-          score, int(bool(renormalize)), scale, _addr(idx), _addr(prob))
+    idx = logits.new_empty((T, topk), dtype=torch.int32)
+    prob = logits.new_empty((T, topk), dtype=torch.float32)
+    _call(dev, "moe_router", logits.data_ptr(), _DTYPE_CODE[logits.dtype], T, E, ld, _addr(bias),
+          topk, score, int(bool(renormalize)), scale, idx.data_ptr(), prob.data_ptr())
     return idx, prob
 
 
@@ -594,35 +598,39 @@ def moe_router_backward(dprob, logits, topk_idx, score: int = 0, renormalize: bo
     dprob [T, k], with moe_router's logits, ids and choices."""
     ld = _need_rows(logits, "logits")
     T, E = logits.shape
-    _need(topk_idx, (torch.int32,), "topk_idx")
-    if topk_idx.dim() != 2 or topk_idx.shape[0] != T:
-        raise ValueError(f"topk_idx: shape {tuple(topk_idx.shape)}, expected [{T}, k]")
-    k = topk_idx.shape[1]
-    _need_shape(dprob, torch.float32, (T, k), "dprob")
-    dev = _one_device(logits, topk_idx, dprob)
-    out = torch.empty((T, E), dtype=logits.dtype, device=dev)
-    _call(dev, "moe_router_backward", _addr(logits), _DTYPE_CODE[logits.dtype], T, E, ld,
-          _addr(topk_idx), _addr(dprob), k, score, int(bool(renormalize)), scale, _addr(out))
+    dev = logits.get_device()
+    k = _topk_of(topk_idx, T, dev)
+    _dense(dprob, torch.float32, (T, k), dev, "dprob")
+    out = logits.new_empty((T, E))
+    _call(dev, "moe_router_backward", logits.data_ptr(), _DTYPE_CODE[logits.dtype], T, E, ld,
+          topk_idx.data_ptr(), dprob.data_ptr(), k, score, int(bool(renormalize)), scale,
+          out.data_ptr())
     return out
 
 
-def _entries(dst_row, prob, tokens=None):
-    _need(dst_row, (torch.int32,), "dst_row")
-    if dst_row.dim() != 2 or (tokens is not None and dst_row.shape[0] != tokens):
-        raise ValueError(f"dst_row: shape {tuple(dst_row.shape)}, expected "
+def _topk_of(ids, tokens, dev, name="topk_idx"):
+    """The entries per token of an int32 [T, k] tensor."""
+    if not (isinstance(ids, torch.Tensor) and ids.dim() == 2
+            and (tokens is None or ids.shape[0] == tokens)):
+        _need(ids, (torch.int32,), name)
+        raise ValueError(f"{name}: shape {tuple(ids.shape)}, expected "
                          f"[{'T' if tokens is None else tokens}, k]")
-    if prob is not None:
-        _need_shape(prob, torch.float32, dst_row.shape, "prob")
-    return dst_row.shape
+    _dense(ids, torch.int32, ids.shape, dev, name)
+    return ids.shape[1]
 
 
-def _rows_out(out, cap, like, expert_offsets, row_src):
+def _rows_out(out, like, dev, expert_offsets, row_src):
+    """The routed rows' tensor, [cap, H] in like's dtype, and cap."""
     for t, n in ((expert_offsets, "expert_offsets"), (row_src, "row_src")):
-        _need(t, (torch.int32,), n)
+        if not isinstance(t, torch.Tensor) or t.dim() != 1:
+            _need(t, (torch.int32,), n)
+            raise ValueError(f"{n}: shape {tuple(t.shape)}, expected one dimension")
+        _dense(t, torch.int32, t.shape, dev, n)
+    shape = (row_src.shape[0], like.shape[1])
     if out is None:
-        return torch.empty((cap, like.shape[1]), dtype=like.dtype, device=like.device)
-    _need_shape(out, like.dtype, (cap, like.shape[1]), "out")
-    return out
+        return like.new_empty(shape), shape[0]
+    _dense(out, like.dtype, shape, dev, "out")
+    return out, shape[0]
 
 
 def moe_sort_tokens(x, dst_row, row_src, expert_offsets, prob=None, out=None):
@@ -631,12 +639,15 @@ def moe_sort_tokens(x, dst_row, row_src, expert_offsets, prob=None, out=None):
     padding rows.  dst_row, row_src and expert_offsets are moe_permute's (its
     `offsets`).  Rows at or beyond the last offset are not written."""
     ld = _need_rows(x, "x")
-    T, k = _entries(dst_row, prob, x.shape[0])
-    rows = _rows_out(out, row_src.numel(), x, expert_offsets, row_src)
-    dev = _one_device(x, dst_row, prob, row_src, expert_offsets, rows)
-    _call(dev, "moe_sort_tokens", _addr(x), _DTYPE_CODE[x.dtype], T, x.shape[1], ld, _addr(dst_row),
-          _addr(prob), k, _addr(row_src), _addr(expert_offsets), expert_offsets.numel() - 1,
-          row_src.numel(), _addr(rows))
+    T, H = x.shape
+    dev = x.get_device()
+    k = _topk_of(dst_row, T, dev, "dst_row")
+    if prob is not None:
+        _dense(prob, torch.float32, (T, k), dev, "prob")
+    rows, cap = _rows_out(out, x, dev, expert_offsets, row_src)
+    _call(dev, "moe_sort_tokens", x.data_ptr(), _DTYPE_CODE[x.dtype], T, H, ld, dst_row.data_ptr(),
+          _addr(prob), k, row_src.data_ptr(), expert_offsets.data_ptr(),
+          expert_offsets.shape[0] - 1, cap, rows.data_ptr())
     return rows
 
 
@@ -644,18 +655,22 @@ def moe_sort_tokens_backward(drows, dst_row, x=None, prob=None):
     """Gradients of moe_sort_tokens from that of its rows: dx [T, H] and, with
     the forward's x given, dprob [T, k] (else None).  Returns (dx, dprob)."""
     ld = _need_rows(drows, "drows")
-    T, k = _entries(dst_row, prob)
-    H = drows.shape[1]
-    ld_x = H
+    cap, H = drows.shape
+    dev = drows.get_device()
+    k = _topk_of(dst_row, None, dev, "dst_row")
+    T = dst_row.shape[0]
+    if prob is not None:
+        _dense(prob, torch.float32, (T, k), dev, "prob")
+    ld_x, dprob = H, None
     if x is not None:
         ld_x = _need_rows(x, "x", H, drows.dtype)
         if x.shape[0] != T:
             raise ValueError(f"x: shape {tuple(x.shape)}, expected {(T, H)}")
-    dev = _one_device(drows, dst_row, prob, x)
-    dx = torch.empty((T, H), dtype=drows.dtype, device=dev)
-    dprob = torch.empty((T, k), dtype=torch.float32, device=dev) if x is not None else None
-    _call(dev, "moe_sort_tokens_backward", _addr(drows), _DTYPE_CODE[drows.dtype], T, H, ld,
-          drows.shape[0], _addr(dst_row), _addr(prob), k, _addr(x), ld_x, _addr(dx), _addr(dprob))
+        _same_device(x, dev, "x")
+        dprob = drows.new_empty((T, k), dtype=torch.float32)
+    dx = drows.new_empty((T, H))
+    _call(dev, "moe_sort_tokens_backward", drows.data_ptr(), _DTYPE_CODE[drows.dtype], T, H, ld,
+          cap, dst_row.data_ptr(), _addr(prob), k, _addr(x), ld_x, dx.data_ptr(), _addr(dprob))
     return dx, dprob
 
 
@@ -664,12 +679,15 @@ def moe_unsort_tokens(rows, dst_row, prob=None):
     rows[dst_row[t, j]] (prob None: plain sums), in the rows' dtype.  Entries
     with dst_row < 0 add nothing."""
     ld = _need_rows(rows, "rows")
-    T, k = _entries(dst_row, prob)
-    H = rows.shape[1]
-    dev = _one_device(rows, dst_row, prob)
-    y = torch.empty((T, H), dtype=rows.dtype, device=dev)
-    _call(dev, "moe_unsort_tokens", _addr(rows), _DTYPE_CODE[rows.dtype], T, H, ld, rows.shape[0],
-          _addr(dst_row), _addr(prob), k, _addr(y))
+    cap, H = rows.shape
+    dev = rows.get_device()
+    k = _topk_of(dst_row, None, dev, "dst_row")
+    T = dst_row.shape[0]
+    if prob is not None:
+        _dense(prob, torch.float32, (T, k), dev, "prob")
+    y = rows.new_empty((T, H))
+    _call(dev, "moe_unsort_tokens", rows.data_ptr(), _DTYPE_CODE[rows.dtype], T, H, ld, cap,
+          dst_row.data_ptr(), _addr(prob), k, y.data_ptr())
     return y
 
 
@@ -679,44 +697,55 @@ def moe_unsort_tokens_backward(dy, dst_row, row_src, expert_offsets, rows=None, 
     the padding rows, nothing written behind the last) and, with the forward's
     rows given, dprob [T, k] (else None).  Returns (drows, dprob)."""
     ld = _need_rows(dy, "dy")
-    T, k = _entries(dst_row, prob, dy.shape[0])
-    H, cap = dy.shape[1], row_src.numel()
-    drows = _rows_out(out, cap, dy, expert_offsets, row_src)
-    ld_rows = H
+    T, H = dy.shape
+    dev = dy.get_device()
+    k = _topk_of(dst_row, T, dev, "dst_row")
+    if prob is not None:
+        _dense(prob, torch.float32, (T, k), dev, "prob")
+    drows, cap = _rows_out(out, dy, dev, expert_offsets, row_src)
+    ld_rows, dprob = H, None
     if rows is not None:
         ld_rows = _need_rows(rows, "rows", H, dy.dtype)
         if rows.shape[0] != cap:
             raise ValueError(f"rows: shape {tuple(rows.shape)}, expected {(cap, H)}")
-    dev = _one_device(dy, dst_row, prob, row_src, expert_offsets, rows, drows)
-    dprob = torch.empty((T, k), dtype=torch.float32, device=dev) if rows is not None else None
-    _call(dev, "moe_unsort_tokens_backward", _addr(dy), _DTYPE_CODE[dy.dtype], T, H, ld,
-          _addr(dst_row), _addr(prob), k, _addr(row_src), _addr(expert_offsets),
-          expert_offsets.numel() - 1, cap, _addr(rows), ld_rows, _addr(drows), _addr(dprob))
+        _same_device(rows, dev, "rows")
+        dprob = dy.new_empty((T, k), dtype=torch.float32)
+    _call(dev, "moe_unsort_tokens_backward", dy.data_ptr(), _DTYPE_CODE[dy.dtype], T, H, ld,
+          dst_row.data_ptr(), _addr(prob), k, row_src.data_ptr(), expert_offsets.data_ptr(),
+          expert_offsets.shape[0] - 1, cap, _addr(rows), ld_rows, drows.data_ptr(), _addr(dprob))
     return drows, dprob
 
 
-def _need_weights(w, name, groups=None, n=None, k=None):
-    """NVFP4 weights whose three tensors fit each other (and the given sizes)."""
-    if not isinstance(w, NvFp4Weights):
-        raise TypeError(f"{name} must be NvFp4Weights")
-    _need(w.codes, (torch.uint8,), f"{name}.codes")
-    if w.codes.dim() != 3:
-        raise ValueError(f"{name}.codes: shape {tuple(w.codes.shape)}, expected [G, N, K/2]")
-    G, N, kh = w.codes.shape
-    want = tuple(v if v is not None else h for v, h in ((groups, G), (n, N), (k, 2 * kh)))
-    if (G, N, 2 * kh) != want:
-        raise ValueError(f"{name}: [G, N, K] is {(G, N, 2 * kh)}, expected {want}")
-    _need_shape(w.scales, torch.uint8, (G, N, kh // 8), f"{name}.scales")
-    _need_shape(w.gscale, torch.float32, (G,), f"{name}.gscale")
-    return G, N, 2 * kh
+def _weights_type(*named):
+    for w, name in named:
+        if not isinstance(w, NvFp4Weights):
+            raise TypeError(f"{name} must be NvFp4Weights")
 
 
-def _out_rows(out, shape, dtype, device):
+def _need_weights(w, name, dev, groups=None, n=None, k=None):
+    """NVFP4 weights whose three tensors fit each other (and the given sizes).
+    Returns [G, N, K]."""
+    codes = w.codes
+    if not isinstance(codes, torch.Tensor) or codes.dim() != 3:
+        _need(codes, (torch.uint8,), f"{name}.codes")
+        raise ValueError(f"{name}.codes: shape {tuple(codes.shape)}, expected [G, N, K/2]")
+    G, N, kh = codes.shape
+    K = 2 * kh
+    if (groups is not None and G != groups) or (n is not None and N != n) or (k is not None and K != k):
+        raise ValueError(f"{name}: [G, N, K] is {(G, N, K)}, expected "
+                         f"{tuple('any' if v is None else v for v in (groups, n, k))}")
+    _dense(codes, torch.uint8, (G, N, kh), dev, "codes of " + name)
+    _dense(w.scales, torch.uint8, (G, N, kh // 8), dev, "scales of " + name)
+    _dense(w.gscale, torch.float32, (G,), dev, "gscale of " + name)
+    return G, N, K
+
+
+def _out_rows(out, shape, dtype, like, dev):
     if dtype not in _DTYPE_CODE:
         raise TypeError(f"out_dtype {dtype} not in {tuple(_DTYPE_CODE)}")
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _need_shape(out, dtype, shape, "out")
+        return like.new_empty(shape, dtype=dtype)
+    _dense(out, dtype, shape, dev, "out")
     return out
 
 
@@ -724,13 +753,14 @@ def nvfp4_matvec(x, w: NvFp4Weights, out_dtype=None, out=None):
     """x [T, K] (float32, bf16 or fp16) times one NVFP4 matrix (w: [1, N, K],
     either layout): [T, N] in out_dtype (x's by default).  For the few rows of
     new tokens: the weights are read once, as they are."""
-    _, N, K = _need_weights(w, "w", groups=1)
-    ld = _need_rows(x, "x", K)
-    T = x.shape[0]
-    dev = _one_device(x, w.codes, w.scales, w.gscale, out)
-    out = _out_rows(out, (T, N), out_dtype if out_dtype is not None else x.dtype, dev)
-    _call(dev, "nvfp4_matvec", _addr(x), _DTYPE_CODE[x.dtype], T, ld, C.byref(w.c_struct()), N, K,
-          _DTYPE_CODE[out.dtype], _addr(out))
+    _weights_type((w, "w"))
+    ld = _need_rows(x, "x")
+    T, K = x.shape
+    dev = x.get_device()
+    _, N, _ = _need_weights(w, "w", dev, 1, None, K)
+    out = _out_rows(out, (T, N), out_dtype if out_dtype is not None else x.dtype, x, dev)
+    _call(dev, "nvfp4_matvec", x.data_ptr(), _DTYPE_CODE[x.dtype], T, ld, C.byref(w.c_struct()), N,
+          K, _DTYPE_CODE[out.dtype], out.data_ptr())
     return out
 
 
@@ -738,23 +768,24 @@ def nvfp4_expert_matvec(x, topk_idx, w: NvFp4Weights, out_dtype=None, out=None):
     """Every entry's row times its expert's NVFP4 matrix (w: [E, N, K]): x
     [T, K], or [T, k, K] with a row per entry, topk_idx int32 [T, k] -> out
     [T, k, N].  Entries with an id outside [0, E) give zeros."""
-    E, N, K = _need_weights(w, "w")
-    _need(topk_idx, (torch.int32,), "topk_idx")
-    if topk_idx.dim() != 2:
-        raise ValueError(f"topk_idx: shape {tuple(topk_idx.shape)}, expected [T, k]")
-    T, k = topk_idx.shape
+    _weights_type((w, "w"))
     by_entry = isinstance(x, torch.Tensor) and x.dim() == 3
+    rows = x
     if by_entry:
-        if not x.is_contiguous() or tuple(x.shape[:2]) != (T, k):
-            raise ValueError(f"x: shape {tuple(x.shape)}, expected contiguous {(T, k, K)}")
-        x = x.view(T * k, x.shape[2])
-    ld = _need_rows(x, "x", K)
-    if x.shape[0] != (T * k if by_entry else T):
-        raise ValueError(f"x: {x.shape[0]} rows for topk_idx {(T, k)}")
-    dev = _one_device(x, topk_idx, w.codes, w.scales, w.gscale, out)
-    out = _out_rows(out, (T, k, N), out_dtype if out_dtype is not None else x.dtype, dev)
-    _call(dev, "nvfp4_expert_matvec", _addr(x), _DTYPE_CODE[x.dtype], T, ld, int(by_entry),
-          _addr(topk_idx), k, C.byref(w.c_struct()), E, N, K, _DTYPE_CODE[out.dtype], _addr(out))
+        if not x.is_contiguous():
+            raise ValueError("x must be contiguous")
+        rows = x.view(x.shape[0] * x.shape[1], x.shape[2])
+    ld = _need_rows(rows, "x")
+    T, K = x.shape[0], x.shape[-1]
+    dev = x.get_device()
+    k = _topk_of(topk_idx, T, dev)
+    if by_entry and x.shape[1] != k:
+        raise ValueError(f"x: shape {tuple(x.shape)}, expected {(T, k, K)}")
+    E, N, _ = _need_weights(w, "w", dev, None, None, K)
+    out = _out_rows(out, (T, k, N), out_dtype if out_dtype is not None else x.dtype, x, dev)
+    _call(dev, "nvfp4_expert_matvec", x.data_ptr(), _DTYPE_CODE[x.dtype], T, ld, int(by_entry),
+          topk_idx.data_ptr(), k, C.byref(w.c_struct()), E, N, K, _DTYPE_CODE[out.dtype],
+          out.data_ptr())
     return out
 
 
@@ -768,23 +799,22 @@ def moe_expert_decode(x, topk_idx, topk_prob, num_experts: int, inter: int, w1: 
     weighted SwiGLU, FC2 and the sum over a token's experts with
     moe_expert_forward's weights.  x [T, H] float32, bf16 or fp16, T * k <=
     4096; returns y [T, H] in x's dtype."""
+    _weights_type((w1, "w1"), (w2, "w2"))
     ld = _need_rows(x, "x")
     T, H = x.shape
-    _need(topk_idx, (torch.int32,), "topk_idx")
-    if topk_idx.dim() != 2 or topk_idx.shape[0] != T:
-        raise ValueError(f"topk_idx: shape {tuple(topk_idx.shape)}, expected [{T}, k]")
-    k = topk_idx.shape[1]
-    _need_shape(topk_prob, torch.float32, (T, k), "topk_prob")
-    _need_weights(w1, "w1", num_experts, 2 * inter, H)
-    _need_weights(w2, "w2", num_experts, H, inter)
-    dev = _one_device(x, topk_idx, topk_prob, w1.codes, w1.scales, w1.gscale, w2.codes, w2.scales,
-                      w2.gscale, workspace, y)
-    y = _out_rows(y, (T, H), x.dtype, dev)
+    dev = x.get_device()
+    k = _topk_of(topk_idx, T, dev)
+    _dense(topk_prob, torch.float32, (T, k), dev, "topk_prob")
+    _need_weights(w1, "w1", dev, num_experts, 2 * inter, H)
+    _need_weights(w2, "w2", dev, num_experts, H, inter)
+    y = _out_rows(y, (T, H), x.dtype, x, dev)
     if workspace is None:
-        workspace = torch.empty(max(moe_expert_decode_workspace_size(T, H, inter, k), 256),
-                                dtype=torch.uint8, device=dev)
-    _need(workspace, (torch.uint8,), "workspace")
-    _call(dev, "moe_expert_decode", _addr(x), _DTYPE_CODE[x.dtype], T, H, inter, ld, _addr(topk_idx),
-          _addr(topk_prob), k, num_experts, C.byref(w1.c_struct()), C.byref(w2.c_struct()), _addr(y),
-          _addr(workspace), workspace.numel())
+        size = lib().moe_expert_decode_workspace_size(T, H, inter, k)
+        workspace = x.new_empty((max(size, 256),), dtype=torch.uint8)
+    else:
+        _need(workspace, (torch.uint8,), "workspace")
+        _same_device(workspace, dev, "workspace")
+    _call(dev, "moe_expert_decode", x.data_ptr(), _DTYPE_CODE[x.dtype], T, H, inter, ld,
+          topk_idx.data_ptr(), topk_prob.data_ptr(), k, num_experts, C.byref(w1.c_struct()),
+          C.byref(w2.c_struct()), y.data_ptr(), workspace.data_ptr(), workspace.numel())
     return y

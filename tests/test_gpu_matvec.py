@@ -3,8 +3,8 @@
 Tolerances: the documented (k + 16) 2^-24 sum |w x| of a binary32 sum of
 exact products, plus the output type's half step.  The layer: errors of h
 carried through D = silu(g) u p (|silu'| <= 1.1, |silu| <= |g|), D's own
-roundings (2^-17 of its two parts, (|g| + 16) 2^-24 of the exponential) and
-FC2's sum."""
+roundings (2^-17 of its two parts with 16-bit x, (|g| + 16) 2^-24 of the
+exponential) and FC2's sum."""
 import numpy as np
 import pytest
 import torch
@@ -146,7 +146,8 @@ def decode_ref(x, ids, prob, m1, m2):
     d = torch.where(ok, g * sig * u * p, torch.zeros_like(h[..., :I]))
     eg, eu = ((H + 16) * 2.0 ** -24 * hm[..., :I], (H + 16) * 2.0 ** -24 * hm[..., I:])
     ed = torch.where(ok, (1.1 * eg * (u.abs() + eu) + (g * sig).abs() * eu) * p.abs()
-                     + d.abs() * (2.0 ** -17 + (g.abs() + 16) * 2.0 ** -24), torch.zeros_like(d))
+                     + d.abs() * ((0.0 if x.dtype == torch.float32 else 2.0 ** -17)
+                                  + (g.abs() + 16) * 2.0 ** -24), torch.zeros_like(d))
     y, ym = R.expert_products(d, ids, m2, True)
     _, ey = R.expert_products(ed, ids, m2, True)
     lim = ey.sum(1) + (I + 32 + ids.shape[1]) * 2.0 ** -24 * ym.sum(1)
