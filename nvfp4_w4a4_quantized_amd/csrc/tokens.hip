@@ -57,6 +57,42 @@ __device__ __forceinline__ void block_sums(float (&v)[kBatch], int n, float* lds
   }
 }
 
+// A thread's piece [c, c + kN) of a row, brought back inside the row: a last,
+// partial piece becomes the row's last kN elements, its first `skip` of which
+// another thread holds too (both write the same values; dot products leave
+// them out).  Rows shorter than a piece are taken element by element.
+template <int N>
+struct Span {
+  int64_t at;
+  int skip, part;   // part: 0, or the elements of a row shorter than a piece
+  __device__ __forceinline__ Span(int64_t c, int64_t hidden)
+      : at(c + N <= hidden || hidden < N ? c : hidden - N), skip((int)(c - at)),
+        part(hidden < N ? (int)hidden : 0) {}
+};
+template <int DT>
+__device__ __forceinline__ void load_span(Piece<DT>& p, const typename Piece<DT>::T* row,
+                                          const Span<Piece<DT>::kN>& s, bool once) {
+  if (s.part) p.load_part(row, s.part);
+  else if (once) p.load_once(row + s.at);
+  else p.load(row + s.at);
+}
+template <int DT>
+__device__ __forceinline__ void store_span(const Piece<DT>& p, typename Piece<DT>::T* row,
+                                           const Span<Piece<DT>::kN>& s) {
+  if (s.part) p.store_part(row, s.part);
+  else p.store(row + s.at);
+}
+// dot += x . y over the piece's own elements
+template <int DT>
+__device__ __forceinline__ void dot_span(float& dot, const Piece<DT>& x, const Piece<DT>& y,
+                                         const Span<Piece<DT>::kN>& s) {
+#pragma unroll
+  for (int i = 0; i < Piece<DT>::kN; ++i) {
+    const float v = x.get(i) * y.get(i);
+    dot += i >= s.skip ? v : 0.0f;
+  }
+}
+
 // Row of entry (t, j), -1 if it has none.
 __device__ __forceinline__ int64_t entry_row(const TokenRowsArgs& a, int64_t t, int j) {
   const int64_t i = t * a.topk + j;
@@ -87,10 +123,8 @@ __global__ __launch_bounds__(256) void spread_kernel(TokenRowsArgs a, int64_t to
       const bool pad = r < r1 && a.row_src[r] < 0;
       for (uint64_t m = __ballot(pad); m != 0; m &= m - 1) {
         T* row = rows + (b + __builtin_ctzll(m)) * a.hidden;
-        for (int64_t c = (int64_t)threadIdx.x * P::kN; c < a.hidden; c += (int64_t)blockDim.x * P::kN) {
-          if (c + P::kN <= a.hidden) zero.store(row + c);
-          else zero.store_part(row + c, (int)(a.hidden - c));
-        }
+        for (int64_t c = (int64_t)threadIdx.x * P::kN; c < a.hidden; c += (int64_t)blockDim.x * P::kN)
+          store_span<DT>(zero, row, Span<P::kN>(c, a.hidden));
       }
     }
     return;
@@ -108,20 +142,16 @@ __global__ __launch_bounds__(256) void spread_kernel(TokenRowsArgs a, int64_t to
         dot[j] = 0.0f;
       }
       for (int64_t c = (int64_t)threadIdx.x * P::kN; c < a.hidden; c += (int64_t)blockDim.x * P::kN) {
-        const bool whole = c + P::kN <= a.hidden;
-        const int part = (int)(a.hidden - c);
+        const Span<P::kN> span(c, a.hidden);
         P x;
-        if (whole) x.load(tok + c);
-        else x.load_part(tok + c, part);
+        load_span<DT>(x, tok, span, false);
         P g[DOT ? kBatch : 1];
         if (DOT) {
 #pragma unroll
-          for (int j = 0; j < kBatch; ++j) {
-            if (row[j] < 0) continue;
-            const T* src = static_cast<const T*>(a.given) + row[j] * a.ld_given + c;
-            if (whole) g[DOT ? j : 0].load_once(src);
-            else g[DOT ? j : 0].load_part(src, part);
-          }
+          for (int j = 0; j < kBatch; ++j)
+            if (row[j] >= 0)
+              load_span<DT>(g[DOT ? j : 0], static_cast<const T*>(a.given) + row[j] * a.ld_given, span,
+                            true);
         }
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
@@ -131,13 +161,8 @@ __global__ __launch_bounds__(256) void spread_kernel(TokenRowsArgs a, int64_t to
 #pragma unroll
             for (int i = 0; i < P::kN; ++i) o.set(i, x.get(i) * w[j]);
           }
-          T* dst = rows + row[j] * a.hidden + c;
-          if (whole) o.store(dst);
-          else o.store_part(dst, part);
-          if (DOT) {
-#pragma unroll
-            for (int i = 0; i < P::kN; ++i) dot[j] += x.get(i) * g[DOT ? j : 0].get(i);
-          }
+          store_span<DT>(o, rows + row[j] * a.hidden, span);
+          if (DOT) dot_span<DT>(dot[j], x, g[DOT ? j : 0], span);
         }
       }
       if (DOT) {
@@ -167,16 +192,12 @@ __global__ __launch_bounds__(256) void collect_kernel(TokenRowsArgs a) {
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) dot[j] = 0.0f;
       for (int64_t c = (int64_t)threadIdx.x * P::kN; c < a.hidden; c += (int64_t)blockDim.x * P::kN) {
-        const bool whole = c + P::kN <= a.hidden;
-        const int part = (int)(a.hidden - c);
+        const Span<P::kN> span(c, a.hidden);
         float sum[P::kN];
 #pragma unroll
         for (int i = 0; i < P::kN; ++i) sum[i] = 0.0f;
         P x;
-        if (DOT) {
-          if (whole) x.load(given + c);
-          else x.load_part(given + c, part);
-        }
+        if (DOT) load_span<DT>(x, given, span, false);
         // the first pass over the columns takes every entry into the sum,
         // a later one (topk > kBatch) only its own entries' dot products
         const int last = j0 == 0 ? a.topk : (j0 + kBatch < a.topk ? j0 + kBatch : a.topk);
@@ -187,9 +208,7 @@ __global__ __launch_bounds__(256) void collect_kernel(TokenRowsArgs a) {
           for (int j = 0; j < kBatch; ++j) {
             row[j] = b + j < last ? entry_row(a, t, b + j) : -1;
             if (row[j] < 0) continue;
-            const T* src = static_cast<const T*>(a.rows) + row[j] * a.ld_rows + c;
-            if (whole) p[j].load_once(src);
-            else p[j].load_part(src, part);
+            load_span<DT>(p[j], static_cast<const T*>(a.rows) + row[j] * a.ld_rows, span, true);
           }
 #pragma unroll
           for (int j = 0; j < kBatch; ++j) {
@@ -200,18 +219,14 @@ __global__ __launch_bounds__(256) void collect_kernel(TokenRowsArgs a) {
               for (int i = 0; i < P::kN; ++i)
                 sum[i] += WEIGHTED ? w * p[j].get(i) : p[j].get(i);
             }
-            if (DOT && b == j0) {
-#pragma unroll
-              for (int i = 0; i < P::kN; ++i) dot[j] += x.get(i) * p[j].get(i);
-            }
+            if (DOT && b == j0) dot_span<DT>(dot[j], x, p[j], span);
           }
         }
         if (j0 == 0) {
           P o;
 #pragma unroll
           for (int i = 0; i < P::kN; ++i) o.set(i, sum[i]);
-          if (whole) o.store(out + c);
-          else o.store_part(out + c, part);
+          store_span<DT>(o, out, span);
         }
       }
       if (DOT) {
