@@ -181,16 +181,29 @@ __device__ __forceinline__ void collect_entries(const MatvecArgs& a, int e, int 
   __syncthreads();
 }
 
-// Stores the values of rows [row, row + 4) of one column (those below n).
-__device__ __forceinline__ void store4(const MatvecArgs& a, int64_t out_row, int64_t row, f32x4_t v) {
-  const int64_t at = out_row * a.n + row;
+// Stores the values of rows [row, row + 4) of one column (those below n): one
+// store where n is a multiple of 4, as row is.
+template <int DT>
+__device__ __forceinline__ void store4_as(void* out, int64_t at, int count, bool four, f32x4_t v) {
+  typename Elem<DT>::type o[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (row + i >= a.n) continue;
-    if (a.out_dtype == 0) static_cast<float*>(a.out)[at + i] = v[i];
-    else if (a.out_dtype == 1) static_cast<uint16_t*>(a.out)[at + i] = Elem<1>::from_float(v[i]);
-    else static_cast<_Float16*>(a.out)[at + i] = (_Float16)v[i];
+  for (int i = 0; i < 4; ++i) o[i] = Elem<DT>::from_float(v[i]);
+  typename Elem<DT>::type* p = static_cast<typename Elem<DT>::type*>(out) + at;
+  if (four) {
+    if (count > 0) __builtin_memcpy(p, o, sizeof(o));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < count) p[i] = o[i];
   }
+}
+__device__ __forceinline__ void store4(const MatvecArgs& a, int64_t out_row, int64_t row, f32x4_t v) {
+  const int64_t at = out_row * a.n + row, left = a.n - row;
+  const int count = left < 4 ? (int)left : 4;
+  const bool four = a.n % 4 == 0;
+  if (a.out_dtype == 0) store4_as<0>(a.out, at, count, four, v);
+  else if (a.out_dtype == 1) store4_as<1>(a.out, at, count, four, v);
+  else store4_as<2>(a.out, at, count, four, v);
 }
 
 // Zero results for the listed entries' rows [row, row + count).
