@@ -36,7 +36,13 @@ def check(got, ref, mag, k, what):
     (1, 1, 16, False), (1, 5, 48, False), (3, 33, 112, False), (17, 100, 144, False),
     (1, 32, 128, True), (2, 96, 256, True), (16, 64, 1024, True), (33, 160, 640, True),
     (5, 1001, 2064, False), (64, 257, 1040, False), (65, 48, 16384, False), (1, 64, 16384, True),
-    (130, 64, 384, True), (1, 5120, 2048, True)])
+    (130, 64, 384, True), (1, 5120, 2048, True),
+    # more weight rows: the kernel that shares x through LDS, at every number of
+    # columns, with rows and stages that end inside a tile
+    (1, 32771, 272, False), (2, 32768, 128, True), (7, 24581, 144, False), (8, 24576, 384, True),
+    (16, 10247, 400, False), (15, 10240, 1024, True), (30, 8193, 112, False), (32, 8192, 640, True),
+    (64, 6145, 1040, False), (70, 6176, 384, True), (64, 32800, 256, True), (40, 32771, 48, False),
+    (33, 6150, 32, False), (64, 6200, 16, False)])
 def test_matvec(T, n, k, tiled, dtype):
     from nvfp4_w4a4_quantized_amd import ops
     rng = np.random.default_rng(T + n + k)
@@ -114,7 +120,9 @@ def make_ids(rng, T, k, E, kind):
     (4, 3, 5, 50, 80, False, "dropped"), (37, 4, 60, 101, 336, False, "dropped"),
     (40, 1, 7, 32, 128, True, "one"), (64, 8, 16, 96, 384, True, "dropped"),
     (512, 8, 8, 32, 128, True, "plain"), (4096, 1, 3, 17, 32, False, "plain"),
-    (2, 2, 1024, 16, 48, False, "plain")])
+    (2, 2, 1024, 16, 48, False, "plain"),
+    (64, 2, 64, 1500, 208, False, "dropped"), (300, 4, 12, 1101, 336, False, "dropped"),
+    (100, 1, 1, 400, 144, False, "one"), (60, 6, 50, 1024, 512, True, "plain")])
 def test_expert_matvec(T, k, E, n, K, tiled, kind, dtype):
     from nvfp4_w4a4_quantized_amd import ops
     rng = np.random.default_rng(T + n + K)
@@ -157,7 +165,9 @@ def decode_ref(x, ids, prob, m1, m2):
 DECODE = [(1, 1, 1, 16, 16, False, "plain"), (1, 8, 128, 256, 128, True, "plain"),
           (3, 2, 4, 48, 80, False, "dropped"), (16, 4, 8, 256, 128, True, "dropped"),
           (37, 4, 20, 272, 112, False, "dropped"), (40, 1, 7, 128, 128, True, "one"),
-          (128, 8, 16, 256, 256, True, "plain"), (512, 8, 12, 64, 48, False, "plain")]
+          (128, 8, 16, 256, 256, True, "plain"), (512, 8, 12, 64, 48, False, "plain"),
+          (3, 20, 24, 48, 80, False, "dropped"), (4, 16, 16, 128, 1040, False, "plain"),
+          (200, 4, 40, 336, 208, False, "dropped"), (100, 2, 60, 512, 384, True, "plain")]
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
@@ -206,3 +216,47 @@ def test_no_tokens():
     prob = torch.empty((0, 2), dtype=torch.float32, device="cuda")
     assert ops.moe_expert_decode(x, ids, prob, 4, 128, w1, w2).shape == (0, 128)
     assert ops.nvfp4_expert_matvec(x, ids, w1).shape == (0, 2, 256)
+
+
+@pytest.mark.parametrize("T,n", [(3, 40), (64, 6160)])
+def test_smallest_values(T, n):
+    """Subnormal fp16 activations count in full, in both kernels."""
+    from nvfp4_w4a4_quantized_amd import ops
+    rng = np.random.default_rng(12)
+    codes, scales, gs = R.make_weights(rng, 1, n, 256)
+    gs[:] = 1.0
+    w = held(codes, scales, gs, False)
+    x = torch.from_numpy(rng.integers(-63, 64, (T, 256)).astype(np.float32) * 2.0 ** -24).half()
+    m = R.decode(codes, scales, gs)[0]
+    y = ops.nvfp4_matvec(x.cuda(), w, out_dtype=torch.float32)
+    check(y, x.double() @ m.t(), x.double().abs() @ m.abs().t(), 256, "subnormal")
+
+
+def test_rows_far_apart():
+    """Rows of x more than 2^31 bytes apart in all."""
+    from nvfp4_w4a4_quantized_amd import ops
+    rng = np.random.default_rng(13)
+    w = held(*R.make_weights(rng, 1, 6208, 64), False)
+    big = torch.empty((64, 20_000_000), dtype=torch.bfloat16, device="cuda")
+    x = big[:, 19_999_000:19_999_064]
+    x.copy_(torch.from_numpy(rng.standard_normal((64, 64)).astype(np.float32)))
+    near = ops.nvfp4_matvec(x.contiguous(), w, out_dtype=torch.float32).double()
+    far = ops.nvfp4_matvec(x, w, out_dtype=torch.float32).double()
+    # two kernels: 80 * 2^-23 of the terms' magnitudes, themselves below 30 in sum
+    assert float((near - far).abs().max()) < 80 * 2.0 ** -23 * 30
+
+
+def test_weights_beyond_four_gigabytes():
+    """The last of 40 experts of 134 MB each, against it alone."""
+    from nvfp4_w4a4_quantized_amd import ops
+    from nvfp4_w4a4_quantized_amd.ops import NvFp4Weights
+    E, n, k = 40, 16384, 16384
+    codes = torch.randint(0, 256, (E, n, k // 2), dtype=torch.uint8, device="cuda")
+    scales = torch.randint(40, 60, (E, n, k // 16), dtype=torch.uint8, device="cuda")
+    gs = torch.full((E,), 0.01, device="cuda")
+    w, last = NvFp4Weights(codes, scales, gs), NvFp4Weights(codes[E - 1:], scales[E - 1:], gs[E - 1:])
+    x = torch.randn((2, k), device="cuda").bfloat16()
+    ids = torch.full((2, 1), E - 1, dtype=torch.int32, device="cuda")
+    y = ops.nvfp4_expert_matvec(x, ids, w, out_dtype=torch.float32)
+    z = ops.nvfp4_matvec(x, last, out_dtype=torch.float32)
+    assert float((y[:, 0] - z).norm() / z.norm()) < 1e-5

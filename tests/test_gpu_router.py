@@ -53,7 +53,8 @@ def bound(logits, ids, score, renorm):
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("kind", ["plain", "ties", "masked", "lowest", "wide"])
 @pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 128, 8), (3, 7, 7), (65, 60, 4), (130, 129, 6),
-                                   (37, 257, 9), (9, 1000, 20), (5, 1024, 1)])
+                                   (37, 257, 9), (9, 1000, 20), (5, 1024, 1),
+                                   (6, 100, 40), (4, 1024, 200), (3, 256, 256)])
 def test_router_matches_the_definition(T, E, k, kind, dtype):
     from nvfp4_w4a4_quantized_amd import ops
     rng = np.random.default_rng(T * 1000 + E + k)
@@ -199,3 +200,15 @@ def test_many_tokens():
     assert torch.equal(ids.cpu(), ref)
     rw = R.router_weights(logits, ref, 0, True)
     assert bool(((w.cpu().double() - rw).abs() <= bound(logits, ref, 0, True) * rw).all())
+
+
+def test_more_than_two_to_the_31_logits():
+    from nvfp4_w4a4_quantized_amd import ops
+    T, E = 2_200_000, 1000
+    logits = torch.randn((T, E), device="cuda", dtype=torch.bfloat16)
+    ids, w = ops.moe_router(logits, 4)
+    tail = logits[-5:].contiguous()
+    i1, w1 = ops.moe_router(tail, 4)
+    assert torch.equal(ids[-5:], i1) and torch.equal(w[-5:], w1)
+    dz = ops.moe_router_backward(w, logits, ids, renormalize=False)
+    assert torch.equal(dz[-5:], ops.moe_router_backward(w1, tail, i1, renormalize=False))

@@ -201,3 +201,24 @@ def test_weight_gradients_against_differences():
         y = ops.moe_unsort_tokens(d["rows"], d["dst"], prob=up).cpu().double()
         num = ((y - base) * c["x"].double()).sum(1)
         assert float((num - dprob[:, j]).abs().max()) < 1e-3   # H * 2^-22 * |y x|, |y x| < 30
+
+
+def test_more_than_two_to_the_31_elements():
+    """Rows whose offsets pass 31 bits: the last tokens' rows, both ways."""
+    from nvfp4_w4a4_quantized_amd import ops
+    T, k, H = 270_000, 8, 1024
+    x = torch.randn((T, H), device="cuda").bfloat16()
+    row = torch.arange(T * k, dtype=torch.int32, device="cuda")
+    dst = (T * k - 1 - row).view(T, k).contiguous()
+    src = (torch.flip(row, (0,)) // k).to(torch.int32)
+    offs = torch.tensor([0, T * k], dtype=torch.int32, device="cuda")
+    prob = torch.full((T, k), 0.125, device="cuda")
+    rows = ops.moe_sort_tokens(x, dst, src, offs)
+    for r in (0, 1, T * k // 2, T * k - 1):
+        assert torch.equal(rows[r], x[int(src[r])])
+    y = ops.moe_unsort_tokens(rows, dst, prob=prob)
+    assert torch.equal(y, x)
+    drows, dprob = ops.moe_unsort_tokens_backward(x, dst, src, offs, rows=rows, prob=prob)
+    assert torch.equal(drows[T * k - 1], (x[0].float() * 0.125).bfloat16())
+    ref = (x[-4:].double() ** 2).sum(1, keepdim=True).expand(4, k)
+    assert bool(((dprob[-4:].double() - ref).abs() <= (H + 2) * 2.0 ** -24 * ref).all())
