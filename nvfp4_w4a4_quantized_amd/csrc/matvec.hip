@@ -24,6 +24,12 @@
 // LDS in wave order, so results do not depend on timing.
 //
 // Bound: the weights' bytes (9/16 per weight); x comes from the caches.
+// Two kernels: matvec_kernel gives every 16 rows a workgroup whose waves split
+// k, for little work and few columns; matvec_rows_kernel gives a workgroup 64
+// or 128 rows and shares x through LDS.  Measured kernel times: one bf16 row
+// by [5120, 2048] 4.9 us (one round of loads, a reduction and two launches'
+// latency: 1.2 TB/s), by [16384, 4096] 3.3 TB/s (both the direct kernel); by
+// [32768, 8192] 1 to 16 rows 4.1 TB/s, 64 rows 2.8 TB/s (the LDS kernel).
 #include "elem.h"
 #include "gemm_common.h"
 #include "launch.h"
@@ -451,15 +457,27 @@ __global__ __launch_bounds__(1024) void decode_down_kernel(MatvecArgs a, int par
 //
 // From a handful of columns on, a wave's own reads of x cost more than its
 // weights (a 16-column operand is 4 KiB a stage beside 1.1 KiB of weights).
-// Here the waves of a workgroup take 32 rows each (16 gate and 16 up rows
-// with SwiGLU) in two groups of four, the groups taking the stages in turn,
-// and share 16 NC columns of x, brought into LDS once per workgroup as the
-// parts' bf16 / fp16 values, double buffered.  A column's stage is 16 pieces
-// of 8 elements, piece p in slot p ^ (column % 16): the 16 lanes that read one
-// piece of 16 columns meet 16 different slots, so neither side has bank
-// conflicts.  Each wave keeps kDepth stages of its weights in flight in
-// registers; loads past the last stage are out of the buffer's range and
-// cost nothing.
+// Here a workgroup's waves take 32 rows each (16 gate and 16 up rows with
+// SwiGLU), in one group or in two that take the stages in turn, and share 16
+// NC columns of x, brought into LDS once per workgroup as the parts' bf16 /
+// fp16 values, double buffered.  Each wave keeps kDepth stages of its weights
+// in flight in registers; loads past the last stage are out of the buffer's
+// range and cost nothing, and what they return, zeros, adds nothing.
+//
+// Shapes (waves of a group x groups), by measurement: experts 4 x 1, as many
+// small workgroups that overlap each other's prologue (entries listed, x
+// brought in) with streaming -- two groups ran the layer of 256 tokens in 141
+// us, two waves a group in 131, against 108; one matrix 2 x 2, 64 rows a
+// workgroup (n 16384, k 4096, 16 rows: 14.4 us, 17.3 with 128 rows), and 4 x 2
+// where 64 columns of x make 128 rows worth a workgroup (55 against 66 us).
+// More stages in flight cost occupancy (four: 127 against 109 us).
+//
+// What bounds it: with 1-2 columns of 16, the weights' stream (FC1 of 256
+// tokens 52 us, 226 MB at 4.4 TB/s; FC2 48 us, where D and the rows add a third
+// to 113 MB).  With 64 columns the compute side shows: a copy without any
+// global traffic took 40 of the 56-65 us (decode, products and LDS reads at two
+// waves a SIMD), and row-major weights add the block scales' scattered 2-byte
+// loads (54 us without them); the tiled layout is the faster one.
 //
 // The last stage of a k that is no multiple of 128 (row-major weights):
 // lanes take the window [min(k0, k - 32), + 32) instead of [k0, + 32), and x
@@ -490,8 +508,8 @@ struct XPiece {
   u32x4_t w[XT == 0 || XT == kPair ? 2 : 1];
 };
 
-// Where piece 4q + s of a column's stage lies, before the exclusive or with
-// the column.  A 16-byte LDS read serves lanes 0-3, 12-15, 20-23 and 24-27 of
+// A column's stage is 16 pieces of 8 elements, piece 4q + s in slot
+// slot_of(q, s) ^ (column % 16).  A 16-byte LDS read serves lanes 0-3, 12-15, 20-23 and 24-27 of
 // each half wave together; with the quarters in this order those lanes, eight
 // columns of quarter q and the eight others of q + 1, meet different banks
 // (in the plain order they met in pairs, 4 extra cycles a read).
@@ -626,7 +644,7 @@ __global__ __launch_bounds__(ROW_WAVES* GROUPS* kWave) void matvec_rows_kernel(M
       const int kw = (k0 < k - 32 ? k0 : k - 32) + 8 * (piece % 4);
       xo_last[i] = kw >= k0 && kw < k ? at + kw * xsize : kNone;
     }
-    // pieces of the next buffers (see kSets)
+    // pieces on their way to the next kSets buffers
     XPiece<XT> xr[kSets][kOwn];
     auto load_xs = [&](int set, int st0) {
 #pragma unroll
@@ -671,7 +689,7 @@ __global__ __launch_bounds__(ROW_WAVES* GROUPS* kWave) void matvec_rows_kernel(M
       for (int d = 0; d < kDepth; ++d) {
         const int turn = t0 + d, buf = d % 2;
         load_xs(d % kSets, (turn + kSets) * kGroups);
-        {   // (past the last stage both operands are zero)
+        {
           const char* xb0 = lds + buf * kBuffer + group * kParts * kPlane;
           f32x2_t s2[kWide];
 #pragma unroll

@@ -18,13 +18,17 @@
 //   sigmoid:               dl_j = dw_j s_j (1 - s_j)
 // All statistics are binary32.
 //
-// Bound: the logits are read once (and the gradient written once); at E = 128
-// the picking itself is the larger part.  A token's row lies in the registers
-// of L lanes, V consecutive experts each, so a pick is a local maximum, a
-// lane reduction by DPP rotations and the same for the lowest index among
-// equals: no shared memory and no barrier.
-#include "launch.h"
+// Bound: the logits are read once (and the gradient written once), but at
+// E = 128 the picking is the larger part: 636 vector instructions a wave of
+// four tokens, of which the eight picks take 490 -- 8.5 of the 11.5 us of 32768
+// tokens (fp32), whose 19 MB would pass in 4.  A token's row lies in the
+// registers of L lanes, V consecutive experts each, so a pick is a local
+// maximum of integer keys, four DPP rotations and the same for the lowest
+// index among equals: no shared memory and no barrier.  16 lanes with 8
+// experts each up to 128 experts (four tokens a wave); 64 lanes above.
+// The gradient of 8191 x 1000 bf16 logits takes 14 us (33 MB: 7 us).
 #include "elem.h"
+#include "launch.h"
 
 #include <math.h>
 
