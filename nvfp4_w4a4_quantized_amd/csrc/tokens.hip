@@ -95,9 +95,29 @@ __device__ __forceinline__ void dot_span(float& dot, const Piece<DT>& x, const P
 
 // Row of entry (t, j), -1 if it has none.
 __device__ __forceinline__ int64_t entry_row(const TokenRowsArgs& a, int64_t t, int j) {
-  const int64_t i = t * a.topk + j;
-  const int64_t r = a.dst_row[i];
+  const int32_t r = a.dst_row[t * a.topk + j];
   return r >= 0 && r < a.rows_cap ? r : -1;
+}
+
+// Rows (-1 for none) and weights of entries [j0, j0 + kBatch) of token t, those
+// past the last included: all loads are issued before the first is looked at.
+// The collect takes its entries so, once per token instead of once per column
+// step: 9.8 against 11.1 us at 1003 tokens of 1111, 8.05 against 8.55 at 256 of
+// 2048. The spread does not (444 against 436 us at 32768 tokens of 4096): its
+// time is traffic, and it looks at a token's entries only once anyway.
+template <bool WEIGHTED>
+__device__ __forceinline__ void load_entries(const TokenRowsArgs& a, int64_t t, int j0,
+                                             int64_t (&row)[kBatch], float (&w)[kBatch]) {
+  int32_t r[kBatch];
+#pragma unroll
+  for (int j = 0; j < kBatch; ++j) {
+    const int64_t i = t * a.topk + (j0 + j < a.topk ? j0 + j : a.topk - 1);
+    r[j] = a.dst_row[i];
+    w[j] = WEIGHTED ? a.prob[i] : 1.0f;
+  }
+#pragma unroll
+  for (int j = 0; j < kBatch; ++j)
+    row[j] = j0 + j < a.topk && r[j] >= 0 && r[j] < a.rows_cap ? r[j] : -1;
 }
 
 }  // namespace
@@ -188,7 +208,9 @@ __global__ __launch_bounds__(256) void collect_kernel(TokenRowsArgs a) {
     // the dot products need the entries outermost, so the column's sum is
     // then taken over the batches in an inner loop of its own.
     for (int j0 = 0; j0 < (DOT ? a.topk : 1); j0 += kBatch) {
-      float dot[kBatch];
+      int64_t row0[kBatch];
+      float w0[kBatch], dot[kBatch];
+      load_entries<WEIGHTED>(a, t, j0, row0, w0);
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) dot[j] = 0.0f;
       for (int64_t c = (int64_t)threadIdx.x * P::kN; c < a.hidden; c += (int64_t)blockDim.x * P::kN) {
@@ -204,9 +226,18 @@ __global__ __launch_bounds__(256) void collect_kernel(TokenRowsArgs a) {
         for (int b = j0; b < last; b += kBatch) {
           P p[kBatch];
           int64_t row[kBatch];
+          float w[kBatch];
+          if (b == j0) {
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+              row[j] = row0[j];
+              w[j] = w0[j];
+            }
+          } else {
+            load_entries<WEIGHTED>(a, t, b, row, w);
+          }
 #pragma unroll
           for (int j = 0; j < kBatch; ++j) {
-            row[j] = b + j < last ? entry_row(a, t, b + j) : -1;
             if (row[j] < 0) continue;
             load_span<DT>(p[j], static_cast<const T*>(a.rows) + row[j] * a.ld_rows, span, true);
           }
@@ -214,10 +245,9 @@ __global__ __launch_bounds__(256) void collect_kernel(TokenRowsArgs a) {
           for (int j = 0; j < kBatch; ++j) {
             if (row[j] < 0) continue;
             if (j0 == 0) {
-              const float w = WEIGHTED ? a.prob[t * a.topk + b + j] : 1.0f;
 #pragma unroll
               for (int i = 0; i < P::kN; ++i)
-                sum[i] += WEIGHTED ? w * p[j].get(i) : p[j].get(i);
+                sum[i] += WEIGHTED ? w[j] * p[j].get(i) : p[j].get(i);
             }
             if (DOT && b == j0) dot_span<DT>(dot[j], x, p[j], span);
           }
@@ -235,7 +265,7 @@ __global__ __launch_bounds__(256) void collect_kernel(TokenRowsArgs a) {
 #pragma unroll
         for (int j = 0; j < kBatch; ++j)
           if ((int)threadIdx.x == j && j < n)
-            a.dprob[t * a.topk + j0 + j] = entry_row(a, t, j0 + j) >= 0 ? dot[j] : 0.0f;
+            a.dprob[t * a.topk + j0 + j] = row0[j] >= 0 ? dot[j] : 0.0f;
       }
     }
   }
