@@ -560,7 +560,7 @@ def _call(dev, what, *args):
     launch goes to the current device; switching, and a Stream object for the
     handle, cost as much as a small call, so neither is done without need.)"""
     stream = torch._C._cuda_getCurrentRawStream(dev)
-    if dev == torch.cuda.current_device():
+    if dev == torch._C._cuda_getDevice():
         status = getattr(lib(), what)(*args, stream)
     else:
         with torch.cuda.device(dev):
