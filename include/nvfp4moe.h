@@ -595,7 +595,10 @@ int moe_unsort_tokens_backward(const void* dy, int dtype, int64_t tokens, int64_
  * Weights are exact in the matrix cores' operands and x is used as it is
  * (binary32 x as the exact sum of three bf16 parts), sums are binary32:
  * |out - exact| <= (k + 16) * 2^-24 * sum_k |w x| before the output's
- * rounding.  Every result is bitwise reproducible.
+ * rounding, while sum_k (q s_b) x stays in binary32's range and no x (of
+ * binary32: no part, 2^-16 of x) is below 2^-126, where it may count as zero.
+ * Infinite x gives the formula's infinities and NaN, NaN gives NaN.  Every
+ * result is bitwise reproducible.
  *   x          [tokens, ld_x] (x_by_entry: [tokens * topk, ld_x]), dtype code
  *   w          NVFP4 weights [n, k] / [num_experts, n, k]; layout 0, or 1
  *              (nvfp4_pack_weights) where n % 32 == 0 and k % 128 == 0

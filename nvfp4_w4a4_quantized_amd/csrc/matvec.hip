@@ -66,12 +66,16 @@ template <int XT>
 __device__ __forceinline__ uint4 x_operand(const XStage<XT>& x, int s, int part) {
   if (XT == kPair) return x.w[(part * 4 + s) % (sizeof(x.w) / 16)];
   if (XT != 0) return x.w[s];
-  // upper halves of the value, of what is left of it, and of the rest
+  // Upper halves of the value (a quiet NaN stays one), of what is left of it, and
+  // of the rest.  The lower parts are the largest finite value's for an
+  // infinity, whose difference would be NaN: they add to it with its sign.
   const uint4 a = x.w[(2 * s) % (sizeof(x.w) / 16)], b = x.w[(2 * s + 1) % (sizeof(x.w) / 16)];
   uint32_t f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   uint32_t o[4];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
+    if (part > 0)
+      f[i] = __float_as_uint(__builtin_amdgcn_fmed3f(__uint_as_float(f[i]), -__FLT_MAX__, __FLT_MAX__));
     for (int p = 0; p < part; ++p)
       f[i] = __float_as_uint(__uint_as_float(f[i]) - __uint_as_float(f[i] & 0xFFFF0000u));
   }

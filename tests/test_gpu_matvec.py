@@ -207,6 +207,85 @@ def test_infinite_activations_stay_in_their_row():
     assert not bool(torch.isfinite(y[2]).any()) and bool(torch.isnan(y[4]).all())
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,n,k", [(3, 40, 272), (64, 6160, 272)])
+def test_infinite_activations_give_the_formula(T, n, k, dtype):
+    """An infinite x gives the infinities (and, against a zero weight or an
+    infinity of the other sign, the NaN) of its formula, in both kernels."""
+    from nvfp4_w4a4_quantized_amd import ops
+    rng = np.random.default_rng(14)
+    codes, scales, gs = R.make_weights(rng, 1, n, k)
+    w = held(codes, scales, gs, False)
+    x = torch.from_numpy(rng.standard_normal((T, k)).astype(np.float32)).to(dtype)
+    x[0, k - 1] = float("inf")
+    x[1, 7] = float("-inf")
+    x[2, [3, 200]] = float("inf")
+    m = R.decode(codes, scales, gs)[0]
+    terms = x[:3].double().unsqueeze(1) * m.unsqueeze(0)
+    y = ops.nvfp4_matvec(x.cuda(), w).cpu()[:3].double()
+    ref = terms.sum(2)
+    assert bool(torch.isinf(ref).any()) and bool(torch.isnan(ref).any())
+    assert torch.equal(torch.nan_to_num(y, nan=7.0), torch.nan_to_num(ref, nan=7.0))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T", [2, 64])
+def test_decode_of_an_infinite_intermediate(T, dtype):
+    """One element of D overflows: y is infinite with its sign, NaN against a
+    zero weight, and the other tokens are as they were."""
+    from nvfp4_w4a4_quantized_amd import ops
+    E, H, I, c = 8, 2048, 384, 77
+    rng = np.random.default_rng(15)
+    w1, w2 = R.make_weights(rng, E, 2 * I, H, std=0.1), R.make_weights(rng, E, H, I, std=0.1)
+    ids = torch.full((T, 2), 3, dtype=torch.int32)
+    ids[0] = torch.tensor([5, 6])
+    keep = w1[0][5, [c, I + c]].clone()
+    w1[0][5] = 0                                # expert 5: D is zero but at c
+    w1[0][5, [c, I + c]] = keep
+    prob = torch.full((T, 2), 0.5)
+    x = torch.from_numpy(rng.standard_normal((T, H)).astype(np.float32) * 4).to(dtype)
+    h, _ = R.expert_products(x[:1], ids[:1, :1], R.decode(*w1))
+    if h[0, 0, c] < 0:                          # a positive gate, so silu(g) is g
+        x[0] = -x[0]
+        h = -h
+    d = float(h[0, 0, c] * h[0, 0, I + c])
+    assert h[0, 0, c] > 20 and abs(d) > 2
+    a, b = held(*w1, True), held(*w2, True)
+    clean = ops.moe_expert_decode(x.cuda(), ids.cuda(), prob.cuda(), E, I, a, b).cpu()
+    prob[0, 0] = 3e38
+    y = ops.moe_expert_decode(x.cuda(), ids.cuda(), prob.cuda(), E, I, a, b).cpu()
+    col = R.decode(*w2)[5][:, c]
+    want = torch.where(col == 0, float("nan"), np.sign(d) * col.sign() * np.inf)
+    assert bool(torch.isnan(want).any()) and bool(torch.isinf(want).any())
+    assert torch.equal(torch.nan_to_num(y[0].double(), nan=7.0), torch.nan_to_num(want, nan=7.0))
+    assert torch.equal(y[1:], clean[1:])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,n,k", [(5, 70, 208), (16, 10247, 400), (64, 6145, 144)])
+def test_any_alignment(T, n, k, dtype):
+    """x at an odd element, its rows an odd distance apart, row-major weights
+    and the output at odd addresses: the aligned call's bits, in both kernels."""
+    from nvfp4_w4a4_quantized_amd import ops
+    from nvfp4_w4a4_quantized_amd.ops import NvFp4Weights
+    rng = np.random.default_rng(16)
+    codes, scales, gs = R.make_weights(rng, 1, n, k)
+
+    def shifted(t, by):
+        t = t.cuda()
+        flat = torch.zeros(t.numel() + 16, dtype=t.dtype, device="cuda")
+        flat[by:by + t.numel()] = t.reshape(-1)
+        return flat[by:by + t.numel()].view(t.shape)
+    x = torch.from_numpy(rng.standard_normal((T, k)).astype(np.float32)).to(dtype).cuda()
+    wide = torch.full((T, k + 21), float("nan"), dtype=dtype, device="cuda")
+    wide[:, 5:5 + k] = x
+    want = ops.nvfp4_matvec(x, held(codes, scales, gs, False))
+    odd = NvFp4Weights(shifted(codes, 3), shifted(scales, 1), shifted(gs, 1))
+    out = shifted(torch.zeros((T, n), dtype=dtype), 1)
+    say("alignment", T, n, k, dtype)
+    assert torch.equal(ops.nvfp4_matvec(wide[:, 5:5 + k], odd, out=out), want)
+
+
 def test_no_tokens():
     from nvfp4_w4a4_quantized_amd import ops
     rng = np.random.default_rng(11)
