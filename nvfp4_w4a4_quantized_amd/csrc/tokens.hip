@@ -103,7 +103,7 @@ __device__ __forceinline__ int64_t entry_row(const TokenRowsArgs& a, int64_t t, 
 // past the last included: all loads are issued before the first is looked at.
 // The collect takes its entries so, once per token instead of once per column
 // step: 9.8 against 11.1 us at 1003 tokens of 1111, 8.05 against 8.55 at 256 of
-// 2048. The spread does not (444 against 436 us at 32768 tokens of 4096): its
+// 2048. The spread does not (444 against 436 us at 32768 tokens of 2048): its
 // time is traffic, and it looks at a token's entries only once anyway.
 template <bool WEIGHTED>
 __device__ __forceinline__ void load_entries(const TokenRowsArgs& a, int64_t t, int j0,
