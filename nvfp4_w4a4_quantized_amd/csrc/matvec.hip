@@ -160,9 +160,11 @@ __device__ __forceinline__ uint4 load_u128(const uint8_t* p) {
 }
 
 // The entries whose expert is e (e == num_groups: of no expert) into `list`,
-// their number into *found.  `ids` holds topk_idx[threadIdx.x + i *
-// blockDim.x], loaded by the caller ahead of other work; more entries are
-// read in rounds of as many loads.
+// returning their number.  The order is the same in every workgroup that lists
+// e (several may share its columns): by wave, each wave's in ascending order.
+// `ids` holds topk_idx[threadIdx.x + i * blockDim.x], loaded by the caller
+// ahead of other work; more entries are read in rounds of as many loads.
+// `counts` is a word of LDS per wave.
 constexpr int kIds = 8;
 __device__ __forceinline__ void load_ids(const MatvecArgs& a, int at, int entries, int (&ids)[kIds]) {
 #pragma unroll
@@ -173,22 +175,47 @@ __device__ __forceinline__ void load_ids(const MatvecArgs& a, int at, int entrie
       ids[i] = a.topk_idx[j < entries ? j : 0];
   }
 }
-__device__ __forceinline__ void collect_entries(const MatvecArgs& a, int e, int (&ids)[kIds],
-                                                int entries, uint16_t* list, int* found) {
-  if (threadIdx.x == 0) *found = 0;
-  __syncthreads();
-  for (int at = threadIdx.x; at - (int)threadIdx.x < entries; at += kIds * blockDim.x) {
-    if (at >= kIds * (int)blockDim.x) load_ids(a, at, entries, ids);
+template <int WAVES>
+__device__ __forceinline__ int collect_entries(const MatvecArgs& a, int e, int (&ids)[kIds],
+                                               int entries, uint16_t* list, int* counts) {
+  constexpr int kThreads = WAVES * kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  int m = 0;
+  for (int base = 0; base < entries; base += kIds * kThreads) {
+    if (base != 0) load_ids(a, base + threadIdx.x, entries, ids);
+    uint64_t mask[kIds];
+    int n = 0;
 #pragma unroll
     for (int i = 0; i < kIds; ++i) {
-      const int j = at + i * (int)blockDim.x;
-      if (j - (int)threadIdx.x >= entries) break;   // (the whole workgroup's)
+      const int first = base + i * kThreads;
+      mask[i] = 0;
+      if (first >= entries) continue;   // (the whole workgroup's)
       const int of = ids[i] >= 0 && ids[i] < a.num_groups ? ids[i] : a.num_groups;
-      // (a column's place does not change its result, so any order will do)
-      if (j < entries && of == e) list[atomicAdd(found, 1)] = (uint16_t)j;
+      mask[i] = __ballot(first + (int)threadIdx.x < entries && of == e);
+      n += __popcll(mask[i]);
     }
+    if (threadIdx.x % kWave == 0) counts[wave] = n;
+    __syncthreads();
+    int c[WAVES], at = m;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) c[w] = counts[w];
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+      at += w < wave ? c[w] : 0;
+      m += c[w];
+    }
+#pragma unroll
+    for (int i = 0; i < kIds; ++i) {
+      if (mask[i] == 0) continue;
+      const int before = __builtin_amdgcn_mbcnt_hi(
+          (uint32_t)(mask[i] >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask[i], 0));
+      if ((mask[i] >> (threadIdx.x % kWave)) & 1)
+        list[at + before] = (uint16_t)(base + i * kThreads + threadIdx.x);
+      at += __popcll(mask[i]);
+    }
+    __syncthreads();
   }
-  __syncthreads();
+  return m;
 }
 
 // Stores the values of rows [row, row + 4) of one column (those below n): one
@@ -471,7 +498,10 @@ __global__ __launch_bounds__(1024) void decode_down_kernel(MatvecArgs a, int par
 // Shapes (waves of a group x groups), by measurement: experts 4 x 1, as many
 // small workgroups that overlap each other's prologue (entries listed, x
 // brought in) with streaming -- two groups ran the layer of 256 tokens in 141
-// us, two waves a group in 131, against 108; one matrix 2 x 2, 64 rows a
+// us, two waves a group in 131, against 108 -- and 2 x 2 where that makes no more
+// than two workgroups a CU, so that latency counts (k 4096, 8 columns: 8 experts
+// of 2048 rows 15.5 against 22 us, 16 of 512 14.6 against 21.8; 32 of 2048, 1024
+// workgroups, 37 against 35); one matrix 2 x 2, 64 rows a
 // workgroup (n 16384, k 4096, 16 rows: 14.4 us, 17.3 with 128 rows), and 4 x 2
 // where 64 columns of x make 128 rows worth a workgroup (55 against 66 us).
 // More stages in flight cost occupancy (four: 127 against 109 us).
@@ -550,8 +580,8 @@ __global__ __launch_bounds__(ROW_WAVES* GROUPS* kWave) void matvec_rows_kernel(M
   // at an address that is no multiple of 16 the buffers' 16-byte accesses run
   // at half their rate (the layer of 256 tokens took 240 us instead of 110).
   extern __shared__ __align__(16) char lds[];
-  int* found = reinterpret_cast<int*>(lds + 2 * kBuffer);
-  uint16_t* list = reinterpret_cast<uint16_t*>(found + 1);
+  int* counts = reinterpret_cast<int*>(lds + 2 * kBuffer);
+  uint16_t* list = reinterpret_cast<uint16_t*>(counts + kThreads / kWave);
   const int lane = threadIdx.x % kWave, wid = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int wave = wid % kRowWaves, group = kGroups == 1 ? 0 : wid / kRowWaves;
   const int r = lane % kTile, q = lane / kTile;
@@ -563,7 +593,8 @@ __global__ __launch_bounds__(ROW_WAVES* GROUPS* kWave) void matvec_rows_kernel(M
   const int entries = EXPERT ? (int)a.tokens * a.topk : 0;
   if (EXPERT) {
     e = blockIdx.y;
-    if (e == a.num_groups && (SWIGLU || a.skip_unrouted)) return;
+    first = blockIdx.z * kCols;
+    if (e == a.num_groups && (SWIGLU || a.skip_unrouted || first != 0)) return;
     load_ids(a, threadIdx.x, entries, ids);
   } else {
     first = blockIdx.y * kCols;
@@ -611,9 +642,8 @@ __global__ __launch_bounds__(ROW_WAVES* GROUPS* kWave) void matvec_rows_kernel(M
 #pragma unroll
   for (int d = 0; d < kDepth; ++d) w[d] = load_w(d);
   if (EXPERT) {
-    collect_entries(a, e, ids, entries, list, found);
-    m = *found;
-    if (m == 0) return;
+    m = collect_entries<kThreads / kWave>(a, e, ids, entries, list, counts);
+    if (first >= m) return;
     if (e == a.num_groups) {   // entries of no expert
       store_zeros(a, list, m, row0 - wave * kWide * kTile, kRowWaves * kWide * kTile);
       return;
@@ -631,7 +661,7 @@ __global__ __launch_bounds__(ROW_WAVES* GROUPS* kWave) void matvec_rows_kernel(M
   const int pi = slot ^ (own % 16), pm = pi / 4;
   const int piece = 4 * ((((pm ^ (pm >> 1)) & 1) << 1) | (pm >> 1)) + pi % 4;   // slot_of's inverse
   const int turns = (stages + kGroups - 1) / kGroups;
-  for (int c0 = first; c0 < m; c0 += kCols) {
+  for (int c0 = first; c0 < m; c0 += kCols * (EXPERT ? (int)gridDim.z : 1)) {
     uint32_t xo[kOwn], xo_last[kOwn];
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) {
@@ -771,6 +801,12 @@ __global__ __launch_bounds__(ROW_WAVES* GROUPS* kWave) void matvec_rows_kernel(M
 
 namespace {
 
+// Experts that can have entries.
+int64_t experts_met(const MatvecArgs& a) {
+  const int64_t entries = a.tokens * a.topk;
+  return entries < a.num_groups ? entries : a.num_groups;
+}
+
 // Whether the kernel with x in LDS is the faster one.  It reads the weights at
 // a higher rate and does not pay for more columns, but needs many workgroups.
 // Measured (GPU time, bf16, tiled; direct kernel / LDS kernel), one matrix:
@@ -778,20 +814,34 @@ namespace {
 //   8.4 / 9.4, 32 rows 12.7 / 11.5; n 12288, 8 rows 8.6 / 9.5, 16 rows 10.7 /
 //   9.5; n 24576, 1 row 10.0 / 12.1, 8 rows 12.9 / 12.2;
 //   k 8192: n 32768, 1 row 46.3 / 36.9.
-// Experts (the layer's two products and the sum; top-8 of 128, hidden 2048,
-// intermediate 768): 4 tokens 36.9 / 48.6 us, 8 tokens 64.2 / 59.0, 64 tokens
-// 195 / 82; top-4 of 16, hidden 1024, intermediate 512: 32 tokens 17.1 / 19.9,
-// 128 tokens 42.1 / 36.4; top-2 of 8, 2048 and 768: 64 tokens 29.6 / 29.4.
-bool rows_kernel_pays(const MatvecArgs& a, bool expert, bool swiglu) {
+// Experts, by 128-row blocks of the experts met and columns each (tiled bf16;
+// direct / LDS kernel): k 1024: 32 blocks, 16 columns 7.3 / 8.9 us; 128 blocks,
+// 4 columns 6.8 / 7.3, 8 columns 7.6 / 7.6, 16 columns 11.1 / 9.4; 256 blocks, 1
+// column 8.3 / 9.5, 2 columns 9.3-10.2 / 9.6, 8 columns 12.3 / 9.7; 512 blocks, 1
+// column 12.7 / 11.9, 16 columns 39.9 / 14.9; k 4096: 64 blocks, 8 columns 11.7 /
+// 14.6; 128 blocks, 2 columns 14.0 / 15.4, 16 columns 29.3 / 19.2; 256 blocks, 1
+// column 18.2 / 18.9, 2 columns 22.5 / 19.3; 1024 blocks, 1 column 71 / 51.
+bool rows_kernel_pays(const MatvecArgs& a, bool expert) {
   if (!expert) {
     const int64_t t = a.tokens;
     return a.n >= (t <= 2 ? 32768 : (t <= 8 ? 24576 : (t <= 16 ? 10240 : (t <= 32 ? 8192 : 6144))));
   }
-  // 128-row blocks of the experts met, and the columns each meets on average
-  const int64_t entries = a.tokens * a.topk;
-  const int64_t hit = entries < a.num_groups ? entries : a.num_groups;
-  const int64_t blocks = hit * (((swiglu ? 2 * a.inter : a.n) + 127) / 128);
-  return blocks * (4 + entries / hit) >= 2688;
+  const int64_t entries = a.tokens * a.topk, blocks = (a.n + 127) / 128;
+  // (No more entries than experts: the direct kernel has a slot per entry, the
+  // LDS kernel one per expert, most of them empty.  The layer's FC1 and FC2,
+  // top-8 of 128, 2048 and 768: 4 tokens, 384 and 512 blocks, 33.5 / 42.7 us; 6
+  // tokens 52.3 / 54.2; 8 tokens 64.2 / 58.6.)
+  return entries <= a.num_groups ? blocks * entries >= 512
+                                 : blocks * (a.num_groups + entries) >= 768;
+}
+
+// Workgroups that share an expert's columns: what its mean number of entries
+// fills, and one (an expert with more has its workgroups take several turns).
+// Against one workgroup for all columns: 128 tokens, top-4 of 16, hidden 1024,
+// intermediate 512: 25 against 35 us; 256 tokens, top-2 of 8, 2048 and 768: 38
+// against 65.
+int64_t column_blocks(const MatvecArgs& a, int64_t cols) {
+  return 1 + a.tokens * a.topk / (a.num_groups * cols);
 }
 
 int matvec_waves(int64_t k) {
@@ -803,12 +853,16 @@ int matvec_waves(int64_t k) {
 }  // namespace
 
 template <int XT, int NC, int ROW_WAVES, int GROUPS, bool SWIGLU, bool EXPERT>
-static void launch_rows(const MatvecArgs& a, size_t list, hipStream_t s) {
+static void launch_rows(const MatvecArgs& a, hipStream_t s) {
   typedef RowsShape<XT, NC, ROW_WAVES, GROUPS> Shape;
+  // behind the buffers: a word per wave and the list of an expert's entries
+  const size_t list = EXPERT ? Shape::kThreads / kWave * 4 + (size_t)(a.tokens * a.topk) * 2 : 0;
   const int64_t per = ROW_WAVES * kTile * (SWIGLU ? 1 : kWide);
   const int64_t rows = SWIGLU ? a.inter : a.n, cols = NC * kTile;
+  // the columns of an expert with more than `cols` go to several workgroups
   const dim3 grid((unsigned)((rows + per - 1) / per),
-                  (unsigned)(EXPERT ? a.num_groups + 1 : (a.tokens + cols - 1) / cols));
+                  (unsigned)(EXPERT ? a.num_groups + 1 : (a.tokens + cols - 1) / cols),
+                  (unsigned)(EXPERT ? column_blocks(a, cols) : 1));
   matvec_rows_kernel<XT, NC, ROW_WAVES, GROUPS, SWIGLU, EXPERT>
       <<<grid, Shape::kThreads, 2 * Shape::kBuffer + list, s>>>(a);
 }
@@ -818,19 +872,23 @@ static void launch_matvec_one(const MatvecArgs& a, hipStream_t s) {
   const int64_t entries = a.tokens * a.topk;
   const int64_t xrows = EXPERT && a.x_by_entry ? entries : a.tokens;
   const int64_t xbytes = ((xrows - 1) * a.ld_x + a.k) * (XT == 0 ? 4 : 2);
-  if (a.k >= 32 && xbytes < kNone && rows_kernel_pays(a, EXPERT, SWIGLU)) {
+  if (a.k >= 32 && xbytes < kNone && rows_kernel_pays(a, EXPERT)) {
     if constexpr (EXPERT) {
       // the entries of an expert scatter about their mean: room for twice as many
-      const size_t list = 4 + (size_t)entries * 2;   // their number and the entries
-      if (2 * entries <= 16 * a.num_groups) launch_rows<XT, 1, 4, 1, SWIGLU, true>(a, list, s);
-      else launch_rows<XT, 2, 4, 1, SWIGLU, true>(a, list, s);
+      const bool one = 2 * entries <= 16 * a.num_groups;
+      // 64-row workgroups whose groups share k while those are at most two a CU
+      const bool few = experts_met(a) * ((a.n + 63) / 64) * column_blocks(a, one ? 16 : 32) <= 512;
+      if (one && few) launch_rows<XT, 1, 2, 2, SWIGLU, true>(a, s);
+      else if (one) launch_rows<XT, 1, 4, 1, SWIGLU, true>(a, s);
+      else if (few) launch_rows<XT, 2, 2, 2, SWIGLU, true>(a, s);
+      else launch_rows<XT, 2, 4, 1, SWIGLU, true>(a, s);
     } else {
-      if (a.tokens <= 16) launch_rows<XT, 1, 2, 2, false, false>(a, 0, s);
-      else if (XT == 0 || a.tokens <= 32) launch_rows<XT, 2, 2, 2, false, false>(a, 0, s);
+      if (a.tokens <= 16) launch_rows<XT, 1, 2, 2, false, false>(a, s);
+      else if (XT == 0 || a.tokens <= 32) launch_rows<XT, 2, 2, 2, false, false>(a, s);
       // x is read once per workgroup: with 64 columns 128 rows each while that
       // leaves a workgroup for every CU
-      else if (a.n >= 128 * 256) launch_rows<XT, XT == 0 ? 2 : 4, 4, 2, false, false>(a, 0, s);
-      else launch_rows<XT, XT == 0 ? 2 : 4, 2, 2, false, false>(a, 0, s);
+      else if (a.n >= 128 * 256) launch_rows<XT, XT == 0 ? 2 : 4, 4, 2, false, false>(a, s);
+      else launch_rows<XT, XT == 0 ? 2 : 4, 2, 2, false, false>(a, s);
     }
     return;
   }

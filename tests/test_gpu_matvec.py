@@ -122,7 +122,11 @@ def make_ids(rng, T, k, E, kind):
     (512, 8, 8, 32, 128, True, "plain"), (4096, 1, 3, 17, 32, False, "plain"),
     (2, 2, 1024, 16, 48, False, "plain"),
     (64, 2, 64, 1500, 208, False, "dropped"), (300, 4, 12, 1101, 336, False, "dropped"),
-    (100, 1, 1, 400, 144, False, "one"), (60, 6, 50, 1024, 512, True, "plain")])
+    (100, 1, 1, 400, 144, False, "one"), (60, 6, 50, 1024, 512, True, "plain"),
+    # workgroups that share an expert's columns, one expert with many more than
+    # the others; two groups of waves with 16 and 32 columns
+    (300, 4, 12, 500, 272, False, "one"), (1000, 4, 12, 1100, 80, False, "one"),
+    (60, 6, 50, 600, 528, False, "dropped"), (128, 4, 16, 512, 384, True, "plain")])
 def test_expert_matvec(T, k, E, n, K, tiled, kind, dtype):
     from nvfp4_w4a4_quantized_amd import ops
     rng = np.random.default_rng(T + n + K)
@@ -167,7 +171,9 @@ DECODE = [(1, 1, 1, 16, 16, False, "plain"), (1, 8, 128, 256, 128, True, "plain"
           (37, 4, 20, 272, 112, False, "dropped"), (40, 1, 7, 128, 128, True, "one"),
           (128, 8, 16, 256, 256, True, "plain"), (512, 8, 12, 64, 48, False, "plain"),
           (3, 20, 24, 48, 80, False, "dropped"), (4, 16, 16, 128, 1040, False, "plain"),
-          (200, 4, 40, 336, 208, False, "dropped"), (100, 2, 60, 512, 384, True, "plain")]
+          (200, 4, 40, 336, 208, False, "dropped"), (100, 2, 60, 512, 384, True, "plain"),
+          (200, 4, 40, 336, 512, False, "dropped"), (100, 2, 60, 512, 256, True, "plain"),
+          (300, 3, 12, 256, 144, False, "one")]
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
