@@ -501,9 +501,12 @@ __global__ __launch_bounds__(1024) void decode_down_kernel(MatvecArgs a, int par
 // us, two waves a group in 131, against 108 -- and 2 x 2 where that makes no more
 // than two workgroups a CU, so that latency counts (k 4096, 8 columns: 8 experts
 // of 2048 rows 15.5 against 22 us, 16 of 512 14.6 against 21.8; 32 of 2048, 1024
-// workgroups, 37 against 35); one matrix 2 x 2, 64 rows a
-// workgroup (n 16384, k 4096, 16 rows: 14.4 us, 17.3 with 128 rows), and 4 x 2
-// where 64 columns of x make 128 rows worth a workgroup (55 against 66 us).
+// workgroups, 37 against 35).  One matrix: 64 rows a workgroup (n 16384, k 4096,
+// 16 rows: 14.4 us, 17.3 with 128 rows) and as many columns as leave a workgroup
+// for every CU (k 8192, 64 rows: n 4096, 16 columns 18 us, 32 22.6, 64 32; n 8192
+// 27, 24, 33); four groups while there is no second workgroup for a CU, else two
+// (k 8192, 16 rows: n 8192 17.5 / 22.7 us; n 24576, k 4096, 64 rows 39 / 33); and
+// 4 x 2 where 64 columns of x make 128 rows worth a workgroup (55 against 66 us).
 // More stages in flight cost occupancy (four: 127 against 109 us).
 //
 // What bounds it: with 1-2 columns of 16, the weights' stream (FC1 of 256
@@ -767,23 +770,28 @@ __global__ __launch_bounds__(ROW_WAVES* GROUPS* kWave) void matvec_rows_kernel(M
         __syncthreads();
       }
     }
-    // the second group's sums join the first's (the buffers are free now)
+    // the other groups' sums join the first's (the buffers are free now)
     f32x4_t* red = reinterpret_cast<f32x4_t*>(lds);
-    if (kGroups == 2 && group == 1) {
+    constexpr int kSums = kRowWaves * kWide * NC * kWave;
+    static_assert((kGroups - 1) * kSums * 16 <= 2 * kBuffer, "the sums fit the buffers");
+    if (kGroups > 1) {
+      if (group > 0) {
 #pragma unroll
-      for (int rt = 0; rt < kWide; ++rt)
+        for (int rt = 0; rt < kWide; ++rt)
 #pragma unroll
-        for (int b = 0; b < NC; ++b) red[((wave * kWide + rt) * NC + b) * kWave + lane] = acc[rt][b];
-    }
-    if (kGroups == 2) {
+          for (int b = 0; b < NC; ++b)
+            red[(group - 1) * kSums + ((wave * kWide + rt) * NC + b) * kWave + lane] = acc[rt][b];
+      }
       __syncthreads();
-      if (group == 1) continue;
+      if (group > 0) continue;
     }
 #pragma unroll
     for (int b = 0; b < NC; ++b) {
 #pragma unroll
       for (int rt = 0; rt < kWide; ++rt) {
-        if (kGroups == 2) acc[rt][b] += red[((wave * kWide + rt) * NC + b) * kWave + lane];
+#pragma unroll
+        for (int g = 1; g < kGroups; ++g)
+          acc[rt][b] += red[(g - 1) * kSums + ((wave * kWide + rt) * NC + b) * kWave + lane];
         acc[rt][b] *= sg;
       }
       const int ci = c0 + b * 16 + r;
@@ -810,10 +818,13 @@ int64_t experts_met(const MatvecArgs& a) {
 // Whether the kernel with x in LDS is the faster one.  It reads the weights at
 // a higher rate and does not pay for more columns, but needs many workgroups.
 // Measured (GPU time, bf16, tiled; direct kernel / LDS kernel), one matrix:
-//   k 2048: n 6144, 16 rows 7.9 / 9.0 us, 64 rows 16.9 / 16.2; n 8192, 16 rows
-//   8.4 / 9.4, 32 rows 12.7 / 11.5; n 12288, 8 rows 8.6 / 9.5, 16 rows 10.7 /
-//   9.5; n 24576, 1 row 10.0 / 12.1, 8 rows 12.9 / 12.2;
-//   k 8192: n 32768, 1 row 46.3 / 36.9.
+//   k 512: n 8192, 16 rows 4.5 / 5.2 us, 32 rows 5.4 / 5.3; n 16384, 4 rows 4.5 /
+//   5.3, 16 rows 5.3 / 5.3; n 32768, 1 row 5.1 / 6.0, 16 rows 8.1 / 6.2;
+//   k 2048: n 4096, 16 rows 5.8 / 7.5, 32 rows 7.8 / 7.6, 64 rows 11.8 / 8.0; n
+//   8192, 4 rows 6.0 / 7.9, 16 rows 8.3 / 7.9, 64 rows 20.9 / 10.3; n 16384, 1 row
+//   7.6 / 8.8, 4 rows 8.6 / 8.8, 16 rows 12.7 / 8.9;
+//   k 8192: n 1024, 64 rows 12.2 / 17.3; n 4096, 16 rows 13.0 / 17.2, 32 rows
+//   21.7 / 17.3; n 16384, 1 row 18.0 / 18.4; n 32768, 1 row 45.6 / 35.
 // Experts, by 128-row blocks of the experts met and columns each (tiled bf16;
 // direct / LDS kernel): k 1024: 32 blocks, 16 columns 7.3 / 8.9 us; 128 blocks,
 // 4 columns 6.8 / 7.3, 8 columns 7.6 / 7.6, 16 columns 11.1 / 9.4; 256 blocks, 1
@@ -824,7 +835,8 @@ int64_t experts_met(const MatvecArgs& a) {
 bool rows_kernel_pays(const MatvecArgs& a, bool expert) {
   if (!expert) {
     const int64_t t = a.tokens;
-    return a.n >= (t <= 2 ? 32768 : (t <= 8 ? 24576 : (t <= 16 ? 10240 : (t <= 32 ? 8192 : 6144))));
+    const int64_t from = t <= 2 ? 32768 : (t <= 8 ? 16384 : (t <= 16 ? 8192 : 4096));
+    return a.n >= (a.k < 1024 ? 2 * from : from);
   }
   const int64_t entries = a.tokens * a.topk, blocks = (a.n + 127) / 128;
   // (No more entries than experts: the direct kernel has a slot per entry, the
@@ -867,6 +879,18 @@ static void launch_rows(const MatvecArgs& a, hipStream_t s) {
       <<<grid, Shape::kThreads, 2 * Shape::kBuffer + list, s>>>(a);
 }
 
+// One matrix, 64-row workgroups: four groups of waves share k while the
+// workgroups are no more than the CUs and k is long enough, else two (binary32
+// x with 32 columns: the LDS holds no more).
+template <int XT, int NC>
+static void launch_groups(const MatvecArgs& a, hipStream_t s) {
+  constexpr int kMost = XT == 0 && NC > 1 ? 2 : 4;
+  const int64_t cols = NC * kTile;
+  const bool few = (a.n + 63) / 64 * ((a.tokens + cols - 1) / cols) <= 256;
+  if (few && a.k >= 1024) launch_rows<XT, NC, 2, kMost, false, false>(a, s);
+  else launch_rows<XT, NC, 2, 2, false, false>(a, s);
+}
+
 template <int XT, bool SWIGLU, bool EXPERT>
 static void launch_matvec_one(const MatvecArgs& a, hipStream_t s) {
   const int64_t entries = a.tokens * a.topk;
@@ -883,12 +907,14 @@ static void launch_matvec_one(const MatvecArgs& a, hipStream_t s) {
       else if (few) launch_rows<XT, 2, 2, 2, SWIGLU, true>(a, s);
       else launch_rows<XT, 2, 4, 1, SWIGLU, true>(a, s);
     } else {
-      if (a.tokens <= 16) launch_rows<XT, 1, 2, 2, false, false>(a, s);
-      else if (XT == 0 || a.tokens <= 32) launch_rows<XT, 2, 2, 2, false, false>(a, s);
-      // x is read once per workgroup: with 64 columns 128 rows each while that
-      // leaves a workgroup for every CU
-      else if (a.n >= 128 * 256) launch_rows<XT, XT == 0 ? 2 : 4, 4, 2, false, false>(a, s);
-      else launch_rows<XT, XT == 0 ? 2 : 4, 2, 2, false, false>(a, s);
+      // as many columns a workgroup as leave one for every CU
+      const auto fills = [&](int64_t cols) {
+        return (a.n + 63) / 64 * ((a.tokens + cols - 1) / cols) >= 256;
+      };
+      if (XT != 0 && a.tokens > 32 && a.n >= 128 * 256) launch_rows<XT, XT == 0 ? 2 : 4, 4, 2, false, false>(a, s);
+      else if (XT != 0 && a.tokens > 32 && fills(64)) launch_groups<XT, XT == 0 ? 2 : 4>(a, s);
+      else if (a.tokens > 16 && fills(32)) launch_groups<XT, 2>(a, s);
+      else launch_groups<XT, 1>(a, s);
     }
     return;
   }

@@ -42,7 +42,11 @@ def check(got, ref, mag, k, what):
     (1, 32771, 272, False), (2, 32768, 128, True), (7, 24581, 144, False), (8, 24576, 384, True),
     (16, 10247, 400, False), (15, 10240, 1024, True), (30, 8193, 112, False), (32, 8192, 640, True),
     (64, 6145, 1040, False), (70, 6176, 384, True), (64, 32800, 256, True), (40, 32771, 48, False),
-    (33, 6150, 32, False), (64, 6200, 16, False)])
+    (33, 6150, 32, False), (64, 6200, 16, False),
+    # columns over workgroups, four groups of waves with 16, 32 and 64 columns
+    (40, 4100, 2064, False), (64, 4096, 1152, True), (50, 8170, 1040, False),
+    (64, 8192, 1280, True), (61, 16380, 1040, False), (70, 16390, 528, False),
+    (12, 16400, 1200, False), (100, 4101, 80, False)])
 def test_matvec(T, n, k, tiled, dtype):
     from nvfp4_w4a4_quantized_amd import ops
     rng = np.random.default_rng(T + n + k)
