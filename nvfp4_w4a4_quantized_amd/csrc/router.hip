@@ -24,8 +24,7 @@
 // tokens (fp32), whose 19 MB would pass in 4.  A token's row lies in the
 // registers of L lanes, V consecutive experts each, so a pick is a local
 // maximum of integer keys, four DPP rotations and the same for the lowest
-// index among equals: no shared memory and no barrier.  16 lanes with 8
-// experts each up to 128 experts (four tokens a wave); 64 lanes above.
+// index among equals: no shared memory and no barrier (router_shape has L and V).
 // The gradient of 8191 x 1000 bf16 logits takes 14 us (33 MB: 7 us).
 #include "elem.h"
 #include "launch.h"
@@ -354,36 +353,51 @@ __global__ __launch_bounds__(kRouterThreads) void router_backward_kernel(RouterB
 
 namespace {
 
-// Lanes per token: 16 (four tokens a wave) up to 128 experts, the wave above.
-struct RouterShape { int lanes; int64_t blocks; size_t lds; };
+// The shape for a call: lanes per token and consecutive experts per lane.  16
+// lanes take four tokens a wave, so a pick costs a quarter of the reduction, with
+// up to 128 experts always and up to 512 where 8192 tokens fill the chip; else
+// the wave takes one.  A lane holds no more experts than needed.  Measured, bf16:
+//   32768 tokens, top-2 of 8: 1 expert a lane 5.4 us, 8 experts 7.2; top-4 of 16
+//   6.0 / 8.8; top-6 of 64: 4 experts 8.1, 8 experts 10.2; top-10 of 512, the
+//   wave: 8 experts 46, 16 experts 70;
+//   16 lanes / the wave: top-6 of 160: 2048 tokens 6.1 / 5.3, 4096 6.1 / 6.5, 8192
+//   6.8 / 9.4, 32768 15.4 / 26.8; its gradient, 4096 tokens 6.3 / 6.0, 8192 6.4 /
+//   8.5; top-10 of 512: 4096 tokens 10.8 / 9.8, 8192 12.7 / 14.9, 32768 37.5 / 46.3;
+//   top-8 of 1000, 8192 tokens 22.3 / 19.3, 32768 72 / 61.
+struct RouterShape { int lanes, per_lane; unsigned blocks; size_t lds; };
 RouterShape router_shape(int64_t tokens, int32_t experts, int32_t topk) {
   RouterShape s;
-  s.lanes = experts <= 128 ? 16 : 64;
+  s.lanes = experts <= 128 || (experts <= 512 && tokens >= 8192) ? 16 : 64;
+  const int least = (experts + s.lanes - 1) / s.lanes;
+  s.per_lane = least == 1 ? 1 : (least <= 4 ? 4 : (least <= 8 ? 8 : (least <= 16 ? 16 : 32)));
   const int groups = kRouterThreads / s.lanes;
-  s.blocks = (tokens + groups - 1) / groups;
-  if (s.blocks > 1 << 20) s.blocks = 1 << 20;
+  const int64_t blocks = (tokens + groups - 1) / groups;
+  s.blocks = (unsigned)(blocks < (1 << 20) ? blocks : 1 << 20);
   s.lds = (size_t)groups * 2 * topk * 4;
   return s;
 }
 
 }  // namespace
 
-#define NVFP4_ROUTER_CASES(KERNEL)                                                     \
-  do {                                                                                 \
-    const RouterShape sh = router_shape(a.tokens, a.num_experts, a.topk);              \
-    const unsigned blocks = (unsigned)sh.blocks;                                       \
-    const int v = a.num_experts <= 128 ? 8 : (a.num_experts <= 256 ? 4 : 16);          \
-    switch (a.dtype * 100 + v) {                                                       \
-      case 8: KERNEL<0, 16, 8><<<blocks, kRouterThreads, sh.lds, s>>>(a); break;       \
-      case 4: KERNEL<0, 64, 4><<<blocks, kRouterThreads, sh.lds, s>>>(a); break;       \
-      case 16: KERNEL<0, 64, 16><<<blocks, kRouterThreads, sh.lds, s>>>(a); break;     \
-      case 108: KERNEL<1, 16, 8><<<blocks, kRouterThreads, sh.lds, s>>>(a); break;     \
-      case 104: KERNEL<1, 64, 4><<<blocks, kRouterThreads, sh.lds, s>>>(a); break;     \
-      case 116: KERNEL<1, 64, 16><<<blocks, kRouterThreads, sh.lds, s>>>(a); break;    \
-      case 208: KERNEL<2, 16, 8><<<blocks, kRouterThreads, sh.lds, s>>>(a); break;     \
-      case 204: KERNEL<2, 64, 4><<<blocks, kRouterThreads, sh.lds, s>>>(a); break;     \
-      default: KERNEL<2, 64, 16><<<blocks, kRouterThreads, sh.lds, s>>>(a); break;     \
-    }                                                                                  \
+#define NVFP4_ROUTER_CASE(KERNEL, L, V)                                               \
+  case L * 100 + V:                                                                   \
+    if (a.dtype == 0) KERNEL<0, L, V><<<sh.blocks, kRouterThreads, sh.lds, s>>>(a);   \
+    else if (a.dtype == 1) KERNEL<1, L, V><<<sh.blocks, kRouterThreads, sh.lds, s>>>(a); \
+    else KERNEL<2, L, V><<<sh.blocks, kRouterThreads, sh.lds, s>>>(a);                \
+    break;
+#define NVFP4_ROUTER_CASES(KERNEL)                                                    \
+  do {                                                                                \
+    const RouterShape sh = router_shape(a.tokens, a.num_experts, a.topk);             \
+    switch (sh.lanes * 100 + sh.per_lane) {                                           \
+      NVFP4_ROUTER_CASE(KERNEL, 16, 1)                                                \
+      NVFP4_ROUTER_CASE(KERNEL, 16, 4)                                                \
+      NVFP4_ROUTER_CASE(KERNEL, 16, 8)                                                \
+      NVFP4_ROUTER_CASE(KERNEL, 16, 16)                                               \
+      NVFP4_ROUTER_CASE(KERNEL, 16, 32)                                               \
+      NVFP4_ROUTER_CASE(KERNEL, 64, 4)                                                \
+      NVFP4_ROUTER_CASE(KERNEL, 64, 8)                                                \
+      NVFP4_ROUTER_CASE(KERNEL, 64, 16)                                               \
+    }                                                                                 \
   } while (0)
 
 hipError_t launch_router(const RouterArgs& a, hipStream_t s) {
@@ -399,5 +413,6 @@ hipError_t launch_router_backward(const RouterBackwardArgs& a, hipStream_t s) {
 }
 
 #undef NVFP4_ROUTER_CASES
+#undef NVFP4_ROUTER_CASE
 
 }  // namespace nvfp4

@@ -54,7 +54,10 @@ def bound(logits, ids, score, renorm):
 @pytest.mark.parametrize("kind", ["plain", "ties", "masked", "lowest", "wide"])
 @pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 128, 8), (3, 7, 7), (65, 60, 4), (130, 129, 6),
                                    (37, 257, 9), (9, 1000, 20), (5, 1024, 1),
-                                   (6, 100, 40), (4, 1024, 200), (3, 256, 256)])
+                                   (6, 100, 40), (4, 1024, 200), (3, 256, 256),
+                                   # the other lanes and experts per lane
+                                   (50, 8, 2), (33, 16, 16), (20, 17, 4), (41, 64, 6),
+                                   (12, 300, 12), (8192, 130, 3), (8200, 290, 5)])
 def test_router_matches_the_definition(T, E, k, kind, dtype):
     from nvfp4_w4a4_quantized_amd import ops
     rng = np.random.default_rng(T * 1000 + E + k)
