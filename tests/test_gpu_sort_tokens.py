@@ -68,7 +68,8 @@ def dots_ref(c):
 @pytest.mark.parametrize("T,k,E,H,align,dropped", [
     (1, 1, 1, 1, 1, 0.0), (1, 8, 128, 2048, 1, 0.0), (5, 2, 3, 7, 16, 0.0), (64, 4, 60, 1111, 16, 0.1),
     (33, 9, 12, 513, 1, 0.2), (70, 20, 24, 64, 128, 0.3), (3, 3, 1000, 40, 2, 0.5),
-    (257, 8, 16, 2056, 1, 0.0), (0, 4, 8, 96, 16, 0.0), (10, 17, 40, 4099, 4, 0.1)])
+    (257, 8, 16, 2056, 1, 0.0), (0, 4, 8, 96, 16, 0.0), (10, 17, 40, 4099, 4, 0.1),
+    (6, 8, 16, 9000, 1, 0.0), (300, 10, 20, 4100, 16, 0.1)])
 def test_sort_and_unsort(T, k, E, H, align, dropped, dtype):
     from nvfp4_w4a4_quantized_amd import ops
     rng = np.random.default_rng(T * 31 + H)
