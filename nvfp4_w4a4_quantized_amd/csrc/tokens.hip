@@ -28,33 +28,34 @@ namespace {
 
 constexpr int kBatch = 8;   // entries whose rows are in flight together
 
-// Sums of n <= kBatch values over the workgroup; every thread gets them all.
-__device__ __forceinline__ void block_sums(float (&v)[kBatch], int n, float* lds) {
+// Sums of n <= kBatch values over the workgroup: thread j < n gets the j-th.
+// (Every thread adding up every sum took 14.4 us instead of 10.9 for the gradient
+// of a sort of 64 tokens of 7168, top-8, whose workgroups have 14 waves.)
+__device__ __forceinline__ float block_sums(const float (&v)[kBatch], int n, float* lds) {
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   const int waves = blockDim.x / kWave;
+  int own = 0;
 #pragma unroll
   for (int j = 0; j < kBatch; ++j) {
     if (j < n) {
-      float s = __uint_as_float(wave_incl_scan_dpp(
+      const uint32_t s = wave_incl_scan_dpp(
           __float_as_uint(v[j]), [](uint32_t a, uint32_t b) {
             return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
-          }));
-      v[j] = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(s), kWave - 1));
+          });
+      const int total = __builtin_amdgcn_readlane((int)s, kWave - 1);
+      own = lane == j ? total : own;
     }
   }
-  if (waves == 1) return;
+  float sum = __int_as_float(own);
+  if (waves == 1) return sum;
   __syncthreads();   // the previous batch's sums have been read
-  if (lane == 0) {
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) lds[wave * kBatch + j] = v[j];
-  }
+  if (lane < kBatch) lds[wave * kBatch + lane] = sum;
   __syncthreads();
-#pragma unroll
-  for (int j = 0; j < kBatch; ++j) {
-    float s = lds[j];
-    for (int w = 1; w < waves; ++w) s += lds[w * kBatch + j];
-    v[j] = s;
+  if ((int)threadIdx.x < n) {
+    sum = lds[threadIdx.x];
+    for (int w = 1; w < waves; ++w) sum += lds[w * kBatch + threadIdx.x];
   }
+  return sum;
 }
 
 // A thread's piece [c, c + kN) of a row, brought back inside the row: a last,
@@ -186,11 +187,9 @@ __global__ __launch_bounds__(256) void spread_kernel(TokenRowsArgs a, int64_t to
         }
       }
       if (DOT) {
-        block_sums(dot, n, sums);
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j)
-          if ((int)threadIdx.x == j && j < n)
-            a.dprob[t * a.topk + j0 + j] = row[j] >= 0 ? dot[j] : 0.0f;
+        // (an entry without a row has added nothing: 0)
+        const float dw = block_sums(dot, n, sums);
+        if ((int)threadIdx.x < n) a.dprob[t * a.topk + j0 + threadIdx.x] = dw;
       }
     }
   }
@@ -261,11 +260,9 @@ __global__ __launch_bounds__(1024) void collect_kernel(TokenRowsArgs a) {
       }
       if (DOT) {
         const int n = a.topk - j0 < kBatch ? a.topk - j0 : kBatch;
-        block_sums(dot, n, sums);
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j)
-          if ((int)threadIdx.x == j && j < n)
-            a.dprob[t * a.topk + j0 + j] = row0[j] >= 0 ? dot[j] : 0.0f;
+        // (an entry without a row has added nothing: 0)
+        const float dw = block_sums(dot, n, sums);
+        if ((int)threadIdx.x < n) a.dprob[t * a.topk + j0 + threadIdx.x] = dw;
       }
     }
   }
@@ -274,11 +271,11 @@ __global__ __launch_bounds__(1024) void collect_kernel(TokenRowsArgs a) {
 namespace {
 
 // Threads of a token's workgroup: one 16-byte piece each while `most` reach,
-// then more pieces per thread.
+// then an even share.
 int token_threads(int64_t hidden, int dtype, int64_t most) {
   const int64_t pieces = (hidden * (dtype == 0 ? 4 : 2) + 15) / 16;
-  const int64_t t = (pieces + 63) / 64 * 64;
-  return (int)(t > most ? most : t);
+  const int64_t steps = (pieces + most - 1) / most;
+  return (int)(((pieces + steps - 1) / steps + 63) / 64 * 64);
 }
 // (blocks x threads stays far below 2^32; larger batches loop)
 int64_t token_grid(int64_t tokens) { return tokens < (1 << 22) ? tokens : (1 << 22); }
