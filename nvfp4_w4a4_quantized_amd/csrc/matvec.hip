@@ -489,7 +489,7 @@ __global__ __launch_bounds__(1024) void decode_down_kernel(MatvecArgs a, int par
 // From a handful of columns on, a wave's own reads of x cost more than its
 // weights (a 16-column operand is 4 KiB a stage beside 1.1 KiB of weights).
 // Here a workgroup's waves take 32 rows each (16 gate and 16 up rows with
-// SwiGLU), in one group or in two that take the stages in turn, and share 16
+// SwiGLU), in one, two or four groups that take the stages in turn, and share 16
 // NC columns of x, brought into LDS once per workgroup as the parts' bf16 /
 // fp16 values, double buffered.  Each wave keeps kDepth stages of its weights
 // in flight in registers; loads past the last stage are out of the buffer's
@@ -507,7 +507,8 @@ __global__ __launch_bounds__(1024) void decode_down_kernel(MatvecArgs a, int par
 // 27, 24, 33); four groups while there is no second workgroup for a CU, else two
 // (k 8192, 16 rows: n 8192 17.5 / 22.7 us; n 24576, k 4096, 64 rows 39 / 33); and
 // 4 x 2 where 64 columns of x make 128 rows worth a workgroup (55 against 66 us).
-// More stages in flight cost occupancy (four: 127 against 109 us).
+// More stages in flight cost occupancy (four: 127 against 109 us), and do not
+// help the small grids either (8 to 15% slower).
 //
 // What bounds it: with 1-2 columns of 16, the weights' stream (FC1 of 256
 // tokens 52 us, 226 MB at 4.4 TB/s; FC2 48 us, where D and the rows add a third
