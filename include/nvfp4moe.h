@@ -612,9 +612,9 @@ int moe_unsort_tokens_backward(const void* dy, int dtype, int64_t tokens, int64_
  * unquantized activations:
  *   h = W1[e] x[t];  D = silu(h[:inter]) * h[inter:] * topk_prob[t, j]
  *   y[t] = sum_j W2[e] D
- * with the products above, D in binary32 for binary32 x and to 2^-17 relative
- * (the sum of two bf16 parts) for 16-bit x, and the sum over j ascending in
- * binary32, rounded once to y's type (x's).  The weights are moe_expert_forward's, in either layout.
+ * with the products above, h and D in binary32 for every type of x, and the
+ * sum over j ascending in binary32, rounded once to y's type (x's).  The
+ * weights are moe_expert_forward's, in either layout.
  *   workspace  moe_expert_decode_workspace_size() bytes, 16-byte aligned;
  *              every word read is written before by the same call
  * Limits: hidden % 16 == 0, inter % 16 == 0, both <= 16384 (% 128 with layout

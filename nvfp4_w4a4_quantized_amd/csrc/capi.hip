@@ -813,17 +813,15 @@ int nvfp4_expert_matvec(const void* x, int x_dtype, int64_t tokens, int64_t ld_x
 }
 
 struct DecodeLayout {
-  uint16_t* d;      // FC2's input: binary32 (over both) or two bf16 parts
-  uint16_t* d_lo;   //   [entries, inter] each
-  float* y_rows;                    // FC2's output [entries, hidden]
+  uint16_t* d;      // FC2's input, binary32 as three bf16 parts: [3, entries, inter]
+  float* y_rows;    // FC2's output [entries, hidden]
   size_t bytes;
 };
 
 static DecodeLayout carve_decode(void* ws, int64_t entries, int64_t hidden, int64_t inter) {
   Carver c(ws);
   DecodeLayout L;
-  L.d = c.take<uint16_t>((size_t)(2 * entries * inter));
-  L.d_lo = L.d + entries * inter;
+  L.d = c.take<uint16_t>((size_t)(3 * entries * inter));
   L.y_rows = c.take<float>((size_t)(entries * hidden));
   L.bytes = c.used;
   return L;
@@ -862,11 +860,10 @@ int moe_expert_decode(const void* x, int x_dtype, int64_t tokens, int64_t hidden
   hipStream_t s = static_cast<hipStream_t>(stream);
   MatvecArgs f1 = matvec_args(x, x_dtype, ld_x, tokens, w1, num_experts, 2 * inter, hidden);
   f1.topk_idx = topk_idx; f1.topk = topk; f1.prob = topk_prob;
-  f1.d = L.d; f1.d_lo = L.d_lo; f1.inter = inter;
+  f1.d = L.d; f1.d_plane = tokens * topk * inter; f1.inter = inter;
   if (launch_matvec(f1, s) != hipSuccess) return NVFP4_HIP_ERROR;
-  MatvecArgs f2 = matvec_args(L.d, x_dtype == 0 ? 0 : 1, inter, tokens, w2, num_experts, hidden,
-                              inter);
-  f2.x_lo = x_dtype == 0 ? nullptr : L.d_lo; f2.x_by_entry = 1; f2.topk_idx = topk_idx; f2.topk = topk;
+  MatvecArgs f2 = matvec_args(L.d, 1, inter, tokens, w2, num_experts, hidden, inter);
+  f2.x_plane = f1.d_plane; f2.x_by_entry = 1; f2.topk_idx = topk_idx; f2.topk = topk;
   if (decode_down_fits(tokens)) {
     f2.out = y; f2.out_dtype = x_dtype;
     return hip_status(launch_decode_down(f2, s));

@@ -234,7 +234,7 @@ hipError_t launch_collect(const TokenRowsArgs& a, hipStream_t s);
 // ---- matvec.hip ----
 struct MatvecArgs {
   const void* x; int x_dtype; int64_t ld_x;   // 0 binary32, 1 bf16, 2 fp16
-  const uint16_t* x_lo;       // non-NULL: x is bf16 high parts, these the low parts
+  int64_t x_plane;            // not 0: x is three planes of bf16 parts, this many elements apart
   int x_by_entry;             // x has a row per entry, not per token
   int64_t tokens;
   const uint8_t* codes; const uint8_t* scales; const float* gscale; int layout;
@@ -242,13 +242,13 @@ struct MatvecArgs {
   const int32_t* topk_idx; int32_t topk;      // NULL, 1: one matrix for every row
   void* out; int out_dtype;   // [rows, n]
   int skip_unrouted;          // entries of no expert are left unwritten (else zeros)
-  // SwiGLU epilogue (n = 2 * inter): D [entries, inter], binary32 (binary32 x)
-  // or its two bf16 parts
-  void* d; uint16_t* d_lo; int64_t inter; const float* prob;
+  // SwiGLU epilogue (n = 2 * inter): D [entries, inter] in binary32, as three
+  // planes of bf16 parts that are d_plane elements apart
+  uint16_t* d; int64_t d_plane, inter; const float* prob;
 };
 hipError_t launch_matvec(const MatvecArgs& a, hipStream_t s);
 // FC2 and the sum over a token's experts in one launch, for a few tokens (a.x
-// and a.x_lo the layer's D, a.out the tokens' rows).
+// the layer's D in its planes, a.out the tokens' rows).
 bool decode_down_fits(int64_t tokens);
 hipError_t launch_decode_down(const MatvecArgs& a, hipStream_t s);
 hipError_t launch_decode_combine(const float* y_rows, const int32_t* idx, int64_t tokens,

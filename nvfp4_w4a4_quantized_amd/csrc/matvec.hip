@@ -9,10 +9,10 @@
 // cores in the type of x; products are exact in the binary32 accumulator and
 // s_g multiplies the sum.  binary32 x is split into three bf16 parts by
 // truncation (8 + 8 + 8 significant bits, an exact sum) and takes three
-// products.  The layer's intermediate D is kept in binary32 for binary32 x;
-// for 16-bit x as the sum of two bf16 parts, high = bf16(D) and low =
-// bf16(D - high), within 2^-17 of the binary32 D: FC2 takes two products
-// instead of three and adds no rounding that shows in a 16-bit result.
+// products.  The layer's intermediate D is a binary32 value whatever the type of
+// x; FC1 writes it as its three parts, one plane each, so that FC2 multiplies
+// them without splitting again (FC2 splitting a binary32 D cost one token of the
+// layer 3 us of 16, 256 tokens 7 of 109).
 //
 // Mapping: a wave multiplies 16 weight rows (32 with SwiGLU: 16 gate and the
 // 16 up rows) with 16 columns, a column being a row of x: v_mfma 16x16x32
@@ -41,35 +41,42 @@ namespace {
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
-// How x travels: 0 binary32, 1 bf16, 2 fp16, 3 two bf16 parts (the layer's D)
-constexpr int kPair = 3;
-constexpr int parts_of(int xt) { return xt == 0 ? 3 : (xt == kPair ? 2 : 1); }
+// How x travels: 0 binary32, 1 bf16, 2 fp16, 3 a binary32 value as three planes of
+// bf16 parts, a.x_plane elements apart (the layer's D)
+constexpr int kPlanes = 3;
+constexpr int parts_of(int xt) { return xt == 0 || xt == kPlanes ? 3 : 1; }
 constexpr int kStage = 128;   // k elements of a stage
 constexpr int kTile = 16;     // weight rows of a tile, columns of a product
 
 // 32 elements of a column: one stage of a lane.
 template <int XT>
 struct XStage {
-  uint4 w[XT == 0 || XT == kPair ? 8 : 4];
+  static constexpr int kWords = XT == 0 ? 8 : (XT == kPlanes ? 12 : 4);
+  uint4 w[kWords];
 };
 
+// `plane`: bytes from one part's plane to the next.
 template <int XT>
-__device__ __forceinline__ XStage<XT> load_x(const char* p, const char* p_lo) {
+__device__ __forceinline__ XStage<XT> load_x(const char* p, int64_t plane) {
   XStage<XT> x;
-  __builtin_memcpy(&x.w[0], p, XT == 0 ? 128 : 64);
-  if (XT == kPair) __builtin_memcpy(&x.w[4 % (sizeof(x.w) / 16)], p_lo, 64);
+  if (XT == kPlanes) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) __builtin_memcpy(&x.w[4 * i % XStage<XT>::kWords], p + i * plane, 64);
+  } else {
+    __builtin_memcpy(&x.w[0], p, XT == 0 ? 128 : 64);
+  }
   return x;
 }
 
 // Part `part` of elements [8s, 8s + 8) of the stage as an operand.
 template <int XT>
 __device__ __forceinline__ uint4 x_operand(const XStage<XT>& x, int s, int part) {
-  if (XT == kPair) return x.w[(part * 4 + s) % (sizeof(x.w) / 16)];
+  if (XT == kPlanes) return x.w[(part * 4 + s) % XStage<XT>::kWords];
   if (XT != 0) return x.w[s];
   // Upper halves of the value (a quiet NaN stays one), of what is left of it, and
   // of the rest.  The lower parts are the largest finite value's for an
   // infinity, whose difference would be NaN: they add to it with its sign.
-  const uint4 a = x.w[(2 * s) % (sizeof(x.w) / 16)], b = x.w[(2 * s + 1) % (sizeof(x.w) / 16)];
+  const uint4 a = x.w[(2 * s) % XStage<XT>::kWords], b = x.w[(2 * s + 1) % XStage<XT>::kWords];
   uint32_t f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   uint32_t o[4];
 #pragma unroll
@@ -250,28 +257,25 @@ __device__ __forceinline__ void store_zeros(const MatvecArgs& a, const uint16_t*
     store4(a, list[i / (count / 4)], row + 4 * (i % (count / 4)), (f32x4_t){0.f, 0.f, 0.f, 0.f});
 }
 
-// The layer's D of one entry, silu(g) u p: binary32 for binary32 x, else its
-// two bf16 parts.
-template <int XT>
+// The layer's D of one entry, silu(g) u p in binary32, as its three bf16 parts:
+// the upper half of its bits, of what is left of it, and the rest -- an exact
+// sum.  The lower parts of an infinity are zero (inf - inf would be NaN).
 __device__ __forceinline__ void store_d4(const MatvecArgs& a, int64_t entry, int64_t col, f32x4_t g,
                                          f32x4_t u, float p) {
-  f32x4_t d;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) d[i] = g[i] / (1.0f + expf(-g[i])) * u[i] * p;
-  if (XT == 0) {
-    __builtin_memcpy(static_cast<float*>(a.d) + entry * a.inter + col, &d, 16);
-    return;
-  }
-  uint16_t hi[4], lo[4];
+  uint16_t part[3][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    hi[i] = Elem<1>::from_float(d[i]);
-    const float h = Elem<1>::to_float(hi[i]);
-    // an infinite D keeps a zero low part (inf - inf would be NaN)
-    lo[i] = Elem<1>::from_float(fabsf(h) < __builtin_huge_valf() ? d[i] - h : 0.0f);
+    float d = g[i] / (1.0f + expf(-g[i])) * u[i] * p;
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+      const uint32_t top = __float_as_uint(d) & 0xFFFF0000u;
+      part[q][i] = (uint16_t)(top >> 16);
+      d = fabsf(d) < __builtin_huge_valf() ? d - __uint_as_float(top) : 0.0f;
+    }
   }
-  __builtin_memcpy(static_cast<uint16_t*>(a.d) + entry * a.inter + col, hi, 8);
-  __builtin_memcpy(a.d_lo + entry * a.inter + col, lo, 8);
+#pragma unroll
+  for (int q = 0; q < 3; ++q)
+    __builtin_memcpy(a.d + q * a.d_plane + entry * a.inter + col, part[q], 8);
 }
 
 }  // namespace
@@ -311,9 +315,10 @@ __device__ __forceinline__ int find_entries(const MatvecArgs& a, int e, int entr
 // half or all of its 32 elements there.
 template <int XT, int RT>
 __device__ __forceinline__ void stage_loop(const MatvecArgs& a, f32x4_t (&acc)[RT],
-                                           const LanePlace (&place)[RT], const char* xp,
-                                           const char* xl, int q, int st, int step) {
+                                           const LanePlace (&place)[RT], const char* xp, int q,
+                                           int st, int step) {
   constexpr int xsize = XT == 0 ? 4 : 2;
+  const int64_t plane = a.x_plane * 2;
   const int64_t cstep = a.layout == 0 ? kStage / 2 : 2048, sstep = a.layout == 0 ? kStage / 16 : 256;
   const int stages = (int)(a.k / kStage);
   for (; st < stages; st += 2 * step) {
@@ -325,13 +330,13 @@ __device__ __forceinline__ void stage_loop(const MatvecArgs& a, f32x4_t (&acc)[R
       c[0][rt] = load_u128(place[rt].codes + st * cstep);
       sb[0][rt] = load_u16(place[rt].scales + st * sstep);
     }
-    const XStage<XT> x0 = load_x<XT>(xp + (int64_t)st * kStage * xsize, xl + st * kStage * 2);
+    const XStage<XT> x0 = load_x<XT>(xp + (int64_t)st * kStage * xsize, plane);
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       c[1][rt] = load_u128(place[rt].codes + st2 * cstep);
       sb[1][rt] = load_u16(place[rt].scales + st2 * sstep);
     }
-    const XStage<XT> x1 = load_x<XT>(xp + (int64_t)st2 * kStage * xsize, xl + st2 * kStage * 2);
+    const XStage<XT> x1 = load_x<XT>(xp + (int64_t)st2 * kStage * xsize, plane);
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) stage_product<XT>(acc[rt], c[0][rt], sb[0][rt], x0);
     if (st2 != st) {
@@ -346,12 +351,12 @@ __device__ __forceinline__ void stage_loop(const MatvecArgs& a, f32x4_t (&acc)[R
     uint32_t sb[RT] = {};
     if (left >= 16) {
       xp += (int64_t)stages * kStage * xsize;
-      xl += stages * kStage * 2;
       if (left >= 32) {
-        x = load_x<XT>(xp, xl);
+        x = load_x<XT>(xp, plane);
       } else {
-        __builtin_memcpy(&x.w[0], xp, 16 * xsize);
-        if (XT == kPair) __builtin_memcpy(&x.w[4 % (sizeof(x.w) / 16)], xl, 32);
+#pragma unroll
+        for (int i = 0; i < (XT == kPlanes ? 3 : 1); ++i)
+          __builtin_memcpy(&x.w[4 * i % XStage<XT>::kWords], xp + i * plane, 16 * xsize);
       }
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
@@ -421,13 +426,11 @@ __global__ __launch_bounds__(512) void matvec_kernel(MatvecArgs a) {
     else if (c0 != 0) find_entries(a, e, entries, 0, c0, r, &entry);
     const int64_t xrow = EXPERT && !a.x_by_entry ? entry / a.topk : entry;
     const char* xp = static_cast<const char*>(a.x) + (xrow * a.ld_x + 32 * q) * xsize;
-    const char* xl = XT == kPair ? reinterpret_cast<const char*>(a.x_lo) + (xrow * a.ld_x + 32 * q) * 2
-                                 : nullptr;
     const float p = SWIGLU ? a.prob[entry] : 1.0f;
     f32x4_t acc[RT];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) acc[rt] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
-    stage_loop<XT, RT>(a, acc, place, xp, xl, q, wave, waves);
+    stage_loop<XT, RT>(a, acc, place, xp, q, wave, waves);
     if (c0 != first) __syncthreads();   // the last chunk's sums have been read
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) red[(wave * RT + rt) * kWave + lane] = acc[rt];
@@ -440,7 +443,7 @@ __global__ __launch_bounds__(512) void matvec_kernel(MatvecArgs a) {
         acc[rt] = s * sg;
       }
       if (c0 + r < m) {
-        if (SWIGLU) store_d4<XT>(a, entry, row0 + 4 * q, acc[0], acc[RT - 1], p);
+        if (SWIGLU) store_d4(a, entry, row0 + 4 * q, acc[0], acc[RT - 1], p);
         else store4(a, entry, row0 + 4 * q, acc[0]);
       }
     }
@@ -451,8 +454,8 @@ __global__ __launch_bounds__(512) void matvec_kernel(MatvecArgs a) {
 // tiles, y = tokens; `parts` waves share the stages of one of the token's
 // entries, the workgroup's wave sets take the entries in turn, and the waves'
 // sums (each times its expert's outer scale) are added in LDS in wave order.
-// All 16 columns of a product are the same row; the first is used.
-template <int XT>
+// D's three parts are three columns of one product (the others repeat the
+// first and are not used), whose results are added in that order.
 __global__ __launch_bounds__(1024) void decode_down_kernel(MatvecArgs a, int parts) {
   extern __shared__ char lds[];
   const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -468,18 +471,16 @@ __global__ __launch_bounds__(1024) void decode_down_kernel(MatvecArgs a, int par
     const float sg = a.gscale[e];
     const int64_t row = row0 + r;
     const LanePlace place[1] = {lane_place(a, e, row < a.n ? row : a.n - 1, q)};
-    const int64_t at = (entry * a.ld_x + 32 * q) * (XT == 0 ? 4 : 2);
+    const int64_t at = (r < 3 ? r : 0) * a.x_plane + entry * a.ld_x + 32 * q;
     f32x4_t acc[1] = {(f32x4_t){0.f, 0.f, 0.f, 0.f}};
-    stage_loop<XT, 1>(a, acc, place, static_cast<const char*>(a.x) + at,
-                      XT == kPair ? reinterpret_cast<const char*>(a.x_lo) + at : nullptr, q,
-                      wave % parts, parts);
+    stage_loop<1, 1>(a, acc, place, static_cast<const char*>(a.x) + at * 2, q, wave % parts, parts);
     sum += acc[0] * sg;
   }
-  if (r == 0) red[wave * 4 + q] = sum;
+  if (r < 3) red[(wave * 3 + r) * 4 + q] = sum;
   __syncthreads();
   if (threadIdx.x < 4) {
     sum = red[threadIdx.x];
-    for (int w = 1; w < waves; ++w) sum += red[w * 4 + threadIdx.x];
+    for (int w = 1; w < 3 * waves; ++w) sum += red[w * 4 + threadIdx.x];
     store4(a, t, row0 + 4 * threadIdx.x, sum);
   }
 }
@@ -543,7 +544,8 @@ struct WStage {
 // 8 elements of a column on their way to LDS.
 template <int XT>
 struct XPiece {
-  u32x4_t w[XT == 0 || XT == kPair ? 2 : 1];
+  static constexpr int kWords = XT == 0 ? 2 : (XT == kPlanes ? 3 : 1);
+  u32x4_t w[kWords];
 };
 
 // A column's stage is 16 pieces of 8 elements, piece 4q + s in slot
@@ -555,10 +557,9 @@ __device__ __forceinline__ int slot_of(int q, int s) { return 4 * ((q >> 1) ^ (q
 
 template <int XT>
 __device__ __forceinline__ uint4 piece_part(const XPiece<XT>& v, int part) {
-  constexpr int kLast = XT == 0 || XT == kPair ? 1 : 0;
-  const u32x4_t& a = v.w[XT == kPair && part == 1 ? kLast : 0];
+  const u32x4_t& a = v.w[XT == kPlanes ? part % XPiece<XT>::kWords : 0];
   if (XT != 0) return make_uint4(a[0], a[1], a[2], a[3]);
-  const u32x4_t& b = v.w[kLast];
+  const u32x4_t& b = v.w[1 % XPiece<XT>::kWords];
   XStage<0> x;
   x.w[0] = make_uint4(a[0], a[1], a[2], a[3]);
   x.w[1] = make_uint4(b[0], b[1], b[2], b[3]);
@@ -658,9 +659,10 @@ __global__ __launch_bounds__(ROW_WAVES* GROUPS* kWave) void matvec_rows_kernel(M
   // one stage).  Columns past the last and stages past the last are out of the
   // buffer's range: zeros, and no traffic.
   const int64_t xrows = EXPERT && a.x_by_entry ? entries : a.tokens;
-  const uint32_t xbytes = (uint32_t)(((xrows - 1) * a.ld_x + a.k) * xsize);   // below 2^31
+  // (the planes one behind the other are one buffer; below 2^31)
+  const uint32_t plane = XT == kPlanes ? (uint32_t)(a.x_plane * 2) : 0;
+  const uint32_t xbytes = (uint32_t)(((xrows - 1) * a.ld_x + a.k) * xsize) + 2 * plane;
   const __amdgpu_buffer_rsrc_t xres = buffer_rsrc(a.x, xbytes);
-  const __amdgpu_buffer_rsrc_t xlow = buffer_rsrc(XT == kPair ? a.x_lo : a.x, xbytes);
   const int slot = threadIdx.x % 16, own = threadIdx.x / 16;
   const int pi = slot ^ (own % 16), pm = pi / 4;
   const int piece = 4 * ((((pm ^ (pm >> 1)) & 1) << 1) | (pm >> 1)) + pi % 4;   // slot_of's inverse
@@ -693,9 +695,10 @@ __global__ __launch_bounds__(ROW_WAVES* GROUPS* kWave) void matvec_rows_kernel(M
         const bool last = ragged && st == stages - 1;
         const uint32_t lo = none ? kNone : (last ? xo_last[i] : xo[i]);
         const int un = none || last ? 0 : st * kStage * xsize;
-        xr[set][i].w[0] = __builtin_amdgcn_raw_buffer_load_b128(xres, lo, un, 0);
-        if (XT == 0) xr[set][i].w[XT == 0 ? 1 : 0] = __builtin_amdgcn_raw_buffer_load_b128(xres, lo + 16, un, 0);
-        if (XT == kPair) xr[set][i].w[XT == kPair ? 1 : 0] = __builtin_amdgcn_raw_buffer_load_b128(xlow, lo, un, 0);
+#pragma unroll
+        for (int w = 0; w < XPiece<XT>::kWords; ++w)
+          xr[set][i].w[w] = __builtin_amdgcn_raw_buffer_load_b128(xres, lo + (XT == 0 ? 16 * w : 0),
+                                                                  un + w * plane, 0);
       }
     };
     auto store_xs = [&](int set, int buf) {
@@ -799,7 +802,7 @@ __global__ __launch_bounds__(ROW_WAVES* GROUPS* kWave) void matvec_rows_kernel(M
       if (ci >= m) continue;
       const int entry = EXPERT ? list[ci] : ci;
       if (SWIGLU) {
-        if (row0 < rows) store_d4<XT>(a, entry, row0 + 4 * q, acc[0][b], acc[1][b], a.prob[entry]);
+        if (row0 < rows) store_d4(a, entry, row0 + 4 * q, acc[0][b], acc[1][b], a.prob[entry]);
       } else {
 #pragma unroll
         for (int rt = 0; rt < kWide; ++rt) store4(a, entry, row0 + rt * kTile + 4 * q, acc[rt][b]);
@@ -896,13 +899,18 @@ template <int XT, bool SWIGLU, bool EXPERT>
 static void launch_matvec_one(const MatvecArgs& a, hipStream_t s) {
   const int64_t entries = a.tokens * a.topk;
   const int64_t xrows = EXPERT && a.x_by_entry ? entries : a.tokens;
-  const int64_t xbytes = ((xrows - 1) * a.ld_x + a.k) * (XT == 0 ? 4 : 2);
+  const int64_t xbytes = ((xrows - 1) * a.ld_x + a.k) * (XT == 0 ? 4 : 2) + 2 * (a.x_plane * 2);
   if (a.k >= 32 && xbytes < kNone && rows_kernel_pays(a, EXPERT)) {
     if constexpr (EXPERT) {
       // the entries of an expert scatter about their mean: room for twice as many
       const bool one = 2 * entries <= 16 * a.num_groups;
-      // 64-row workgroups whose groups share k while those are at most two a CU
-      const bool few = experts_met(a) * ((a.n + 63) / 64) * column_blocks(a, one ? 16 : 32) <= 512;
+      // 64-row workgroups whose groups share k while those are at most two a CU,
+      // or one where the LDS holds no second (three parts of 32 columns: 128 tokens,
+      // top-4 of 16 experts of [1024, 1024], binary32, 512 of them 24.3 us, half as
+      // many 128-row workgroups 17.0)
+      const int64_t most = !one && parts_of(XT) == 3 ? 256 : 512;
+      const bool few = experts_met(a) * ((a.n + 63) / 64) * column_blocks(a, one ? 16 : 32) <= most;
+      static_assert(parts_of(XT) != 3 || 4 * RowsShape<XT, 2, 2, 2>::kBuffer > 160 * 1024, "see `most`");
       if (one && few) launch_rows<XT, 1, 2, 2, SWIGLU, true>(a, s);
       else if (one) launch_rows<XT, 1, 4, 1, SWIGLU, true>(a, s);
       else if (few) launch_rows<XT, 2, 2, 2, SWIGLU, true>(a, s);
@@ -931,7 +939,7 @@ static void launch_matvec_one(const MatvecArgs& a, hipStream_t s) {
 hipError_t launch_matvec(const MatvecArgs& a, hipStream_t s) {
   if (a.tokens == 0) return hipSuccess;
   const bool swiglu = a.d != nullptr, expert = a.topk_idx != nullptr;
-  const int xt = a.x_lo ? kPair : a.x_dtype;
+  const int xt = a.x_plane ? kPlanes : a.x_dtype;
   switch (xt * 4 + (swiglu ? 2 : 0) + (expert ? 1 : 0)) {
     case 0: launch_matvec_one<0, false, false>(a, s); break;
     case 1: launch_matvec_one<0, false, true>(a, s); break;
@@ -942,7 +950,7 @@ hipError_t launch_matvec(const MatvecArgs& a, hipStream_t s) {
     case 8: launch_matvec_one<2, false, false>(a, s); break;
     case 9: launch_matvec_one<2, false, true>(a, s); break;
     case 11: launch_matvec_one<2, true, true>(a, s); break;
-    default: launch_matvec_one<kPair, false, true>(a, s); break;
+    default: launch_matvec_one<kPlanes, false, true>(a, s); break;
   }
   return hipGetLastError();
 }
@@ -961,9 +969,8 @@ hipError_t launch_decode_down(const MatvecArgs& a, hipStream_t s) {
   if (parts > (stages + 1) / 2) parts = (int)((stages + 1) / 2);
   const int waves = sets * parts;
   const dim3 grid((unsigned)((a.n + kTile - 1) / kTile), (unsigned)a.tokens);
-  const size_t lds = (size_t)waves * 4 * sizeof(f32x4_t);
-  if (a.x_lo) decode_down_kernel<kPair><<<grid, waves * kWave, lds, s>>>(a, parts);
-  else decode_down_kernel<0><<<grid, waves * kWave, lds, s>>>(a, parts);
+  const size_t lds = (size_t)waves * 3 * 4 * sizeof(f32x4_t);
+  decode_down_kernel<<<grid, waves * kWave, lds, s>>>(a, parts);
   return hipGetLastError();
 }
 

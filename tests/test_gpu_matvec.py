@@ -349,3 +349,48 @@ def test_weights_beyond_four_gigabytes():
     y = ops.nvfp4_expert_matvec(x, ids, w, out_dtype=torch.float32)
     z = ops.nvfp4_matvec(x, last, out_dtype=torch.float32)
     assert float((y[:, 0] - z).norm() / z.norm()) < 1e-5
+
+
+def empty_weights(groups, n, k):
+    """All-zero codes with block scales of one, outer scales of one."""
+    return (torch.zeros((groups, n, k // 2), dtype=torch.uint8),
+            torch.full((groups, n, k // 16), 0x38, dtype=torch.uint8), torch.ones(groups))
+
+
+def put(w, row, col, code, scale=0x38):
+    """Element [:, row, col] = code (E2M1), its block's scale byte."""
+    assert int(w[0][:, row, col // 2].max()) == 0
+    w[0][:, row, col // 2] = code << (4 * (col % 2))
+    w[1][:, row, col // 16] = scale
+
+
+# sizes of the layer that reach, for FC2: the kernel with the sum (up to four
+# tokens), the direct kernel, and the kernel that shares D through LDS
+REACH = [(1, 2, 8, 512, 128), (4, 2, 8, 512, 384), (20, 2, 8, 512, 128), (100, 2, 8, 512, 128)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,k,E,H,I", REACH)
+def test_decode_keeps_d_in_binary32(T, k, E, H, I, dtype):
+    """Two elements of D that differ in their 21st significant bit and cancel
+    in FC2: every value up to y is a binary32 one, so y is exact."""
+    from nvfp4_w4a4_quantized_amd import ops
+    w1, w2 = empty_weights(E, 2 * I, H), empty_weights(E, H, I)
+    for c in (0, 1):
+        put(w1, c, 0, 6, 0x50)              # gate: 4 * 8 = 32, so silu(32) = 32
+        put(w1, I + c, 0, 2)                # up: 1
+        put(w1, I + c, 16, 2, 2)            #   + 2^-8
+    put(w1, I, 32, 1, 1)                    #   + 2^-10 * x, the first element alone
+    for n in range(H):
+        w2[0][:, n, 0] = 2 | (10 << 4)      # 8 D[0] - 8 D[1]
+        w2[1][:, n, 0] = 0x50
+    x = torch.zeros((T, H))
+    x[:, [0, 16]] = 1.0
+    x[:, 32] = 2.0 ** -10
+    ids = torch.arange(T * k, dtype=torch.int32).view(T, k) % E
+    prob = torch.full((T, k), 0.5)
+    say("decode, D in binary32", T, k, E, H, I, dtype)
+    y = ops.moe_expert_decode(x.to(dtype).cuda(), ids.cuda(), prob.cuda(), E, I, held(*w1, True),
+                              held(*w2, True))
+    # k entries of 8 * (32 * 2^-20) * 0.5
+    assert torch.equal(y.cpu().double(), torch.full((T, H), k * 2.0 ** -13, dtype=torch.float64))
