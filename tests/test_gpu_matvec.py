@@ -394,3 +394,60 @@ def test_decode_keeps_d_in_binary32(T, k, E, H, I, dtype):
                               held(*w2, True))
     # k entries of 8 * (32 * 2^-20) * 0.5
     assert torch.equal(y.cpu().double(), torch.full((T, H), k * 2.0 ** -13, dtype=torch.float64))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,k,E,H,I", REACH)
+def test_decode_of_far_negative_gates(T, k, E, H, I, dtype):
+    """Gates of -85 to -100, where binary32 exp(-g) overflows while silu(g) u p
+    is a normal number.  Tolerance: D, the outer scale and the sum of k = 2
+    equal terms round once each (2^-24), and D's two lower parts may count as
+    zero below 2^-126, times the weights' 2^100 in each entry."""
+    from nvfp4_w4a4_quantized_amd import ops
+    w1, w2 = empty_weights(E, 2 * I, H), empty_weights(E, H, I)
+    x = torch.zeros((T, H))
+    for j in range(16):
+        put(w1, j, j, 2)                    # gate j: x[j]
+        put(w1, I + j, 16 + j, 7, 0x7E)     # up j: 6 * 448 * x[16 + j]
+        x[:, j] = -85.0 - j
+        x[:, 16 + j] = 2.0 ** 15
+    for n in range(H):
+        put(w2, n, n % 16, 2)
+    w2[2][:] = 2.0 ** 100
+    ids = torch.arange(T * k, dtype=torch.int32).view(T, k) % E
+    prob = torch.full((T, k), 0.75)
+    g, u = x[0, :16].double(), 2688.0 * x[0, 16:32].double()
+    d = g * torch.exp(g) / (1.0 + torch.exp(g)) * u * 0.75
+    assert bool((d.abs() > 2.0 ** -126).all())
+    ref = (k * 2.0 ** 100 * d).repeat(H // 16).expand(T, H)
+    say("decode, far negative gates", T, k, E, H, I, dtype)
+    y = ops.moe_expert_decode(x.to(dtype).cuda(), ids.cuda(), prob.cuda(), E, I, held(*w1, True),
+                              held(*w2, True))
+    bad = R.outside(y, ref, 4 * 2.0 ** -24 * ref.abs() + k * 2 * 2.0 ** -26)
+    assert not bool(bad.any()), f"{int(bad.sum())} of {bad.numel()} outside"
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,k,E,H,I", REACH)
+def test_decode_of_far_negative_gates_and_infinite_up(T, k, E, H, I, dtype):
+    """silu(g) is below zero however far g is, so an up value past binary32's
+    range makes D an infinity and no NaN."""
+    from nvfp4_w4a4_quantized_amd import ops
+    w1 = empty_weights(E, 2 * I, H)
+    w1[2][:] = 2.0 ** 100
+    gates = [-90.0, -100.0, -500.0, -800.0, -2.0 ** 40]
+    x = torch.zeros((T, H))
+    for j, g in enumerate(gates):
+        put(w1, j, j, 2)
+        put(w1, I + j, 16 + j, 7 if j % 2 else 15, 0x7E)   # +-2688 x[16 + j]
+        x[:, j] = g * 2.0 ** -100
+    for j in range(len(gates)):
+        w2 = empty_weights(E, H, I)
+        w2[0][:, :, j // 2] = 2 << (4 * (j % 2))
+        xs = x.clone()
+        xs[:, 16 + j] = 2.0 ** 20           # up: 2688 * 2^120, past the range
+        say("decode, infinite up", T, k, E, H, I, dtype, gates[j])
+        y = ops.moe_expert_decode(xs.to(dtype).cuda(), (torch.arange(T * k).view(T, k) % E).int().cuda(),
+                                  torch.full((T, k), 0.5).cuda(), E, I, held(*w1, True),
+                                  held(*w2, True)).cpu()
+        assert torch.equal(y.float(), torch.full((T, H), -np.inf if j % 2 else np.inf))
