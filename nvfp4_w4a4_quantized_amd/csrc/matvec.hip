@@ -257,13 +257,13 @@ __device__ __forceinline__ void store_zeros(const MatvecArgs& a, const uint16_t*
     store4(a, list[i / (count / 4)], row + 4 * (i % (count / 4)), (f32x4_t){0.f, 0.f, 0.f, 0.f});
 }
 
-// silu(g) u p.  Below g = -80, where binary32 exp(-g) overflows and e^g leaves the
-// normal range, silu(g) = g e^g (1 + e^g is one) with e^g = 2^n e^f, |f| <= ln 2 / 2,
-// and the powers of two and the product are binary64: the rounding to binary32 is
-// the only one at the small end.  Below -700 g counts as -700, where D is zero for
-// any finite u and p and an infinity for an infinite u.  Both branches share the
-// exponential: a binary64 exp in a branch of its own took 20 to 50 registers and a
-// wave per SIMD from the kernels.
+// silu(g) u p; the product is binary64 and rounded once, so no part of it leaves
+// binary32's range before the whole does.  Below g = -80, where binary32 exp(-g)
+// overflows and e^g leaves the normal range, silu(g) = g e^g (1 + e^g is one) with
+// e^g = 2^n e^f, |f| <= ln 2 / 2, the power of two applied in binary64.  Below -700
+// g counts as -700, where D is zero for any finite u and p and an infinity for an
+// infinite u.  Both branches share the exponential: a binary64 exp in a branch of
+// its own took 20 to 50 registers and a wave per SIMD from the kernels.
 __device__ __forceinline__ float weighted_swiglu(float g, float u, float p) {
   constexpr double kLn2 = 0.69314718055994530942;
   constexpr float kHigh = (float)kLn2, kLow = (float)(kLn2 - kHigh);
@@ -271,8 +271,8 @@ __device__ __forceinline__ float weighted_swiglu(float g, float u, float p) {
   const float gt = fmaxf(g, -700.0f), n = rintf(gt * (float)(1.0 / kLn2));
   const float f = fmaf(-n, kLow, fmaf(-n, kHigh, gt));
   const float e = expf(tail ? f : -g);
-  const double s = ldexp((double)gt * e, (int)n);
-  return tail ? (float)(s * u * p) : g / (1.0f + e) * u * p;
+  const double s = tail ? ldexp((double)gt * e, (int)n) : (double)(g / (1.0f + e));
+  return (float)(s * u * p);
 }
 
 // The layer's D of one entry, silu(g) u p in binary32, as its three bf16 parts:

@@ -451,3 +451,36 @@ def test_decode_of_far_negative_gates_and_infinite_up(T, k, E, H, I, dtype):
                                   torch.full((T, k), 0.5).cuda(), E, I, held(*w1, True),
                                   held(*w2, True)).cpu()
         assert torch.equal(y.float(), torch.full((T, H), -np.inf if j % 2 else np.inf))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,k,E,H,I", REACH)
+@pytest.mark.parametrize("large", [True, False])
+def test_decode_whose_partial_products_leave_the_range(large, T, k, E, H, I, dtype):
+    """silu(g) u overflows (g = u = 2^70, p = 2^-100) or falls below the normal
+    range (g = -79, u = 2^-30, p = 2^60) while D = silu(g) u p does neither.
+    Tolerance: the exponential's (|g| + 16) 2^-24, and 2^-24 for each of D, the
+    outer scale and the sum."""
+    from nvfp4_w4a4_quantized_amd import ops
+    w1, w2 = empty_weights(E, 2 * I, H), empty_weights(E, H, I)
+    x = torch.zeros((T, H))
+    if large:
+        w1[2][:], prob, d, tol = 2.0 ** 60, 2.0 ** -100, 2.0 ** 40, 3
+        put(w1, 0, 0, 2)
+        put(w1, I, 16, 2)
+        x[:, 0] = x[:, 16] = 2.0 ** 10
+    else:
+        w1[2][:], prob, tol = 2.0 ** -10, 2.0 ** 60, 79 + 16 + 3
+        put(w1, 0, 0, 2, 0x70)              # 2^7
+        put(w1, I, 16, 1, 1)                # 2^-10
+        x[:, 0], x[:, 16] = -79.0 * 8, 2.0 ** -10
+        d = -79.0 / (1.0 + np.exp(79.0)) * 2.0 ** 30
+    w2[0][:, :, 0] = 2
+    w2[2][:] = 2.0 ** -round(np.log2(abs(d)))
+    ids = torch.arange(T * k, dtype=torch.int32).view(T, k) % E
+    say("decode, partial products", large, T, k, E, H, I, dtype)
+    y = ops.moe_expert_decode(x.to(dtype).cuda(), ids.cuda(), torch.full((T, k), prob).cuda(), E, I,
+                              held(*w1, True), held(*w2, True))
+    ref = torch.full((T, H), k * d * float(w2[2][0]), dtype=torch.float64)
+    bad = R.outside(y, ref, tol * 2.0 ** -24 * ref.abs())
+    assert not bool(bad.any()), f"{int(bad.sum())} of {bad.numel()} outside"
