@@ -598,7 +598,9 @@ int moe_unsort_tokens_backward(const void* dy, int dtype, int64_t tokens, int64_
  * rounding, while sum_k (q s_b) x stays in binary32's range and no x (of
  * binary32: no part, 2^-16 of x) is below 2^-126, where it may count as zero.
  * Infinite x gives the formula's infinities and NaN, NaN gives NaN.  Every
- * result is bitwise reproducible.
+ * result is bitwise reproducible; the order of the sum over k goes by the
+ * call's sizes, so a row's last bits may differ between calls with other
+ * numbers of rows or entries.
  *   x          [tokens, ld_x] (x_by_entry: [tokens * topk, ld_x]), dtype code
  *   w          NVFP4 weights [n, k] / [num_experts, n, k]; layout 0, or 1
  *              (nvfp4_pack_weights) where n % 32 == 0 and k % 128 == 0
@@ -612,9 +614,9 @@ int moe_unsort_tokens_backward(const void* dy, int dtype, int64_t tokens, int64_
  * unquantized activations:
  *   h = W1[e] x[t];  D = silu(h[:inter]) * h[inter:] * topk_prob[t, j]
  *   y[t] = sum_j W2[e] D
- * with the products above, h and D in binary32 for every type of x, and the
- * sum over j ascending in binary32, rounded once to y's type (x's).  The
- * weights are moe_expert_forward's, in either layout.
+ * with the products above, h, D and every entry's W2 D in binary32 for every
+ * type of x, and the sum over j ascending in binary32, rounded once to y's type
+ * (x's).  The weights are moe_expert_forward's, in either layout.
  *   workspace  moe_expert_decode_workspace_size() bytes, 16-byte aligned;
  *              every word read is written before by the same call
  * Limits: hidden % 16 == 0, inter % 16 == 0, both <= 16384 (% 128 with layout

@@ -394,6 +394,12 @@ __device__ __forceinline__ void stage_loop(const MatvecArgs& a, f32x4_t (&acc)[R
   }
 }
 
+// The value N lanes further on in the lane's row of 16 (zero past its end).
+template <int N>
+__device__ __forceinline__ float row_ahead(float v) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x100 + N, 0xf, 0xf, true));   // row_shl:N
+}
+
 // Grid: x = 16-row tiles of the output, y = slots (EXPERT) or chunks of 16
 // columns.  A slot is an entry when there are no more entries than experts
 // (the first entry of an expert does the work of all of its entries), else an
@@ -470,35 +476,46 @@ __global__ __launch_bounds__(512) void matvec_kernel(MatvecArgs a) {
 
 // The layer's FC2 and the sum over a token's experts in one: grid x = 16-row
 // tiles, y = tokens; `parts` waves share the stages of one of the token's
-// entries, the workgroup's wave sets take the entries in turn, and the waves'
-// sums (each times its expert's outer scale) are added in LDS in wave order.
-// D's three parts are three columns of one product (the others repeat the
-// first and are not used), whose results are added in that order.
+// entries and the workgroup's wave sets take the entries in turn.  D's three
+// parts are three columns of one product (the others repeat the first and are
+// not used).  An entry's sums meet in LDS, so that it is whole, and rounded,
+// before the entries are added in ascending order, as in the separate kernels.
 __global__ __launch_bounds__(1024) void decode_down_kernel(MatvecArgs a, int parts) {
   extern __shared__ char lds[];
   const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int waves = blockDim.x / kWave, sets = waves / parts;
   const int r = lane % kTile, q = lane / kTile;
   const int64_t row0 = (int64_t)blockIdx.x * kTile, t = blockIdx.y;
-  f32x4_t* red = reinterpret_cast<f32x4_t*>(lds);
-  f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
+  f32x4_t* red = reinterpret_cast<f32x4_t*>(lds);               // [topk, parts, 4]
+  float* outer = reinterpret_cast<float*>(red + a.topk * parts * 4);   // [topk]
   for (int j = wave / parts; j < a.topk; j += sets) {
     const int64_t entry = t * a.topk + j;
     const int e = a.topk_idx[entry];
-    if (e < 0 || e >= a.num_groups) continue;
-    const float sg = a.gscale[e];
-    const int64_t row = row0 + r;
-    const LanePlace place[1] = {lane_place(a, e, row < a.n ? row : a.n - 1, q)};
-    const int64_t at = (r < 3 ? r : 0) * a.x_plane + entry * a.ld_x + 32 * q;
+    float sg = 0.0f;                                            // an entry of no expert adds zero
     f32x4_t acc[1] = {(f32x4_t){0.f, 0.f, 0.f, 0.f}};
-    stage_loop<1, 1>(a, acc, place, static_cast<const char*>(a.x) + at * 2, q, wave % parts, parts);
-    sum += acc[0] * sg;
+    if (e >= 0 && e < a.num_groups) {
+      sg = a.gscale[e];
+      const int64_t row = row0 + r;
+      const LanePlace place[1] = {lane_place(a, e, row < a.n ? row : a.n - 1, q)};
+      const int64_t at = (r < 3 ? r : 0) * a.x_plane + entry * a.ld_x + 32 * q;
+      stage_loop<1, 1>(a, acc, place, static_cast<const char*>(a.x) + at * 2, q, wave % parts, parts);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[0][i] = acc[0][i] + row_ahead<1>(acc[0][i]) + row_ahead<2>(acc[0][i]);
+    }
+    if (r == 0) red[(j * parts + wave % parts) * 4 + q] = acc[0];
+    if (lane == 0) outer[j] = sg;
   }
-  if (r < 3) red[(wave * 3 + r) * 4 + q] = sum;
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.topk * 4; i += blockDim.x) {
+    f32x4_t* own = red + i / 4 * parts * 4 + i % 4;
+    f32x4_t y = own[0];
+    for (int p = 1; p < parts; ++p) y += own[4 * p];
+    own[0] = y * outer[i / 4];
+  }
   __syncthreads();
   if (threadIdx.x < 4) {
-    sum = red[threadIdx.x];
-    for (int w = 1; w < 3 * waves; ++w) sum += red[w * 4 + threadIdx.x];
+    f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < a.topk; ++j) sum += red[j * parts * 4 + threadIdx.x];
     store4(a, t, row0 + 4 * threadIdx.x, sum);
   }
 }
@@ -987,7 +1004,7 @@ hipError_t launch_decode_down(const MatvecArgs& a, hipStream_t s) {
   if (parts > (stages + 1) / 2) parts = (int)((stages + 1) / 2);
   const int waves = sets * parts;
   const dim3 grid((unsigned)((a.n + kTile - 1) / kTile), (unsigned)a.tokens);
-  const size_t lds = (size_t)waves * 3 * 4 * sizeof(f32x4_t);
+  const size_t lds = (size_t)a.topk * (parts * 4 * sizeof(f32x4_t) + 4);
   decode_down_kernel<<<grid, waves * kWave, lds, s>>>(a, parts);
   return hipGetLastError();
 }

@@ -484,3 +484,43 @@ def test_decode_whose_partial_products_leave_the_range(large, T, k, E, H, I, dty
     ref = torch.full((T, H), k * d * float(w2[2][0]), dtype=torch.float64)
     bad = R.outside(y, ref, tol * 2.0 ** -24 * ref.abs())
     assert not bool(bad.any()), f"{int(bad.sum())} of {bad.numel()} outside"
+
+
+# the kernel with the sum, the separate sum with either kernel for FC2, and
+# entries past the sixteenth in each
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,k,E,H,I", [(1, 3, 8, 512, 128), (2, 3, 8, 512, 640), (20, 3, 8, 512, 384),
+                                       (100, 3, 8, 512, 384), (1, 20, 24, 512, 128), (4, 40, 40, 128, 384),
+                                       (6, 20, 24, 512, 128), (40, 20, 24, 512, 384),
+                                       (1, 1024, 1024, 128, 128)])
+def test_decode_adds_whole_entries_in_their_order(T, k, E, H, I, dtype):
+    """y is the sum over j, ascending, of the binary32 results of the entries:
+    with three entries 1, 2^30 - 2^30 (its halves a stage apart in k) and 0 it
+    is 1, with 2^30, 1, ..., -2^30 (more than sixteen entries) it is 0 as 2^30 +
+    1 rounds to 2^30; any other order or grouping gives another sum."""
+    from nvfp4_w4a4_quantized_amd import ops
+    w1, w2 = empty_weights(E, 2 * I, H), empty_weights(E, H, I)
+    far = I - 1 if I > 128 else 1           # another stage of 128, or the same one
+    for c in (0, 16, far):
+        put(w1, c, 0, 6, 0x50)              # gate 32: silu(32) = 32
+        put(w1, I + c, 0, 2)                # up 1
+    x = torch.zeros((T, H))
+    x[:, 0] = 1.0
+    big = w2[2]
+    if k == 3:
+        w2[0][0, :, 0] = 2                                       # expert 0: D[0]
+        w2[0][1, :, 0] = 2                                       # expert 1: D[0] - D[far]
+        w2[0][1, :, far // 2] |= 10 << (4 * (far % 2))
+        big[0], big[1] = 2.0 ** -4, 2.0 ** 26
+        want = 1.0
+    else:
+        w2[0][0, :, 0] = 2                                       # 2^30 from entry 0
+        w2[0][1, :, 0] = 2                                       # 1 from entry 1
+        w2[0][16, :, 0] = 10                                     # -2^30 from entry 16
+        big[0], big[1], big[16] = 2.0 ** 26, 2.0 ** -4, 2.0 ** 26
+        want = 0.0
+    ids = torch.arange(k, dtype=torch.int32).expand(T, k).contiguous()
+    say("decode, order of the sum", T, k, E, H, I, dtype)
+    y = ops.moe_expert_decode(x.to(dtype).cuda(), ids.cuda(), torch.full((T, k), 0.5).cuda(), E, I,
+                              held(*w1, True), held(*w2, True))
+    assert torch.equal(y.cpu().double(), torch.full((T, H), want, dtype=torch.float64))
