@@ -515,12 +515,24 @@ int moe_expert_backward(const uint16_t* dy, const uint16_t* x, int64_t tokens, i
  * in binary32.  Logits of -inf mask an expert; a row that holds a NaN or
  * +inf logit gets NaN weights (the ids stay valid).
  *   logits     [tokens, ld_logits], dtype code; bias nullable float
- *              [num_experts], finite or -inf (masks the expert)
+ *              [num_experts], finite or -inf (masks the expert).  It shifts the
+ *              logit, whatever the score: a correction of the scores themselves,
+ *              as load balancing without an auxiliary loss learns it, is
+ *              moe_router_score_bias's.
  *   topk_idx   out int32 [tokens, topk];  topk_prob out float [tokens, topk]
  * Limits: 1 <= topk <= num_experts <= 1024; tokens * topk < 2^31; scale finite.
  *
+ * moe_router_score_bias -- the same with the choice by the corrected score:
+ *   key[t, e]  = fl32(s[t, e] + score_bias[e]),  s the binary32 score before any
+ *                renormalization: softmax over all experts, or sigmoid
+ * and -inf where the logit is -inf.  score_bias [num_experts] (not NULL), finite
+ * or -inf.  The score is within (6 max |l| + num_experts + 16) 2^-24 of its value,
+ * relative, and may be zero below 2^-126; keys that come closer to each other
+ * may be in either order (equal logits with equal biases are ties).
+ *
  * moe_router_backward -- the logits' gradient from the weights' (dprob, e.g.
- * moe_expert_backward's), with q = w above, dw = scale * dprob, S the picks:
+ * moe_expert_backward's), for both forms of the choice, with q = w above, dw =
+ * scale * dprob, S the picks:
  *     score 0, renormalize 0: dl_e = [e in S] q_e dw_e - P_e sum_S q dw,
  *                             P the softmax over all experts
  *     score 0, renormalize 1: dl_j = q_j (dw_j - sum_S q dw), 0 outside S
@@ -534,6 +546,10 @@ int moe_expert_backward(const uint16_t* dy, const uint16_t* x, int64_t tokens, i
 int moe_router(const void* logits, int dtype, int64_t tokens, int32_t num_experts,
                int64_t ld_logits, const float* bias, int32_t topk, int score, int renormalize,
                float scale, int32_t* topk_idx, float* topk_prob, void* stream);
+int moe_router_score_bias(const void* logits, int dtype, int64_t tokens, int32_t num_experts,
+                          int64_t ld_logits, const float* score_bias, int32_t topk, int score,
+                          int renormalize, float scale, int32_t* topk_idx, float* topk_prob,
+                          void* stream);
 int moe_router_backward(const void* logits, int dtype, int64_t tokens, int32_t num_experts,
                         int64_t ld_logits, const int32_t* topk_idx, const float* dprob,
                         int32_t topk, int score, int renormalize, float scale, void* dlogits,

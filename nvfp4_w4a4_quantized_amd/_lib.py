@@ -121,6 +121,8 @@ def _load(path):
     L.moe_router.restype = C.c_int
     L.moe_router.argtypes = [_vp, C.c_int, _i64, _i32, _i64, _vp, _i32, C.c_int, C.c_int,
                              C.c_float, _vp, _vp, _vp]
+    L.moe_router_score_bias.restype = C.c_int
+    L.moe_router_score_bias.argtypes = L.moe_router.argtypes
     L.moe_router_backward.restype = C.c_int
     L.moe_router_backward.argtypes = [_vp, C.c_int, _i64, _i32, _i64, _vp, _vp, _i32, C.c_int,
                                       C.c_int, C.c_float, _vp, _vp]

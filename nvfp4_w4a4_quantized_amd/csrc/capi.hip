@@ -632,18 +632,35 @@ static int router_args_status(const void* logits, int dtype, int64_t tokens, int
   return NVFP4_OK;
 }
 
-int moe_router(const void* logits, int dtype, int64_t tokens, int32_t num_experts,
-               int64_t ld_logits, const float* bias, int32_t topk, int score, int renormalize,
-               float scale, int32_t* topk_idx, float* topk_prob, void* stream) {
+static int router_call(const void* logits, int dtype, int64_t tokens, int32_t num_experts,
+                       int64_t ld_logits, const float* bias, int bias_on_score, int32_t topk,
+                       int score, int renormalize, float scale, int32_t* topk_idx,
+                       float* topk_prob, void* stream) {
   const int st = router_args_status(logits, dtype, tokens, num_experts, ld_logits, topk, score,
                                     renormalize, scale);
   if (st != NVFP4_OK) return st;
   if (tokens > 0 && (!topk_idx || !topk_prob)) return NVFP4_INVALID_ARGUMENT;
   if (!aligned(bias, 4) || !aligned(topk_idx, 4) || !aligned(topk_prob, 4))
     return NVFP4_INVALID_ARGUMENT;
-  RouterArgs a{logits, dtype, tokens, num_experts, ld_logits, bias,
+  RouterArgs a{logits, dtype, tokens, num_experts, ld_logits, bias, bias_on_score,
                topk,   score, renormalize, scale, topk_idx, topk_prob};
   return hip_status(launch_router(a, static_cast<hipStream_t>(stream)));
+}
+
+int moe_router(const void* logits, int dtype, int64_t tokens, int32_t num_experts,
+               int64_t ld_logits, const float* bias, int32_t topk, int score, int renormalize,
+               float scale, int32_t* topk_idx, float* topk_prob, void* stream) {
+  return router_call(logits, dtype, tokens, num_experts, ld_logits, bias, 0, topk, score,
+                     renormalize, scale, topk_idx, topk_prob, stream);
+}
+
+int moe_router_score_bias(const void* logits, int dtype, int64_t tokens, int32_t num_experts,
+                          int64_t ld_logits, const float* score_bias, int32_t topk, int score,
+                          int renormalize, float scale, int32_t* topk_idx, float* topk_prob,
+                          void* stream) {
+  if (!score_bias) return NVFP4_INVALID_ARGUMENT;
+  return router_call(logits, dtype, tokens, num_experts, ld_logits, score_bias, 1, topk, score,
+                     renormalize, scale, topk_idx, topk_prob, stream);
 }
 
 int moe_router_backward(const void* logits, int dtype, int64_t tokens, int32_t num_experts,

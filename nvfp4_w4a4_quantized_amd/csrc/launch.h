@@ -197,7 +197,8 @@ hipError_t launch_combine(const void* y_rows, int y_rows_dtype, const int32_t* d
 // ---- router.hip ----
 struct RouterArgs {
   const void* logits; int dtype; int64_t tokens; int32_t num_experts; int64_t ld;
-  const float* bias;          // nullable [num_experts], added for the choice only
+  const float* bias;          // nullable [num_experts], added for the choice only:
+  int bias_on_score;          // to the score (1) or to the logit (0)
   int32_t topk; int score; int renormalize; float scale;
   int32_t* topk_idx; float* topk_prob;
 };

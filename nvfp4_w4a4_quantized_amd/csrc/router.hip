@@ -2,7 +2,9 @@
 //
 // For a token's logits l over E experts (and an optional bias b that counts
 // for the choice alone):
-//   key_e = fl32(l_e + b_e); the k largest keys are picked, ties to the lower
+//   key_e = fl32(l_e + b_e), or, with the bias on the score, fl32(s_e + b_e) where
+//   s is the softmax over all experts or the sigmoid (the two rank differently:
+//   the score saturates); the k largest keys are picked, ties to the lower
 //   expert id; an expert whose key is -inf (masked) is never picked, so a
 //   token may have fewer than k picks (expert id -1, weight 0);
 //   softmax score: w_j = exp(l_j) / sum over all experts, or, renormalised,
@@ -174,7 +176,9 @@ __device__ __forceinline__ void wave_lds_fence() {
 
 }  // namespace
 
-template <int DT, int L, int V>
+// SCORE_BIAS: a.bias is added to the scores (in a kernel of its own: the scores
+// beside the logits take 12 to 28 registers, a wave per SIMD at 16 a lane).
+template <int DT, int L, int V, bool SCORE_BIAS>
 __global__ __launch_bounds__(kRouterThreads) void router_kernel(RouterArgs a) {
   extern __shared__ char lds[];
   constexpr int kGroups = kRouterThreads / L;
@@ -194,9 +198,18 @@ __global__ __launch_bounds__(kRouterThreads) void router_kernel(RouterArgs a) {
 #pragma unroll
     for (int i = 0; i < V; ++i) bad = bad || !(v[i] < __builtin_huge_valf());
     float mx = 0.0f, sum = 0.0f;
-    if (a.score == 0 && !a.renormalize) {
+    if (a.score == 0 && (!a.renormalize || SCORE_BIAS)) {
       float p[V];
       row_softmax<L, V>(v, p, &mx, &sum);
+      if (SCORE_BIAS) {
+        const float inv = 1.0f / sum;
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = v[i] > kNegInf ? p[i] * inv : kNegInf;
+      }
+    }
+    if (a.score == 1 && SCORE_BIAS) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = v[i] > kNegInf ? sigmoid(v[i]) : kNegInf;
     }
     if (a.bias) {
 #pragma unroll
@@ -379,36 +392,47 @@ RouterShape router_shape(int64_t tokens, int32_t experts, int32_t topk) {
 
 }  // namespace
 
-#define NVFP4_ROUTER_CASE(KERNEL, L, V)                                               \
-  case L * 100 + V:                                                                   \
-    if (a.dtype == 0) KERNEL<0, L, V><<<sh.blocks, kRouterThreads, sh.lds, s>>>(a);   \
-    else if (a.dtype == 1) KERNEL<1, L, V><<<sh.blocks, kRouterThreads, sh.lds, s>>>(a); \
-    else KERNEL<2, L, V><<<sh.blocks, kRouterThreads, sh.lds, s>>>(a);                \
+// LAUNCH(dtype, lanes, per lane) for the call's shape
+#define NVFP4_ROUTER_CASE(LAUNCH, L, V)        \
+  case L * 100 + V:                            \
+    if (a.dtype == 0) LAUNCH(0, L, V);         \
+    else if (a.dtype == 1) LAUNCH(1, L, V);    \
+    else LAUNCH(2, L, V);                      \
     break;
-#define NVFP4_ROUTER_CASES(KERNEL)                                                    \
-  do {                                                                                \
-    const RouterShape sh = router_shape(a.tokens, a.num_experts, a.topk);             \
-    switch (sh.lanes * 100 + sh.per_lane) {                                           \
-      NVFP4_ROUTER_CASE(KERNEL, 16, 1)                                                \
-      NVFP4_ROUTER_CASE(KERNEL, 16, 4)                                                \
-      NVFP4_ROUTER_CASE(KERNEL, 16, 8)                                                \
-      NVFP4_ROUTER_CASE(KERNEL, 16, 16)                                               \
-      NVFP4_ROUTER_CASE(KERNEL, 16, 32)                                               \
-      NVFP4_ROUTER_CASE(KERNEL, 64, 4)                                                \
-      NVFP4_ROUTER_CASE(KERNEL, 64, 8)                                                \
-      NVFP4_ROUTER_CASE(KERNEL, 64, 16)                                               \
-    }                                                                                 \
+#define NVFP4_ROUTER_CASES(LAUNCH)                                        \
+  do {                                                                    \
+    const RouterShape sh = router_shape(a.tokens, a.num_experts, a.topk); \
+    switch (sh.lanes * 100 + sh.per_lane) {                               \
+      NVFP4_ROUTER_CASE(LAUNCH, 16, 1)                                    \
+      NVFP4_ROUTER_CASE(LAUNCH, 16, 4)                                    \
+      NVFP4_ROUTER_CASE(LAUNCH, 16, 8)                                    \
+      NVFP4_ROUTER_CASE(LAUNCH, 16, 16)                                   \
+      NVFP4_ROUTER_CASE(LAUNCH, 16, 32)                                   \
+      NVFP4_ROUTER_CASE(LAUNCH, 64, 4)                                    \
+      NVFP4_ROUTER_CASE(LAUNCH, 64, 8)                                    \
+      NVFP4_ROUTER_CASE(LAUNCH, 64, 16)                                   \
+    }                                                                     \
   } while (0)
 
 hipError_t launch_router(const RouterArgs& a, hipStream_t s) {
   if (a.tokens == 0) return hipSuccess;
-  NVFP4_ROUTER_CASES(router_kernel);
+#define NVFP4_ROUTER(D, L, V) \
+  router_kernel<D, L, V, false><<<sh.blocks, kRouterThreads, sh.lds, s>>>(a)
+#define NVFP4_ROUTER_SCORE_BIAS(D, L, V) \
+  router_kernel<D, L, V, true><<<sh.blocks, kRouterThreads, sh.lds, s>>>(a)
+  if (a.bias_on_score) NVFP4_ROUTER_CASES(NVFP4_ROUTER_SCORE_BIAS);
+  else NVFP4_ROUTER_CASES(NVFP4_ROUTER);
+#undef NVFP4_ROUTER_SCORE_BIAS
+#undef NVFP4_ROUTER
   return hipGetLastError();
 }
 
 hipError_t launch_router_backward(const RouterBackwardArgs& a, hipStream_t s) {
   if (a.tokens == 0) return hipSuccess;
-  NVFP4_ROUTER_CASES(router_backward_kernel);
+#define NVFP4_ROUTER_BACKWARD(D, L, V) \
+  router_backward_kernel<D, L, V><<<sh.blocks, kRouterThreads, sh.lds, s>>>(a)
+  NVFP4_ROUTER_CASES(NVFP4_ROUTER_BACKWARD);
+#undef NVFP4_ROUTER_BACKWARD
   return hipGetLastError();
 }
 

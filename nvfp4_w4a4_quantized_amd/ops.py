@@ -570,24 +570,32 @@ def _call(dev, what, *args):
 
 
 def moe_router(logits, topk: int, bias=None, score: int = 0, renormalize: bool = True,
-               scale: float = 1.0):
+               scale: float = 1.0, score_bias=None):
     """The top-k experts of every token and their weights, from router logits
     [T, E] (float32, bf16 or fp16).  Returns (topk_idx int32 [T, k], topk_prob
     float32 [T, k]), the arguments of moe_permute and the expert layers.
     score 0: softmax over all experts, 1: sigmoid; renormalize: divided by the
-    picks' sum; scale multiplies the weights.  bias float32 [E] is added for
-    the choice alone.  Experts whose logit is -inf are never picked; a token
-    with fewer than k left gets ids -1 with weight 0."""
+    picks' sum; scale multiplies the weights.  For the choice alone, bias
+    float32 [E] is added to the logits, or score_bias float32 [E] to the scores
+    (softmax or sigmoid over all experts, as a learned load-balancing correction
+    is); not both.  Experts whose logit is -inf are never picked; a token with
+    fewer than k left gets ids -1 with weight 0."""
     ld = _need_rows(logits, "logits")
     T, E = logits.shape
     dev = logits.get_device()
     if bias is not None:
         _dense(bias, torch.float32, (E,), dev, "bias")
+    what = "moe_router"
+    if score_bias is not None:
+        if bias is not None:
+            raise ValueError("moe_router: either bias or score_bias")
+        _dense(score_bias, torch.float32, (E,), dev, "score_bias")
+        what, bias = "moe_router_score_bias", score_bias
     if not 1 <= topk <= E:
         raise NvFp4Error(f"moe_router: topk {topk} of {E} experts")
     idx = logits.new_empty((T, topk), dtype=torch.int32)
     prob = logits.new_empty((T, topk), dtype=torch.float32)
-    _call(dev, "moe_router", logits.data_ptr(), _DTYPE_CODE[logits.dtype], T, E, ld, _addr(bias),
+    _call(dev, what, logits.data_ptr(), _DTYPE_CODE[logits.dtype], T, E, ld, _addr(bias),
           topk, score, int(bool(renormalize)), scale, idx.data_ptr(), prob.data_ptr())
     return idx, prob
 

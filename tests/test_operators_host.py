@@ -127,3 +127,11 @@ def test_python_checks():
         ops.moe_router([1.0], 1)
     with pytest.raises(TypeError):
         ops.nvfp4_matvec(x, x)
+
+
+def test_router_score_bias(L):
+    # logits, dtype, tokens, experts, ld, score bias, topk, score, renorm, scale, idx, prob, stream
+    good = [F, 1, 4, 60, 60, F, 6, 1, 1, 1.0, F, F, None]
+    for i, v in ((0, None), (0, ODD), (1, 3), (2, -1), (3, 0), (3, 1025), (4, 59), (5, None), (5, ODD),
+                 (6, 0), (6, 61), (7, 2), (8, 2), (9, NAN), (10, None), (11, ODD), (2, 1 << 40)):
+        assert L.moe_router_score_bias(*change(good, i, v)) == INVALID, (i, v)
