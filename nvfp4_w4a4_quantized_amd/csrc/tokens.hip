@@ -31,8 +31,14 @@ constexpr int kBatch = 8;   // entries whose rows are in flight together
 // Sums of n <= kBatch values over the workgroup: thread j < n gets the j-th.
 // (Every thread adding up every sum took 14.4 us instead of 10.9 for the gradient
 // of a sort of 64 tokens of 7168, top-8, whose workgroups have 14 waves.)
+// The thread's number is made opaque, so that its lane, addresses and comparisons
+// are not kept in registers through the columns' loop: the collect then runs five
+// waves a SIMD instead of four (32768 tokens of 512, top-8: 62.6 against 68.5 us;
+// of 500, top-4: 46.2 against 50.6).
 __device__ __forceinline__ float block_sums(const float (&v)[kBatch], int n, float* lds) {
-  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  int tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));
+  const int lane = tid % kWave, wave = tid / kWave;
   const int waves = blockDim.x / kWave;
   int own = 0;
 #pragma unroll
@@ -51,9 +57,9 @@ __device__ __forceinline__ float block_sums(const float (&v)[kBatch], int n, flo
   __syncthreads();   // the previous batch's sums have been read
   if (lane < kBatch) lds[wave * kBatch + lane] = sum;
   __syncthreads();
-  if ((int)threadIdx.x < n) {
-    sum = lds[threadIdx.x];
-    for (int w = 1; w < waves; ++w) sum += lds[w * kBatch + threadIdx.x];
+  if (tid < n) {
+    sum = lds[tid];
+    for (int w = 1; w < waves; ++w) sum += lds[w * kBatch + tid];
   }
   return sum;
 }
