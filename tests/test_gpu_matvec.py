@@ -524,3 +524,79 @@ def test_decode_adds_whole_entries_in_their_order(T, k, E, H, I, dtype):
     y = ops.moe_expert_decode(x.to(dtype).cuda(), ids.cuda(), torch.full((T, k), 0.5).cuda(), E, I,
                               held(*w1, True), held(*w2, True))
     assert torch.equal(y.cpu().double(), torch.full((T, H), want, dtype=torch.float64))
+
+
+def shifted(t, by):
+    """t on the device, `by` elements behind an aligned address."""
+    flat = torch.zeros(t.numel() + 16, dtype=t.dtype, device="cuda")
+    flat[by:by + t.numel()] = t.reshape(-1).cuda()
+    return flat[by:by + t.numel()].view(t.shape)
+
+
+def strided(x, left, right):
+    """The rows of x inside rows of NaN: odd addresses and row distances."""
+    wide = torch.full((x.shape[0], left + x.shape[1] + right), float("nan"), dtype=x.dtype, device="cuda")
+    wide[:, left:left + x.shape[1]] = x.cuda()
+    return wide[:, left:left + x.shape[1]]
+
+
+# the direct kernel (a slot per entry, a slot per expert) and the kernel that
+# shares x through LDS in its four shapes (16 or 32 columns, one group or two)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,k,E,n,K", [(2, 3, 8, 70, 208), (20, 3, 8, 70, 208), (60, 6, 50, 2049, 144),
+                                       (60, 6, 50, 600, 528), (300, 4, 12, 4100, 144), (128, 4, 16, 500, 400)])
+def test_expert_matvec_of_strided_rows_and_odd_addresses(T, k, E, n, K, dtype):
+    from nvfp4_w4a4_quantized_amd import ops
+    from nvfp4_w4a4_quantized_amd.ops import NvFp4Weights
+    rng = np.random.default_rng(T + n + K)
+    codes, scales, gs = R.make_weights(rng, E, n, K)
+    ids = make_ids(rng, T, k, E, "dropped").cuda()
+    x = torch.from_numpy(rng.standard_normal((T, K)).astype(np.float32)).to(dtype)
+    say("expert_matvec, strides", T, k, E, n, K, dtype)
+    want = ops.nvfp4_expert_matvec(x.cuda(), ids, held(codes, scales, gs, False))
+    odd = NvFp4Weights(shifted(codes, 3), shifted(scales, 1), shifted(gs, 1))
+    out = shifted(torch.zeros((T, k, n), dtype=dtype), 1)
+    assert torch.equal(ops.nvfp4_expert_matvec(strided(x, 5, 8), ids, odd, out=out), want)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,k,E,H,I", [(3, 2, 8, 512, 384), (20, 2, 8, 512, 384), (100, 2, 8, 512, 384),
+                                       (200, 4, 40, 640, 512)])
+def test_decode_of_strided_rows_and_either_layout(T, k, E, H, I, dtype):
+    """Rows at odd addresses, each projection in either layout, row-major weights
+    at odd addresses: the bits of the plain call."""
+    from nvfp4_w4a4_quantized_amd import ops
+    from nvfp4_w4a4_quantized_amd.ops import NvFp4Weights
+    rng = np.random.default_rng(T + H + I)
+    w1, w2 = R.make_weights(rng, E, 2 * I, H, std=0.1), R.make_weights(rng, E, H, I, std=0.1)
+    ids = make_ids(rng, T, k, E, "dropped").cuda()
+    prob = torch.from_numpy(rng.random((T, k)).astype(np.float32)).cuda()
+    x = torch.from_numpy(rng.standard_normal((T, H)).astype(np.float32)).to(dtype)
+    say("decode, strides and layouts", T, k, E, H, I, dtype)
+    want = ops.moe_expert_decode(x.cuda(), ids, prob, E, I, held(*w1, False), held(*w2, False))
+
+    def odd(w):
+        return NvFp4Weights(shifted(w[0], 3), shifted(w[1], 1), shifted(w[2], 1))
+    for a, b in ((held(*w1, True), held(*w2, False)), (held(*w1, False), held(*w2, True)),
+                 (odd(w1), odd(w2)), (held(*w1, True), odd(w2))):
+        y = ops.moe_expert_decode(strided(x, 3, 8), ids, prob, E, I, a, b,
+                                  y=shifted(torch.zeros((T, H), dtype=dtype), 1))
+        assert torch.equal(y, want)
+
+
+def test_weights_beyond_four_gigabytes_through_lds():
+    """As many entries of the last of 40 experts of 134 MB as take the kernel
+    that shares x through LDS, against that expert alone."""
+    from nvfp4_w4a4_quantized_amd import ops
+    from nvfp4_w4a4_quantized_amd.ops import NvFp4Weights
+    E, n, k = 40, 16384, 16384
+    codes = torch.randint(0, 256, (E, n, k // 2), dtype=torch.uint8, device="cuda")
+    scales = torch.randint(40, 60, (E, n, k // 16), dtype=torch.uint8, device="cuda")
+    gs = torch.full((E,), 0.01, device="cuda")
+    w, last = NvFp4Weights(codes, scales, gs), NvFp4Weights(codes[E - 1:], scales[E - 1:], gs[E - 1:])
+    x = torch.randn((8, k), device="cuda").bfloat16()
+    ids = torch.full((8, 1), E - 1, dtype=torch.int32, device="cuda")
+    say("weights beyond 4 GB, LDS kernel")
+    y = ops.nvfp4_expert_matvec(x, ids, w, out_dtype=torch.float32)
+    z = ops.nvfp4_matvec(x, last, out_dtype=torch.float32)
+    assert float((y[:, 0] - z).norm() / z.norm()) < 1e-5
