@@ -937,19 +937,38 @@ static void launch_matvec_one(const MatvecArgs& a, hipStream_t s) {
   const int64_t xbytes = ((xrows - 1) * a.ld_x + a.k) * (XT == 0 ? 4 : 2) + 2 * (a.x_plane * 2);
   if (a.k >= 32 && xbytes < kNone && rows_kernel_pays(a, EXPERT)) {
     if constexpr (EXPERT) {
-      // the entries of an expert scatter about their mean: room for twice as many
-      const bool one = 2 * entries <= 16 * a.num_groups;
+      const auto workgroups = [&](int64_t per, int64_t cols) {
+        return experts_met(a) * ((a.n + per - 1) / per) * column_blocks(a, cols);
+      };
+      // the entries of an expert scatter about their mean: room for twice as many.
+      // D's planes take less room and time with 16 columns, which costs more where
+      // the experts with more of them, whose weights are read twice, are many
+      // (FC2 in three parts, whole layer, 16 / 32 columns: hidden 1024, intermediate
+      // 512, top-4 of 16: 96 tokens 27.5 / 30.2 us, 256 tokens 33.0 / 34.1; 2048 and
+      // 768: top-2 of 8, 256 tokens 39.4 / 41.4; top-8 of 64, 128 tokens, 2048
+      // workgroups, 71.9 / 66.8)
+      const bool one = 2 * entries <= 16 * a.num_groups ||
+                       (XT == kPlanes && workgroups(128, 16) <= 1024);
       // 64-row workgroups whose groups share k while those are at most two a CU,
       // or one where the LDS holds no second (three parts of 32 columns: 128 tokens,
       // top-4 of 16 experts of [1024, 1024], binary32, 512 of them 24.3 us, half as
       // many 128-row workgroups 17.0)
       const int64_t most = !one && parts_of(XT) == 3 ? 256 : 512;
-      const bool few = experts_met(a) * ((a.n + 63) / 64) * column_blocks(a, one ? 16 : 32) <= most;
+      const bool few = workgroups(64, one ? 16 : 32) <= most;
       static_assert(parts_of(XT) != 3 || 4 * RowsShape<XT, 2, 2, 2>::kBuffer > 160 * 1024, "see `most`");
-      if (one && few) launch_rows<XT, 1, 2, 2, SWIGLU, true>(a, s);
-      else if (one) launch_rows<XT, 1, 4, 1, SWIGLU, true>(a, s);
-      else if (few) launch_rows<XT, 2, 2, 2, SWIGLU, true>(a, s);
-      else launch_rows<XT, 2, 4, 1, SWIGLU, true>(a, s);
+      if (one && few) return launch_rows<XT, 1, 2, 2, SWIGLU, true>(a, s);
+      if (one) return launch_rows<XT, 1, 4, 1, SWIGLU, true>(a, s);
+      if (few) return launch_rows<XT, 2, 2, 2, SWIGLU, true>(a, s);
+      // 32 columns of D's planes leave the LDS room for three workgroups a CU: eight
+      // waves that share them instead of four where two of those fill every CU
+      // (whole layer, 8 / 4 waves: 256 tokens, top-8 of 128, 2048 and 768, 1024
+      // workgroups, 111 / 116 us; 512 tokens 186 / 209; 128 tokens, top-8 of 32, 512
+      // workgroups, 58.3 / 61.8; 200 tokens, top-4 of 60, 1040 and 400, 300
+      // workgroups, 39.4 / 38.0)
+      if constexpr (XT == kPlanes) {
+        if (workgroups(256, 32) >= 512) return launch_rows<XT, 2, 8, 1, SWIGLU, true>(a, s);
+      }
+      return launch_rows<XT, 2, 4, 1, SWIGLU, true>(a, s);
     } else {
       // as many columns a workgroup as leave one for every CU
       const auto fills = [&](int64_t cols) {
