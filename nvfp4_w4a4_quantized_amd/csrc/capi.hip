@@ -881,7 +881,7 @@ int moe_expert_decode(const void* x, int x_dtype, int64_t tokens, int64_t hidden
   if (launch_matvec(f1, s) != hipSuccess) return NVFP4_HIP_ERROR;
   MatvecArgs f2 = matvec_args(L.d, 1, inter, tokens, w2, num_experts, hidden, inter);
   f2.x_plane = f1.d_plane; f2.x_by_entry = 1; f2.topk_idx = topk_idx; f2.topk = topk;
-  if (decode_down_fits(tokens)) {
+  if (decode_down_fits(tokens, topk, num_experts)) {
     f2.out = y; f2.out_dtype = x_dtype;
     return hip_status(launch_decode_down(f2, s));
   }

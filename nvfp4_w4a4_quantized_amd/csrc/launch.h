@@ -250,7 +250,7 @@ struct MatvecArgs {
 hipError_t launch_matvec(const MatvecArgs& a, hipStream_t s);
 // FC2 and the sum over a token's experts in one launch, for a few tokens (a.x
 // the layer's D in its planes, a.out the tokens' rows).
-bool decode_down_fits(int64_t tokens);
+bool decode_down_fits(int64_t tokens, int32_t topk, int32_t num_experts);
 hipError_t launch_decode_down(const MatvecArgs& a, hipStream_t s);
 hipError_t launch_decode_combine(const float* y_rows, const int32_t* idx, int64_t tokens,
                                  int32_t topk, int32_t num_experts, int64_t hidden, int y_dtype,

@@ -1009,11 +1009,17 @@ hipError_t launch_matvec(const MatvecArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Measured (the whole layer, separate / fused sum): top-8 of 128, hidden 2048,
-// intermediate 768: 1 token 18.2 / 16.2 us, 4 tokens 36.9 / 33.7, 8 tokens
-// 64.2 / 64.6; top-4 of 16, hidden 1024, intermediate 512: 4 tokens 13.4 / 11.1,
-// 8 tokens 14.4 / 12.9, 16 tokens 15.2 / 16.8; top-2 of 8: 8 tokens 16.5 / 18.2.
-bool decode_down_fits(int64_t tokens) { return tokens <= 4; }
+// It reads an expert's weights for every entry, so beyond four tokens it needs
+// entries that seldom share one.  Measured (the whole layer, separate / fused sum,
+// hidden 2048, intermediate 768 but where said): top-8 of 128: 5 tokens 48.2 / 41.2
+// us, 8 tokens 61.4 / 58.9, 12 tokens 66.2 / 70.9; top-4 of 32: 5 tokens 27.1 / 25.2,
+// 8 tokens 30.4 / 31.0, 12 tokens 32.2 / 38.5; top-4 of 16, 1024 and 512: 8 tokens
+// 15.4 / 12.7, 12 tokens 15.8 / 15.3; top-2 of 8: 8 tokens 17.4 / 16.9, 12 tokens
+// 18.4 / 20.1; top-8 of 16 (2.5 entries an expert): 5 tokens 26.7 / 27.6, 8 tokens
+// 28.2 / 33.7.
+bool decode_down_fits(int64_t tokens, int32_t topk, int32_t num_experts) {
+  return tokens <= 4 || (tokens <= 8 && tokens * topk <= 2 * (int64_t)num_experts);
+}
 
 hipError_t launch_decode_down(const MatvecArgs& a, hipStream_t s) {
   if (a.tokens == 0) return hipSuccess;

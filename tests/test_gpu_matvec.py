@@ -365,8 +365,9 @@ def put(w, row, col, code, scale=0x38):
 
 
 # sizes of the layer that reach, for FC2: the kernel with the sum (up to four
-# tokens), the direct kernel, and the kernel that shares D through LDS
-REACH = [(1, 2, 8, 512, 128), (4, 2, 8, 512, 384), (20, 2, 8, 512, 128), (100, 2, 8, 512, 128)]
+# tokens, up to eight), the direct kernel, and the kernel that shares D through LDS
+REACH = [(1, 2, 8, 512, 128), (4, 2, 8, 512, 384), (8, 2, 8, 512, 128), (20, 2, 8, 512, 128),
+         (100, 2, 8, 512, 128)]
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
@@ -489,7 +490,8 @@ def test_decode_whose_partial_products_leave_the_range(large, T, k, E, H, I, dty
 # the kernel with the sum, the separate sum with either kernel for FC2, and
 # entries past the sixteenth in each
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("T,k,E,H,I", [(1, 3, 8, 512, 128), (2, 3, 8, 512, 640), (20, 3, 8, 512, 384),
+@pytest.mark.parametrize("T,k,E,H,I", [(1, 3, 8, 512, 128), (2, 3, 8, 512, 640), (5, 3, 8, 512, 384),
+                                       (6, 3, 8, 512, 384), (20, 3, 8, 512, 384),
                                        (100, 3, 8, 512, 384), (1, 20, 24, 512, 128), (4, 40, 40, 128, 384),
                                        (6, 20, 24, 512, 128), (40, 20, 24, 512, 384),
                                        (1, 1024, 1024, 128, 128)])
