@@ -268,7 +268,7 @@ __device__ __forceinline__ float weighted_swiglu(float g, float u, float p) {
   constexpr double kLn2 = 0.69314718055994530942;
   constexpr float kHigh = (float)kLn2, kLow = (float)(kLn2 - kHigh);
   const bool tail = g < -80.0f && g >= -__FLT_MAX__;
-  const float gt = fmaxf(g, -700.0f), n = rintf(gt * (float)(1.0 / kLn2));
+  const float gt = __builtin_amdgcn_fmed3f(g, -700.0f, 0.0f), n = rintf(gt * (float)(1.0 / kLn2));
   const float f = fmaf(-n, kLow, fmaf(-n, kHigh, gt));
   const float e = expf(tail ? f : -g);
   const double s = tail ? ldexp((double)gt * e, (int)n) : (double)(g / (1.0f + e));
