@@ -548,10 +548,11 @@ __global__ __launch_bounds__(1024) void decode_down_kernel(MatvecArgs a, int par
 //
 // What bounds it: with 1-2 columns of 16, the weights' stream (FC1 of 256
 // tokens 54 us, 226 MB at 4.2 TB/s; FC2 47 us, where D's three planes, which
-// eight row blocks read each, and the rows come on top of 113 MB).  With 64 columns the compute side shows: a copy without any
-// global traffic took 40 of the 56-65 us (decode, products and LDS reads at two
-// waves a SIMD), and row-major weights add the block scales' scattered 2-byte
-// loads (54 us without them); the tiled layout is the faster one.
+// eight row blocks read each, and the rows come on top of 113 MB).  With 64
+// columns the compute side shows: a copy without any global traffic took 40 of
+// the 56-65 us (decode, products and LDS reads at two waves a SIMD), and
+// row-major weights add the block scales' scattered 2-byte loads (54 us without
+// them); the tiled layout is the faster one.
 //
 // The last stage of a k that is no multiple of 128 (row-major weights):
 // lanes take the window [min(k0, k - 32), + 32) instead of [k0, + 32), and x
