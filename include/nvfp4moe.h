@@ -652,6 +652,61 @@ int moe_expert_decode(const void* x, int x_dtype, int64_t tokens, int64_t hidden
                       void* y, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
+ * Low-rank adapters of many requests beside a shared projection, on unquantized
+ * tensors.  Token t uses adapter s = ids[t]; an id outside [0, adapters) is a
+ * token without one (h, g zero).
+ *   lora_forward      h[t] = A[s] x[t]
+ *                     out[t] = base[t] + scale[s] B[s] h[t]
+ *   lora_backward     g[t] = scale[s] B[s]^T dy[t]
+ *                     dx[t] = base[t] + A[s]^T g[t]
+ *                     da[s] = sum over s's tokens of g[t] x[t]^T
+ *                     db[s] = sum over s's tokens of scale[s] dy[t] h[t]^T
+ *   nvfp4_lora_matvec out[t] = W x[t] + scale[s] B[s] h[t]   (nvfp4_matvec's W)
+ * base NULL: nothing is added (zeros).  scale NULL: all ones.  h, g and every sum
+ * are binary32 and each output is rounded once; results are bitwise
+ * reproducible.  The order of the sums goes by the call's sizes: a row's last
+ * bits may differ between calls with other numbers of tokens.  16-bit inputs
+ * below 2^-126 (bf16) may count as zero.  Infinities and NaN of a token stay in
+ * its own rows and, on the way back, its adapter's gradients.
+ *   x, dy      [tokens, ld], dtype code; a [adapters, rank, k] and b [adapters,
+ *              n, rank] dense, of the same type (adapters of a smaller rank hold
+ *              zeros in the rest)
+ *   ids        int32 [tokens];  scale float [adapters]
+ *   base       [tokens, ld_base] in the output's type; it may be the output itself
+ *              (ld_base == width), and may not overlap it otherwise
+ *   out        [tokens, n], out_dtype;  dx [tokens, k], dtype
+ *   h          float [tokens, rank]: lora_forward's nullable output, and
+ *              lora_backward's input (NULL: computed again from x)
+ *   da, db     float [adapters, rank, k], [adapters, n, rank]: every adapter
+ *              written (zeros for those without tokens)
+ *   workspace  *_workspace_size() bytes, 16-byte aligned; every word read is
+ *              written before by the same call
+ * Limits (NVFP4_UNSUPPORTED beyond): rank <= 256; adapters <= 1024; tokens <=
+ * 2^24; n, k <= 2^18; nvfp4_lora_matvec: tokens <= 65536 and nvfp4_matvec's.
+ * A batch is read fastest when the tokens of a request lie together: beyond 256
+ * tokens, 64 consecutive ones are multiplied adapter by adapter.
+ * ---------------------------------------------------------------------- */
+size_t lora_forward_workspace_size(int64_t tokens, int64_t k, int32_t rank);
+int lora_forward(const void* x, int dtype, int64_t tokens, int64_t k, int64_t ld_x,
+                 const int32_t* ids, const void* a, const void* b, const float* scale,
+                 int32_t adapters, int32_t rank, int64_t n, const void* base, int64_t ld_base,
+                 int out_dtype, void* out, float* h, void* workspace, size_t workspace_bytes,
+                 void* stream);
+size_t lora_backward_workspace_size(int dtype, int64_t tokens, int64_t k, int64_t n,
+                                    int32_t adapters, int32_t rank);
+int lora_backward(const void* dy, int dtype, int64_t tokens, int64_t n, int64_t ld_dy,
+                  const void* x, int64_t k, int64_t ld_x, const int32_t* ids, const void* a,
+                  const void* b, const float* scale, int32_t adapters, int32_t rank, const float* h,
+                  const void* base, int64_t ld_base, void* dx, float* da, float* db,
+                  void* workspace, size_t workspace_bytes, void* stream);
+size_t nvfp4_lora_matvec_workspace_size(int64_t tokens, int64_t n, int64_t k, int32_t rank);
+int nvfp4_lora_matvec(const void* x, int x_dtype, int64_t tokens, int64_t ld_x,
+                      const nvfp4_weights* w, int64_t n, int64_t k, const int32_t* ids,
+                      const void* a, const void* b, const float* scale, int32_t adapters,
+                      int32_t rank, int out_dtype, void* out, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * Profiling helpers: thin wrappers over hipEventCreate / hipEventRecord /
  * hipEventElapsedTime / hipEventDestroy so a caller without HIP headers can
  * time the stages of moe_expert_forward on its stream.  (These allocate a

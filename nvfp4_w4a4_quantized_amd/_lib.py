@@ -149,6 +149,21 @@ def _load(path):
     L.moe_expert_decode.argtypes = [_vp, C.c_int, _i64, _i64, _i64, _i64, _vp, _vp, _i32, _i32,
                                     C.POINTER(Weights), C.POINTER(Weights), _vp, _vp, C.c_size_t,
                                     _vp]
+    L.lora_forward_workspace_size.restype = C.c_size_t
+    L.lora_forward_workspace_size.argtypes = [_i64, _i64, _i32]
+    L.lora_forward.restype = C.c_int
+    L.lora_forward.argtypes = [_vp, C.c_int, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _i32, _i32, _i64,
+                               _vp, _i64, C.c_int, _vp, _vp, _vp, C.c_size_t, _vp]
+    L.lora_backward_workspace_size.restype = C.c_size_t
+    L.lora_backward_workspace_size.argtypes = [C.c_int, _i64, _i64, _i64, _i32, _i32]
+    L.lora_backward.restype = C.c_int
+    L.lora_backward.argtypes = [_vp, C.c_int, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _vp,
+                                _i32, _i32, _vp, _vp, _i64, _vp, _vp, _vp, _vp, C.c_size_t, _vp]
+    L.nvfp4_lora_matvec_workspace_size.restype = C.c_size_t
+    L.nvfp4_lora_matvec_workspace_size.argtypes = [_i64, _i64, _i64, _i32]
+    L.nvfp4_lora_matvec.restype = C.c_int
+    L.nvfp4_lora_matvec.argtypes = [_vp, C.c_int, _i64, _i64, C.POINTER(Weights), _i64, _i64, _vp,
+                                    _vp, _vp, _vp, _i32, _i32, C.c_int, _vp, _vp, C.c_size_t, _vp]
     L.nvfp4_event_create.restype = C.c_int
     L.nvfp4_event_create.argtypes = [C.POINTER(_vp)]
     L.nvfp4_event_record.restype = C.c_int

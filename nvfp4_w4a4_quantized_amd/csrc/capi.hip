@@ -891,6 +891,218 @@ int moe_expert_decode(const void* x, int x_dtype, int64_t tokens, int64_t hidden
                                           x_dtype, y, s));
 }
 
+// ---- low-rank adapters ----
+
+constexpr int64_t kMaxLoraTokens = 1 << 24, kMaxLoraWidth = 1 << 18;
+constexpr int32_t kMaxRank = 256;
+
+// What every adapter call asks of its sizes and adapters.
+static int lora_status(int dtype, int64_t tokens, int64_t k, int64_t n, const int32_t* ids,
+                       const void* a, const void* b, const float* scale, int32_t adapters,
+                       int32_t rank) {
+  if (!valid_dtype(dtype) || tokens < 0 || k < 1 || n < 1 || adapters < 1 || rank < 1)
+    return NVFP4_INVALID_ARGUMENT;
+  if (tokens > kMaxLoraTokens || k > kMaxLoraWidth || n > kMaxLoraWidth ||
+      adapters > kMaxAdapters || rank > kMaxRank)
+    return NVFP4_UNSUPPORTED;
+  const size_t e = dtype_size(dtype);
+  if (!a || !b || !aligned(a, e) || !aligned(b, e) || !aligned(scale, 4) || !aligned(ids, 4) ||
+      (tokens > 0 && !ids))
+    return NVFP4_INVALID_ARGUMENT;
+  return NVFP4_OK;
+}
+
+static bool rows_ok(const void* p, int64_t tokens, int64_t width, int64_t ld, int dtype) {
+  return ld >= width && (p || tokens == 0) && aligned(p, dtype_size(dtype));
+}
+
+static LoraDownArgs lora_down(const void* x, int dtype, int64_t tokens, int64_t k, int64_t ld_x,
+                              const int32_t* ids, const void* a, int32_t adapters, int32_t rank,
+                              float* h) {
+  LoraDownArgs d{};
+  d.x = x; d.dtype = dtype; d.tokens = tokens; d.k = k; d.ld_x = ld_x;
+  d.ids = ids; d.adapters = adapters; d.rank = rank; d.a = a; d.h = h;
+  return d;
+}
+
+static LoraUpArgs lora_up(const float* h, int shares, int64_t tokens, int64_t n, const int32_t* ids,
+                          const void* b, int dtype, const float* scale, int32_t adapters,
+                          int32_t rank, const void* base, int base_dtype, int64_t ld_base, void* out,
+                          int out_dtype) {
+  LoraUpArgs u{};
+  u.h = h; u.shares = shares; u.tokens = tokens; u.n = n;
+  u.ids = ids; u.adapters = adapters; u.rank = rank; u.b = b; u.dtype = dtype; u.scale = scale;
+  u.base = base; u.base_dtype = base_dtype; u.ld_base = ld_base; u.out = out; u.out_dtype = out_dtype;
+  return u;
+}
+
+size_t lora_forward_workspace_size(int64_t tokens, int64_t k, int32_t rank) {
+  if (tokens < 0 || tokens > kMaxLoraTokens || k < 1 || k > kMaxLoraWidth || rank < 1 ||
+      rank > kMaxRank)
+    return 0;
+  Carver c(nullptr);
+  c.take<float>((size_t)(lora_shares(tokens, k) * tokens * rank));
+  return c.used;
+}
+
+int lora_forward(const void* x, int dtype, int64_t tokens, int64_t k, int64_t ld_x,
+                 const int32_t* ids, const void* a, const void* b, const float* scale,
+                 int32_t adapters, int32_t rank, int64_t n, const void* base, int64_t ld_base,
+                 int out_dtype, void* out, float* h, void* workspace, size_t workspace_bytes,
+                 void* stream) {
+  const int st = lora_status(dtype, tokens, k, n, ids, a, b, scale, adapters, rank);
+  if (st != NVFP4_OK) return st;
+  if (!valid_dtype(out_dtype) || !rows_ok(x, tokens, k, ld_x, dtype) ||
+      !rows_ok(out, tokens, n, n, out_dtype) || !aligned(h, 4) ||
+      (base && !rows_ok(base, tokens, n, ld_base, out_dtype)))
+    return NVFP4_INVALID_ARGUMENT;
+  if (tokens == 0) return NVFP4_OK;
+  if (!workspace || !aligned(workspace, 16)) return NVFP4_INVALID_ARGUMENT;
+  if (workspace_bytes < lora_forward_workspace_size(tokens, k, rank)) return NVFP4_WORKSPACE_TOO_SMALL;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  float* shares = static_cast<float*>(workspace);
+  if (launch_lora_down(lora_down(x, dtype, tokens, k, ld_x, ids, a, adapters, rank, shares), s) !=
+      hipSuccess)
+    return NVFP4_HIP_ERROR;
+  LoraUpArgs u = lora_up(shares, lora_shares(tokens, k), tokens, n, ids, b, dtype, scale, adapters,
+                         rank, base, out_dtype, ld_base, out, out_dtype);
+  u.h_out = h;
+  return hip_status(launch_lora_up(u, s));
+}
+
+struct LoraMatvecLayout {
+  float* shares;    // [shares, tokens, rank]
+  float* y;         // [tokens, n]: the projection's sums before the adapters'
+  size_t bytes;
+};
+
+static LoraMatvecLayout carve_lora_matvec(void* ws, int64_t tokens, int64_t n, int64_t k, int32_t rank) {
+  Carver c(ws);
+  LoraMatvecLayout L;
+  L.shares = c.take<float>((size_t)(lora_shares(tokens, k) * tokens * rank));
+  L.y = c.take<float>((size_t)(tokens * n));
+  L.bytes = c.used;
+  return L;
+}
+
+size_t nvfp4_lora_matvec_workspace_size(int64_t tokens, int64_t n, int64_t k, int32_t rank) {
+  if (tokens < 0 || tokens > 65536 || n < 1 || n > kMaxLoraWidth || k < 1 || k > kMaxK || rank < 1 ||
+      rank > kMaxRank)
+    return 0;
+  return carve_lora_matvec(nullptr, tokens, n, k, rank).bytes;
+}
+
+int nvfp4_lora_matvec(const void* x, int x_dtype, int64_t tokens, int64_t ld_x,
+                      const nvfp4_weights* w, int64_t n, int64_t k, const int32_t* ids,
+                      const void* a, const void* b, const float* scale, int32_t adapters,
+                      int32_t rank, int out_dtype, void* out, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  int st = matvec_weights_status(w, n, k);
+  if (st == NVFP4_OK) st = lora_status(x_dtype, tokens, k, n, ids, a, b, scale, adapters, rank);
+  if (st != NVFP4_OK) return st;
+  if (tokens > 65536) return NVFP4_UNSUPPORTED;
+  if (!valid_dtype(out_dtype) || !rows_ok(x, tokens, k, ld_x, x_dtype) ||
+      !rows_ok(out, tokens, n, n, out_dtype))
+    return NVFP4_INVALID_ARGUMENT;
+  if (tokens == 0) return NVFP4_OK;
+  if (!workspace || !aligned(workspace, 16)) return NVFP4_INVALID_ARGUMENT;
+  const LoraMatvecLayout L = carve_lora_matvec(workspace, tokens, n, k, rank);
+  if (workspace_bytes < L.bytes) return NVFP4_WORKSPACE_TOO_SMALL;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (launch_lora_down(lora_down(x, x_dtype, tokens, k, ld_x, ids, a, adapters, rank, L.shares), s) !=
+      hipSuccess)
+    return NVFP4_HIP_ERROR;
+  MatvecArgs m = matvec_args(x, x_dtype, ld_x, tokens, w, 1, n, k);
+  m.out = L.y; m.out_dtype = 0;
+  if (launch_matvec(m, s) != hipSuccess) return NVFP4_HIP_ERROR;
+  return hip_status(launch_lora_up(lora_up(L.shares, lora_shares(tokens, k), tokens, n, ids, b,
+                                           x_dtype, scale, adapters, rank, L.y, 0, n, out, out_dtype),
+                                   s));
+}
+
+struct LoraBackwardLayout {
+  void* at; void* bt;         // A and B transposed: [S, K, R], [S, R, N]
+  float* shares;              // of g, then (without the forward's h) of h
+  float* g; float* h;         // [tokens, rank]
+  int32_t* rows; int4* entries; int32_t* chunk0;
+  float* parts;
+  int32_t chunk, max_entries;
+  size_t bytes;
+};
+
+static LoraBackwardLayout carve_lora_backward(void* ws, int dtype, int64_t T, int64_t k, int64_t n,
+                                              int32_t S, int32_t rank) {
+  Carver c(ws);
+  LoraBackwardLayout L;
+  const size_t e = dtype_size(dtype), wide = (size_t)rank * (size_t)(k + n);
+  L.at = c.take<char>(e * S * rank * k);
+  L.bt = c.take<char>(e * S * rank * n);
+  const int sk = lora_shares(T, k), sn = lora_shares(T, n);
+  L.shares = c.take<float>((size_t)((sk > sn ? sk : sn) * T * rank));
+  L.g = c.take<float>((size_t)(T * rank));
+  L.h = c.take<float>((size_t)(T * rank));
+  L.rows = c.take<int32_t>((size_t)T);
+  L.chunk = lora_chunk(T, k, n);
+  L.max_entries = (int32_t)(T / L.chunk) + S;
+  L.entries = c.take<int4>((size_t)L.max_entries);
+  L.chunk0 = c.take<int32_t>((size_t)S + 1);
+  L.parts = c.take<float>(L.max_entries > S ? L.max_entries * wide : 0);
+  L.bytes = c.used;
+  return L;
+}
+
+size_t lora_backward_workspace_size(int dtype, int64_t tokens, int64_t k, int64_t n,
+                                    int32_t adapters, int32_t rank) {
+  if (!valid_dtype(dtype) || tokens < 0 || tokens > kMaxLoraTokens || k < 1 || n < 1 ||
+      k > kMaxLoraWidth || n > kMaxLoraWidth || adapters < 1 || adapters > kMaxAdapters || rank < 1 ||
+      rank > kMaxRank)
+    return 0;
+  return carve_lora_backward(nullptr, dtype, tokens, k, n, adapters, rank).bytes;
+}
+
+int lora_backward(const void* dy, int dtype, int64_t tokens, int64_t n, int64_t ld_dy,
+                  const void* x, int64_t k, int64_t ld_x, const int32_t* ids, const void* a,
+                  const void* b, const float* scale, int32_t adapters, int32_t rank, const float* h,
+                  const void* base, int64_t ld_base, void* dx, float* da, float* db,
+                  void* workspace, size_t workspace_bytes, void* stream) {
+  const int st = lora_status(dtype, tokens, k, n, ids, a, b, scale, adapters, rank);
+  if (st != NVFP4_OK) return st;
+  if (!rows_ok(dy, tokens, n, ld_dy, dtype) || !rows_ok(x, tokens, k, ld_x, dtype) ||
+      (base && !rows_ok(base, tokens, k, ld_base, dtype)) || !rows_ok(dx, tokens, k, k, dtype) ||
+      !da || !db || !aligned(da, 4) || !aligned(db, 4) || !aligned(h, 4) || !workspace ||
+      !aligned(workspace, 16))
+    return NVFP4_INVALID_ARGUMENT;
+  const LoraBackwardLayout L = carve_lora_backward(workspace, dtype, tokens, k, n, adapters, rank);
+  if (workspace_bytes < L.bytes) return NVFP4_WORKSPACE_TOO_SMALL;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e = hipSuccess;
+  if (!h) {
+    e = launch_lora_down(lora_down(x, dtype, tokens, k, ld_x, ids, a, adapters, rank, L.shares), s);
+    if (e == hipSuccess)
+      e = launch_lora_join_shares(L.shares, lora_shares(tokens, k), tokens * rank, L.h, s);
+  }
+  if (e == hipSuccess) e = launch_lora_transpose(a, dtype, adapters, rank, k, L.at, s);
+  if (e == hipSuccess) e = launch_lora_transpose(b, dtype, adapters, n, rank, L.bt, s);
+  if (e == hipSuccess)
+    e = launch_lora_down(lora_down(dy, dtype, tokens, n, ld_dy, ids, L.bt, adapters, rank, L.shares), s);
+  if (e == hipSuccess) {
+    LoraUpArgs u = lora_up(L.shares, lora_shares(tokens, n), tokens, k, ids, L.at, dtype, scale,
+                           adapters, rank, base, dtype, ld_base, dx, dtype);
+    u.h_out = L.g; u.h_scaled = 1;
+    e = launch_lora_up(u, s);
+  }
+  LoraSortArgs so{};
+  so.ids = ids; so.tokens = tokens; so.adapters = adapters; so.chunk = L.chunk;
+  so.max_entries = L.max_entries; so.rows = L.rows; so.entries = L.entries; so.chunk0 = L.chunk0;
+  if (e == hipSuccess) e = launch_lora_sort(so, s);
+  LoraGradArgs gr{};
+  gr.x = x; gr.dy = dy; gr.dtype = dtype; gr.k = k; gr.n = n; gr.ld_x = ld_x; gr.ld_dy = ld_dy;
+  gr.g = L.g; gr.h = h ? h : L.h; gr.scale = scale; gr.adapters = adapters; gr.rank = rank;
+  gr.rows = L.rows; gr.entries = L.entries; gr.da = da; gr.db = db; gr.parts = L.parts;
+  if (e == hipSuccess) e = launch_lora_grad(gr, L.max_entries, L.chunk0, s);
+  return hip_status(e);
+}
+
 int nvfp4_event_create(void** event) {
   if (!event) return NVFP4_INVALID_ARGUMENT;
   hipEvent_t ev;

@@ -256,4 +256,50 @@ hipError_t launch_decode_combine(const float* y_rows, const int32_t* idx, int64_
                                  int32_t topk, int32_t num_experts, int64_t hidden, int y_dtype,
                                  void* y, hipStream_t s);
 
+// ---- lora.hip ----
+constexpr int kMaxAdapters = 1024;
+struct LoraDownArgs {
+  const void* x; int dtype; int64_t tokens, k, ld_x;   // the long rows
+  const int32_t* ids; int32_t adapters, rank;
+  const void* a;              // [adapters, rank, k]
+  float* h;                   // [lora_shares(tokens, k), tokens, rank]
+  int64_t share; int by_token;   // (the launcher's)
+};
+struct LoraUpArgs {
+  const float* h; int shares; // [shares, tokens, rank], added up
+  int64_t tokens, n;
+  const int32_t* ids; int32_t adapters, rank;
+  const void* b; int dtype;   // [adapters, n, rank]
+  const float* scale;         // nullable [adapters]
+  const void* base; int base_dtype; int64_t ld_base;   // nullable [tokens, ld_base]: the output's type or binary32
+  void* out; int out_dtype;   // [tokens, n]
+  float* h_out; int h_scaled; // nullable [tokens, rank]: h, times the scale if h_scaled
+  int by_token;               // (the launcher's)
+};
+struct LoraSortArgs {
+  const int32_t* ids; int64_t tokens; int32_t adapters, chunk, max_entries;
+  int32_t* rows;              // [tokens]
+  int4* entries;              // [max_entries]
+  int32_t* chunk0;            // [adapters + 1]
+};
+struct LoraGradArgs {
+  const void* x; const void* dy; int dtype; int64_t k, n, ld_x, ld_dy;
+  const float* g; const float* h;          // [tokens, rank]; g with the scale, h without
+  const float* scale; int32_t adapters, rank;
+  const int32_t* rows; const int4* entries;
+  float* da; float* db;       // [adapters, rank, k], [adapters, n, rank]
+  float* parts;               // [max_entries, rank * (k + n)]
+};
+int lora_shares(int64_t tokens, int64_t k);
+int32_t lora_chunk(int64_t tokens, int64_t k, int64_t n);
+hipError_t launch_lora_down(LoraDownArgs a, hipStream_t s);
+hipError_t launch_lora_up(LoraUpArgs a, hipStream_t s);
+hipError_t launch_lora_transpose(const void* in, int dtype, int64_t groups, int64_t rows, int64_t cols,
+                                 void* out, hipStream_t s);
+hipError_t launch_lora_join_shares(const float* in, int shares, int64_t elements, float* out,
+                                   hipStream_t s);
+hipError_t launch_lora_sort(const LoraSortArgs& a, hipStream_t s);
+hipError_t launch_lora_grad(const LoraGradArgs& a, int32_t max_entries, const int32_t* chunk0,
+                            hipStream_t s);
+
 }  // namespace nvfp4

@@ -1,0 +1,651 @@
+// lora.hip -- low-rank adapters of many requests beside a shared projection:
+//   h[t] = A[s] x[t]          y[t] = base[t] + c_s B[s] h[t]        s = ids[t]
+// and their gradients, with g[t] = c_s B[s]^T dy[t]:
+//   dx[t] = base[t] + A[s]^T g[t]
+//   dA[s] = sum over s's tokens of g[t] x[t]^T,  dB[s] = of c_s dy[t] h[t]^T
+// A token whose id is no adapter has h = 0 and y = base.
+//
+// Both directions are the same two products: "down" contracts a long row with
+// the rank's rows ([S, R, K], K contiguous), "up" multiplies R values into a
+// long row ([S, N, R], R contiguous).  The way back takes B and A transposed,
+// by a copy of them (the adapters are small beside the tokens).
+//
+// Tokens of one adapter are multiplied together.  Few tokens (up to kWindow):
+// a workgroup per token looks its adapter's tokens up and the first of them
+// does the work of all.  Many: a workgroup takes 64 consecutive tokens and
+// does one adapter after the other, so a batch whose requests lie together
+// reads each token's row once and an adapter once per 64 tokens.
+//
+// Arithmetic: down multiplies in the type of x by MFMA 16x16x32 (binary32:
+// 16x16x4) into binary32; h and g stay binary32 and everything they enter is a
+// binary32 product (MFMA 16x16x4 of the exactly widened B, A, x and dy).  Sums
+// over K that several workgroups share are joined in workgroup order, sums
+// over tokens in token order per chunk: results do not depend on timing.
+#include "elem.h"
+#include "launch.h"
+
+namespace nvfp4 {
+
+namespace {
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+
+constexpr int kWindow = 256;    // most tokens that workgroups per token look through
+constexpr int kGroup = 64;      // tokens multiplied at once
+constexpr int kWaves = 4;
+constexpr int kThreads = kWaves * kWave;
+constexpr int kRanks = 64;      // ranks of one pass
+
+// ---- the tokens of one adapter ------------------------------------------
+
+struct TokenList {
+  uint16_t at[kWindow];         // offsets from the window's first token
+  uint64_t mask[kWaves];
+};
+
+__device__ __forceinline__ int key_of(int id, int adapters) {
+  return id >= 0 && id < adapters ? id : -1;
+}
+
+__device__ __forceinline__ int bits_below(uint64_t mask) {
+  return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32),
+                                   __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+}
+
+// f(adapter or -1, number of listed tokens, first token of the window) for
+// every adapter that this workgroup is to do.  Every thread calls f alike, and
+// the list stays as it is until f returns.
+template <typename F>
+__device__ __forceinline__ void for_each_adapter(const int32_t* ids, int64_t tokens, int adapters,
+                                                 bool by_token, TokenList& list, F f) {
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  if (by_token) {
+    const int slot = blockIdx.x;
+    const int key = key_of(ids[slot], adapters);
+    const bool in = (int)threadIdx.x < (int)tokens;
+    const bool mine = in && key_of(ids[in ? threadIdx.x : 0], adapters) == key;
+    const uint64_t mask = __ballot(mine);
+    if (lane == 0) list.mask[wave] = mask;
+    __syncthreads();
+    int m = 0, before = 0;
+    bool earlier = false;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const uint64_t b = list.mask[w];
+      if (w < wave) before += __popcll(b);
+      m += __popcll(b);
+      const int to = slot - w * kWave;      // tokens of this wave before the slot
+      if (to > 0) earlier |= (to >= kWave ? b : b & ((1ull << to) - 1)) != 0;
+    }
+    if (earlier) return;
+    if (mine) list.at[before + bits_below(mask)] = (uint16_t)threadIdx.x;
+    __syncthreads();
+    f(key, m, (int64_t)0);
+    return;
+  }
+  const int64_t first = (int64_t)blockIdx.x * kGroup;
+  const bool in = first + lane < tokens;
+  const int key = in ? key_of(ids[first + lane], adapters) : -2;
+  uint64_t todo = __ballot(in);
+  while (todo != 0) {
+    const int k = __shfl(key, __builtin_ctzll(todo));
+    const uint64_t mask = __ballot(key == k);
+    if (wave == 0 && key == k) list.at[bits_below(mask)] = (uint16_t)lane;
+    __syncthreads();
+    f(k, (int)__popcll(mask), first);
+    __syncthreads();
+    todo &= ~mask;
+  }
+}
+
+// ---- down: the long rows' products with the rank's rows --------------------
+
+// 16 bytes of a row from element `at`, zeros from element `end` on.
+template <int DT>
+__device__ __forceinline__ Piece<DT> piece_until(const typename Elem<DT>::type* row, int64_t at,
+                                                 int64_t end) {
+  Piece<DT> p;
+  if (at + Piece<DT>::kN <= end) p.load(row + at);
+  else p.load_part(row + at, at < end ? (int)(end - at) : 0);
+  return p;
+}
+
+template <int DT>
+__device__ __forceinline__ f32x4_t product(const Piece<DT>& a, const Piece<DT>& b, f32x4_t acc) {
+  if constexpr (DT == 0) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[e], b.v[e], acc, 0, 0, 0);
+    return acc;
+  } else if constexpr (DT == 1) {
+    bf16x8_t u, v;
+    __builtin_memcpy(&u, a.v, 16);
+    __builtin_memcpy(&v, b.v, 16);
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(u, v, acc, 0, 0, 0);
+  } else {
+    half8_t u, v;
+    __builtin_memcpy(&u, a.v, 16);
+    __builtin_memcpy(&v, b.v, 16);
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(u, v, acc, 0, 0, 0);
+  }
+}
+
+// Grid: x = tokens or groups of 64 tokens, y = shares of K, z = 64 ranks each.
+// A wave takes every fourth 128-byte piece of the rows; lane l has bytes
+// 16 (l / 16) of 64 of rank l % 16 and of token l % 16, RT times 16 ranks by
+// four times 16 tokens.
+template <int DT, int RT>
+__global__ __launch_bounds__(kThreads) void lora_down_kernel(LoraDownArgs p) {
+  typedef typename Elem<DT>::type T;
+  constexpr int E = Piece<DT>::kN, kStep = 8 * E;   // elements of a piece; of 128 bytes
+  __shared__ TokenList list;
+  __shared__ f32x4_t red[kWaves][4][kWave];
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  const int i = lane % 16, q = lane / 16;
+  const int r0 = blockIdx.z * kRanks;
+  const int64_t k0 = blockIdx.y * p.share, k1 = k0 + p.share < p.k ? k0 + p.share : p.k;
+  float* const out = p.h + blockIdx.y * p.tokens * p.rank;
+  for_each_adapter(p.ids, p.tokens, p.adapters, p.by_token, list, [&](int s, int m, int64_t first) {
+    for (int g0 = 0; g0 < m; g0 += kGroup) {
+      const int left = m - g0;
+      f32x4_t acc[RT][4];
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[rt][j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+      if (s >= 0) {
+        const T* xr[4];
+        const T* ar[RT];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int at = 16 * j + i;
+          xr[j] = static_cast<const T*>(p.x) + (first + list.at[g0 + (at < left ? at : 0)]) * p.ld_x;
+        }
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          const int r = r0 + 16 * rt + i;
+          ar[rt] = static_cast<const T*>(p.a) + ((int64_t)s * p.rank + (r < p.rank ? r : p.rank - 1)) * p.k;
+        }
+        for (int64_t c = k0 + wave * kStep; c < k1; c += kWaves * kStep) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int64_t at = c + u * 4 * E + q * E;
+            Piece<DT> a[RT];
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) a[rt] = piece_until<DT>(ar[rt], at, k1);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if (16 * j >= left) continue;
+              const Piece<DT> x = piece_until<DT>(xr[j], at, k1);
+#pragma unroll
+              for (int rt = 0; rt < RT; ++rt) acc[rt][j] = product<DT>(a[rt], x, acc[rt][j]);
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) red[wave][j][lane] = acc[rt][j];
+        __syncthreads();
+        f32x4_t v = red[0][wave][lane];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) v += red[w][wave][lane];
+        const int at = 16 * wave + i, r = r0 + 16 * rt + 4 * q;
+        if (at < left) {
+          float* o = out + (first + list.at[g0 + at]) * p.rank + r;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (r + e < p.rank) o[e] = v[e];
+        }
+      }
+    }
+  });
+}
+
+// ---- up: the rank's values into long rows ----------------------------------
+
+template <int DT>
+__device__ __forceinline__ f32x4_t four_until(const typename Elem<DT>::type* row, int at, int end) {
+  typename Elem<DT>::type v[4];
+  if (at + 4 <= end) {
+    __builtin_memcpy(v, row + at, sizeof(v));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = at + e < end ? row[at + e] : (typename Elem<DT>::type)0;
+  }
+  return (f32x4_t){Elem<DT>::to_float(v[0]), Elem<DT>::to_float(v[1]), Elem<DT>::to_float(v[2]),
+                   Elem<DT>::to_float(v[3])};
+}
+
+template <int DT>
+__device__ __forceinline__ void add16(const void* base, int64_t at, int count, float (&v)[16]) {
+  typedef typename Elem<DT>::type T;
+  const T* b = static_cast<const T*>(base) + at;
+  if (count >= 16) {
+#pragma unroll
+    for (int c = 0; c < 16; c += Piece<DT>::kN) {
+      Piece<DT> p;
+      p.load(b + c);
+#pragma unroll
+      for (int e = 0; e < Piece<DT>::kN; ++e) v[c + e] += p.get(e);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      if (e < count) v[e] += Elem<DT>::to_float(b[e]);
+  }
+}
+
+// Grid: x = tokens or groups of 64 tokens, y = 256 columns each, 64 a wave.
+// MFMA row 16 (i / 4) + 4 j + i % 4 of the wave's 64 is row i of product j, so
+// that a lane ends with 16 consecutive columns of its token.
+template <int DT, int OT>
+__global__ __launch_bounds__(kThreads) void lora_up_kernel(LoraUpArgs p) {
+  typedef typename Elem<DT>::type T;
+  typedef typename Elem<OT>::type O;
+  constexpr int kLd = kRanks + 4;
+  __shared__ TokenList list;
+  __shared__ __align__(16) float hs[kGroup * kLd];
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  const int i = lane % 16, q = lane / 16;
+  const int64_t n0 = (int64_t)blockIdx.y * kThreads + wave * kWave;
+  for_each_adapter(p.ids, p.tokens, p.adapters, p.by_token, list, [&](int s, int m, int64_t first) {
+    const float c = s >= 0 ? (p.scale ? p.scale[s] : 1.0f) : 0.0f;
+    for (int g0 = 0; g0 < m; g0 += kGroup) {
+      const int left = m - g0 < kGroup ? m - g0 : kGroup;
+      f32x4_t acc[4][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) acc[j][t] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+      for (int r0 = 0; r0 < p.rank; r0 += kRanks) {
+        const int ranks = p.rank - r0 < kRanks ? p.rank - r0 : kRanks;
+        const int padded = (ranks + 15) / 16 * 16;
+        __syncthreads();
+        for (int v = threadIdx.x; v < left * padded; v += kThreads) {
+          const int t = v / padded, r = v % padded;
+          const int64_t at = (first + list.at[g0 + t]) * p.rank + r0 + r;
+          float h = 0.0f;
+          if (r < ranks) {
+            if (s >= 0) {
+              h = p.h[at];
+              for (int w = 1; w < p.shares; ++w) h += p.h[w * p.tokens * p.rank + at];
+            }
+            if (p.h_out && blockIdx.y == 0) p.h_out[at] = p.h_scaled ? c * h : h;
+          }
+          hs[t * kLd + r] = c * h;
+        }
+        __syncthreads();
+        if (s < 0 || n0 >= p.n) continue;
+        for (int rb = 0; rb < padded; rb += 16) {
+          f32x4_t h[4];
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+            h[t] = 16 * t < left
+                       ? *reinterpret_cast<const f32x4_t*>(hs + (16 * t + i < left ? 16 * t + i : 0) * kLd + rb + 4 * q)
+                       : (f32x4_t){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int64_t n = n0 + 16 * (i / 4) + 4 * j + i % 4;
+            const T* row = static_cast<const T*>(p.b) + ((int64_t)s * p.n + (n < p.n ? n : p.n - 1)) * p.rank;
+            const f32x4_t b = four_until<DT>(row, r0 + rb + 4 * q, p.rank);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              if (16 * t >= left) continue;
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                acc[j][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(b[e], h[t][e], acc[j][t], 0, 0, 0);
+            }
+          }
+        }
+      }
+      const int64_t n = n0 + 16 * q;
+      if (n >= p.n) continue;
+      const int count = p.n - n < 16 ? (int)(p.n - n) : 16;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const int at = 16 * t + i;
+        if (at >= left) continue;
+        const int64_t tok = first + list.at[g0 + at];
+        float v[16];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[4 * j + e] = acc[j][t][e];
+        if (p.base) {
+          if (p.base_dtype == OT) add16<OT>(p.base, tok * p.ld_base + n, count, v);
+          else add16<0>(p.base, tok * p.ld_base + n, count, v);
+        }
+        O* o = static_cast<O*>(p.out) + tok * p.n + n;
+        if (count == 16) {
+#pragma unroll
+          for (int c0 = 0; c0 < 16; c0 += Piece<OT>::kN) {
+            Piece<OT> w;
+#pragma unroll
+            for (int e = 0; e < Piece<OT>::kN; ++e) w.set(e, v[c0 + e]);
+            w.store(o + c0);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (e < count) o[e] = Elem<OT>::from_float(v[e]);
+        }
+      }
+    }
+  });
+}
+
+// ---- the way back -----------------------------------------------------------
+
+// [groups, rows, cols] to [groups, cols, rows], 32 x 32 elements a workgroup.
+template <typename T>
+__global__ __launch_bounds__(256) void lora_transpose_kernel(const T* in, int64_t rows, int64_t cols,
+                                                             T* out) {
+  __shared__ T tile[32][33];
+  const int64_t r0 = (int64_t)blockIdx.y * 32, c0 = (int64_t)blockIdx.x * 32;
+  const int64_t group = (int64_t)blockIdx.z * rows * cols;
+  const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
+  for (int r = ty; r < 32; r += 8)
+    if (r0 + r < rows && c0 + tx < cols) tile[r][tx] = in[group + (r0 + r) * cols + c0 + tx];
+  __syncthreads();
+  for (int c = ty; c < 32; c += 8)
+    if (c0 + c < cols && r0 + tx < rows) out[group + (c0 + c) * rows + r0 + tx] = tile[tx][c];
+}
+
+// h[t, r] = the sum of its shares, in order.
+__global__ __launch_bounds__(256) void lora_join_shares_kernel(const float* in, int shares,
+                                                               int64_t elements, float* out) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= elements) return;
+  float v = in[i];
+  for (int w = 1; w < shares; ++w) v += in[w * elements + i];
+  out[i] = v;
+}
+
+// Tokens in adapter order (ascending inside an adapter) and the chunks that
+// the gradients are summed in: one workgroup, sixteen waves with a consecutive
+// share of the tokens each.  entry = {adapter, first row, end row, number of
+// its adapter's chunks}; every adapter has one chunk at least, unused entries
+// have adapter -1.  chunk0[s] is adapter s's first chunk.
+constexpr int kSortWaves = 16;
+__global__ __launch_bounds__(kSortWaves * kWave) void lora_sort_kernel(LoraSortArgs p) {
+  __shared__ int32_t place[kSortWaves * kMaxAdapters];   // [wave][adapter]
+  __shared__ int32_t sums[2][kSortWaves];
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  const int S = p.adapters, tokens = (int)p.tokens;
+  const int per = (tokens + kSortWaves * kWave - 1) / (kSortWaves * kWave) * kWave;
+  const int t0 = wave * per < tokens ? wave * per : tokens, t1 = t0 + per < tokens ? t0 + per : tokens;
+  int32_t* mine = place + wave * S;
+  for (int i = threadIdx.x; i < kSortWaves * S; i += blockDim.x) place[i] = 0;
+  __syncthreads();
+  for (int t = t0 + lane; t < t1; t += kWave) {
+    const int k = key_of(p.ids[t], S);
+    if (k >= 0) atomicAdd(&mine[k], 1);       // (a count: the order does not matter)
+  }
+  __syncthreads();
+  // thread s: adapter s's tokens and chunks, then sums over the adapters before
+  const int s = threadIdx.x;
+  int count = 0;
+  if (s < S)
+    for (int w = 0; w < kSortWaves; ++w) {
+      const int c = place[w * S + s];
+      place[w * S + s] = count;
+      count += c;
+    }
+  const int chunks = s < S ? (count > p.chunk ? (count + p.chunk - 1) / p.chunk : 1) : 0;
+  int v[2] = {count, chunks}, before[2];
+#pragma unroll
+  for (int a = 0; a < 2; ++a) {
+    int x = v[a];
+    for (int d = 1; d < kWave; d *= 2) {
+      const int y = __shfl_up(x, d);
+      if (lane >= d) x += y;
+    }
+    if (lane == kWave - 1) sums[a][wave] = x;
+    before[a] = x - v[a];
+  }
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) {
+    before[0] += sums[0][w];
+    before[1] += sums[1][w];
+  }
+  if (s < S) {
+    for (int w = 0; w < kSortWaves; ++w) place[w * S + s] += before[0];
+    p.chunk0[s] = before[1];
+    for (int c = 0; c < chunks; ++c) {
+      const int r0 = before[0] + c * p.chunk;
+      const int r1 = r0 + p.chunk < before[0] + count ? r0 + p.chunk : before[0] + count;
+      p.entries[before[1] + c] = make_int4(s, r0, r1, chunks);
+    }
+    if (s == S - 1) {
+      p.chunk0[S] = before[1] + chunks;
+      for (int c = before[1] + chunks; c < p.max_entries; ++c) p.entries[c] = make_int4(-1, 0, 0, 0);
+    }
+  }
+  __syncthreads();
+  volatile int32_t* next = mine;      // written by one lane, read by the others of its wave
+  for (int base = t0; base < t1; base += kWave) {
+    const int t = base + lane;
+    const int k = t < t1 ? key_of(p.ids[t], S) : -1;
+    uint64_t todo = __ballot(k >= 0);
+    while (todo != 0) {
+      const int one = __builtin_ctzll(todo), key = __shfl(k, one);
+      const uint64_t mask = __ballot(k == key);
+      const int at = next[key];
+      if (k == key) p.rows[at + bits_below(mask)] = t;
+      __builtin_amdgcn_wave_barrier();
+      if (lane == one) next[key] = at + __popcll(mask);
+      __builtin_amdgcn_wave_barrier();
+      todo &= ~mask;
+    }
+  }
+}
+
+// Grid: x = 128 columns of x, then of dy; y = chunks; z = 64 ranks each.  The
+// waves take the chunk's tokens in turn, four at a time: lane l has rank
+// l % 16 and columns 8 (l % 16) .. + 7 of token l / 16, so the rows are read
+// 16 bytes a lane and nothing is transposed.  An adapter of one chunk writes
+// its gradient, others a part each.
+template <int DT, int RT>
+__global__ __launch_bounds__(kThreads) void lora_grad_kernel(LoraGradArgs p) {
+  typedef typename Elem<DT>::type T;
+  __shared__ f32x4_t red[kWaves][8][kWave];
+  const int4 e = p.entries[blockIdx.y];
+  if (e.x < 0) return;
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  const int i = lane % 16, q = lane / 16, z0 = blockIdx.z * kRanks;
+  const int tiles_a = (int)((p.k + 127) / 128);
+  const bool down = (int)blockIdx.x < tiles_a;       // dA (g, x), else dB (c h, dy)
+  const int64_t width = down ? p.k : p.n, ld = down ? p.ld_x : p.ld_dy;
+  const int64_t c0 = (int64_t)(down ? blockIdx.x : blockIdx.x - tiles_a) * 128 + 8 * i;
+  const T* long_rows = static_cast<const T*>(down ? p.x : p.dy);
+  const float* values = down ? p.g : p.h;
+  const float c = down || !p.scale ? 1.0f : p.scale[e.x];
+  f32x4_t acc[RT][8];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[rt][j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+  constexpr int U = 4;
+  for (int t = e.y + 4 * wave; t < e.z; t += U * 4 * kWaves) {
+    int64_t tok[U];
+    bool in[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = t + u * 4 * kWaves + q;
+      in[u] = r < e.z;
+      tok[u] = p.rows[in[u] ? r : e.z - 1];
+    }
+    float v[U][RT], x[U][8];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        const int r = z0 + 16 * rt + i;
+        v[u][rt] = values[tok[u] * p.rank + (r < p.rank ? r : p.rank - 1)];
+      }
+      const T* row = long_rows + tok[u] * ld;
+#pragma unroll
+      for (int h = 0; h < 8; h += Piece<DT>::kN) {
+        const Piece<DT> piece = piece_until<DT>(row, c0 + h, width);
+#pragma unroll
+        for (int b = 0; b < Piece<DT>::kN; ++b) x[u][h + b] = in[u] ? piece.get(b) : 0.0f;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        const float a = in[u] ? c * v[u][rt] : 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          acc[rt][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(a, x[u][j], acc[rt][j], 0, 0, 0);
+      }
+  }
+  const int64_t wide = (int64_t)p.rank * (p.k + p.n);
+  float* out = e.w > 1 ? p.parts + blockIdx.y * wide + (down ? 0 : p.rank * p.k)
+                       : (down ? p.da + (int64_t)e.x * p.rank * p.k : p.db + (int64_t)e.x * p.rank * p.n);
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) red[wave][j][lane] = acc[rt][j];
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int j = 2 * wave + h;
+      f32x4_t v = red[0][j][lane];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) v += red[w][j][lane];
+      const int64_t col = c0 + j;
+      const int r = z0 + 16 * rt + 4 * q;
+      if (col >= width) continue;
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        if (r + b < p.rank) out[down ? (r + b) * p.k + col : col * p.rank + r + b] = v[b];
+    }
+  }
+}
+
+// The gradients of adapters of several chunks: the parts added in chunk order.
+__global__ __launch_bounds__(256) void lora_join_parts_kernel(LoraGradArgs p, const int32_t* chunk0) {
+  const int s = blockIdx.y, c0 = chunk0[s], c1 = chunk0[s + 1];
+  if (c1 - c0 < 2) return;
+  const int64_t na = p.rank * p.k, wide = na + p.rank * p.n;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= wide) return;
+  float v = p.parts[c0 * wide + i];
+  for (int c = c0 + 1; c < c1; ++c) v += p.parts[c * wide + i];
+  if (i < na) p.da[s * na + i] = v;
+  else p.db[s * (wide - na) + i - na] = v;
+}
+
+template <int DT>
+void down_dt(const LoraDownArgs& a, dim3 grid, hipStream_t s) {
+  if (a.rank <= 16) lora_down_kernel<DT, 1><<<grid, kThreads, 0, s>>>(a);
+  else if (a.rank <= 32) lora_down_kernel<DT, 2><<<grid, kThreads, 0, s>>>(a);
+  else lora_down_kernel<DT, 4><<<grid, kThreads, 0, s>>>(a);
+}
+
+template <int DT>
+void up_dt(const LoraUpArgs& a, dim3 grid, hipStream_t s) {
+  if (a.out_dtype == 0) lora_up_kernel<DT, 0><<<grid, kThreads, 0, s>>>(a);
+  else if (a.out_dtype == 1) lora_up_kernel<DT, 1><<<grid, kThreads, 0, s>>>(a);
+  else lora_up_kernel<DT, 2><<<grid, kThreads, 0, s>>>(a);
+}
+
+template <int DT>
+void grad_dt(const LoraGradArgs& a, dim3 grid, hipStream_t s) {
+  if (a.rank <= 16) lora_grad_kernel<DT, 1><<<grid, kThreads, 0, s>>>(a);
+  else if (a.rank <= 32) lora_grad_kernel<DT, 2><<<grid, kThreads, 0, s>>>(a);
+  else lora_grad_kernel<DT, 4><<<grid, kThreads, 0, s>>>(a);
+}
+
+int64_t token_blocks(int64_t tokens) {
+  return tokens <= kWindow ? tokens : (tokens + kGroup - 1) / kGroup;
+}
+
+}  // namespace
+
+// Shares of K: as many as bring the launch to two workgroups a CU, of no less
+// than one 128-byte piece a wave.
+int lora_shares(int64_t tokens, int64_t k) {
+  const int64_t blocks = token_blocks(tokens), most = (k + 255) / 256;
+  int64_t w = blocks > 0 ? (512 + blocks - 1) / blocks : 1;
+  w = w < most ? w : most;
+  return (int)(w < 1 ? 1 : (w > 16 ? 16 : w));
+}
+
+// Tokens of a chunk of the gradients: enough chunks for three workgroups a CU.
+int32_t lora_chunk(int64_t tokens, int64_t k, int64_t n) {
+  const int64_t tiles = (k + 127) / 128 + (n + 127) / 128;
+  const int64_t want = (768 + tiles - 1) / tiles;
+  const int64_t c = ((tokens + want - 1) / want + 63) / 64 * 64;
+  return (int32_t)(c < 64 ? 64 : c);
+}
+
+hipError_t launch_lora_down(LoraDownArgs a, hipStream_t s) {
+  if (a.tokens == 0) return hipSuccess;
+  const int shares = lora_shares(a.tokens, a.k);
+  a.by_token = a.tokens <= kWindow;
+  a.share = ((a.k + shares - 1) / shares + 255) / 256 * 256;
+  const dim3 grid((unsigned)token_blocks(a.tokens), shares, (a.rank + kRanks - 1) / kRanks);
+  if (a.dtype == 0) down_dt<0>(a, grid, s);
+  else if (a.dtype == 1) down_dt<1>(a, grid, s);
+  else down_dt<2>(a, grid, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_lora_up(LoraUpArgs a, hipStream_t s) {
+  if (a.tokens == 0) return hipSuccess;
+  a.by_token = a.tokens <= kWindow;
+  const dim3 grid((unsigned)token_blocks(a.tokens), (unsigned)((a.n + kThreads - 1) / kThreads));
+  if (a.dtype == 0) up_dt<0>(a, grid, s);
+  else if (a.dtype == 1) up_dt<1>(a, grid, s);
+  else up_dt<2>(a, grid, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_lora_transpose(const void* in, int dtype, int64_t groups, int64_t rows, int64_t cols,
+                                 void* out, hipStream_t s) {
+  const dim3 grid((unsigned)((cols + 31) / 32), (unsigned)((rows + 31) / 32), (unsigned)groups);
+  if (dtype == 0)
+    lora_transpose_kernel<<<grid, 256, 0, s>>>(static_cast<const uint32_t*>(in), rows, cols,
+                                               static_cast<uint32_t*>(out));
+  else
+    lora_transpose_kernel<<<grid, 256, 0, s>>>(static_cast<const uint16_t*>(in), rows, cols,
+                                               static_cast<uint16_t*>(out));
+  return hipGetLastError();
+}
+
+hipError_t launch_lora_join_shares(const float* in, int shares, int64_t elements, float* out,
+                                   hipStream_t s) {
+  if (elements == 0) return hipSuccess;
+  lora_join_shares_kernel<<<(unsigned)((elements + 255) / 256), 256, 0, s>>>(in, shares, elements, out);
+  return hipGetLastError();
+}
+
+hipError_t launch_lora_sort(const LoraSortArgs& a, hipStream_t s) {
+  lora_sort_kernel<<<1, kSortWaves * kWave, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_lora_grad(const LoraGradArgs& a, int32_t max_entries, const int32_t* chunk0,
+                            hipStream_t s) {
+  const unsigned tiles = (unsigned)((a.k + 127) / 128 + (a.n + 127) / 128);
+  const dim3 grid(tiles, (unsigned)max_entries, (a.rank + kRanks - 1) / kRanks);
+  if (a.dtype == 0) grad_dt<0>(a, grid, s);
+  else if (a.dtype == 1) grad_dt<1>(a, grid, s);
+  else grad_dt<2>(a, grid, s);
+  if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
+  if (max_entries > a.adapters) {      // some adapter may have several chunks
+    const int64_t wide = a.rank * (a.k + a.n);
+    lora_join_parts_kernel<<<dim3((unsigned)((wide + 255) / 256), (unsigned)a.adapters), 256, 0, s>>>(a, chunk0);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace nvfp4

@@ -23,7 +23,9 @@ __all__ = ["nvfp4_quantize", "moe_rows_capacity", "moe_permute", "moe_permute_no
            "StageTimer", "BackwardTimer", "moe_router", "moe_router_backward",
            "moe_sort_tokens", "moe_sort_tokens_backward", "moe_unsort_tokens",
            "moe_unsort_tokens_backward", "nvfp4_matvec", "nvfp4_expert_matvec",
-           "moe_expert_decode", "moe_expert_decode_workspace_size"]
+           "moe_expert_decode", "moe_expert_decode_workspace_size", "lora_forward",
+           "lora_forward_workspace_size", "lora_backward", "lora_backward_workspace_size",
+           "nvfp4_lora_matvec", "nvfp4_lora_matvec_workspace_size"]
 
 SINGLE_PASS_TILE = 256   # intermediate columns per online-scale tile of the single-pass layer
 
@@ -826,3 +828,125 @@ def moe_expert_decode(x, topk_idx, topk_prob, num_experts: int, inter: int, w1: 
           topk_idx.data_ptr(), topk_prob.data_ptr(), k, num_experts, C.byref(w1.c_struct()),
           C.byref(w2.c_struct()), y.data_ptr(), workspace.data_ptr(), workspace.numel())
     return y
+
+
+# ---- low-rank adapters -------------------------------------------------------
+
+def lora_forward_workspace_size(tokens, k, rank) -> int:
+    return int(lib().lora_forward_workspace_size(tokens, k, rank))
+
+
+def lora_backward_workspace_size(dtype, tokens, k, n, adapters, rank) -> int:
+    return int(lib().lora_backward_workspace_size(_DTYPE_CODE[dtype], tokens, k, n, adapters, rank))
+
+
+def nvfp4_lora_matvec_workspace_size(tokens, n, k, rank) -> int:
+    return int(lib().nvfp4_lora_matvec_workspace_size(tokens, n, k, rank))
+
+
+def _need_adapters(a, b, ids, scale, tokens, k, dtype, dev):
+    """Adapters a [S, R, K] and b [S, N, R] of this dtype, a token's adapter and
+    the scales.  Returns (S, R, N)."""
+    for t, name in ((a, "a"), (b, "b")):
+        if not isinstance(t, torch.Tensor) or t.dim() != 3:
+            _need(t, (dtype,), name)
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected three dimensions")
+    S, R, _ = a.shape
+    N = b.shape[1]
+    _dense(a, dtype, (S, R, k), dev, "a")
+    _dense(b, dtype, (S, N, R), dev, "b")
+    _dense(ids, torch.int32, (tokens,), dev, "ids")
+    if scale is not None:
+        _dense(scale, torch.float32, (S,), dev, "scale")
+    return S, R, N
+
+
+def _base_rows(base, tokens, width, dtype, dev):
+    """The distance of base's rows (its width where there is none)."""
+    if base is None:
+        return width
+    ld = _need_rows(base, "base", width, dtype)
+    if base.shape[0] != tokens:
+        raise ValueError(f"base: shape {tuple(base.shape)}, expected {(tokens, width)}")
+    _same_device(base, dev, "base")
+    return ld
+
+
+def _work_bytes(workspace, size, like, dev):
+    if workspace is None:
+        return like.new_empty((max(size, 256),), dtype=torch.uint8)
+    _need(workspace, (torch.uint8,), "workspace")
+    _same_device(workspace, dev, "workspace")
+    return workspace
+
+
+def lora_forward(x, a, b, ids, scale=None, base=None, out_dtype=None, out=None,
+                 return_h: bool = False, workspace=None):
+    """Low-rank adapters of many requests: y[t] = base[t] + scale[s] b[s] (a[s]
+    x[t]) with s = ids[t].  x [T, K], a [S, R, K], b [S, N, R] of one type
+    (float32, bf16 or fp16), ids int32 [T] (outside [0, S): no adapter), scale
+    float32 [S], base [T, N] in the output's type (the projection's output; `out`
+    may be base itself).  Returns y [T, N] in out_dtype (x's by default), with
+    return_h also h = a[s] x[t] float32 [T, R], lora_backward's argument."""
+    ld = _need_rows(x, "x")
+    T, K = x.shape
+    dev = x.get_device()
+    S, R, N = _need_adapters(a, b, ids, scale, T, K, x.dtype, dev)
+    out = _out_rows(out, (T, N), out_dtype if out_dtype is not None else x.dtype, x, dev)
+    ld_base = _base_rows(base, T, N, out.dtype, dev)
+    h = x.new_empty((T, R), dtype=torch.float32) if return_h else None
+    ws = _work_bytes(workspace, lib().lora_forward_workspace_size(T, K, R), x, dev)
+    _call(dev, "lora_forward", x.data_ptr(), _DTYPE_CODE[x.dtype], T, K, ld, ids.data_ptr(),
+          a.data_ptr(), b.data_ptr(), _addr(scale), S, R, N, _addr(base), ld_base,
+          _DTYPE_CODE[out.dtype], out.data_ptr(), _addr(h), ws.data_ptr(), ws.numel())
+    return (out, h) if return_h else out
+
+
+def lora_backward(dy, x, a, b, ids, scale=None, h=None, base=None, out=None, workspace=None):
+    """Gradients of lora_forward from dy [T, N] (x's type): dx [T, K] (x's type)
+    = base[t] + a[s]^T g[t] with g[t] = scale[s] b[s]^T dy[t] (base: the rest of
+    x's gradient; `out` may be base itself), da float32 [S, R, K] and db float32
+    [S, N, R].  h: the forward's (None: computed again).  Returns (dx, da, db)."""
+    ld_dy = _need_rows(dy, "dy")
+    T, N = dy.shape
+    dev = dy.get_device()
+    ld_x = _need_rows(x, "x", None, dy.dtype)
+    K = x.shape[1]
+    if x.shape[0] != T:
+        raise ValueError(f"x: shape {tuple(x.shape)}, expected {(T, K)}")
+    _same_device(x, dev, "x")
+    S, R, n = _need_adapters(a, b, ids, scale, T, K, dy.dtype, dev)
+    if n != N:
+        raise ValueError(f"b: shape {tuple(b.shape)}, expected {(S, N, R)}")
+    if h is not None:
+        _dense(h, torch.float32, (T, R), dev, "h")
+    ld_base = _base_rows(base, T, K, dy.dtype, dev)
+    dx = _out_rows(out, (T, K), dy.dtype, dy, dev)
+    da = dy.new_empty((S, R, K), dtype=torch.float32)
+    db = dy.new_empty((S, N, R), dtype=torch.float32)
+    code = _DTYPE_CODE[dy.dtype]
+    ws = _work_bytes(workspace, lib().lora_backward_workspace_size(code, T, K, N, S, R), dy, dev)
+    _call(dev, "lora_backward", dy.data_ptr(), code, T, N, ld_dy, x.data_ptr(), K, ld_x,
+          ids.data_ptr(), a.data_ptr(), b.data_ptr(), _addr(scale), S, R, _addr(h), _addr(base),
+          ld_base, dx.data_ptr(), da.data_ptr(), db.data_ptr(), ws.data_ptr(), ws.numel())
+    return dx, da, db
+
+
+def nvfp4_lora_matvec(x, w: NvFp4Weights, a, b, ids, scale=None, out_dtype=None, out=None,
+                      workspace=None):
+    """nvfp4_matvec with every row's low-rank adapter: x [T, K] times one NVFP4
+    matrix (w: [1, N, K], either layout) plus scale[s] b[s] (a[s] x[t]), s =
+    ids[t]; a, b, ids and scale as lora_forward's.  Returns [T, N] in out_dtype
+    (x's by default), rounded once."""
+    _weights_type((w, "w"))
+    ld = _need_rows(x, "x")
+    T, K = x.shape
+    dev = x.get_device()
+    S, R, N = _need_adapters(a, b, ids, scale, T, K, x.dtype, dev)
+    _need_weights(w, "w", dev, 1, N, K)
+    out = _out_rows(out, (T, N), out_dtype if out_dtype is not None else x.dtype, x, dev)
+    ws = _work_bytes(workspace, lib().nvfp4_lora_matvec_workspace_size(T, N, K, R), x, dev)
+    _call(dev, "nvfp4_lora_matvec", x.data_ptr(), _DTYPE_CODE[x.dtype], T, ld,
+          C.byref(w.c_struct()), N, K, ids.data_ptr(), a.data_ptr(), b.data_ptr(), _addr(scale), S,
+          R, _DTYPE_CODE[out.dtype], out.data_ptr(), ws.data_ptr(), ws.numel())
+    return out
