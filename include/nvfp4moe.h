@@ -707,6 +707,36 @@ int nvfp4_lora_matvec(const void* x, int x_dtype, int64_t tokens, int64_t ld_x,
                       size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
+ * newton_schulz -- the orthogonalised update of weight gradients (a batch of
+ * matrices, e.g. moe_expert_backward's dw1 and dw2 or lora_backward's da and db):
+ *   X = G / (|G|_F + eps)
+ *   steps times:  A = X X^T (or X^T X where rows > cols: the smaller one)
+ *                 X = a X + (b A + c A A) X      (X (b A + c A A))
+ *   out = scale * X
+ * The norm is binary64.  X is kept to 22 bits.  float32 and fp16 results take
+ * products of all 22 bits, summed in binary32 (errors as of a binary32
+ * computation); bf16 results take products of the upper 11 bits, which stay
+ * below bf16's own rounding (2e-3 of the result's norm).  A zero matrix gives
+ * zeros; one that holds an infinity or NaN gives NaN throughout, and no other
+ * matrix is touched by it.  Results are bitwise reproducible.
+ *   g          [batch, rows, cols], dtype code; rows ld_row apart, matrices
+ *              ld_batch apart (elements)
+ *   out        dense [batch, rows, cols], out_dtype; may be g itself
+ *   a, b, c    the quintic's coefficients, the same every step.  Singular values
+ *              start in [0, 1]; coefficients that let them grow past 8, or b A + c
+ *              A A past 8192, are NVFP4_UNSUPPORTED.
+ *   workspace  newton_schulz_workspace_size() bytes (at most about 1 GiB, or one
+ *              matrix's), 16-byte aligned; every word read is written before by
+ *              the same call
+ * Limits: rows, cols <= 16384; batch <= 2^20; steps <= 64.
+ * ---------------------------------------------------------------------- */
+size_t newton_schulz_workspace_size(int64_t batch, int64_t rows, int64_t cols, int out_dtype);
+int newton_schulz(const void* g, int dtype, int64_t batch, int64_t rows, int64_t cols,
+                  int64_t ld_row, int64_t ld_batch, int steps, float a, float b, float c, float eps,
+                  float scale, int out_dtype, void* out, void* workspace, size_t workspace_bytes,
+                  void* stream);
+
+/* ------------------------------------------------------------------------
  * Profiling helpers: thin wrappers over hipEventCreate / hipEventRecord /
  * hipEventElapsedTime / hipEventDestroy so a caller without HIP headers can
  * time the stages of moe_expert_forward on its stream.  (These allocate a

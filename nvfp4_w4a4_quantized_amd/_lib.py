@@ -164,6 +164,12 @@ def _load(path):
     L.nvfp4_lora_matvec.restype = C.c_int
     L.nvfp4_lora_matvec.argtypes = [_vp, C.c_int, _i64, _i64, C.POINTER(Weights), _i64, _i64, _vp,
                                     _vp, _vp, _vp, _i32, _i32, C.c_int, _vp, _vp, C.c_size_t, _vp]
+    L.newton_schulz_workspace_size.restype = C.c_size_t
+    L.newton_schulz_workspace_size.argtypes = [_i64, _i64, _i64, C.c_int]
+    L.newton_schulz.restype = C.c_int
+    L.newton_schulz.argtypes = [_vp, C.c_int, _i64, _i64, _i64, _i64, _i64, C.c_int, C.c_float,
+                                C.c_float, C.c_float, C.c_float, C.c_float, C.c_int, _vp, _vp,
+                                C.c_size_t, _vp]
     L.nvfp4_event_create.restype = C.c_int
     L.nvfp4_event_create.argtypes = [C.POINTER(_vp)]
     L.nvfp4_event_record.restype = C.c_int

@@ -22,8 +22,8 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libnvfp4moe.so")
 DEBUG_LIB = os.path.join(HERE, "libnvfp4moe_debug.so")
 SOURCES = ["quantize.hip", "route.hip", "gemm.hip", "single_pass.hip", "backward.hip",
-           "combine.hip", "router.hip", "tokens.hip", "matvec.hip", "lora.hip", "capi.hip",
-           "noalloc.hip"]
+           "combine.hip", "router.hip", "tokens.hip", "matvec.hip", "lora.hip",
+           "newton_schulz.hip", "capi.hip", "noalloc.hip"]
 DEBUG_SOURCES = ["route.hip", "capi.hip"]      # the sources that read NVFP4_DEBUG_CHECKS
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -1103,6 +1103,74 @@ int lora_backward(const void* dy, int dtype, int64_t tokens, int64_t n, int64_t 
   return hip_status(e);
 }
 
+// ---- the orthogonalised update ----
+
+constexpr int64_t kMaxSide = 16384, kMaxMatrices = 1 << 20;
+constexpr int kMaxSteps = 64;
+
+struct NsLayout {
+  double* norms; int32_t* k0;
+  _Float16* x[4]; _Float16* sq[4];
+  size_t bytes;
+};
+
+static NsLayout carve_ns(void* ws, int64_t batch, int64_t rows, int64_t cols, bool exact) {
+  Carver c(ws);
+  NsLayout L{};
+  const int64_t m = ns_batch(batch, rows, cols), n = rows < cols ? rows : cols;
+  const size_t xs = (size_t)(m * rows) * round_up((size_t)cols, 64);
+  const size_t ns = (size_t)(m * n) * round_up((size_t)n, 64);
+  L.norms = c.take<double>((size_t)(m * ns_norm_parts(m, rows)));
+  L.k0 = c.take<int32_t>((size_t)m);
+  for (int i = 0; i < 4; ++i) L.x[i] = c.take<_Float16>(xs);
+  for (int i = 0; i < 4; ++i)
+    if (exact || i % 2 == 0) L.sq[i] = c.take<_Float16>(ns);
+  L.bytes = c.used;
+  return L;
+}
+
+static int ns_status(int64_t batch, int64_t rows, int64_t cols, int out_dtype) {
+  if (batch < 0 || rows < 1 || cols < 1 || !valid_dtype(out_dtype)) return NVFP4_INVALID_ARGUMENT;
+  if (rows > kMaxSide || cols > kMaxSide || batch > kMaxMatrices) return NVFP4_UNSUPPORTED;
+  return NVFP4_OK;
+}
+
+size_t newton_schulz_workspace_size(int64_t batch, int64_t rows, int64_t cols, int out_dtype) {
+  if (ns_status(batch, rows, cols, out_dtype) != NVFP4_OK || batch == 0) return 0;
+  return carve_ns(nullptr, batch, rows, cols, out_dtype != 1).bytes;
+}
+
+int newton_schulz(const void* g, int dtype, int64_t batch, int64_t rows, int64_t cols,
+                  int64_t ld_row, int64_t ld_batch, int steps, float a, float b, float c, float eps,
+                  float scale, int out_dtype, void* out, void* workspace, size_t workspace_bytes,
+                  void* stream) {
+  const int st = ns_status(batch, rows, cols, out_dtype);
+  if (st != NVFP4_OK) return st;
+  const float big = 3.4e38f;
+  if (!valid_dtype(dtype) || ld_row < cols || ld_batch < 0 || steps < 1 || !(eps >= 0.0f) ||
+      !(eps <= big) || !(scale >= -big && scale <= big) || !(a >= -big && a <= big) ||
+      !(b >= -big && b <= big) || !(c >= -big && c <= big))
+    return NVFP4_INVALID_ARGUMENT;
+  if (batch > 0 && (!g || !out || !workspace)) return NVFP4_INVALID_ARGUMENT;
+  if (!aligned(g, dtype_size(dtype)) || !aligned(out, dtype_size(out_dtype)) || !aligned(workspace, 16))
+    return NVFP4_INVALID_ARGUMENT;
+  NsArgs n{};
+  if (steps > kMaxSteps || !ns_bounds(steps, a, b, c, &n.scales)) return NVFP4_UNSUPPORTED;
+  if (batch == 0) return NVFP4_OK;
+  const bool exact = out_dtype != 1;
+  const NsLayout L = carve_ns(workspace, batch, rows, cols, exact);
+  if (workspace_bytes < L.bytes) return NVFP4_WORKSPACE_TOO_SMALL;
+  n.src.g = g; n.src.dtype = dtype; n.src.rows = rows; n.src.cols = cols;
+  n.src.ld_row = ld_row; n.src.ld_batch = ld_batch; n.batch = batch;
+  n.steps = steps; n.a = a; n.b = b; n.c = c; n.eps = eps; n.out_scale = scale; n.exact = exact;
+  n.out = out; n.out_dtype = out_dtype; n.norms = L.norms; n.k0 = L.k0;
+  for (int i = 0; i < 4; ++i) {
+    n.x[i] = L.x[i];
+    n.sq[i] = L.sq[i];
+  }
+  return hip_status(launch_newton_schulz(n, static_cast<hipStream_t>(stream)));
+}
+
 int nvfp4_event_create(void** event) {
   if (!event) return NVFP4_INVALID_ARGUMENT;
   hipEvent_t ev;

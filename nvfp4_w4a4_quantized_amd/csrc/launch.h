@@ -302,4 +302,41 @@ hipError_t launch_lora_sort(const LoraSortArgs& a, hipStream_t s);
 hipError_t launch_lora_grad(const LoraGradArgs& a, int32_t max_entries, const int32_t* chunk0,
                             hipStream_t s);
 
+// ---- newton_schulz.hip ----
+struct NsSource {
+  const void* g; int dtype; int64_t rows, cols, ld_row, ld_batch;
+};
+struct NsScales {             // powers of two that X, A and P are kept times
+  float x, a, p;
+  int growth;                 // bits that a small X may grow by per step
+};
+struct NsMatrix {             // a batch of matrices in two binary16 parts
+  const _Float16* hi; const _Float16* lo;
+  int64_t stride, ld;         // elements
+  uint32_t bytes;             // of one matrix's part
+};
+struct NsGemmArgs {
+  NsMatrix a, b, y;           // C = f A B (+ g Y), in both parts of Y (y.lo nullable)
+  int64_t batch, m, n, k;
+  int parts;                  // 1: hi hi; 3: hi hi + hi lo + lo hi
+  float f, g, up;
+  const int32_t* k0; int drop, growth;   // X is kept times 2^max(k0 - drop, 0)
+  _Float16* c_hi; _Float16* c_lo; int64_t c_stride, ldc;   // c_lo nullable
+  void* out; int out_dtype; int wide;    // the last step's: dense rows of n
+};
+struct NsArgs {
+  NsSource src; int64_t batch;
+  int steps; float a, b, c; double eps; float out_scale;
+  int exact;                  // products of both parts
+  NsScales scales;
+  void* out; int out_dtype;
+  double* norms; int32_t* k0;
+  _Float16* x[4];             // X hi, lo, the next X hi, lo
+  _Float16* sq[4];            // A hi, lo, P hi, lo
+};
+bool ns_bounds(int steps, float a, float b, float c, NsScales* out);
+int64_t ns_batch(int64_t batch, int64_t rows, int64_t cols);
+int ns_norm_parts(int64_t batch, int64_t rows);
+hipError_t launch_newton_schulz(const NsArgs& a, hipStream_t s);
+
 }  // namespace nvfp4

@@ -25,7 +25,8 @@ __all__ = ["nvfp4_quantize", "moe_rows_capacity", "moe_permute", "moe_permute_no
            "moe_unsort_tokens_backward", "nvfp4_matvec", "nvfp4_expert_matvec",
            "moe_expert_decode", "moe_expert_decode_workspace_size", "lora_forward",
            "lora_forward_workspace_size", "lora_backward", "lora_backward_workspace_size",
-           "nvfp4_lora_matvec", "nvfp4_lora_matvec_workspace_size"]
+           "nvfp4_lora_matvec", "nvfp4_lora_matvec_workspace_size", "newton_schulz",
+           "newton_schulz_workspace_size"]
 
 SINGLE_PASS_TILE = 256   # intermediate columns per online-scale tile of the single-pass layer
 
@@ -949,4 +950,44 @@ def nvfp4_lora_matvec(x, w: NvFp4Weights, a, b, ids, scale=None, out_dtype=None,
     _call(dev, "nvfp4_lora_matvec", x.data_ptr(), _DTYPE_CODE[x.dtype], T, ld,
           C.byref(w.c_struct()), N, K, ids.data_ptr(), a.data_ptr(), b.data_ptr(), _addr(scale), S,
           R, _DTYPE_CODE[out.dtype], out.data_ptr(), ws.data_ptr(), ws.numel())
+    return out
+
+
+# ---- the orthogonalised update -------------------------------------------------
+
+def newton_schulz_workspace_size(batch, rows, cols, out_dtype) -> int:
+    return int(lib().newton_schulz_workspace_size(batch, rows, cols, _DTYPE_CODE[out_dtype]))
+
+
+def newton_schulz(g, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315), eps: float = 1e-7,
+                  scale: float = 1.0, out_dtype=None, out=None, workspace=None):
+    """The orthogonalised update of a weight gradient g [rows, cols], or of a
+    batch [E, rows, cols] of them (float32, bf16 or fp16; the last dimension
+    dense): X = g / (|g|_F + eps), then `steps` times X = a X + (b A + c A A) X
+    with A = X X^T (from the other side where rows > cols), times scale.
+    Returns g's shape in out_dtype (g's by default; `out` may be g itself).
+    bf16 results take faster products, below bf16's own rounding."""
+    if not isinstance(g, torch.Tensor):
+        raise TypeError("g must be a torch.Tensor")
+    if not g.is_cuda:
+        raise NvFp4Error(f"g must be a device tensor (got {g.device})")
+    if g.dtype not in _DTYPE_CODE:
+        raise TypeError(f"g: dtype {g.dtype} not in {tuple(_DTYPE_CODE)}")
+    if g.dim() not in (2, 3):
+        raise ValueError(f"g: shape {tuple(g.shape)}, expected [rows, cols] or [E, rows, cols]")
+    rows, cols = g.shape[-2:]
+    E = g.shape[0] if g.dim() == 3 else 1
+    if rows < 1 or cols < 1:
+        raise ValueError(f"g: shape {tuple(g.shape)}, expected elements")
+    ld_row = g.stride(-2) if rows > 1 else cols
+    ld_batch = g.stride(0) if E > 1 else 0
+    if (g.stride(-1) != 1 and cols > 1) or ld_row < cols:
+        raise ValueError(f"g: rows must be dense and must not overlap (strides {g.stride()})")
+    a, b, c = coefficients
+    dev = g.get_device()
+    out = _out_rows(out, g.shape, out_dtype if out_dtype is not None else g.dtype, g, dev)
+    code = _DTYPE_CODE[out.dtype]
+    ws = _work_bytes(workspace, lib().newton_schulz_workspace_size(E, rows, cols, code), g, dev)
+    _call(dev, "newton_schulz", g.data_ptr(), _DTYPE_CODE[g.dtype], E, rows, cols, ld_row, ld_batch,
+          steps, a, b, c, eps, scale, code, out.data_ptr(), ws.data_ptr(), ws.numel())
     return out

@@ -68,3 +68,20 @@ def make_ids(gen, T, S, kind):
         ids = torch.where(torch.rand(T, generator=gen) < 0.4,
                           out[torch.randint(0, 6, (T,), generator=gen)], ids)
     return ids.to(torch.int32)
+
+
+def newton_schulz(g, steps, coefficients, eps, scale=1.0):
+    """The orthogonalised update, from the definition, on g's device."""
+    a, b, c = coefficients
+    x = g.double()
+    tall = x.shape[-2] > x.shape[-1]
+    x = x / (x.square().sum(dim=(-2, -1), keepdim=True).sqrt() + eps)
+    for _ in range(steps):
+        xt = x.transpose(-2, -1).contiguous()
+        if tall:
+            s = torch.matmul(xt, x)
+            x = a * x + torch.matmul(x, b * s + c * torch.matmul(s, s))
+        else:
+            s = torch.matmul(x, xt)
+            x = a * x + torch.matmul(b * s + c * torch.matmul(s, s), x)
+    return scale * x

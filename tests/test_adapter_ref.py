@@ -96,3 +96,44 @@ def test_python_checks():
         ops.lora_forward([1.0], t, t, x)
     with pytest.raises(TypeError):
         ops.nvfp4_lora_matvec(x, x, t, t, x)
+
+
+def test_newton_schulz_refusals(L):  # noqa: F811
+    # g, dtype, batch, rows, cols, ld_row, ld_batch, steps, a, b, c, eps, scale, out_dtype, out, ws, bytes, s
+    good = [F, 0, 2, 40, 60, 60, 2400, 5, 3.4445, -4.775, 2.0315, 1e-7, 1.0, 1, F, F, 1 << 40, None]
+    inf, nan = float("inf"), float("nan")
+    for i, v in ((0, None), (0, ODD), (1, 3), (2, -1), (3, 0), (4, 0), (5, 59), (6, -1), (7, 0), (8, nan),
+                 (9, inf), (10, -inf), (11, -1.0), (11, nan), (11, inf), (12, nan), (12, inf), (13, 3),
+                 (14, None), (14, ODD), (15, None), (15, C.c_void_p(0x1008))):
+        assert L.newton_schulz(*change(good, i, v)) == INVALID, (i, v)
+    for i, v in ((2, (1 << 20) + 1), (3, 16385), (7, 65), (8, 9.0), (9, 40.0), (10, -30.0)):
+        assert L.newton_schulz(*change(good, i, v)) == UNSUPPORTED, (i, v)
+    assert L.newton_schulz(*change(change(good, 4, 16385), 5, 16385)) == UNSUPPORTED
+    for code in (0, 1, 2):
+        size = L.newton_schulz_workspace_size(2, 40, 60, code)
+        assert L.newton_schulz(*change(change(good, 13, code), 16, size - 1)) == WS_SMALL
+    assert L.newton_schulz(*change(good, 2, 0)) == 0
+    assert L.newton_schulz_workspace_size(0, 40, 60, 1) == 0
+    assert L.newton_schulz_workspace_size(2, 40, 16385, 1) == 0
+
+
+def test_newton_schulz_brings_singular_values_near_one():
+    """The definition itself: the usual coefficients take every singular value
+    that is not far below the largest to [0.68, 1.21], on either side."""
+    gen = torch.Generator().manual_seed(1)
+    for shape in ((12, 40), (40, 12), (2, 9, 9)):
+        g = torch.randn(*shape, generator=gen, dtype=torch.float64)
+        x = A.newton_schulz(g, 5, (3.4445, -4.7750, 2.0315), 1e-7)
+        s0, s1 = torch.linalg.svdvals(g), torch.linalg.svdvals(x)
+        kept = (s0 > 0.05 * s0.amax(-1, keepdim=True)).flip(-1)
+        assert bool(((s1 < 1.21) & (s1 > 0.68)).all()) or bool(((s1 > 0.68).sum(-1) >= kept.sum(-1)).all())
+        p = A.newton_schulz(-2.0 * g.transpose(-2, -1), 5, (3.4445, -4.7750, 2.0315), 0.0)
+        assert torch.allclose(p.transpose(-2, -1), -x, atol=1e-5)
+
+
+def test_newton_schulz_python_checks():
+    for call in (lambda: ops.newton_schulz(torch.zeros(3, 4)),):
+        with pytest.raises(NvFp4Error):
+            call()
+    with pytest.raises(TypeError):
+        ops.newton_schulz([1.0])
