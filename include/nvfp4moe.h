@@ -718,14 +718,15 @@ int nvfp4_lora_matvec(const void* x, int x_dtype, int64_t tokens, int64_t ld_x,
  * computation); bf16 results take products of the upper 11 bits, which stay
  * below bf16's own rounding (2e-3 of the result's norm).  A zero matrix gives
  * zeros; one that holds an infinity or NaN gives NaN throughout, and no other
- * matrix is touched by it.  Results are bitwise reproducible.
+ * matrix is touched by it.  Results are bitwise reproducible; a matrix's last
+ * bits may differ between calls with other numbers of matrices.
  *   g          [batch, rows, cols], dtype code; rows ld_row apart, matrices
  *              ld_batch apart (elements)
  *   out        dense [batch, rows, cols], out_dtype; may be g itself
  *   a, b, c    the quintic's coefficients, the same every step.  Singular values
  *              start in [0, 1]; coefficients that let them grow past 8, or b A + c
  *              A A past 8192, are NVFP4_UNSUPPORTED.
- *   workspace  newton_schulz_workspace_size() bytes (at most about 1 GiB, or one
+ *   workspace  newton_schulz_workspace_size() bytes (at most about 4 GiB, or one
  *              matrix's), 16-byte aligned; every word read is written before by
  *              the same call
  * Limits: rows, cols <= 16384; batch <= 2^20; steps <= 64.

@@ -316,13 +316,14 @@ struct NsMatrix {             // a batch of matrices in two binary16 parts
   uint32_t bytes;             // of one matrix's part
 };
 struct NsGemmArgs {
-  NsMatrix a, b, y;           // C = f A B (+ g Y), in both parts of Y (y.lo nullable)
+  NsMatrix a, b, y;           // C = f A B (+ g Y)
   int64_t batch, m, n, k;
-  int parts;                  // 1: hi hi; 3: hi hi + hi lo + lo hi
+  int32_t tiles;              // of a matrix (the launcher's)
+  int exact;                  // hi hi + hi lo + lo hi, else hi hi (A and P have no lo then)
   float f, g, up;
   const int32_t* k0; int drop, growth;   // X is kept times 2^max(k0 - drop, 0)
-  _Float16* c_hi; _Float16* c_lo; int64_t c_stride, ldc;   // c_lo nullable
-  void* out; int out_dtype; int wide;    // the last step's: dense rows of n
+  _Float16* c_hi; _Float16* c_lo; int64_t c_stride, ldc;
+  void* out; int out_dtype;              // the last step's: dense rows of n
 };
 struct NsArgs {
   NsSource src; int64_t batch;

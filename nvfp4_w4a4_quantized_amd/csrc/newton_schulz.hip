@@ -35,8 +35,6 @@ typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
 typedef short short4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) short4_t lds_short4_t;
 
-constexpr int kBK = 32;       // k of a stage
-
 enum { kGram = 0, kPoly = 1, kApply = 2, kLast = 3 };
 
 // ---- the norm and the first X ------------------------------------------------
@@ -105,22 +103,23 @@ __global__ __launch_bounds__(256) void ns_start_kernel(NsSource g, const double*
 
 // LDS tiles are unpadded and XOR-swizzled in 16-byte chunks (a direct-to-LDS
 // load writes one contiguous KiB per wave instruction):
-//   K-contiguous [T rows][32 k]: chunk c of row r at c ^ (r / 4) % 4
-//   K-major [32 k][T columns]: chunk c of row r at c ^ 4 (r % 4)  (T = 64: 2 (r % 4))
-template <int T>
-__device__ __forceinline__ int swz_major(int r, int c) {
-  return c ^ ((T >= 128 ? 4 : 2) * (r & 3));
+//   K-contiguous [T rows][BK k]: chunk c of row r at c ^ r % 8 (BK = 64), or
+//     c ^ (r / 4) % 4 (BK = 32)
+//   K-major [BK k][T columns]: chunk c of row r at c ^ 4 (r % 4)
+__device__ __forceinline__ int swz_major(int r, int c) { return c ^ (4 * (r & 3)); }
+template <int BK>
+__device__ __forceinline__ int swz_row(int r, int c) {
+  return BK == 64 ? c ^ (r & 7) : c ^ ((r >> 2) & 3);
 }
-__device__ __forceinline__ int swz_row(int r, int c) { return c ^ ((r >> 2) & 3); }
 
 // The matrix-core operand: lane l has row (column) r0 + l % 32 of the tile and
 // k = k0 + 8 (l / 32) + 0..7.
-template <int T, bool MAJOR>
+template <int T, int BK, bool MAJOR>
 __device__ __forceinline__ half8_t fragment(const _Float16* s, int r0, int k0, int lane) {
   if constexpr (MAJOR) {
     const int r = k0 + (lane >> 5) * 8 + ((lane & 15) >> 2);
     const int col = r0 + ((lane >> 4) & 1) * 16 + 4 * (lane & 3);
-    const int off = 8 * swz_major<T>(r, col >> 3) + (col & 7);   // rows r and r + 4 share it
+    const int off = 8 * swz_major(r, col >> 3) + (col & 7);      // rows r and r + 4 share it
     const short4_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4_t*)(s + r * T + off));
     const short4_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4_t*)(s + (r + 4) * T + off));
     const auto both = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
@@ -129,106 +128,111 @@ __device__ __forceinline__ half8_t fragment(const _Float16* s, int r0, int k0, i
     return v;
   } else {
     const int r = r0 + (lane & 31), c = (k0 >> 3) + (lane >> 5);
-    return *reinterpret_cast<const half8_t*>(s + r * 32 + 8 * swz_row(r, c));
+    return *reinterpret_cast<const half8_t*>(s + r * BK + 8 * swz_row<BK>(r, c));
   }
 }
 
-__device__ __forceinline__ void split(const float (&v)[4], half4_t* hi, half4_t* lo) {
+__device__ __forceinline__ void split(const float (&v)[8], half8_t* hi, half8_t* lo) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 8; ++i) {
     const _Float16 h = (_Float16)v[i];
     (*hi)[i] = h;
     (*lo)[i] = (_Float16)(v[i] - (float)h);
   }
 }
 
-// Four consecutive results of the last step.
+// Eight consecutive results of the last step, `count` of them inside.
 template <int OT>
-__device__ __forceinline__ void put4(void* out, int64_t at, int count, bool wide, const float (&v)[4]) {
-  typename Elem<OT>::type o[4], *p = static_cast<typename Elem<OT>::type*>(out) + at;
+__device__ __forceinline__ void put8(void* out, int64_t at, int64_t count, const float (&v)[8]) {
+  typename Elem<OT>::type o[8], *p = static_cast<typename Elem<OT>::type*>(out) + at;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = Elem<OT>::from_float(v[i]);
-  if (wide) {
+  for (int i = 0; i < 8; ++i) o[i] = Elem<OT>::from_float(v[i]);
+  if (count >= 8) {
     __builtin_memcpy(p, o, sizeof(o));
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 8; ++i)
       if (i < count) p[i] = o[i];
   }
 }
 
-// T x T tiles, NW waves in two rows, each IB x JB blocks of 32 x 32.
-template <int T>
-struct TileShape;
-template <>
-struct TileShape<256> {
-  static constexpr int kNW = 8, kIB = 4, kJB = 2;
+// A workgroup's TM x TN tile, 2 x 2 waves that take every stage (KG = 1), or two
+// such groups that take half of each stage's k and add their sums in LDS.
+template <int TM_, int TN_, int KG_, int RING_>
+struct Tile {
+  static constexpr int TM = TM_, TN = TN_, KG = KG_, RING = RING_, BK = 32 * KG_, NW = 4 * KG_;
 };
-template <>
-struct TileShape<128> {
-  static constexpr int kNW = 4, kIB = 2, kJB = 2;
-};
+using Wide = Tile<256, 128, 1, 3>;     // 72 KiB of LDS: two workgroups a CU
+using Deep = Tile<128, 128, 2, 4>;     // 128 KiB: one, with twice the waves on a tile
 
-// C = A B over k with the epilogue EPI; AM, BM: the operand is K-major.
-template <int T, bool AM, bool BMAJ, int EPI>
-__global__ __launch_bounds__(64 * TileShape<T>::kNW, T == 256 ? 1 : 2) void ns_gemm_kernel(NsGemmArgs p) {
-  constexpr int NW = TileShape<T>::kNW, IB = TileShape<T>::kIB, JB = TileShape<T>::kJB;
-  constexpr int REGION = T * kBK * 2;           // bytes of one operand's stage
-  constexpr int QN = REGION / 1024 / NW;        // its load instructions per wave
-  __shared__ __align__(16) uint8_t S0[2 * REGION];
-  __shared__ __align__(16) uint8_t S1[2 * REGION];
-  __shared__ __align__(16) uint8_t S2[2 * REGION];
-  __shared__ __align__(16) uint8_t S3[2 * REGION];
+// C = A B over k with the epilogue EPI; AM, BMAJ: the operand is K-major;
+// EXACT: products of both parts, and A and P have two.
+template <typename S, bool AM, bool BMAJ, int EPI, bool EXACT>
+__global__ __launch_bounds__(64 * S::NW, 2) void ns_gemm_kernel(NsGemmArgs p) {
+  constexpr int TM = S::TM, TN = S::TN, KG = S::KG, RING = S::RING, BK = S::BK, NW = S::NW;
+  constexpr int IB = TM / 64, JB = TN / 64;       // a wave's blocks of 32 x 32
+  constexpr int A_BYTES = TM * BK * 2, B_BYTES = TN * BK * 2;
+  constexpr int QA = A_BYTES / 1024 / NW, QB = B_BYTES / 1024 / NW;   // load instructions per wave
+  // one array per slot, so that the compiler sees that a load into one slot
+  // does not write the slot being read
+  constexpr int SLOT = A_BYTES + B_BYTES;
+  __shared__ __align__(16) uint8_t S0[SLOT];
+  __shared__ __align__(16) uint8_t S1[SLOT];
+  __shared__ __align__(16) uint8_t S2[SLOT];
+  __shared__ __align__(16) uint8_t S3[RING == 4 ? SLOT : 16];
   constexpr bool SYM = EPI == kGram || EPI == kPoly;
+  constexpr int kParts = EXACT ? 3 : 1;
   const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
 
   // consecutive tiles of a matrix on one XCD (workgroups go round the eight)
   const int nb = gridDim.x, xcd = blockIdx.x % 8, in = blockIdx.x / 8;
   const int t = xcd * (nb / 8) + (xcd < nb % 8 ? xcd : nb % 8) + in;
-  const int tiles_n = (int)((p.n + T - 1) / T);
-  const int tiles_m = (int)((p.m + T - 1) / T);
-  const int per = SYM ? tiles_n * (tiles_n + 1) / 2 : tiles_m * tiles_n;
-  const int e = t / per;
-  int ti = 0, tj = t % per;
+  const int tiles_n = (int)((p.n + TN - 1) / TN);
+  const int e32 = t / p.tiles;
+  const int64_t e = e32;
+  int ti = 0, tj = t - e32 * p.tiles;
   if (SYM) {
-    while (tj >= tiles_n - ti) {                // row ti has tiles_n - ti tiles
-      tj -= tiles_n - ti;
-      ++ti;
-    }
-    tj += ti;
+    // row ti has the column tiles from the one that holds its first diagonal
+    // element on
+    for (; tj >= tiles_n - ti * (TM / TN); ++ti) tj -= tiles_n - ti * (TM / TN);
+    tj += ti * (TM / TN);
   } else {
     ti = tj / tiles_n;
     tj %= tiles_n;
   }
-  const int64_t m0 = (int64_t)ti * T, n0 = (int64_t)tj * T;
+  const bool mirror = SYM && tj >= (ti + 1) * (TM / TN);      // wholly above the diagonal
+  const int64_t m0 = (int64_t)ti * TM, n0 = (int64_t)tj * TN;
 
   const __amdgpu_buffer_rsrc_t ahi = buffer_rsrc(p.a.hi + e * p.a.stride, p.a.bytes);
   const __amdgpu_buffer_rsrc_t bhi = buffer_rsrc(p.b.hi + e * p.b.stride, p.b.bytes);
   const __amdgpu_buffer_rsrc_t alo = buffer_rsrc(p.a.lo + e * p.a.stride, p.a.bytes);
   const __amdgpu_buffer_rsrc_t blo = buffer_rsrc(p.b.lo + e * p.b.stride, p.b.bytes);
-  const int steps = (int)((p.k + kBK - 1) / kBK), nst = steps * p.parts;
+  const int steps = (int)((p.k + BK - 1) / BK), nst = steps * kParts;
 
   // A lane's offsets of stage 0.  Rows past the matrix lie past its resource
   // and read zeros; columns past ld are masked.
-  uint32_t ao[QN], bo[QN];
-  auto place = [&](bool major, int64_t first, int64_t ld, int q) -> uint32_t {
+  auto place = [&](auto major, auto tile, int64_t first, int64_t ld, int q) -> uint32_t {
     const int i = wave + NW * q;
-    if (major) {
-      constexpr int kLanes = T / 8, kRows = kWave / kLanes;   // lanes of a row; rows of an instruction
-      const int r = i * kRows + lane / kLanes, c = swz_major<T>(r, lane % kLanes);
+    if constexpr (decltype(major)::value) {
+      constexpr int kLanes = decltype(tile)::value / 8, kRows = kWave / kLanes;   // lanes of a row, rows of an instruction
+      const int r = i * kRows + lane / kLanes, c = swz_major(r, lane % kLanes);
       const int64_t col = first + 8 * c;
       return col < ld ? (uint32_t)((r * ld + col) * 2) : kNone;
+    } else {
+      constexpr int kLanes = BK / 8, kRows = kWave / kLanes;
+      const int r = kRows * i + lane / kLanes, c = swz_row<BK>(r, lane % kLanes);
+      return (uint32_t)(((first + r) * ld + 8 * c) * 2);
     }
-    const int r = 16 * i + lane / 4, c = swz_row(r, lane % 4);
-    return (uint32_t)(((first + r) * ld + 8 * c) * 2);
   };
+  using TMc = std::integral_constant<int, TM>;
+  using TNc = std::integral_constant<int, TN>;
+  uint32_t ao[QA], bo[QB];
 #pragma unroll
-  for (int q = 0; q < QN; ++q) {
-    ao[q] = place(AM, m0, p.a.ld, q);
-    bo[q] = place(BMAJ, n0, p.b.ld, q);
-  }
-  const uint32_t astep = AM ? (uint32_t)(p.a.ld * kBK * 2) : kBK * 2;
-  const uint32_t bstep = BMAJ ? (uint32_t)(p.b.ld * kBK * 2) : kBK * 2;
+  for (int q = 0; q < QA; ++q) ao[q] = place(std::bool_constant<AM>{}, TMc{}, m0, p.a.ld, q);
+#pragma unroll
+  for (int q = 0; q < QB; ++q) bo[q] = place(std::bool_constant<BMAJ>{}, TNc{}, n0, p.b.ld, q);
+  const uint32_t astep = AM ? (uint32_t)(p.a.ld * BK * 2) : BK * 2;
+  const uint32_t bstep = BMAJ ? (uint32_t)(p.b.ld * BK * 2) : BK * 2;
 
   auto slot = [&](auto u) -> uint8_t* {
     constexpr int U = decltype(u)::value;
@@ -237,25 +241,26 @@ __global__ __launch_bounds__(64 * TileShape<T>::kNW, T == 256 ? 1 : 2) void ns_g
     else if constexpr (U == 2) return S2;
     else return S3;
   };
-  // stage st: step st / parts of k, and of the parts hi hi, hi lo, lo hi the
-  // (st % parts)-th; stages past the last read zeros
-  int step = 0, part = 0;
+  // stage st: step st / kParts of k, and of the parts hi hi, hi lo, lo hi the
+  // (st % kParts)-th; stages past the last read zeros
+  int part = 0;
+  uint32_t sa = 0, sb = 0;
   auto load = [&](auto u, int st) {
     uint8_t* s = slot(u);
     const bool live = st < nst;
-    const uint32_t sa = (uint32_t)step * astep, sb = (uint32_t)step * bstep;
-    const __amdgpu_buffer_rsrc_t ra = part == 2 ? alo : ahi, rb = part == 1 ? blo : bhi;
+    const __amdgpu_buffer_rsrc_t ra = EXACT && part == 2 ? alo : ahi, rb = EXACT && part == 1 ? blo : bhi;
 #pragma unroll
-    for (int q = 0; q < QN; ++q)
+    for (int q = 0; q < QA; ++q)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void_t*)(s + (wave + NW * q) * 1024), 16,
                                                (int)(live ? ao[q] + sa : kNone), 0, 0, 0);
 #pragma unroll
-    for (int q = 0; q < QN; ++q)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void_t*)(s + REGION + (wave + NW * q) * 1024), 16,
+    for (int q = 0; q < QB; ++q)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void_t*)(s + A_BYTES + (wave + NW * q) * 1024), 16,
                                                (int)(live ? bo[q] + sb : kNone), 0, 0, 0);
-    if (++part == p.parts) {
+    if (++part == kParts) {
       part = 0;
-      ++step;
+      sa += astep;
+      sb += bstep;
     }
   };
 
@@ -266,132 +271,233 @@ __global__ __launch_bounds__(64 * TileShape<T>::kNW, T == 256 ? 1 : 2) void ns_g
     for (int j = 0; j < JB; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
-  const int wm = wave % 2, wn = wave / 2;
-  const int rm = wm * IB * 32, rn = wn * JB * 32;        // the wave's first row and column
+  const int group = wave / 4;
+  const int rm = (wave % 2) * (TM / 2), rn = (wave / 2 % 2) * (TN / 2);   // the wave's first row and column
   auto multiply = [&](auto u) {
     const _Float16* la = reinterpret_cast<const _Float16*>(slot(u));
-    const _Float16* lb = reinterpret_cast<const _Float16*>(slot(u) + REGION);
-    half8_t fa[kBK / 16][IB], fb[kBK / 16][JB];
+    const _Float16* lb = reinterpret_cast<const _Float16*>(slot(u) + A_BYTES);
+    half8_t fa[2][IB], fb[2][JB];
 #pragma unroll
-    for (int kk = 0; kk < kBK / 16; ++kk) {
+    for (int kk = 0; kk < 2; ++kk) {
+      const int k = 32 * group + 16 * kk;
 #pragma unroll
-      for (int j = 0; j < JB; ++j) fb[kk][j] = fragment<T, BMAJ>(lb, rn + j * 32, kk * 16, lane);
+      for (int j = 0; j < JB; ++j) fb[kk][j] = fragment<TN, BK, BMAJ>(lb, rn + j * 32, k, lane);
 #pragma unroll
-      for (int i = 0; i < IB; ++i) fa[kk][i] = fragment<T, AM>(la, rm + i * 32, kk * 16, lane);
+      for (int i = 0; i < IB; ++i) fa[kk][i] = fragment<TM, BK, AM>(la, rm + i * 32, k, lane);
     }
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-    for (int kk = 0; kk < kBK / 16; ++kk)
+    for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
       for (int i = 0; i < IB; ++i)
 #pragma unroll
         for (int j = 0; j < JB; ++j)
           acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fb[kk][j], fa[kk][i], acc[i][j], 0, 0, 0);
+    __builtin_amdgcn_s_setprio(0);
   };
 
-  // Stages st + 1 .. st + 3 are in flight while stage st is multiplied: the
-  // wait leaves the two newest stages' loads outstanding, the barrier (without
-  // a fence, which would wait for all) says that every wave's loads of st have
-  // landed and that slot st + 3 is no longer read.
-  constexpr int WAIT = 2 * 2 * QN;
-  constexpr int WAIT_IMM = (WAIT & 15) | ((WAIT >> 4) << 14) | (7 << 4) | (15 << 8);
+  // Stages st + 1 .. st + RING - 1 are in flight while stage st is multiplied.
+  // Before a turn's barrier a wave waits for its own loads of stage st (leaving
+  // those of the later stages outstanding) and for its LDS reads of stage st - 1,
+  // which the products may still be waiting for: behind the barrier every
+  // wave's part of stage st has landed, and the slot of stage st - 1 is free for
+  // stage st + RING - 1.
+  constexpr int WAIT = (RING - 2) * (QA + QB);
+  constexpr int WAIT_IMM = (WAIT & 15) | ((WAIT >> 4) << 14) | (7 << 4);       // vmcnt(WAIT) lgkmcnt(0)
   using C0 = std::integral_constant<int, 0>;
   using C1 = std::integral_constant<int, 1>;
   using C2 = std::integral_constant<int, 2>;
   using C3 = std::integral_constant<int, 3>;
   auto turn = [&](auto u, int st) {
-    using Next = std::integral_constant<int, (decltype(u)::value + 3) % 4>;
+    using Next = std::integral_constant<int, (decltype(u)::value + RING - 1) % RING>;
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
     __builtin_amdgcn_s_waitcnt(WAIT_IMM);
     __builtin_amdgcn_s_barrier();
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
-    load(Next{}, st + 3);
-    if (st < nst) multiply(u);
+    load(Next{}, st + RING - 1);
+    multiply(u);
   };
   load(C0{}, 0);
   load(C1{}, 1);
-  load(C2{}, 2);
-  for (int st = 0; st < nst; st += 4) {
+  if constexpr (RING == 4) load(C2{}, 2);
+  int st = 0;
+  for (; st + RING <= nst; st += RING) {
     turn(C0{}, st);
     turn(C1{}, st + 1);
     turn(C2{}, st + 2);
-    turn(C3{}, st + 3);
+    if constexpr (RING == 4) turn(C3{}, st + 3);
   }
-  __builtin_amdgcn_s_waitcnt((7 << 4) | (15 << 8));      // no load into LDS outlives the loop
+  if (st < nst) turn(C0{}, st);
+  if (st + 1 < nst) turn(C1{}, st + 1);
+  if (RING == 4 && st + 2 < nst) turn(C2{}, st + 2);
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_s_waitcnt(7 << 4);      // no load into LDS outlives the loop, no read is left
+  __builtin_amdgcn_s_barrier();
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
 
-  // ---- epilogue: the operands are swapped in the products, so acc[i][j][4 q + c]
-  // is row l % 32 and column 8 q + 4 (l / 32) + c of block (i, j).
-  const int h = lane >> 5, l32 = lane & 31;
+  // Two groups: each takes one of the wave's row blocks and the other's sums of it.
+  if constexpr (KG == 2) {
+    float* give = reinterpret_cast<float*>((wave / 4 == 0 ? S0 : S1) + (wave % 4) * 8192) + lane * 4;
+    const float* take = reinterpret_cast<const float*>((wave / 4 == 0 ? S1 : S0) + (wave % 4) * 8192) + lane * 4;
+#pragma unroll
+    for (int j = 0; j < JB; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float four[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) four[c] = group == 0 ? acc[1][j][4 * q + c] : acc[0][j][4 * q + c];
+        __builtin_memcpy(give + (j * 4 + q) * 256, four, 16);
+      }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < JB; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float four[4];
+        __builtin_memcpy(four, take + (j * 4 + q) * 256, 16);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          acc[0][j][4 * q + c] = (group == 0 ? acc[0][j][4 * q + c] : acc[1][j][4 * q + c]) + four[c];
+      }
+  }
+
+  // ---- epilogue.  The operands are swapped in the products, so acc[i][j][4 q +
+  // c] is row l % 32 and column 8 q + 4 (l / 32) + c of block (i, j).  32 rows x
+  // 64 columns at a time go through the wave's own 8 KiB of the ring (16-byte
+  // chunk c of row r at c ^ r % 16), so that memory is read and written in
+  // 128-byte rows, and in 64-byte ones of the mirrored tile.
+  float* const tile = reinterpret_cast<float*>(
+      KG == 2 ? (wave / 4 == 0 ? S2 : S3) + (wave % 4) * 8192 : (wave < 2 ? S0 : S1) + (wave % 2) * 8192);
+  const int h = lane >> 5, l32 = lane & 31, lr = lane / 8, lc = lane % 8;
   const int k0 = p.k0[e], kj = k0 - p.drop > 0 ? k0 - p.drop : 0;
   const int kn = kj - p.growth > 0 ? kj - p.growth : 0;
   const float f = EPI == kGram ? ldexpf(p.f, -2 * kj) : p.f;
   const float up = EPI == kApply ? ldexpf(1.0f, kn - kj) : (EPI == kLast ? ldexpf(p.up, -kj) : 1.0f);
+  // Eight values of Y from (row, col) on, and the eight results f acc + g Y there.
+  constexpr bool kLow = EXACT || EPI == kApply || EPI == kLast;    // Y has a lower part
+  struct Given {
+    half8_t hi, lo;
+  };
+  auto given = [&](int64_t row, int64_t col) -> Given {
+    Given y;
+    const int64_t at = e * p.y.stride + row * p.y.ld + col;
+    y.hi = *reinterpret_cast<const half8_t*>(p.y.hi + at);
+    if constexpr (kLow) y.lo = *reinterpret_cast<const half8_t*>(p.y.lo + at);
+    return y;
+  };
+  auto finish = [&](int64_t row, int64_t col, const Given& y, float (&v)[8]) {
 #pragma unroll
-  for (int i = 0; i < IB; ++i) {
-    const int64_t row = m0 + rm + i * 32 + l32;
-    if (row >= p.m) continue;
+    for (int c = 0; c < 8; ++c) {
+      v[c] *= f;
+      if constexpr (EPI != kGram) {
+        if constexpr (kLow) v[c] = fmaf(p.g, (float)y.lo[c], v[c]);
+        v[c] = up * (v[c] + p.g * (float)y.hi[c]);
+      }
+    }
+    if constexpr (EPI == kLast) {
+      const int64_t at = (e * p.m + row) * p.n + col, count = p.n - col;
+      if (p.out_dtype == 0) put8<0>(p.out, at, count, v);
+      else if (p.out_dtype == 1) put8<1>(p.out, at, count, v);
+      else put8<2>(p.out, at, count, v);
+    } else {
+      half8_t hi, lo;
+      split(v, &hi, &lo);
+      const int64_t at = e * p.c_stride + row * p.ldc + col;
+      *reinterpret_cast<half8_t*>(p.c_hi + at) = hi;
+      if constexpr (EXACT || EPI == kApply) *reinterpret_cast<half8_t*>(p.c_lo + at) = lo;
+    }
+  };
+  constexpr int kBlocks = KG == 2 ? 1 : IB;
+  const int64_t col0 = n0 + rn, col = col0 + 8 * lc;
+  const bool col_in = col < (EPI == kLast ? p.n : p.ldc);
+  auto block_row = [&](int i) { return m0 + rm + 32 * (KG == 2 ? group : i); };
+  // Y of a block's rows; rows and columns outside take the last ones' (unused)
+  auto fetch = [&](int i, Given (&y)[4]) {
+    if constexpr (EPI != kGram) {
 #pragma unroll
-    for (int j = 0; j < JB; ++j) {
+      for (int it = 0; it < 4; ++it) {
+        const int64_t row = block_row(i) + 8 * it + lr;
+        y[it] = given(row < p.m ? row : p.m - 1, col_in ? col : 0);
+      }
+    }
+  };
+  Given y[2][4];
+  fetch(0, y[0]);
+#pragma unroll
+  for (int i = 0; i < kBlocks; ++i) {
+    if (i + 1 < kBlocks) fetch(i + 1, y[(i + 1) % 2]);
+    const int64_t row0 = block_row(i);
+#pragma unroll
+    for (int j = 0; j < JB; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int64_t col = n0 + rn + j * 32 + 8 * q + 4 * h;
-        if (col >= p.ldc) continue;
-        float v[4];
+        const int c = 8 * j + 2 * q + h;
+        const float16_t& a = acc[i][j];
+        const float four[4] = {a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]};
+        __builtin_memcpy(tile + l32 * 64 + 4 * (c ^ (l32 & 15)), four, 16);
+      }
 #pragma unroll
-        for (int c = 0; c < 4; ++c) v[c] = f * acc[i][j][4 * q + c];
-        const int64_t at = (int64_t)e * p.c_stride + row * p.ldc + col;
-        if constexpr (EPI == kPoly || EPI == kApply || EPI == kLast) {
-          // b A + c A A, or a X + P X, from both parts
-          const half4_t yh = *reinterpret_cast<const half4_t*>(p.y.hi + e * p.y.stride + row * p.y.ld + col);
-          const half4_t yl = p.y.lo ? *reinterpret_cast<const half4_t*>(p.y.lo + e * p.y.stride + row * p.y.ld + col)
-                                    : (half4_t){0, 0, 0, 0};
+    for (int it = 0; it < 4; ++it) {
+      const int r = 8 * it + lr;
+      float v[8];
+      __builtin_memcpy(v, tile + r * 64 + 4 * ((2 * lc) ^ (r & 15)), 16);
+      __builtin_memcpy(v + 4, tile + r * 64 + 4 * ((2 * lc + 1) ^ (r & 15)), 16);
+      if (row0 + r < p.m && col_in) finish(row0 + r, col, y[i % 2][it], v);
+    }
+    if (mirror) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) v[c] = up * (fmaf(p.g, (float)yl[c], v[c]) + p.g * (float)yh[c]);
+      for (int it = 0; it < 4; ++it) {
+        const int c = 16 * it + lane / 4;
+        const int64_t row = col0 + c, to = row0 + 8 * (lane % 4);
+        if (row >= p.n || to >= p.ldc) continue;
+        float v[8];
+#pragma unroll
+        for (int b = 0; b < 8; ++b) {
+          const int r = 8 * (lane % 4) + b;
+          v[b] = tile[r * 64 + 4 * ((c / 4) ^ (r & 15)) + c % 4];
         }
-        if constexpr (EPI == kLast) {
-          const int count = p.n - col < 4 ? (int)(p.n - col) : 4;
-          if (count <= 0) continue;
-          const int64_t o = ((int64_t)e * p.m + row) * p.n + col;
-          if (p.out_dtype == 0) put4<0>(p.out, o, count, p.wide, v);
-          else if (p.out_dtype == 1) put4<1>(p.out, o, count, p.wide, v);
-          else put4<2>(p.out, o, count, p.wide, v);
-        } else {
-          half4_t hi, lo;
-          split(v, &hi, &lo);
-          *reinterpret_cast<half4_t*>(p.c_hi + at) = hi;
-          if (p.c_lo) *reinterpret_cast<half4_t*>(p.c_lo + at) = lo;
-          if (SYM && ti < tj) {                  // the mirrored tile
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              if (col + c >= p.n) continue;
-              const int64_t to = (int64_t)e * p.c_stride + (col + c) * p.ldc + row;
-              p.c_hi[to] = hi[c];
-              if (p.c_lo) p.c_lo[to] = lo[c];
-            }
-          }
-        }
+        Given m = {};
+        if constexpr (EPI == kPoly) m = given(row, to);
+        finish(row, to, m, v);
       }
     }
   }
 }
 
-template <int T, bool AM, bool BM, int EPI>
-hipError_t gemm(const NsGemmArgs& a, hipStream_t s) {
-  const int64_t tm = (a.m + T - 1) / T, tn = (a.n + T - 1) / T;
-  const int64_t per = EPI == kGram || EPI == kPoly ? tn * (tn + 1) / 2 : tm * tn;
-  ns_gemm_kernel<T, AM, BM, EPI><<<(unsigned)(per * a.batch), 64 * TileShape<T>::kNW, 0, s>>>(a);
+template <typename S>
+int64_t tiles_of(bool sym, int64_t m, int64_t n) {
+  const int64_t tm = (m + S::TM - 1) / S::TM, tn = (n + S::TN - 1) / S::TN;
+  if (!sym) return tm * tn;
+  int64_t t = 0;
+  for (int64_t i = 0; i * (S::TM / S::TN) < tn; ++i) t += tn - i * (S::TM / S::TN);
+  return t;
+}
+
+template <typename S, bool AM, bool BM, int EPI, bool EXACT>
+hipError_t gemm(NsGemmArgs a, hipStream_t s) {
+  a.tiles = (int32_t)tiles_of<S>(EPI == kGram || EPI == kPoly, a.m, a.n);
+  ns_gemm_kernel<S, AM, BM, EPI, EXACT><<<(unsigned)(a.tiles * a.batch), 64 * S::NW, 0, s>>>(a);
   return hipGetLastError();
 }
 
-template <int T>
+template <typename S, bool EXACT>
 hipError_t one_product(int epi, bool tall, const NsGemmArgs& a, hipStream_t s) {
-  if (epi == kGram) return tall ? gemm<T, true, true, kGram>(a, s) : gemm<T, false, false, kGram>(a, s);
-  if (epi == kPoly) return gemm<T, false, false, kPoly>(a, s);
-  if (epi == kApply) return tall ? gemm<T, false, true, kApply>(a, s) : gemm<T, false, true, kApply>(a, s);
-  return gemm<T, false, true, kLast>(a, s);
+  if (epi == kGram)
+    return tall ? gemm<S, true, true, kGram, EXACT>(a, s) : gemm<S, false, false, kGram, EXACT>(a, s);
+  if (epi == kPoly) return gemm<S, false, false, kPoly, EXACT>(a, s);
+  if (epi == kApply) return gemm<S, false, true, kApply, EXACT>(a, s);
+  return gemm<S, false, true, kLast, EXACT>(a, s);
 }
 
 hipError_t product(int epi, bool tall, const NsGemmArgs& a, hipStream_t s) {
-  return one_product<128>(epi, tall, a, s);
+  // Wide where it has a tile for every CU.  Deep / Wide, microseconds a launch:
+  // 44 Gram tiles of 5120 x 2048 46 / 76, 80 (exact) of four 1000 x 2047 61 / 92;
+  // 256 update tiles of the latter 71 / 61, 320 of the former 71 / 65; 128
+  // matrices of 2048 x 768: A 242 / 214, P 139 / 142, X 682 / 562.
+  if (a.batch * tiles_of<Wide>(epi == kGram || epi == kPoly, a.m, a.n) >= 256)
+    return a.exact ? one_product<Wide, true>(epi, tall, a, s) : one_product<Wide, false>(epi, tall, a, s);
+  return a.exact ? one_product<Deep, true>(epi, tall, a, s) : one_product<Deep, false>(epi, tall, a, s);
 }
 
 int64_t pad64(int64_t v) { return (v + 63) / 64 * 64; }
@@ -438,11 +544,13 @@ bool ns_bounds(int steps, float a, float b, float c, NsScales* out) {
   return true;
 }
 
-// Matrices that are taken together: as many as fit 1 GiB of workspace.
+// Matrices that are taken together: as many as fit 4 GiB of workspace (128 of
+// 2048 x 768 together take 5.2 ms; 62 at a time 5.7, 16, whose X would stay in
+// the last-level cache, 5.7: their launches do not fill the last round of CUs).
 int64_t ns_batch(int64_t batch, int64_t rows, int64_t cols) {
   const int64_t n = rows < cols ? rows : cols;
   const int64_t one = 8 * rows * pad64(cols) + 8 * n * pad64(n);
-  int64_t c = (1LL << 30) / one;
+  int64_t c = (4LL << 30) / one;
   c = c < 1 ? 1 : (c > 32768 ? 32768 : c);
   return c < batch ? c : batch;
 }
@@ -483,18 +591,17 @@ hipError_t launch_newton_schulz(const NsArgs& a, hipStream_t s) {
       const NsMatrix A = {a.sq[0], a.sq[1], ns, ldn, (uint32_t)(ns * 2)};
       const NsMatrix P = {a.sq[2], a.sq[3], ns, ldn, (uint32_t)(ns * 2)};
       NsGemmArgs g{};
-      g.batch = m; g.parts = a.exact ? 3 : 1; g.k0 = a.k0; g.growth = a.scales.growth;
+      g.batch = m; g.exact = a.exact; g.k0 = a.k0; g.growth = a.scales.growth;
       g.drop = i * a.scales.growth;
       // A
       g.a = g.b = X; g.m = g.n = n; g.k = tall ? src.rows : src.cols;
-      g.c_hi = a.sq[0]; g.c_lo = a.exact ? a.sq[1] : nullptr; g.c_stride = ns; g.ldc = ldn;
+      g.c_hi = a.sq[0]; g.c_lo = a.sq[1]; g.c_stride = ns; g.ldc = ldn;
       g.f = a.scales.a / (a.scales.x * a.scales.x);
       st = product(kGram, tall, g, s);
       if (st != hipSuccess) break;
       // P
       g.a = g.b = g.y = A; g.k = n;
-      if (!a.exact) g.y.lo = nullptr;
-      g.c_hi = a.sq[2]; g.c_lo = a.exact ? a.sq[3] : nullptr;
+      g.c_hi = a.sq[2]; g.c_lo = a.sq[3];
       g.f = a.c * a.scales.p / (a.scales.a * a.scales.a);
       g.g = a.b * a.scales.p / a.scales.a;
       st = product(kPoly, tall, g, s);
@@ -507,7 +614,6 @@ hipError_t launch_newton_schulz(const NsArgs& a, hipStream_t s) {
       g.f = 1.0f / a.scales.p; g.g = a.a; g.up = a.out_scale / a.scales.x;
       g.out = static_cast<char*>(a.out) + (size_t)(first * src.rows * src.cols) * e1;
       g.out_dtype = a.out_dtype;
-      g.wide = src.cols % 4 == 0;
       st = product(last ? kLast : kApply, tall, g, s);
       _Float16* sw = x; x = y; y = sw;
       sw = xl; xl = yl; yl = sw;
