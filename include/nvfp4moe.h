@@ -716,7 +716,8 @@ int nvfp4_lora_matvec(const void* x, int x_dtype, int64_t tokens, int64_t ld_x,
  * The norm is binary64.  X is kept to 22 bits.  float32 and fp16 results take
  * products of all 22 bits, summed in binary32 (errors as of a binary32
  * computation); bf16 results take products of the upper 11 bits, which stay
- * below bf16's own rounding (2e-3 of the result's norm).  A zero matrix gives
+ * below bf16's own rounding (2e-3 of the result's norm).  Matrices with a side
+ * of at most 64 are computed in binary64 (unless a^(2 steps) > 2^26).  A zero matrix gives
  * zeros; one that holds an infinity or NaN gives NaN throughout, and no other
  * matrix is touched by it.  Results are bitwise reproducible; a matrix's last
  * bits may differ between calls with other numbers of matrices.

@@ -23,7 +23,7 @@ LIB = os.path.join(HERE, "libnvfp4moe.so")
 DEBUG_LIB = os.path.join(HERE, "libnvfp4moe_debug.so")
 SOURCES = ["quantize.hip", "route.hip", "gemm.hip", "single_pass.hip", "backward.hip",
            "combine.hip", "router.hip", "tokens.hip", "matvec.hip", "lora.hip",
-           "newton_schulz.hip", "capi.hip", "noalloc.hip"]
+           "newton_schulz.hip", "newton_schulz_small.hip", "capi.hip", "noalloc.hip"]
 DEBUG_SOURCES = ["route.hip", "capi.hip"]      # the sources that read NVFP4_DEBUG_CHECKS
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

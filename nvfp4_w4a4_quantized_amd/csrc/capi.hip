@@ -1111,6 +1111,7 @@ constexpr int kMaxSteps = 64;
 struct NsLayout {
   double* norms; int32_t* k0;
   _Float16* x[4]; _Float16* sq[4];
+  double* parts; double* q;   // of a short side alone
   size_t bytes;
 };
 
@@ -1126,6 +1127,13 @@ static NsLayout carve_ns(void* ws, int64_t batch, int64_t rows, int64_t cols, bo
   for (int i = 0; i < 4; ++i)
     if (exact || i % 2 == 0) L.sq[i] = c.take<_Float16>(ns);
   L.bytes = c.used;
+  if (n <= 64) {              // (whichever of the two the coefficients choose)
+    Carver d(ws);
+    const int64_t most = ns_small_batch(batch), side = ns_small_side(n), tiles = side / 16 * (side / 16 + 1) / 2;
+    L.parts = d.take<double>((size_t)(most * ns_small_shares(most, rows < cols ? cols : rows) * tiles * 256));
+    L.q = d.take<double>((size_t)(most * side * side));
+    if (d.used > L.bytes) L.bytes = d.used;
+  }
   return L;
 }
 
@@ -1168,6 +1176,9 @@ int newton_schulz(const void* g, int dtype, int64_t batch, int64_t rows, int64_t
     n.x[i] = L.x[i];
     n.sq[i] = L.sq[i];
   }
+  n.small_parts = L.parts; n.small_q = L.q;
+  if (ns_is_small(rows, cols, steps, a, b, c))
+    return hip_status(launch_newton_schulz_small(n, static_cast<hipStream_t>(stream)));
   return hip_status(launch_newton_schulz(n, static_cast<hipStream_t>(stream)));
 }
 

@@ -334,10 +334,18 @@ struct NsArgs {
   double* norms; int32_t* k0;
   _Float16* x[4];             // X hi, lo, the next X hi, lo
   _Float16* sq[4];            // A hi, lo, P hi, lo
+  double* small_parts; double* small_q;   // of a short side alone
 };
 bool ns_bounds(int steps, float a, float b, float c, NsScales* out);
 int64_t ns_batch(int64_t batch, int64_t rows, int64_t cols);
 int ns_norm_parts(int64_t batch, int64_t rows);
 hipError_t launch_newton_schulz(const NsArgs& a, hipStream_t s);
+
+// ---- newton_schulz_small.hip ----
+bool ns_is_small(int64_t rows, int64_t cols, int steps, float a, float b, float c);
+int64_t ns_small_side(int64_t n);
+int ns_small_shares(int64_t batch, int64_t m);
+int64_t ns_small_batch(int64_t batch);
+hipError_t launch_newton_schulz_small(const NsArgs& a, hipStream_t s);
 
 }  // namespace nvfp4
