@@ -263,7 +263,7 @@ struct LoraDownArgs {
   const int32_t* ids; int32_t adapters, rank;
   const void* a;              // [adapters, rank, k]
   float* h;                   // [lora_shares(tokens, k), tokens, rank]
-  int64_t share; int by_token;   // (the launcher's)
+  int64_t share;              // (the launcher's)
 };
 struct LoraUpArgs {
   const float* h; int shares; // [shares, tokens, rank], added up
@@ -274,7 +274,7 @@ struct LoraUpArgs {
   const void* base; int base_dtype; int64_t ld_base;   // nullable [tokens, ld_base]: the output's type or binary32
   void* out; int out_dtype;   // [tokens, n]
   float* h_out; int h_scaled; // nullable [tokens, rank]: h, times the scale if h_scaled
-  int by_token;               // (the launcher's)
+  int64_t wide;               // (the launcher's)
 };
 struct LoraSortArgs {
   const int32_t* ids; int64_t tokens; int32_t adapters, chunk, max_entries;

@@ -12,15 +12,18 @@
 //
 // Tokens of one adapter are multiplied together.  Few tokens (up to kWindow):
 // a workgroup per token looks its adapter's tokens up and the first of them
-// does the work of all.  Many: a workgroup takes 64 consecutive tokens and
-// does one adapter after the other, so a batch whose requests lie together
-// reads each token's row once and an adapter once per 64 tokens.
+// does the work of all.  Many: a workgroup takes 64 consecutive tokens and does
+// one adapter after the other, each keeping the results of its own tokens, so a
+// batch whose requests lie together reads each token's row once and an adapter
+// once per 64 tokens.
 //
 // Arithmetic: down multiplies in the type of x by MFMA 16x16x32 (binary32:
-// 16x16x4) into binary32; h and g stay binary32 and everything they enter is a
-// binary32 product (MFMA 16x16x4 of the exactly widened B, A, x and dy).  Sums
-// over K that several workgroups share are joined in workgroup order, sums
-// over tokens in token order per chunk: results do not depend on timing.
+// 16x16x4) into binary32; h and g stay binary32.  What they enter are binary32
+// products: of bf16 B, A, x and dy with the three bf16 parts of the binary32
+// value, an exact sum (MFMA 16x16x32), else MFMA 16x16x4 of the exactly widened
+// values.  Sums over K that several workgroups share are joined in workgroup
+// order, sums over tokens in token order per chunk: results do not depend on
+// timing.
 #include "elem.h"
 #include "launch.h"
 
@@ -39,11 +42,6 @@ constexpr int kRanks = 64;      // ranks of one pass
 
 // ---- the tokens of one adapter ------------------------------------------
 
-struct TokenList {
-  uint16_t at[kWindow];         // offsets from the window's first token
-  uint64_t mask[kWaves];
-};
-
 __device__ __forceinline__ int key_of(int id, int adapters) {
   return id >= 0 && id < adapters ? id : -1;
 }
@@ -53,50 +51,42 @@ __device__ __forceinline__ int bits_below(uint64_t mask) {
                                    __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
 }
 
-// f(adapter or -1, number of listed tokens, first token of the window) for
-// every adapter that this workgroup is to do.  Every thread calls f alike, and
-// the list stays as it is until f returns.
-template <typename F>
-__device__ __forceinline__ void for_each_adapter(const int32_t* ids, int64_t tokens, int adapters,
-                                                 bool by_token, TokenList& list, F f) {
+struct TokenList {
+  uint16_t at[kWindow];
+  uint64_t mask[kWaves];
+};
+
+// The tokens (up to kWindow in all) that share token `slot`'s adapter, into
+// list.at in ascending order; returns their number, 0 if the slot is not the
+// first of them.
+__device__ __forceinline__ int tokens_like(const int32_t* ids, int tokens, int adapters, int slot,
+                                           TokenList& list, int* adapter) {
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-  if (by_token) {
-    const int slot = blockIdx.x;
-    const int key = key_of(ids[slot], adapters);
-    const bool in = (int)threadIdx.x < (int)tokens;
-    const bool mine = in && key_of(ids[in ? threadIdx.x : 0], adapters) == key;
-    const uint64_t mask = __ballot(mine);
-    if (lane == 0) list.mask[wave] = mask;
-    __syncthreads();
-    int m = 0, before = 0;
-    bool earlier = false;
+  const int key = key_of(ids[slot], adapters);
+  const bool in = (int)threadIdx.x < tokens;
+  const bool mine = in && key_of(ids[in ? threadIdx.x : 0], adapters) == key;
+  const uint64_t mask = __ballot(mine);
+  if (lane == 0) list.mask[wave] = mask;
+  __syncthreads();
+  int m = 0, before = 0;
+  bool earlier = false;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      const uint64_t b = list.mask[w];
-      if (w < wave) before += __popcll(b);
-      m += __popcll(b);
-      const int to = slot - w * kWave;      // tokens of this wave before the slot
-      if (to > 0) earlier |= (to >= kWave ? b : b & ((1ull << to) - 1)) != 0;
-    }
-    if (earlier) return;
-    if (mine) list.at[before + bits_below(mask)] = (uint16_t)threadIdx.x;
-    __syncthreads();
-    f(key, m, (int64_t)0);
-    return;
+  for (int w = 0; w < kWaves; ++w) {
+    const uint64_t b = list.mask[w];
+    if (w < wave) before += __popcll(b);
+    m += __popcll(b);
+    const int to = slot - w * kWave;      // tokens of this wave before the slot
+    if (to > 0) earlier |= (to >= kWave ? b : b & ((1ull << to) - 1)) != 0;
   }
-  const int64_t first = (int64_t)blockIdx.x * kGroup;
-  const bool in = first + lane < tokens;
-  const int key = in ? key_of(ids[first + lane], adapters) : -2;
-  uint64_t todo = __ballot(in);
-  while (todo != 0) {
-    const int k = __shfl(key, __builtin_ctzll(todo));
-    const uint64_t mask = __ballot(key == k);
-    if (wave == 0 && key == k) list.at[bits_below(mask)] = (uint16_t)lane;
-    __syncthreads();
-    f(k, (int)__popcll(mask), first);
-    __syncthreads();
-    todo &= ~mask;
-  }
+  if (mine && !earlier) list.at[before + bits_below(mask)] = (uint16_t)threadIdx.x;
+  __syncthreads();
+  *adapter = key;
+  return earlier ? 0 : m;
+}
+
+// Lane l's key among 64 consecutive tokens: the adapter, -1 without, -2 past the last.
+__device__ __forceinline__ int key_at(const int32_t* ids, int64_t tokens, int adapters, int64_t t) {
+  return t < tokens ? key_of(ids[t], adapters) : -2;
 }
 
 // ---- down: the long rows' products with the rank's rows --------------------
@@ -131,97 +121,191 @@ __device__ __forceinline__ f32x4_t product(const Piece<DT>& a, const Piece<DT>& 
   }
 }
 
-// Grid: x = tokens or groups of 64 tokens, y = shares of K, z = 64 ranks each.
-// A wave takes every fourth 128-byte piece of the rows; lane l has bytes
-// 16 (l / 16) of 64 of rank l % 16 and of token l % 16, RT times 16 ranks by
-// four times 16 tokens.
-template <int DT, int RT>
+// acc[rt][j] += ranks' rows ar[rt] times tokens' rows xr[j] over [k0, k1), a
+// wave's share of it: every fourth 128-byte piece.  Lane l has bytes 16 (l / 16)
+// of each 64 of its rows.
+template <int DT, int RT, int TT>
+__device__ __forceinline__ void down_products(const typename Elem<DT>::type* const (&ar)[RT],
+                                              const typename Elem<DT>::type* const (&xr)[TT],
+                                              int64_t k0, int64_t k1, int wave, int q,
+                                              f32x4_t (&acc)[RT][TT]) {
+  constexpr int E = Piece<DT>::kN, kStep = 8 * E;   // elements of a piece; of 128 bytes
+  int64_t c = k0 + wave * kStep;
+  // whole pieces without a branch, so that their loads are in flight together
+  for (; c + kStep <= k1; c += kWaves * kStep) {
+    Piece<DT> a[2][RT], x[2][TT];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+#pragma unroll
+      for (int j = 0; j < TT; ++j) x[u][j].load(xr[j] + c + (4 * u + q) * E);
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) a[u][rt].load(ar[rt] + c + (4 * u + q) * E);
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int j = 0; j < TT; ++j) acc[rt][j] = product<DT>(a[u][rt], x[u][j], acc[rt][j]);
+  }
+  if (c < k1) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int64_t at = c + (4 * u + q) * E;
+      Piece<DT> a[RT];
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) a[rt] = piece_until<DT>(ar[rt], at, k1);
+#pragma unroll
+      for (int j = 0; j < TT; ++j) {
+        const Piece<DT> x = piece_until<DT>(xr[j], at, k1);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) acc[rt][j] = product<DT>(a[rt], x, acc[rt][j]);
+      }
+    }
+  }
+}
+
+// Grid: x = tokens (SLOT) or groups of 64 tokens, y = shares of K, z = 64 ranks
+// each.  TT times 16 tokens at once; position p of a group is token
+// first + list.at[p] (SLOT) or first + p.
+template <int DT, int RT, bool SLOT>
 __global__ __launch_bounds__(kThreads) void lora_down_kernel(LoraDownArgs p) {
   typedef typename Elem<DT>::type T;
-  constexpr int E = Piece<DT>::kN, kStep = 8 * E;   // elements of a piece; of 128 bytes
+  constexpr int TT = SLOT ? 1 : 4;
   __shared__ TokenList list;
-  __shared__ f32x4_t red[kWaves][4][kWave];
+  __shared__ f32x4_t red[kWaves][TT][kWave];
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   const int i = lane % 16, q = lane / 16;
   const int r0 = blockIdx.z * kRanks;
   const int64_t k0 = blockIdx.y * p.share, k1 = k0 + p.share < p.k ? k0 + p.share : p.k;
   float* const out = p.h + blockIdx.y * p.tokens * p.rank;
-  for_each_adapter(p.ids, p.tokens, p.adapters, p.by_token, list, [&](int s, int m, int64_t first) {
-    for (int g0 = 0; g0 < m; g0 += kGroup) {
-      const int left = m - g0;
-      f32x4_t acc[RT][4];
+  const T* const x = static_cast<const T*>(p.x);
+  auto one = [&](int s, const T* const (&xr)[TT], auto keep) {
+    f32x4_t acc[RT][TT];
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
+    for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[rt][j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
-      if (s >= 0) {
-        const T* xr[4];
-        const T* ar[RT];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int at = 16 * j + i;
-          xr[j] = static_cast<const T*>(p.x) + (first + list.at[g0 + (at < left ? at : 0)]) * p.ld_x;
-        }
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-          const int r = r0 + 16 * rt + i;
-          ar[rt] = static_cast<const T*>(p.a) + ((int64_t)s * p.rank + (r < p.rank ? r : p.rank - 1)) * p.k;
-        }
-        for (int64_t c = k0 + wave * kStep; c < k1; c += kWaves * kStep) {
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int64_t at = c + u * 4 * E + q * E;
-            Piece<DT> a[RT];
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) a[rt] = piece_until<DT>(ar[rt], at, k1);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if (16 * j >= left) continue;
-              const Piece<DT> x = piece_until<DT>(xr[j], at, k1);
-#pragma unroll
-              for (int rt = 0; rt < RT; ++rt) acc[rt][j] = product<DT>(a[rt], x, acc[rt][j]);
-            }
-          }
-        }
-      }
+      for (int j = 0; j < TT; ++j) acc[rt][j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+    if (s >= 0) {
+      const T* ar[RT];
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < 4; ++j) red[wave][j][lane] = acc[rt][j];
-        __syncthreads();
-        f32x4_t v = red[0][wave][lane];
-#pragma unroll
-        for (int w = 1; w < kWaves; ++w) v += red[w][wave][lane];
-        const int at = 16 * wave + i, r = r0 + 16 * rt + 4 * q;
-        if (at < left) {
-          float* o = out + (first + list.at[g0 + at]) * p.rank + r;
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (r + e < p.rank) o[e] = v[e];
-        }
+        const int r = r0 + 16 * rt + i;
+        ar[rt] = static_cast<const T*>(p.a) + ((int64_t)s * p.rank + (r < p.rank ? r : p.rank - 1)) * p.k;
       }
+      down_products<DT, RT, TT>(ar, xr, k0, k1, wave, q, acc);
     }
-  });
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < TT; ++j) red[wave][j][lane] = acc[rt][j];
+      __syncthreads();
+      if (wave >= TT) continue;
+      f32x4_t v = red[0][wave % TT][lane];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) v += red[w][wave % TT][lane];
+      const int r = r0 + 16 * rt + 4 * q;
+      const int64_t tok = keep(16 * wave + i);
+      if (tok < 0) continue;
+      float* o = out + tok * p.rank + r;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (r + e < p.rank) o[e] = v[e];
+    }
+  };
+  if constexpr (SLOT) {
+    int s;
+    const int m = tokens_like(p.ids, (int)p.tokens, p.adapters, blockIdx.x, list, &s);
+    for (int g0 = 0; g0 < m; g0 += 16) {
+      const T* xr[1] = {x + list.at[g0 + i < m ? g0 + i : g0] * p.ld_x};
+      one(s, xr, [&](int at) -> int64_t { return g0 + at < m ? list.at[g0 + at] : -1; });
+    }
+  } else {
+    const int64_t first = (int64_t)blockIdx.x * kGroup;
+    const int key = key_at(p.ids, p.tokens, p.adapters, first + lane);
+    uint64_t todo = __ballot(key != -2);
+    while (todo != 0) {
+      const int lead = __builtin_ctzll(todo), s = __shfl(key, lead);
+      const uint64_t mask = __ballot(key == s);
+      // (other adapters' columns take the first token's row: no more is read)
+      const T* xr[TT];
+#pragma unroll
+      for (int j = 0; j < TT; ++j)
+        xr[j] = x + (first + ((mask >> (16 * j + i)) & 1 ? 16 * j + i : lead)) * p.ld_x;
+      one(s, xr, [&](int at) -> int64_t { return (mask >> at) & 1 ? first + at : -1; });
+      todo &= ~mask;
+    }
+  }
 }
 
 // ---- up: the rank's values into long rows ----------------------------------
 
-template <int DT>
-__device__ __forceinline__ f32x4_t four_until(const typename Elem<DT>::type* row, int at, int end) {
-  typename Elem<DT>::type v[4];
-  if (at + 4 <= end) {
-    __builtin_memcpy(v, row + at, sizeof(v));
-  } else {
+// The three bf16 parts of a binary32 value: the upper half of its bits, of what
+// is left of it, and the rest.  The lower parts of an infinity are the largest
+// finite value's: they add to it with its sign.
+__device__ __forceinline__ void bf16_parts(float v, uint16_t (&part)[3]) {
+  part[0] = (uint16_t)(__float_as_uint(v) >> 16);
+  v = __builtin_amdgcn_fmed3f(v, -__FLT_MAX__, __FLT_MAX__);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = at + e < end ? row[at + e] : (typename Elem<DT>::type)0;
+  for (int i = 1; i < 3; ++i) {
+    v -= __uint_as_float(__float_as_uint(v) & 0xFFFF0000u);
+    part[i] = (uint16_t)(__float_as_uint(v) >> 16);
   }
-  return (f32x4_t){Elem<DT>::to_float(v[0]), Elem<DT>::to_float(v[1]), Elem<DT>::to_float(v[2]),
-                   Elem<DT>::to_float(v[3])};
 }
 
+// c h of up to TOK tokens and 64 ranks, as the products' operand.  bf16: a step
+// is 32 k of one MFMA, tokens' rows of 64 bytes (16-byte chunk k of row t at
+// k ^ (t / 4) % 4).  Up to 16 ranks take two steps, the first two parts beside
+// each other and the third beside zeros; more take three, a part each, per 32
+// ranks.  Else: rows of binary32.
+template <int DT, int TOK>
+struct Ranked {
+  static constexpr int kLd = kRanks + 4;
+  union {
+    uint16_t part[DT == 1 ? 6 * TOK * 32 : 8];
+    float row[DT == 1 ? 4 : TOK * kLd];
+  };
+  static __device__ __forceinline__ int at(int step, int t, int k) {
+    return (step * TOK + t) * 32 + 8 * ((k / 8) ^ ((t >> 2) & 3)) + k % 8;
+  }
+  __device__ __forceinline__ void put(int t, int r, bool narrow, float v) {
+    if constexpr (DT == 1) {
+      uint16_t b[3];
+      bf16_parts(v, b);
+      if (narrow) {
+        part[at(0, t, r)] = b[0];
+        part[at(0, t, 16 + r)] = b[1];
+        part[at(1, t, r)] = b[2];
+        part[at(1, t, 16 + r)] = 0;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 3; ++i) part[at(r / 32 * 3 + i, t, r % 32)] = b[i];
+      }
+    } else {
+      row[t * kLd + r] = v;
+    }
+  }
+};
+
+// The rows' values of B from rank r on: 8 of bf16, 4 of the others.
 template <int DT>
-__device__ __forceinline__ void add16(const void* base, int64_t at, int count, float (&v)[16]) {
+struct RankPiece {
+  static constexpr int kN = DT == 1 ? 8 : 4;
+  typename Elem<DT>::type v[kN];
+  __device__ __forceinline__ void load(const typename Elem<DT>::type* row, int r, int end) {
+    if (r + kN <= end) {
+      __builtin_memcpy(v, row + r, sizeof(v));
+    } else {
+#pragma unroll
+      for (int e = 0; e < kN; ++e) v[e] = r + e < end ? row[r + e] : (typename Elem<DT>::type)0;
+    }
+  }
+};
+
+// Values of 16 columns from `at` on, `count` of them inside.
+template <int DT>
+__device__ __forceinline__ void get16(const void* base, int64_t at, int count, float (&v)[16]) {
   typedef typename Elem<DT>::type T;
   const T* b = static_cast<const T*>(base) + at;
   if (count >= 16) {
@@ -230,112 +314,232 @@ __device__ __forceinline__ void add16(const void* base, int64_t at, int count, f
       Piece<DT> p;
       p.load(b + c);
 #pragma unroll
-      for (int e = 0; e < Piece<DT>::kN; ++e) v[c + e] += p.get(e);
+      for (int e = 0; e < Piece<DT>::kN; ++e) v[c + e] = p.get(e);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = e < count ? Elem<DT>::to_float(b[e]) : 0.0f;
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ void put16(void* out, int64_t at, int count, const float (&v)[16]) {
+  typename Elem<DT>::type* o = static_cast<typename Elem<DT>::type*>(out) + at;
+  if (count >= 16) {
+#pragma unroll
+    for (int c = 0; c < 16; c += Piece<DT>::kN) {
+      Piece<DT> w;
+#pragma unroll
+      for (int e = 0; e < Piece<DT>::kN; ++e) w.set(e, v[c + e]);
+      w.store(o + c);
     }
   } else {
 #pragma unroll
     for (int e = 0; e < 16; ++e)
-      if (e < count) v[e] += Elem<DT>::to_float(b[e]);
+      if (e < count) o[e] = Elem<DT>::from_float(v[e]);
   }
 }
 
-// Grid: x = tokens or groups of 64 tokens, y = 256 columns each, 64 a wave.
-// MFMA row 16 (i / 4) + 4 j + i % 4 of the wave's 64 is row i of product j, so
-// that a lane ends with 16 consecutive columns of its token.
-template <int DT, int OT>
+// Grid: x = tokens (SLOT) or groups of 64 tokens, y = p.wide columns each, 64 a
+// wave at a time.  MFMA row 16 (i / 4) + 4 j + i % 4 of the wave's 64 is row i of
+// product j, so that a lane ends with 16 consecutive columns of its token.  The
+// sums start from the base's values.
+template <int DT, int OT, bool SLOT>
 __global__ __launch_bounds__(kThreads) void lora_up_kernel(LoraUpArgs p) {
   typedef typename Elem<DT>::type T;
-  typedef typename Elem<OT>::type O;
-  constexpr int kLd = kRanks + 4;
+  constexpr int TT = SLOT ? 1 : 4, TOK = 16 * TT;
+  constexpr int kPieces = DT == 1 ? 2 : 4;      // of 64 ranks
   __shared__ TokenList list;
-  __shared__ __align__(16) float hs[kGroup * kLd];
+  __shared__ __align__(16) Ranked<DT, TOK> hs;
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   const int i = lane % 16, q = lane / 16;
-  const int64_t n0 = (int64_t)blockIdx.y * kThreads + wave * kWave;
-  for_each_adapter(p.ids, p.tokens, p.adapters, p.by_token, list, [&](int s, int m, int64_t first) {
-    const float c = s >= 0 ? (p.scale ? p.scale[s] : 1.0f) : 0.0f;
-    for (int g0 = 0; g0 < m; g0 += kGroup) {
-      const int left = m - g0 < kGroup ? m - g0 : kGroup;
-      f32x4_t acc[4][4];
+  const int64_t first = SLOT ? 0 : (int64_t)blockIdx.x * kGroup;
+  const int64_t n_end = (int64_t)(blockIdx.y + 1) * p.wide < p.n ? (int64_t)(blockIdx.y + 1) * p.wide : p.n;
+  int s = -1, m = TOK, key = -2;
+  if constexpr (SLOT) {
+    m = tokens_like(p.ids, (int)p.tokens, p.adapters, blockIdx.x, list, &s);
+  } else {
+    key = key_at(p.ids, p.tokens, p.adapters, first + lane);
+  }
+
+  // h of the tokens in `mask` (positions of the group), zeros for the others
+  auto stage = [&](int adapter, uint64_t mask, int g0, int r0, float c, bool narrow) {
+    const int ranks = p.rank - r0 < kRanks ? p.rank - r0 : kRanks;
+    const int padded = DT == 1 ? (narrow ? 16 : (ranks + 31) / 32 * 32) : (ranks + 15) / 16 * 16;
+    for (int v = threadIdx.x; v < TOK * padded; v += kThreads) {
+      const int t = v / padded, r = v % padded;
+      float h = 0.0f;
+      if ((mask >> t) & 1 && r < ranks) {
+        const int64_t tok = SLOT ? list.at[g0 + t] : first + t;
+        const int64_t at = tok * p.rank + r0 + r, step = p.tokens * p.rank;
+        if (adapter >= 0) {
+          // eight shares in flight, added in order
+          h = p.h[at];
+          for (int w = 1; w < p.shares; w += 8) {
+            float more[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+            for (int u = 0; u < 8; ++u) more[u] = w + u < p.shares ? p.h[at + (w + u) * step] : 0.0f;
 #pragma unroll
-        for (int t = 0; t < 4; ++t) acc[j][t] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
-      for (int r0 = 0; r0 < p.rank; r0 += kRanks) {
-        const int ranks = p.rank - r0 < kRanks ? p.rank - r0 : kRanks;
-        const int padded = (ranks + 15) / 16 * 16;
-        __syncthreads();
-        for (int v = threadIdx.x; v < left * padded; v += kThreads) {
-          const int t = v / padded, r = v % padded;
-          const int64_t at = (first + list.at[g0 + t]) * p.rank + r0 + r;
-          float h = 0.0f;
-          if (r < ranks) {
-            if (s >= 0) {
-              h = p.h[at];
-              for (int w = 1; w < p.shares; ++w) h += p.h[w * p.tokens * p.rank + at];
-            }
-            if (p.h_out && blockIdx.y == 0) p.h_out[at] = p.h_scaled ? c * h : h;
+            for (int u = 0; u < 8; ++u) h = w + u < p.shares ? h + more[u] : h;
           }
-          hs[t * kLd + r] = c * h;
         }
-        __syncthreads();
-        if (s < 0 || n0 >= p.n) continue;
-        for (int rb = 0; rb < padded; rb += 16) {
-          f32x4_t h[4];
+        if (p.h_out && blockIdx.y == 0) p.h_out[at] = p.h_scaled ? c * h : h;
+        h *= c;
+      }
+      hs.put(t, r, narrow, h);
+    }
+  };
+  // acc += the adapter's rows of B from column n0 + ... times h, for ranks r0 ..
+  auto multiply = [&](const RankPiece<DT> (&b)[kPieces], int j, int r0, bool narrow, f32x4_t (&acc)[TT]) {
+    const int ranks = p.rank - r0 < kRanks ? p.rank - r0 : kRanks;
+    if constexpr (DT == 1) {
+      const int steps = narrow ? 2 : (ranks + 31) / 32 * 3;
 #pragma unroll
-          for (int t = 0; t < 4; ++t)
-            h[t] = 16 * t < left
-                       ? *reinterpret_cast<const f32x4_t*>(hs + (16 * t + i < left ? 16 * t + i : 0) * kLd + rb + 4 * q)
-                       : (f32x4_t){0.f, 0.f, 0.f, 0.f};
+      for (int st = 0; st < 6; ++st) {
+        if (st >= steps) continue;
+        bf16x8_t u;
+        __builtin_memcpy(&u, b[narrow ? 0 : st / 3].v, 16);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int64_t n = n0 + 16 * (i / 4) + 4 * j + i % 4;
-            const T* row = static_cast<const T*>(p.b) + ((int64_t)s * p.n + (n < p.n ? n : p.n - 1)) * p.rank;
-            const f32x4_t b = four_until<DT>(row, r0 + rb + 4 * q, p.rank);
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-              if (16 * t >= left) continue;
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                acc[j][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(b[e], h[t][e], acc[j][t], 0, 0, 0);
-            }
-          }
+        for (int t = 0; t < TT; ++t) {
+          const bf16x8_t h = *reinterpret_cast<const bf16x8_t*>(hs.part + Ranked<DT, TOK>::at(st, 16 * t + i, 8 * q));
+          acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u, h, acc[t], 0, 0, 0);
         }
       }
-      const int64_t n = n0 + 16 * q;
-      if (n >= p.n) continue;
-      const int count = p.n - n < 16 ? (int)(p.n - n) : 16;
+    } else {
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const int at = 16 * t + i;
-        if (at >= left) continue;
-        const int64_t tok = first + list.at[g0 + at];
-        float v[16];
+      for (int rb = 0; rb < 4; ++rb) {
+        if (16 * rb >= ranks) continue;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int t = 0; t < TT; ++t) {
+          const f32x4_t h = *reinterpret_cast<const f32x4_t*>(hs.row + (16 * t + i) * Ranked<DT, TOK>::kLd + 16 * rb + 4 * q);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[4 * j + e] = acc[j][t][e];
-        if (p.base) {
-          if (p.base_dtype == OT) add16<OT>(p.base, tok * p.ld_base + n, count, v);
-          else add16<0>(p.base, tok * p.ld_base + n, count, v);
-        }
-        O* o = static_cast<O*>(p.out) + tok * p.n + n;
-        if (count == 16) {
-#pragma unroll
-          for (int c0 = 0; c0 < 16; c0 += Piece<OT>::kN) {
-            Piece<OT> w;
-#pragma unroll
-            for (int e = 0; e < Piece<OT>::kN; ++e) w.set(e, v[c0 + e]);
-            w.store(o + c0);
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (e < count) o[e] = Elem<OT>::from_float(v[e]);
+          for (int e = 0; e < 4; ++e)
+            acc[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(Elem<DT>::to_float(b[rb].v[e]), h[e], acc[t], 0, 0, 0);
         }
       }
     }
-  });
+  };
+  auto load_b = [&](int adapter, int64_t n0, int j, int r0, bool narrow, RankPiece<DT> (&b)[kPieces]) {
+    const int64_t n = n0 + 16 * (i / 4) + 4 * j + i % 4;
+    const T* row = static_cast<const T*>(p.b) + ((int64_t)adapter * p.n + (n < p.n ? n : p.n - 1)) * p.rank;
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+      const int r = r0 + (DT == 1 ? (narrow ? 8 * (q % 2) : 32 * k + 8 * q) : 16 * k + 4 * q);
+      if ((DT == 1 ? 32 : 16) * k < p.rank - r0) b[k].load(row, r, p.rank);
+    }
+  };
+  auto token = [&](int g0, int at) -> int64_t { return SLOT ? list.at[g0 + at] : first + at; };
+  auto base16 = [&](int64_t tok, int64_t n, int count, float (&v)[16]) {
+    if (p.base && count > 0) {
+      if (p.base_dtype == OT) get16<OT>(p.base, tok * p.ld_base + n, count, v);
+      else get16<0>(p.base, tok * p.ld_base + n, count, v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[e] = 0.0f;
+    }
+  };
+  const bool narrow = p.rank <= 16;
+  const uint64_t here = SLOT ? 0 : __ballot(key != -2);
+
+  for (int g0 = 0; g0 < m; g0 += TOK) {
+    const uint64_t in = SLOT ? (m - g0 >= TOK ? (1ull << TOK % 64) - 1 : (1ull << (m - g0)) - 1) : here;
+    if constexpr (SLOT) {
+      // one adapter: its ranks once, if they fit, for all of the columns
+      const float c = s >= 0 && p.scale ? p.scale[s] : 1.0f;
+      const bool once = p.rank <= kRanks;
+      for (int64_t n0 = (int64_t)blockIdx.y * p.wide + wave * kWave; n0 - wave * kWave < n_end; n0 += kThreads) {
+        const int64_t n = n0 + 16 * q;
+        const int count = n_end - n < 16 ? (int)(n_end - n) : 16;
+        const int64_t tok = token(g0, (in >> i) & 1 ? i : 0);
+        f32x4_t acc[4][1];
+        float v[16];
+        base16(tok, n, count, v);
+        for (int r0 = 0; r0 < p.rank; r0 += kRanks) {
+          RankPiece<DT> b[4][kPieces];
+          if (s >= 0) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) load_b(s, n0, j, r0, narrow, b[j]);
+          }
+          if (!once || n0 - wave * kWave == (int64_t)blockIdx.y * p.wide) {
+            __syncthreads();
+            stage(s, in, g0, r0, c, narrow);
+            __syncthreads();
+          }
+          if (r0 == 0) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[j][0][e] = v[4 * j + e];
+          }
+          if (s >= 0) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) multiply(b[j], j, r0, narrow, acc[j]);
+          }
+        }
+        if (count > 0 && (in >> i) & 1) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[4 * j + e] = acc[j][0][e];
+          put16<OT>(p.out, tok * p.n + n, count, v);
+        }
+      }
+    } else {
+      // the group's adapters one after the other, 64 columns a wave
+      const int64_t n0 = (int64_t)blockIdx.y * p.wide + wave * kWave, n = n0 + 16 * q;
+      const int count = n_end - n < 16 ? (int)(n_end - n) : 16;
+      f32x4_t acc[4][TT];
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        float v[16];
+        base16(token(0, (in >> (16 * t + i)) & 1 ? 16 * t + i : 0), n, count, v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[j][t][e] = v[4 * j + e];
+      }
+      uint64_t todo = in;
+      while (todo != 0) {
+        const int a = __shfl(key, __builtin_ctzll(todo));
+        const uint64_t mask = __ballot(key == a);
+        todo &= ~mask;
+        const float c = a >= 0 && p.scale ? p.scale[a] : 1.0f;
+        for (int r0 = 0; r0 < p.rank; r0 += kRanks) {
+          RankPiece<DT> b[4][kPieces];
+          if (a >= 0) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) load_b(a, n0, j, r0, narrow, b[j]);
+          }
+          __syncthreads();
+          stage(a, mask, 0, r0, c, narrow);
+          __syncthreads();
+          if (a < 0) continue;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            f32x4_t now[TT];
+#pragma unroll
+            for (int t = 0; t < TT; ++t) now[t] = acc[j][t];
+            multiply(b[j], j, r0, narrow, now);
+#pragma unroll
+            for (int t = 0; t < TT; ++t)
+              if ((mask >> (16 * t + i)) & 1) acc[j][t] = now[t];
+          }
+        }
+      }
+      if (count > 0) {
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+          if (!((in >> (16 * t + i)) & 1)) continue;
+          float v[16];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[4 * j + e] = acc[j][t][e];
+          put16<OT>(p.out, (first + 16 * t + i) * p.n + n, count, v);
+        }
+      }
+    }
+  }
 }
 
 // ---- the way back -----------------------------------------------------------
@@ -545,16 +749,29 @@ __global__ __launch_bounds__(256) void lora_join_parts_kernel(LoraGradArgs p, co
 
 template <int DT>
 void down_dt(const LoraDownArgs& a, dim3 grid, hipStream_t s) {
-  if (a.rank <= 16) lora_down_kernel<DT, 1><<<grid, kThreads, 0, s>>>(a);
-  else if (a.rank <= 32) lora_down_kernel<DT, 2><<<grid, kThreads, 0, s>>>(a);
-  else lora_down_kernel<DT, 4><<<grid, kThreads, 0, s>>>(a);
+  const bool slot = a.tokens <= kWindow;
+  if (a.rank <= 16)
+    slot ? lora_down_kernel<DT, 1, true><<<grid, kThreads, 0, s>>>(a)
+         : lora_down_kernel<DT, 1, false><<<grid, kThreads, 0, s>>>(a);
+  else if (a.rank <= 32)
+    slot ? lora_down_kernel<DT, 2, true><<<grid, kThreads, 0, s>>>(a)
+         : lora_down_kernel<DT, 2, false><<<grid, kThreads, 0, s>>>(a);
+  else
+    slot ? lora_down_kernel<DT, 4, true><<<grid, kThreads, 0, s>>>(a)
+         : lora_down_kernel<DT, 4, false><<<grid, kThreads, 0, s>>>(a);
+}
+
+template <int DT, int OT>
+void up_out(const LoraUpArgs& a, dim3 grid, hipStream_t s) {
+  if (a.tokens <= kWindow) lora_up_kernel<DT, OT, true><<<grid, kThreads, 0, s>>>(a);
+  else lora_up_kernel<DT, OT, false><<<grid, kThreads, 0, s>>>(a);
 }
 
 template <int DT>
 void up_dt(const LoraUpArgs& a, dim3 grid, hipStream_t s) {
-  if (a.out_dtype == 0) lora_up_kernel<DT, 0><<<grid, kThreads, 0, s>>>(a);
-  else if (a.out_dtype == 1) lora_up_kernel<DT, 1><<<grid, kThreads, 0, s>>>(a);
-  else lora_up_kernel<DT, 2><<<grid, kThreads, 0, s>>>(a);
+  if (a.out_dtype == 0) up_out<DT, 0>(a, grid, s);
+  else if (a.out_dtype == 1) up_out<DT, 1>(a, grid, s);
+  else up_out<DT, 2>(a, grid, s);
 }
 
 template <int DT>
@@ -590,7 +807,6 @@ int32_t lora_chunk(int64_t tokens, int64_t k, int64_t n) {
 hipError_t launch_lora_down(LoraDownArgs a, hipStream_t s) {
   if (a.tokens == 0) return hipSuccess;
   const int shares = lora_shares(a.tokens, a.k);
-  a.by_token = a.tokens <= kWindow;
   a.share = ((a.k + shares - 1) / shares + 255) / 256 * 256;
   const dim3 grid((unsigned)token_blocks(a.tokens), shares, (a.rank + kRanks - 1) / kRanks);
   if (a.dtype == 0) down_dt<0>(a, grid, s);
@@ -601,8 +817,11 @@ hipError_t launch_lora_down(LoraDownArgs a, hipStream_t s) {
 
 hipError_t launch_lora_up(LoraUpArgs a, hipStream_t s) {
   if (a.tokens == 0) return hipSuccess;
-  a.by_token = a.tokens <= kWindow;
-  const dim3 grid((unsigned)token_blocks(a.tokens), (unsigned)((a.n + kThreads - 1) / kThreads));
+  // 256 columns a workgroup; more for a token's, while eight workgroups a CU are left
+  a.wide = kThreads;
+  if (a.tokens <= kWindow)
+    while (a.wide < 4096 && a.tokens * ((a.n + a.wide - 1) / a.wide) > 2048) a.wide *= 2;
+  const dim3 grid((unsigned)token_blocks(a.tokens), (unsigned)((a.n + a.wide - 1) / a.wide));
   if (a.dtype == 0) up_dt<0>(a, grid, s);
   else if (a.dtype == 1) up_dt<1>(a, grid, s);
   else up_dt<2>(a, grid, s);
