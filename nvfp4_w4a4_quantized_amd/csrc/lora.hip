@@ -24,6 +24,8 @@
 // values.  Sums over K that several workgroups share are joined in workgroup
 // order, sums over tokens in token order per chunk: results do not depend on
 // timing.
+#include <type_traits>
+
 #include "elem.h"
 #include "launch.h"
 
@@ -35,7 +37,6 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kWindow = 256;    // most tokens that workgroups per token look through
-constexpr int kGroup = 64;      // tokens multiplied at once
 constexpr int kWaves = 4;
 constexpr int kThreads = kWaves * kWave;
 constexpr int kRanks = 64;      // ranks of one pass
@@ -165,13 +166,11 @@ __device__ __forceinline__ void down_products(const typename Elem<DT>::type* con
   }
 }
 
-// Grid: x = tokens (SLOT) or groups of 64 tokens, y = shares of K, z = 64 ranks
-// each.  TT times 16 tokens at once; position p of a group is token
-// first + list.at[p] (SLOT) or first + p.
-template <int DT, int RT, bool SLOT>
+// Grid: x = tokens (SLOT) or groups of 16 TT tokens, y = shares of K, z = 64
+// ranks each.  Position p of a group is token list.at[g0 + p] (SLOT) or first + p.
+template <int DT, int RT, int TT, bool SLOT>
 __global__ __launch_bounds__(kThreads) void lora_down_kernel(LoraDownArgs p) {
   typedef typename Elem<DT>::type T;
-  constexpr int TT = SLOT ? 1 : 4;
   __shared__ TokenList list;
   __shared__ f32x4_t red[kWaves][TT][kWave];
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
@@ -222,8 +221,8 @@ __global__ __launch_bounds__(kThreads) void lora_down_kernel(LoraDownArgs p) {
       one(s, xr, [&](int at) -> int64_t { return g0 + at < m ? list.at[g0 + at] : -1; });
     }
   } else {
-    const int64_t first = (int64_t)blockIdx.x * kGroup;
-    const int key = key_at(p.ids, p.tokens, p.adapters, first + lane);
+    const int64_t first = (int64_t)blockIdx.x * (16 * TT);
+    const int key = lane < 16 * TT ? key_at(p.ids, p.tokens, p.adapters, first + lane) : -2;
     uint64_t todo = __ballot(key != -2);
     while (todo != 0) {
       const int lead = __builtin_ctzll(todo), s = __shfl(key, lead);
@@ -254,16 +253,16 @@ __device__ __forceinline__ void bf16_parts(float v, uint16_t (&part)[3]) {
   }
 }
 
-// c h of up to TOK tokens and 64 ranks, as the products' operand.  bf16: a step
+// c h of up to TOK tokens and PASS ranks, as the products' operand.  bf16: a step
 // is 32 k of one MFMA, tokens' rows of 64 bytes (16-byte chunk k of row t at
 // k ^ (t / 4) % 4).  Up to 16 ranks take two steps, the first two parts beside
 // each other and the third beside zeros; more take three, a part each, per 32
 // ranks.  Else: rows of binary32.
-template <int DT, int TOK>
+template <int DT, int TOK, int PASS>
 struct Ranked {
-  static constexpr int kLd = kRanks + 4;
+  static constexpr int kLd = PASS + 4;
   union {
-    uint16_t part[DT == 1 ? 6 * TOK * 32 : 8];
+    uint16_t part[DT == 1 ? 3 * TOK * PASS : 8];
     float row[DT == 1 ? 4 : TOK * kLd];
   };
   static __device__ __forceinline__ int at(int step, int t, int k) {
@@ -340,190 +339,226 @@ __device__ __forceinline__ void put16(void* out, int64_t at, int count, const fl
   }
 }
 
-// Grid: x = tokens (SLOT) or groups of 64 tokens, y = p.wide columns each, 64 a
-// wave at a time.  MFMA row 16 (i / 4) + 4 j + i % 4 of the wave's 64 is row i of
-// product j, so that a lane ends with 16 consecutive columns of its token.  The
-// sums start from the base's values.
-template <int DT, int OT, bool SLOT>
-__global__ __launch_bounds__(kThreads) void lora_up_kernel(LoraUpArgs p) {
+// Grid: x = tokens (SLOT) or groups of 16 TT tokens, y = p.wide columns each, 64
+// a wave at a time.  MFMA row 16 (i / 4) + 4 j + i % 4 of the wave's 64 is row i
+// of product j, so that a lane ends with 16 consecutive columns of its token.
+// The sums start from the base's values, which are loaded a turn ahead.  BIG:
+// more than 32 ranks, 64 at a time.
+template <int DT, int OT, int TT, bool SLOT, bool BIG>
+__global__ __launch_bounds__(kThreads, BIG ? 2 : 3) void lora_up_kernel(LoraUpArgs p) {
   typedef typename Elem<DT>::type T;
-  constexpr int TT = SLOT ? 1 : 4, TOK = 16 * TT;
-  constexpr int kPieces = DT == 1 ? 2 : 4;      // of 64 ranks
+  typedef typename Elem<OT>::type O;
+  constexpr int TOK = 16 * TT;
+  constexpr int kPass = BIG ? kRanks : 32, kPieces = kPass / (DT == 1 ? 32 : 16);
+  constexpr int kBase = 16 / Piece<OT>::kN;     // of 16 columns
   __shared__ TokenList list;
-  __shared__ __align__(16) Ranked<DT, TOK> hs;
+  __shared__ __align__(16) Ranked<DT, TOK, kPass> hs;
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   const int i = lane % 16, q = lane / 16;
-  const int64_t first = SLOT ? 0 : (int64_t)blockIdx.x * kGroup;
-  const int64_t n_end = (int64_t)(blockIdx.y + 1) * p.wide < p.n ? (int64_t)(blockIdx.y + 1) * p.wide : p.n;
+  const int64_t first = SLOT ? 0 : (int64_t)blockIdx.x * TOK;
+  const int64_t w0 = (int64_t)blockIdx.y * p.wide, n_end = w0 + p.wide < p.n ? w0 + p.wide : p.n;
   int s = -1, m = TOK, key = -2;
   if constexpr (SLOT) {
     m = tokens_like(p.ids, (int)p.tokens, p.adapters, blockIdx.x, list, &s);
   } else {
-    key = key_at(p.ids, p.tokens, p.adapters, first + lane);
+    key = lane < TOK ? key_at(p.ids, p.tokens, p.adapters, first + lane) : -2;
   }
-
-  // h of the tokens in `mask` (positions of the group), zeros for the others
-  auto stage = [&](int adapter, uint64_t mask, int g0, int r0, float c, bool narrow) {
-    const int ranks = p.rank - r0 < kRanks ? p.rank - r0 : kRanks;
-    const int padded = DT == 1 ? (narrow ? 16 : (ranks + 31) / 32 * 32) : (ranks + 15) / 16 * 16;
-    for (int v = threadIdx.x; v < TOK * padded; v += kThreads) {
-      const int t = v / padded, r = v % padded;
-      float h = 0.0f;
-      if ((mask >> t) & 1 && r < ranks) {
-        const int64_t tok = SLOT ? list.at[g0 + t] : first + t;
-        const int64_t at = tok * p.rank + r0 + r, step = p.tokens * p.rank;
-        if (adapter >= 0) {
-          // eight shares in flight, added in order
-          h = p.h[at];
-          for (int w = 1; w < p.shares; w += 8) {
-            float more[8];
-#pragma unroll
-            for (int u = 0; u < 8; ++u) more[u] = w + u < p.shares ? p.h[at + (w + u) * step] : 0.0f;
-#pragma unroll
-            for (int u = 0; u < 8; ++u) h = w + u < p.shares ? h + more[u] : h;
-          }
-        }
-        if (p.h_out && blockIdx.y == 0) p.h_out[at] = p.h_scaled ? c * h : h;
-        h *= c;
-      }
-      hs.put(t, r, narrow, h);
-    }
-  };
-  // acc += the adapter's rows of B from column n0 + ... times h, for ranks r0 ..
-  auto multiply = [&](const RankPiece<DT> (&b)[kPieces], int j, int r0, bool narrow, f32x4_t (&acc)[TT]) {
-    const int ranks = p.rank - r0 < kRanks ? p.rank - r0 : kRanks;
-    if constexpr (DT == 1) {
-      const int steps = narrow ? 2 : (ranks + 31) / 32 * 3;
-#pragma unroll
-      for (int st = 0; st < 6; ++st) {
-        if (st >= steps) continue;
-        bf16x8_t u;
-        __builtin_memcpy(&u, b[narrow ? 0 : st / 3].v, 16);
-#pragma unroll
-        for (int t = 0; t < TT; ++t) {
-          const bf16x8_t h = *reinterpret_cast<const bf16x8_t*>(hs.part + Ranked<DT, TOK>::at(st, 16 * t + i, 8 * q));
-          acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u, h, acc[t], 0, 0, 0);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int rb = 0; rb < 4; ++rb) {
-        if (16 * rb >= ranks) continue;
-#pragma unroll
-        for (int t = 0; t < TT; ++t) {
-          const f32x4_t h = *reinterpret_cast<const f32x4_t*>(hs.row + (16 * t + i) * Ranked<DT, TOK>::kLd + 16 * rb + 4 * q);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            acc[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(Elem<DT>::to_float(b[rb].v[e]), h[e], acc[t], 0, 0, 0);
-        }
-      }
-    }
-  };
-  auto load_b = [&](int adapter, int64_t n0, int j, int r0, bool narrow, RankPiece<DT> (&b)[kPieces]) {
-    const int64_t n = n0 + 16 * (i / 4) + 4 * j + i % 4;
-    const T* row = static_cast<const T*>(p.b) + ((int64_t)adapter * p.n + (n < p.n ? n : p.n - 1)) * p.rank;
-#pragma unroll
-    for (int k = 0; k < kPieces; ++k) {
-      const int r = r0 + (DT == 1 ? (narrow ? 8 * (q % 2) : 32 * k + 8 * q) : 16 * k + 4 * q);
-      if ((DT == 1 ? 32 : 16) * k < p.rank - r0) b[k].load(row, r, p.rank);
-    }
-  };
-  auto token = [&](int g0, int at) -> int64_t { return SLOT ? list.at[g0 + at] : first + at; };
-  auto base16 = [&](int64_t tok, int64_t n, int count, float (&v)[16]) {
-    if (p.base && count > 0) {
-      if (p.base_dtype == OT) get16<OT>(p.base, tok * p.ld_base + n, count, v);
-      else get16<0>(p.base, tok * p.ld_base + n, count, v);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) v[e] = 0.0f;
-    }
-  };
-  const bool narrow = p.rank <= 16;
+  const bool narrow = !BIG && p.rank <= 16;
   const uint64_t here = SLOT ? 0 : __ballot(key != -2);
 
   for (int g0 = 0; g0 < m; g0 += TOK) {
-    const uint64_t in = SLOT ? (m - g0 >= TOK ? (1ull << TOK % 64) - 1 : (1ull << (m - g0)) - 1) : here;
-    if constexpr (SLOT) {
-      // one adapter: its ranks once, if they fit, for all of the columns
-      const float c = s >= 0 && p.scale ? p.scale[s] : 1.0f;
-      const bool once = p.rank <= kRanks;
-      for (int64_t n0 = (int64_t)blockIdx.y * p.wide + wave * kWave; n0 - wave * kWave < n_end; n0 += kThreads) {
-        const int64_t n = n0 + 16 * q;
-        const int count = n_end - n < 16 ? (int)(n_end - n) : 16;
-        const int64_t tok = token(g0, (in >> i) & 1 ? i : 0);
-        f32x4_t acc[4][1];
-        float v[16];
-        base16(tok, n, count, v);
-        for (int r0 = 0; r0 < p.rank; r0 += kRanks) {
-          RankPiece<DT> b[4][kPieces];
-          if (s >= 0) {
+    const uint64_t in = SLOT ? (m - g0 >= TOK ? (1ull << (TOK % 64)) - 1 : (1ull << (m - g0)) - 1) : here;
+    auto token = [&](int at) -> int64_t { return SLOT ? list.at[g0 + at] : first + at; };
+
+    // c h of the group's tokens, ranks r0 and on: four of a token's ranks a
+    // thread, eight shares of them in flight, added in order
+    auto stage = [&](int r0) {
+      const int ranks = p.rank - r0 < kPass ? p.rank - r0 : kPass;
+      const int padded = DT == 1 ? (narrow ? 16 : (ranks + 31) / 32 * 32) : (ranks + 15) / 16 * 16;
+      const int64_t step = p.tokens * p.rank;
+      const bool dense = p.rank % 4 == 0;
+      for (int v = threadIdx.x; v < TOK * padded / 4; v += kThreads) {
+        const int t = v / (padded / 4), r = 4 * (v % (padded / 4));
+        float h[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if ((in >> t) & 1 && r < ranks) {
+          const int64_t tok = token(t), at = tok * p.rank + r0 + r;
+          const int a = SLOT ? s : key_of(p.ids[tok], p.adapters);
+          if (a >= 0) {
+            const float c = p.scale ? p.scale[a] : 1.0f;
+            if (dense) {
+              __builtin_memcpy(h, p.h + at, 16);
+              for (int w = 1; w < p.shares; w += 8) {
+                float more[8][4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) load_b(s, n0, j, r0, narrow, b[j]);
+                for (int u = 0; u < 8; ++u)
+                  __builtin_memcpy(more[u], p.h + at + (w + u < p.shares ? w + u : 0) * step, 16);
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) h[e] = w + u < p.shares ? h[e] + more[u][e] : h[e];
+              }
+            } else {
+              for (int w = 0; w < p.shares; ++w)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (r + e < ranks) h[e] = w == 0 ? p.h[at + e] : h[e] + p.h[at + e + w * step];
+            }
+            if (p.h_out && blockIdx.y == 0 && !p.h_scaled) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (r + e < ranks) p.h_out[at + e] = h[e];
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[e] *= c;
           }
-          if (!once || n0 - wave * kWave == (int64_t)blockIdx.y * p.wide) {
-            __syncthreads();
-            stage(s, in, g0, r0, c, narrow);
-            __syncthreads();
-          }
-          if (r0 == 0) {
+          if (p.h_out && blockIdx.y == 0 && (p.h_scaled || a < 0)) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) acc[j][0][e] = v[4 * j + e];
-          }
-          if (s >= 0) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) multiply(b[j], j, r0, narrow, acc[j]);
+            for (int e = 0; e < 4; ++e)
+              if (r + e < ranks) p.h_out[at + e] = h[e];
           }
         }
-        if (count > 0 && (in >> i) & 1) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+        for (int e = 0; e < 4; ++e) hs.put(t, r + e, narrow, h[e]);
+      }
+    };
+    auto load_b = [&](int adapter, int64_t n0, int j, int r0, RankPiece<DT> (&b)[kPieces]) {
+      const int64_t n = n0 + 16 * (i / 4) + 4 * j + i % 4;
+      const T* row = static_cast<const T*>(p.b) + ((int64_t)adapter * p.n + (n < p.n ? n : p.n - 1)) * p.rank;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[4 * j + e] = acc[j][0][e];
-          put16<OT>(p.out, tok * p.n + n, count, v);
+      for (int k = 0; k < kPieces; ++k) {
+        const int r = r0 + (DT == 1 ? (narrow ? 8 * (q % 2) : 32 * k + 8 * q) : 16 * k + 4 * q);
+        if ((DT == 1 ? 32 : 16) * k < p.rank - r0) b[k].load(row, r, p.rank);
+      }
+    };
+    // acc[j][t] += B h for the columns of j in [J0, J1)
+    auto multiply = [&](const RankPiece<DT> (&b)[4][kPieces], int r0, auto J0, auto J1, f32x4_t (&acc)[4][TT]) {
+      const int ranks = p.rank - r0 < kPass ? p.rank - r0 : kPass;
+      constexpr int j0 = decltype(J0)::value, j1 = decltype(J1)::value;
+      if constexpr (DT == 1) {
+        const int steps = narrow ? 2 : (ranks + 31) / 32 * 3;
+#pragma unroll
+        for (int st = 0; st < 3 * kPieces; ++st) {
+          if (st >= steps) continue;
+#pragma unroll
+          for (int t = 0; t < TT; ++t) {
+            const bf16x8_t h = *reinterpret_cast<const bf16x8_t*>(hs.part + Ranked<DT, TOK, kPass>::at(st, 16 * t + i, 8 * q));
+#pragma unroll
+            for (int j = j0; j < j1; ++j) {
+              bf16x8_t u;
+              __builtin_memcpy(&u, b[j][st / 3].v, 16);
+              acc[j][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u, h, acc[j][t], 0, 0, 0);
+            }
+          }
+        }
+      } else {
+#pragma unroll
+        for (int rb = 0; rb < kPieces; ++rb) {
+          if (16 * rb >= ranks) continue;
+#pragma unroll
+          for (int t = 0; t < TT; ++t) {
+            const f32x4_t h = *reinterpret_cast<const f32x4_t*>(hs.row + (16 * t + i) * Ranked<DT, TOK, kPass>::kLd + 16 * rb + 4 * q);
+#pragma unroll
+            for (int j = j0; j < j1; ++j)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                acc[j][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(Elem<DT>::to_float(b[j][rb].v[e]), h[e], acc[j][t], 0, 0, 0);
+          }
         }
       }
-    } else {
-      // the group's adapters one after the other, 64 columns a wave
-      const int64_t n0 = (int64_t)blockIdx.y * p.wide + wave * kWave, n = n0 + 16 * q;
-      const int count = n_end - n < 16 ? (int)(n_end - n) : 16;
+    };
+    using C0 = std::integral_constant<int, 0>;
+    using C4 = std::integral_constant<int, 4>;
+    // the lane's columns from n on, and its tokens' base there
+    auto columns = [&](int64_t n0) -> int {
+      const int64_t left = n_end - n0 - 16 * q;
+      return left < 16 ? (int)left : 16;
+    };
+    const bool same = p.base && p.base_dtype == OT;
+    auto fetch = [&](int64_t n0, Piece<OT> (&raw)[TT][kBase]) {
+      const int count = columns(n0);
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        if (!same || count < 16) continue;
+        const O* b = static_cast<const O*>(p.base) + token((in >> (16 * t + i)) & 1 ? 16 * t + i : 0) * p.ld_base + n0 + 16 * q;
+#pragma unroll
+        for (int c = 0; c < kBase; ++c) raw[t][c].load(b + c * Piece<OT>::kN);
+      }
+    };
+    Piece<OT> raw[TT][kBase];
+    const bool once = !BIG || p.rank <= kPass;
+    fetch(w0 + wave * kWave, raw);
+    if (once) {
+      __syncthreads();
+      stage(0);
+      __syncthreads();
+    }
+    for (int64_t turn = w0; turn < n_end; turn += kThreads) {
+      const int64_t n0 = turn + wave * kWave, n = n0 + 16 * q;
+      const int count = columns(n0);
       f32x4_t acc[4][TT];
+      uint64_t todo = in;
+      int a = SLOT ? s : __shfl(key, __builtin_ctzll(todo));
+      RankPiece<DT> b[4][kPieces];
+      if (a >= 0) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) load_b(a, n0, j, 0, b[j]);
+      }
 #pragma unroll
       for (int t = 0; t < TT; ++t) {
         float v[16];
-        base16(token(0, (in >> (16 * t + i)) & 1 ? 16 * t + i : 0), n, count, v);
+        if (same && count >= 16) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = raw[t][e / Piece<OT>::kN].get(e % Piece<OT>::kN);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = 0.0f;
+          const int64_t tok = token((in >> (16 * t + i)) & 1 ? 16 * t + i : 0);
+          if (same && count > 0) get16<OT>(p.base, tok * p.ld_base + n, count, v);
+          else if (p.base && count > 0) get16<0>(p.base, tok * p.ld_base + n, count, v);
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[j][t][e] = v[4 * j + e];
       }
-      uint64_t todo = in;
-      while (todo != 0) {
-        const int a = __shfl(key, __builtin_ctzll(todo));
-        const uint64_t mask = __ballot(key == a);
+      if (turn + kThreads < n_end) fetch(n0 + kThreads, raw);
+      for (;;) {
+        const uint64_t mask = SLOT ? in : __ballot(key == a);
         todo &= ~mask;
-        const float c = a >= 0 && p.scale ? p.scale[a] : 1.0f;
-        for (int r0 = 0; r0 < p.rank; r0 += kRanks) {
-          RankPiece<DT> b[4][kPieces];
-          if (a >= 0) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) load_b(a, n0, j, r0, narrow, b[j]);
+        for (int r0 = 0; r0 < (BIG ? p.rank : 1); r0 += kPass) {
+          if (!once) {
+            __syncthreads();
+            stage(r0);
+            __syncthreads();
           }
-          __syncthreads();
-          stage(a, mask, 0, r0, c, narrow);
-          __syncthreads();
           if (a < 0) continue;
+          if (r0 > 0) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            f32x4_t now[TT];
-#pragma unroll
-            for (int t = 0; t < TT; ++t) now[t] = acc[j][t];
-            multiply(b[j], j, r0, narrow, now);
-#pragma unroll
-            for (int t = 0; t < TT; ++t)
-              if ((mask >> (16 * t + i)) & 1) acc[j][t] = now[t];
+            for (int j = 0; j < 4; ++j) load_b(a, n0, j, r0, b[j]);
           }
+          if (mask == in) {
+            multiply(b, r0, C0{}, C4{}, acc);
+          } else {
+            // only its own tokens take an adapter's results: another's infinity
+            // or NaN times their zeros would not be zero
+            f32x4_t now[4][TT];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int t = 0; t < TT; ++t) now[j][t] = acc[j][t];
+            multiply(b, r0, C0{}, C4{}, now);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int t = 0; t < TT; ++t)
+                if ((mask >> (16 * t + i)) & 1) acc[j][t] = now[j][t];
+          }
+        }
+        if (todo == 0) break;
+        a = __shfl(key, __builtin_ctzll(todo));
+        if (a >= 0) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) load_b(a, n0, j, 0, b[j]);
         }
       }
       if (count > 0) {
@@ -535,7 +570,7 @@ __global__ __launch_bounds__(kThreads) void lora_up_kernel(LoraUpArgs p) {
           for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[4 * j + e] = acc[j][t][e];
-          put16<OT>(p.out, (first + 16 * t + i) * p.n + n, count, v);
+          put16<OT>(p.out, token(16 * t + i) * p.n + n, count, v);
         }
       }
     }
@@ -747,31 +782,37 @@ __global__ __launch_bounds__(256) void lora_join_parts_kernel(LoraGradArgs p, co
   else p.db[s * (wide - na) + i - na] = v;
 }
 
+template <int DT, int RT>
+void down_rt(const LoraDownArgs& a, int group, dim3 grid, hipStream_t s) {
+  if (group == 1) lora_down_kernel<DT, RT, 1, true><<<grid, kThreads, 0, s>>>(a);
+  else if (group == 16) lora_down_kernel<DT, RT, 1, false><<<grid, kThreads, 0, s>>>(a);
+  else if (group == 32) lora_down_kernel<DT, RT, 2, false><<<grid, kThreads, 0, s>>>(a);
+  else lora_down_kernel<DT, RT, 4, false><<<grid, kThreads, 0, s>>>(a);
+}
+
 template <int DT>
-void down_dt(const LoraDownArgs& a, dim3 grid, hipStream_t s) {
-  const bool slot = a.tokens <= kWindow;
-  if (a.rank <= 16)
-    slot ? lora_down_kernel<DT, 1, true><<<grid, kThreads, 0, s>>>(a)
-         : lora_down_kernel<DT, 1, false><<<grid, kThreads, 0, s>>>(a);
-  else if (a.rank <= 32)
-    slot ? lora_down_kernel<DT, 2, true><<<grid, kThreads, 0, s>>>(a)
-         : lora_down_kernel<DT, 2, false><<<grid, kThreads, 0, s>>>(a);
-  else
-    slot ? lora_down_kernel<DT, 4, true><<<grid, kThreads, 0, s>>>(a)
-         : lora_down_kernel<DT, 4, false><<<grid, kThreads, 0, s>>>(a);
+void down_dt(const LoraDownArgs& a, int group, dim3 grid, hipStream_t s) {
+  if (a.rank <= 16) down_rt<DT, 1>(a, group, grid, s);
+  else if (a.rank <= 32) down_rt<DT, 2>(a, group, grid, s);
+  else down_rt<DT, 4>(a, group, grid, s);
 }
 
 template <int DT, int OT>
-void up_out(const LoraUpArgs& a, dim3 grid, hipStream_t s) {
-  if (a.tokens <= kWindow) lora_up_kernel<DT, OT, true><<<grid, kThreads, 0, s>>>(a);
-  else lora_up_kernel<DT, OT, false><<<grid, kThreads, 0, s>>>(a);
+void up_out(const LoraUpArgs& a, int group, dim3 grid, hipStream_t s) {
+  const bool big = a.rank > 32;
+  if (group == 1)
+    big ? lora_up_kernel<DT, OT, 1, true, true><<<grid, kThreads, 0, s>>>(a)
+        : lora_up_kernel<DT, OT, 1, true, false><<<grid, kThreads, 0, s>>>(a);
+  else
+    big ? lora_up_kernel<DT, OT, 2, false, true><<<grid, kThreads, 0, s>>>(a)
+        : lora_up_kernel<DT, OT, 2, false, false><<<grid, kThreads, 0, s>>>(a);
 }
 
 template <int DT>
-void up_dt(const LoraUpArgs& a, dim3 grid, hipStream_t s) {
-  if (a.out_dtype == 0) up_out<DT, 0>(a, grid, s);
-  else if (a.out_dtype == 1) up_out<DT, 1>(a, grid, s);
-  else up_out<DT, 2>(a, grid, s);
+void up_dt(const LoraUpArgs& a, int group, dim3 grid, hipStream_t s) {
+  if (a.out_dtype == 0) up_out<DT, 0>(a, group, grid, s);
+  else if (a.out_dtype == 1) up_out<DT, 1>(a, group, grid, s);
+  else up_out<DT, 2>(a, group, grid, s);
 }
 
 template <int DT>
@@ -781,16 +822,23 @@ void grad_dt(const LoraGradArgs& a, dim3 grid, hipStream_t s) {
   else lora_grad_kernel<DT, 4><<<grid, kThreads, 0, s>>>(a);
 }
 
-int64_t token_blocks(int64_t tokens) {
-  return tokens <= kWindow ? tokens : (tokens + kGroup - 1) / kGroup;
+// Tokens of a workgroup of the down products (1: the slots of up to kWindow): as
+// many as leave two workgroups a CU, so that the adapter is read least often, but
+// more than 16 where its rows are long ones of many ranks.
+int down_group(int64_t tokens, int32_t rank) {
+  if (tokens <= kWindow) return 1;
+  if (tokens >= 64 * 512) return 64;
+  return tokens >= 32 * 512 || rank > 32 ? 32 : 16;
 }
+int up_group(int64_t tokens) { return tokens <= kWindow ? 1 : 32; }
+int64_t groups(int64_t tokens, int group) { return (tokens + group - 1) / group; }
 
 }  // namespace
 
 // Shares of K: as many as bring the launch to two workgroups a CU, of no less
 // than one 128-byte piece a wave.
-int lora_shares(int64_t tokens, int64_t k) {
-  const int64_t blocks = token_blocks(tokens), most = (k + 255) / 256;
+int lora_shares(int64_t tokens, int64_t k, int32_t rank) {
+  const int64_t blocks = groups(tokens, down_group(tokens, rank)), most = (k + 255) / 256;
   int64_t w = blocks > 0 ? (512 + blocks - 1) / blocks : 1;
   w = w < most ? w : most;
   return (int)(w < 1 ? 1 : (w > 16 ? 16 : w));
@@ -806,25 +854,26 @@ int32_t lora_chunk(int64_t tokens, int64_t k, int64_t n) {
 
 hipError_t launch_lora_down(LoraDownArgs a, hipStream_t s) {
   if (a.tokens == 0) return hipSuccess;
-  const int shares = lora_shares(a.tokens, a.k);
+  const int shares = lora_shares(a.tokens, a.k, a.rank), group = down_group(a.tokens, a.rank);
   a.share = ((a.k + shares - 1) / shares + 255) / 256 * 256;
-  const dim3 grid((unsigned)token_blocks(a.tokens), shares, (a.rank + kRanks - 1) / kRanks);
-  if (a.dtype == 0) down_dt<0>(a, grid, s);
-  else if (a.dtype == 1) down_dt<1>(a, grid, s);
-  else down_dt<2>(a, grid, s);
+  const dim3 grid((unsigned)groups(a.tokens, group), shares, (a.rank + kRanks - 1) / kRanks);
+  if (a.dtype == 0) down_dt<0>(a, group, grid, s);
+  else if (a.dtype == 1) down_dt<1>(a, group, grid, s);
+  else down_dt<2>(a, group, grid, s);
   return hipGetLastError();
 }
 
 hipError_t launch_lora_up(LoraUpArgs a, hipStream_t s) {
   if (a.tokens == 0) return hipSuccess;
-  // 256 columns a workgroup; more for a token's, while eight workgroups a CU are left
+  const int group = up_group(a.tokens);
+  // 256 columns a workgroup; more while there are enough for eight (four) a CU
+  const int64_t many = group == 1 ? 2048 : 1024, blocks = groups(a.tokens, group);
   a.wide = kThreads;
-  if (a.tokens <= kWindow)
-    while (a.wide < 4096 && a.tokens * ((a.n + a.wide - 1) / a.wide) > 2048) a.wide *= 2;
-  const dim3 grid((unsigned)token_blocks(a.tokens), (unsigned)((a.n + a.wide - 1) / a.wide));
-  if (a.dtype == 0) up_dt<0>(a, grid, s);
-  else if (a.dtype == 1) up_dt<1>(a, grid, s);
-  else up_dt<2>(a, grid, s);
+  while (a.wide < 4096 && blocks * ((a.n + 2 * a.wide - 1) / (2 * a.wide)) >= many) a.wide *= 2;
+  const dim3 grid((unsigned)blocks, (unsigned)((a.n + a.wide - 1) / a.wide));
+  if (a.dtype == 0) up_dt<0>(a, group, grid, s);
+  else if (a.dtype == 1) up_dt<1>(a, group, grid, s);
+  else up_dt<2>(a, group, grid, s);
   return hipGetLastError();
 }
 
