@@ -1042,7 +1042,7 @@ static LoraBackwardLayout carve_lora_backward(void* ws, int dtype, int64_t T, in
   L.g = c.take<float>((size_t)(T * rank));
   L.h = c.take<float>((size_t)(T * rank));
   L.rows = c.take<int32_t>((size_t)T);
-  L.chunk = lora_chunk(T, k, n);
+  L.chunk = lora_chunk(dtype, T, k, n, rank);
   L.max_entries = (int32_t)(T / L.chunk) + S;
   L.entries = c.take<int4>((size_t)L.max_entries);
   L.chunk0 = c.take<int32_t>((size_t)S + 1);
@@ -1081,8 +1081,12 @@ int lora_backward(const void* dy, int dtype, int64_t tokens, int64_t n, int64_t 
     if (e == hipSuccess)
       e = launch_lora_join_shares(L.shares, lora_shares(tokens, k, rank), tokens * rank, L.h, s);
   }
-  if (e == hipSuccess) e = launch_lora_transpose(a, dtype, adapters, rank, k, L.at, s);
-  if (e == hipSuccess) e = launch_lora_transpose(b, dtype, adapters, n, rank, L.bt, s);
+  LoraPrepareArgs pr{};
+  pr.sort.ids = ids; pr.sort.tokens = tokens; pr.sort.adapters = adapters; pr.sort.chunk = L.chunk;
+  pr.sort.max_entries = L.max_entries; pr.sort.rows = L.rows; pr.sort.entries = L.entries;
+  pr.sort.chunk0 = L.chunk0;
+  pr.a = a; pr.b = b; pr.dtype = dtype; pr.k = k; pr.n = n; pr.rank = rank; pr.at = L.at; pr.bt = L.bt;
+  if (e == hipSuccess) e = launch_lora_prepare(pr, s);
   if (e == hipSuccess)
     e = launch_lora_down(lora_down(dy, dtype, tokens, n, ld_dy, ids, L.bt, adapters, rank, L.shares), s);
   if (e == hipSuccess) {
@@ -1091,10 +1095,6 @@ int lora_backward(const void* dy, int dtype, int64_t tokens, int64_t n, int64_t 
     u.h_out = L.g; u.h_scaled = 1;
     e = launch_lora_up(u, s);
   }
-  LoraSortArgs so{};
-  so.ids = ids; so.tokens = tokens; so.adapters = adapters; so.chunk = L.chunk;
-  so.max_entries = L.max_entries; so.rows = L.rows; so.entries = L.entries; so.chunk0 = L.chunk0;
-  if (e == hipSuccess) e = launch_lora_sort(so, s);
   LoraGradArgs gr{};
   gr.x = x; gr.dy = dy; gr.dtype = dtype; gr.k = k; gr.n = n; gr.ld_x = ld_x; gr.ld_dy = ld_dy;
   gr.g = L.g; gr.h = h ? h : L.h; gr.scale = scale; gr.adapters = adapters; gr.rank = rank;

@@ -282,6 +282,11 @@ struct LoraSortArgs {
   int4* entries;              // [max_entries]
   int32_t* chunk0;            // [adapters + 1]
 };
+struct LoraPrepareArgs {
+  LoraSortArgs sort;
+  const void* a; const void* b; int dtype; int64_t k, n; int32_t rank;
+  void* at; void* bt;         // [adapters, k, rank], [adapters, rank, n]
+};
 struct LoraGradArgs {
   const void* x; const void* dy; int dtype; int64_t k, n, ld_x, ld_dy;
   const float* g; const float* h;          // [tokens, rank]; g with the scale, h without
@@ -291,14 +296,12 @@ struct LoraGradArgs {
   float* parts;               // [max_entries, rank * (k + n)]
 };
 int lora_shares(int64_t tokens, int64_t k, int32_t rank);
-int32_t lora_chunk(int64_t tokens, int64_t k, int64_t n);
+int32_t lora_chunk(int dtype, int64_t tokens, int64_t k, int64_t n, int32_t rank);
 hipError_t launch_lora_down(LoraDownArgs a, hipStream_t s);
 hipError_t launch_lora_up(LoraUpArgs a, hipStream_t s);
-hipError_t launch_lora_transpose(const void* in, int dtype, int64_t groups, int64_t rows, int64_t cols,
-                                 void* out, hipStream_t s);
+hipError_t launch_lora_prepare(const LoraPrepareArgs& a, hipStream_t s);
 hipError_t launch_lora_join_shares(const float* in, int shares, int64_t elements, float* out,
                                    hipStream_t s);
-hipError_t launch_lora_sort(const LoraSortArgs& a, hipStream_t s);
 hipError_t launch_lora_grad(const LoraGradArgs& a, int32_t max_entries, const int32_t* chunk0,
                             hipStream_t s);
 

@@ -579,21 +579,6 @@ __global__ __launch_bounds__(kThreads, BIG ? 2 : 3) void lora_up_kernel(LoraUpAr
 
 // ---- the way back -----------------------------------------------------------
 
-// [groups, rows, cols] to [groups, cols, rows], 32 x 32 elements a workgroup.
-template <typename T>
-__global__ __launch_bounds__(256) void lora_transpose_kernel(const T* in, int64_t rows, int64_t cols,
-                                                             T* out) {
-  __shared__ T tile[32][33];
-  const int64_t r0 = (int64_t)blockIdx.y * 32, c0 = (int64_t)blockIdx.x * 32;
-  const int64_t group = (int64_t)blockIdx.z * rows * cols;
-  const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
-  for (int r = ty; r < 32; r += 8)
-    if (r0 + r < rows && c0 + tx < cols) tile[r][tx] = in[group + (r0 + r) * cols + c0 + tx];
-  __syncthreads();
-  for (int c = ty; c < 32; c += 8)
-    if (c0 + c < cols && r0 + tx < rows) out[group + (c0 + c) * rows + r0 + tx] = tile[tx][c];
-}
-
 // h[t, r] = the sum of its shares, in order.
 __global__ __launch_bounds__(256) void lora_join_shares_kernel(const float* in, int shares,
                                                                int64_t elements, float* out) {
@@ -604,26 +589,68 @@ __global__ __launch_bounds__(256) void lora_join_shares_kernel(const float* in, 
   out[i] = v;
 }
 
-// Tokens in adapter order (ascending inside an adapter) and the chunks that
-// the gradients are summed in: one workgroup, sixteen waves with a consecutive
-// share of the tokens each.  entry = {adapter, first row, end row, number of
-// its adapter's chunks}; every adapter has one chunk at least, unused entries
-// have adapter -1.  chunk0[s] is adapter s's first chunk.
-constexpr int kSortWaves = 16;
-__global__ __launch_bounds__(kSortWaves * kWave) void lora_sort_kernel(LoraSortArgs p) {
-  __shared__ int32_t place[kSortWaves * kMaxAdapters];   // [wave][adapter]
-  __shared__ int32_t sums[2][kSortWaves];
+// What the way back lays out first, in one launch: workgroup 0 sorts the tokens,
+// the others transpose A and B, 64 x 64 elements each.
+//
+// The sort: tokens in adapter order (ascending inside an adapter) and the chunks
+// that the gradients are summed in, by sixteen waves with a consecutive share of
+// the tokens each.  entry = {adapter, first row, end row, number of its adapter's
+// chunks}; every adapter has one chunk at least, unused entries have adapter -1.
+// chunk0[s] is adapter s's first chunk.
+constexpr int kSortWaves = 16, kAhead = 16;
+
+// Calls f(first token, key) for every 64 tokens of [t0, t1), kAhead loads in flight.
+template <typename F>
+__device__ __forceinline__ void walk_keys(const LoraSortArgs& p, int t0, int t1, F f) {
+  const int lane = threadIdx.x % kWave;
+  for (int base = t0; base < t1; base += kAhead * kWave) {
+    int id[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int t = base + u * kWave + lane;
+      id[u] = p.ids[t < t1 ? t : t1 - 1];
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int t = base + u * kWave + lane;
+      if (base + u * kWave < t1) f(t, t < t1 ? key_of(id[u], p.adapters) : -1);
+    }
+  }
+}
+
+__device__ __forceinline__ void lora_sort(const LoraSortArgs& p, int32_t* place, int32_t (*sums)[kSortWaves]) {
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   const int S = p.adapters, tokens = (int)p.tokens;
   const int per = (tokens + kSortWaves * kWave - 1) / (kSortWaves * kWave) * kWave;
   const int t0 = wave * per < tokens ? wave * per : tokens, t1 = t0 + per < tokens ? t0 + per : tokens;
-  int32_t* mine = place + wave * S;
-  for (int i = threadIdx.x; i < kSortWaves * S; i += blockDim.x) place[i] = 0;
+  // written by one lane, read by the others of its wave
+  volatile int32_t* mine = place + wave * S;           // [wave][adapter]
+  for (int i = threadIdx.x; i < kSortWaves * S; i += kSortWaves * kWave) place[i] = 0;
   __syncthreads();
-  for (int t = t0 + lane; t < t1; t += kWave) {
-    const int k = key_of(p.ids[t], S);
-    if (k >= 0) atomicAdd(&mine[k], 1);       // (a count: the order does not matter)
-  }
+  // The run's adapter and its count so far stay in registers: a request's tokens
+  // lie together, and a turn through LDS for every 64 takes 27 us for 32768.
+  int run = -1, at = 0;
+  auto open = [&](int key) {
+    if (key == run) return;
+    if (run >= 0 && lane == 0) mine[run] = at;
+    __builtin_amdgcn_wave_barrier();
+    if (key >= 0) at = mine[key];
+    __builtin_amdgcn_wave_barrier();
+    run = key;
+  };
+  auto each = [&](int k, auto f) {
+    uint64_t todo = __ballot(k >= 0);
+    while (todo != 0) {
+      const int key = __builtin_amdgcn_readfirstlane(__shfl(k, __builtin_ctzll(todo)));
+      const uint64_t mask = __ballot(k == key);
+      open(key);
+      f(key, mask);
+      at += __popcll(mask);
+      todo &= ~mask;
+    }
+  };
+  walk_keys(p, t0, t1, [&](int, int k) { each(k, [](int, uint64_t) {}); });
+  open(-1);
   __syncthreads();
   // thread s: adapter s's tokens and chunks, then sums over the adapters before
   const int s = threadIdx.x;
@@ -665,22 +692,46 @@ __global__ __launch_bounds__(kSortWaves * kWave) void lora_sort_kernel(LoraSortA
     }
   }
   __syncthreads();
-  volatile int32_t* next = mine;      // written by one lane, read by the others of its wave
-  for (int base = t0; base < t1; base += kWave) {
-    const int t = base + lane;
-    const int k = t < t1 ? key_of(p.ids[t], S) : -1;
-    uint64_t todo = __ballot(k >= 0);
-    while (todo != 0) {
-      const int one = __builtin_ctzll(todo), key = __shfl(k, one);
-      const uint64_t mask = __ballot(k == key);
-      const int at = next[key];
+  walk_keys(p, t0, t1, [&](int t, int k) {
+    each(k, [&](int key, uint64_t mask) {
       if (k == key) p.rows[at + bits_below(mask)] = t;
-      __builtin_amdgcn_wave_barrier();
-      if (lane == one) next[key] = at + __popcll(mask);
-      __builtin_amdgcn_wave_barrier();
-      todo &= ~mask;
-    }
+    });
+  });
+}
+
+// Tile t of [groups, rows, cols] to [groups, cols, rows].
+template <typename T>
+__device__ __forceinline__ void transpose_tile(const T* in, int64_t rows, int64_t cols, T* out, int64_t t,
+                                               T (*tile)[65]) {
+  const int64_t tc = (cols + 63) / 64, tr = (rows + 63) / 64;
+  const int64_t r0 = t / tc % tr * 64, c0 = t % tc * 64, group = t / (tc * tr) * rows * cols;
+  const int tx = threadIdx.x % 64, ty = threadIdx.x / 64;
+#pragma unroll
+  for (int r = ty; r < 64; r += kSortWaves)
+    if (r0 + r < rows && c0 + tx < cols) tile[r][tx] = in[group + (r0 + r) * cols + c0 + tx];
+  __syncthreads();
+#pragma unroll
+  for (int c = ty; c < 64; c += kSortWaves)
+    if (c0 + c < cols && r0 + tx < rows) out[group + (c0 + c) * rows + r0 + tx] = tile[tx][c];
+}
+
+template <typename T>
+__global__ __launch_bounds__(kSortWaves * kWave) void lora_prepare_kernel(LoraPrepareArgs p) {
+  union Shared {
+    struct {
+      int32_t place[kSortWaves * kMaxAdapters];
+      int32_t sums[2][kSortWaves];
+    } sort;
+    T tile[64][65];
+  };
+  __shared__ Shared sh;
+  if (blockIdx.x == 0) {
+    lora_sort(p.sort, sh.sort.place, sh.sort.sums);
+    return;
   }
+  const int64_t t = (int64_t)blockIdx.x - 1, na = (int64_t)p.sort.adapters * ((p.rank + 63) / 64) * ((p.k + 63) / 64);
+  if (t < na) transpose_tile(static_cast<const T*>(p.a), p.rank, p.k, static_cast<T*>(p.at), t, sh.tile);
+  else transpose_tile(static_cast<const T*>(p.b), p.n, p.rank, static_cast<T*>(p.bt), t - na, sh.tile);
 }
 
 // Grid: x = 128 columns of x, then of dy; y = chunks; z = 64 ranks each.  The
@@ -769,6 +820,174 @@ __global__ __launch_bounds__(kThreads) void lora_grad_kernel(LoraGradArgs p) {
   }
 }
 
+// The same for bf16 rows on MFMA 16x16x32: the g or c h of 32 tokens go through
+// LDS as their three bf16 parts, token by token of a rank, and the rows' values
+// are brought from eight tokens' registers into a column's by byte permutes.  Four
+// waves of 128 columns, or (64 ranks, whose sums take the registers) eight of 64.
+// Grid: x = 512 columns of x, then of dy.
+// The binary32 form above is bound by its matrix instructions from rank 32 on
+// (rank 64: 512 us for 470 MB).
+template <int RT>
+__global__ __launch_bounds__(512, 4) void lora_grad16_kernel(LoraGradArgs p) {
+  constexpr int R = 16 * RT, W = 8, C = 4;    // waves, columns of a lane
+  // [part][rank][32 tokens], 16-byte chunk c of row r at c ^ (r / 4) % 4
+  __shared__ __align__(16) uint16_t parts[2][3 * R * 32];
+  const int4 e = p.entries[blockIdx.y];
+  if (e.x < 0) return;
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  const int i = lane % 16, q = lane / 16, z0 = blockIdx.z * kRanks;
+  const int tiles_a = (int)((p.k + 511) / 512);
+  const bool down = (int)blockIdx.x < tiles_a;       // dA (g, x), else dB (c h, dy)
+  const int64_t width = down ? p.k : p.n, ld = down ? p.ld_x : p.ld_dy;
+  const int64_t c0 = (int64_t)(down ? blockIdx.x : blockIdx.x - tiles_a) * 512 + 16 * C * wave + C * i;
+  const uint16_t* const rows = static_cast<const uint16_t*>(down ? p.x : p.dy);
+  const float* const values = down ? p.g : p.h;
+  const float c = down || !p.scale ? 1.0f : p.scale[e.x];
+  const bool whole = c0 + C <= width;
+  f32x4_t acc[RT][C];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+    for (int j = 0; j < C; ++j) acc[rt][j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+
+  // Tokens of the 32 from the chunk's row t on: the lane's eight, whose columns it
+  // reads, and the one whose values the thread spreads (rows past the last: it).
+  struct Tokens {
+    int x[8], v;
+  };
+  auto tokens = [&](int t, Tokens& k) {
+    const int r = t + 8 * q, rv = t + (int)threadIdx.x / (2 * W);
+    if (r + 8 <= e.z) {
+      __builtin_memcpy(k.x, p.rows + r, 32);
+    } else {
+#pragma unroll
+      for (int u = 0; u < 8; ++u) k.x[u] = p.rows[r + u < e.z ? r + u : e.z - 1];
+    }
+    k.v = p.rows[rv < e.z ? rv : e.z - 1];
+  };
+  struct Columns {
+    uint16_t v[C];
+  };
+  auto fetch = [&](const Tokens& k, Columns (&x)[8]) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const uint16_t* row = rows + k.x[u] * ld + c0;
+      if (whole) {
+        __builtin_memcpy(x[u].v, row, sizeof(x[u].v));
+      } else {
+#pragma unroll
+        for (int j = 0; j < C; ++j) x[u].v[j] = c0 + j < width ? row[j] : (uint16_t)0;
+      }
+    }
+  };
+  constexpr int kMine = R / (2 * W);      // ranks of a thread
+  auto gather = [&](int t, const Tokens& k, float (&v)[kMine]) {
+    const bool in = t + (int)threadIdx.x / (2 * W) < e.z;
+    const float* from = values + (int64_t)k.v * p.rank + z0;
+#pragma unroll
+    for (int m = 0; m < kMine; ++m) {
+      const int rank = threadIdx.x % (2 * W) + 2 * W * m;
+      v[m] = in && z0 + rank < p.rank ? c * from[rank] : 0.0f;
+    }
+  };
+  auto spread = [&](uint16_t* to, const float (&v)[kMine]) {
+    const int t = threadIdx.x / (2 * W);
+#pragma unroll
+    for (int m = 0; m < kMine; ++m) {
+      const int r = threadIdx.x % (2 * W) + 2 * W * m;
+      uint16_t b[3];
+      bf16_parts(v[m], b);
+#pragma unroll
+      for (int k = 0; k < 3; ++k) to[(k * R + r) * 32 + 8 * ((t / 8) ^ ((r >> 2) & 3)) + t % 8] = b[k];
+    }
+  };
+  Columns x[8];
+  Tokens next;
+  float v[kMine];
+  const int start = e.y;
+  if (start < e.z) {
+    tokens(start, next);
+    gather(start, next, v);
+    fetch(next, x);
+    tokens(start + 32 < e.z ? start + 32 : start, next);
+    spread(parts[0], v);
+  }
+  int at = 0;
+  for (int t = start; t < e.z; t += 32, at ^= 1) {
+    __syncthreads();
+    const bool more = t + 32 < e.z;
+    if (more) gather(t + 32, next, v);
+    // column b of the lane's: a dword of two tokens from words b / 2 of both
+    bf16x8_t col[C];
+#pragma unroll
+    for (int b = 0; b < C; ++b) {
+      uint32_t w[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        uint32_t lo, hi;
+        __builtin_memcpy(&lo, x[2 * u].v + b / 2 * 2, 4);
+        __builtin_memcpy(&hi, x[2 * u + 1].v + b / 2 * 2, 4);
+        w[u] = __builtin_amdgcn_perm(hi, lo, b % 2 ? 0x07060302u : 0x05040100u);
+        // (rows past the chunk's last are that row again: no infinity times zero)
+        const int r = t + 8 * q + 2 * u;
+        w[u] = r + 1 < e.z ? w[u] : (r < e.z ? w[u] & 0xFFFFu : 0u);
+      }
+      __builtin_memcpy(&col[b], w, 16);
+    }
+    if (more) {
+      fetch(next, x);
+      tokens(t + 64 < e.z ? t + 64 : t, next);
+    }
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        const int r = 16 * rt + i;
+        const bf16x8_t a = *reinterpret_cast<const bf16x8_t*>(parts[at] + (k * R + r) * 32 + 8 * (q ^ ((r >> 2) & 3)));
+#pragma unroll
+        for (int b = 0; b < C; ++b) acc[rt][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, col[b], acc[rt][b], 0, 0, 0);
+      }
+    if (more) spread(parts[at ^ 1], v);
+  }
+  const int64_t wide = (int64_t)p.rank * (p.k + p.n);
+  float* out = e.w > 1 ? p.parts + blockIdx.y * wide + (down ? 0 : p.rank * p.k)
+                       : (down ? p.da + (int64_t)e.x * p.rank * p.k : p.db + (int64_t)e.x * p.rank * p.n);
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    const int r = z0 + 16 * rt + 4 * q;
+    if (down) {
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        if (r + b >= p.rank) continue;
+        float* o = out + (r + b) * p.k + c0;
+        float f[C];
+#pragma unroll
+        for (int j = 0; j < C; ++j) f[j] = acc[rt][j][b];
+        if (whole) {
+          __builtin_memcpy(o, f, sizeof(f));
+        } else {
+#pragma unroll
+          for (int j = 0; j < C; ++j)
+            if (c0 + j < width) o[j] = f[j];
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < C; ++j) {
+        if (c0 + j >= width) continue;
+        float* o = out + (c0 + j) * p.rank + r;
+        if (r + 4 <= p.rank) {
+          __builtin_memcpy(o, &acc[rt][j], 16);
+        } else {
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+            if (r + b < p.rank) o[b] = acc[rt][j][b];
+        }
+      }
+    }
+  }
+}
+
 // The gradients of adapters of several chunks: the parts added in chunk order.
 __global__ __launch_bounds__(256) void lora_join_parts_kernel(LoraGradArgs p, const int32_t* chunk0) {
   const int s = blockIdx.y, c0 = chunk0[s], c1 = chunk0[s + 1];
@@ -845,9 +1064,10 @@ int lora_shares(int64_t tokens, int64_t k, int32_t rank) {
 }
 
 // Tokens of a chunk of the gradients: enough chunks for three workgroups a CU.
-int32_t lora_chunk(int64_t tokens, int64_t k, int64_t n) {
-  const int64_t tiles = (k + 127) / 128 + (n + 127) / 128;
-  const int64_t want = (768 + tiles - 1) / tiles;
+int32_t lora_chunk(int dtype, int64_t tokens, int64_t k, int64_t n, int32_t rank) {
+  const int64_t each = dtype == 1 ? 512 : 128, tiles = (k + each - 1) / each + (n + each - 1) / each;
+  // (each chunk's sums of more than 32 ranks are as long to write as 600 tokens' rows)
+  const int64_t want = ((rank > 32 ? 512 : 768) + tiles - 1) / tiles;
   const int64_t c = ((tokens + want - 1) / want + 63) / 64 * 64;
   return (int32_t)(c < 64 ? 64 : c);
 }
@@ -877,15 +1097,11 @@ hipError_t launch_lora_up(LoraUpArgs a, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_lora_transpose(const void* in, int dtype, int64_t groups, int64_t rows, int64_t cols,
-                                 void* out, hipStream_t s) {
-  const dim3 grid((unsigned)((cols + 31) / 32), (unsigned)((rows + 31) / 32), (unsigned)groups);
-  if (dtype == 0)
-    lora_transpose_kernel<<<grid, 256, 0, s>>>(static_cast<const uint32_t*>(in), rows, cols,
-                                               static_cast<uint32_t*>(out));
-  else
-    lora_transpose_kernel<<<grid, 256, 0, s>>>(static_cast<const uint16_t*>(in), rows, cols,
-                                               static_cast<uint16_t*>(out));
+hipError_t launch_lora_prepare(const LoraPrepareArgs& a, hipStream_t s) {
+  const int64_t ranks = (a.rank + 63) / 64, S = a.sort.adapters;
+  const int64_t tiles = S * ranks * ((a.k + 63) / 64 + (a.n + 63) / 64);
+  if (a.dtype == 0) lora_prepare_kernel<uint32_t><<<(unsigned)(1 + tiles), kSortWaves * kWave, 0, s>>>(a);
+  else lora_prepare_kernel<uint16_t><<<(unsigned)(1 + tiles), kSortWaves * kWave, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -896,18 +1112,16 @@ hipError_t launch_lora_join_shares(const float* in, int shares, int64_t elements
   return hipGetLastError();
 }
 
-hipError_t launch_lora_sort(const LoraSortArgs& a, hipStream_t s) {
-  lora_sort_kernel<<<1, kSortWaves * kWave, 0, s>>>(a);
-  return hipGetLastError();
-}
-
 hipError_t launch_lora_grad(const LoraGradArgs& a, int32_t max_entries, const int32_t* chunk0,
                             hipStream_t s) {
-  const unsigned tiles = (unsigned)((a.k + 127) / 128 + (a.n + 127) / 128);
+  const int64_t each = a.dtype == 1 ? 512 : 128;
+  const unsigned tiles = (unsigned)((a.k + each - 1) / each + (a.n + each - 1) / each);
   const dim3 grid(tiles, (unsigned)max_entries, (a.rank + kRanks - 1) / kRanks);
   if (a.dtype == 0) grad_dt<0>(a, grid, s);
-  else if (a.dtype == 1) grad_dt<1>(a, grid, s);
-  else grad_dt<2>(a, grid, s);
+  else if (a.dtype == 2) grad_dt<2>(a, grid, s);
+  else if (a.rank <= 16) lora_grad16_kernel<1><<<grid, 512, 0, s>>>(a);
+  else if (a.rank <= 32) lora_grad16_kernel<2><<<grid, 512, 0, s>>>(a);
+  else lora_grad16_kernel<4><<<grid, 512, 0, s>>>(a);
   if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
   if (max_entries > a.adapters) {      // some adapter may have several chunks
     const int64_t wide = a.rank * (a.k + a.n);
