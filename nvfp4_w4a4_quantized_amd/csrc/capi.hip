@@ -961,12 +961,15 @@ int lora_forward(const void* x, int dtype, int64_t tokens, int64_t k, int64_t ld
   if (workspace_bytes < lora_forward_workspace_size(tokens, k, rank)) return NVFP4_WORKSPACE_TOO_SMALL;
   hipStream_t s = static_cast<hipStream_t>(stream);
   float* shares = static_cast<float*>(workspace);
-  if (launch_lora_down(lora_down(x, dtype, tokens, k, ld_x, ids, a, adapters, rank, shares), s) !=
-      hipSuccess)
+  const bool direct = lora_direct(dtype, tokens, k, n, rank);
+  if (!direct &&
+      launch_lora_down(lora_down(x, dtype, tokens, k, ld_x, ids, a, adapters, rank, shares), s) !=
+          hipSuccess)
     return NVFP4_HIP_ERROR;
   LoraUpArgs u = lora_up(shares, lora_shares(tokens, k, rank), tokens, n, ids, b, dtype, scale, adapters,
                          rank, base, out_dtype, ld_base, out, out_dtype);
   u.h_out = h;
+  if (direct) { u.x = x; u.a = a; u.k = k; u.ld_x = ld_x; }
   return hip_status(launch_lora_up(u, s));
 }
 
@@ -1009,15 +1012,18 @@ int nvfp4_lora_matvec(const void* x, int x_dtype, int64_t tokens, int64_t ld_x,
   const LoraMatvecLayout L = carve_lora_matvec(workspace, tokens, n, k, rank);
   if (workspace_bytes < L.bytes) return NVFP4_WORKSPACE_TOO_SMALL;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (launch_lora_down(lora_down(x, x_dtype, tokens, k, ld_x, ids, a, adapters, rank, L.shares), s) !=
-      hipSuccess)
+  const bool direct = lora_direct(x_dtype, tokens, k, n, rank);
+  if (!direct &&
+      launch_lora_down(lora_down(x, x_dtype, tokens, k, ld_x, ids, a, adapters, rank, L.shares), s) !=
+          hipSuccess)
     return NVFP4_HIP_ERROR;
   MatvecArgs m = matvec_args(x, x_dtype, ld_x, tokens, w, 1, n, k);
   m.out = L.y; m.out_dtype = 0;
   if (launch_matvec(m, s) != hipSuccess) return NVFP4_HIP_ERROR;
-  return hip_status(launch_lora_up(lora_up(L.shares, lora_shares(tokens, k, rank), tokens, n, ids, b,
-                                           x_dtype, scale, adapters, rank, L.y, 0, n, out, out_dtype),
-                                   s));
+  LoraUpArgs u = lora_up(L.shares, lora_shares(tokens, k, rank), tokens, n, ids, b, x_dtype, scale,
+                         adapters, rank, L.y, 0, n, out, out_dtype);
+  if (direct) { u.x = x; u.a = a; u.k = k; u.ld_x = ld_x; }
+  return hip_status(launch_lora_up(u, s));
 }
 
 struct LoraBackwardLayout {

@@ -274,6 +274,9 @@ struct LoraUpArgs {
   const void* base; int base_dtype; int64_t ld_base;   // nullable [tokens, ld_base]: the output's type or binary32
   void* out; int out_dtype;   // [tokens, n]
   float* h_out; int h_scaled; // nullable [tokens, rank]: h, times the scale if h_scaled
+  // not NULL: h is computed by the same launch, from x [tokens, ld_x] and a
+  // [adapters, rank, k] (lora_direct)
+  const void* x; const void* a; int64_t k, ld_x;
   int64_t wide;               // (the launcher's)
 };
 struct LoraSortArgs {
@@ -295,6 +298,7 @@ struct LoraGradArgs {
   float* da; float* db;       // [adapters, rank, k], [adapters, n, rank]
   float* parts;               // [max_entries, rank * (k + n)]
 };
+bool lora_direct(int dtype, int64_t tokens, int64_t k, int64_t n, int32_t rank);
 int lora_shares(int64_t tokens, int64_t k, int32_t rank);
 int32_t lora_chunk(int dtype, int64_t tokens, int64_t k, int64_t n, int32_t rank);
 hipError_t launch_lora_down(LoraDownArgs a, hipStream_t s);

@@ -343,8 +343,9 @@ __device__ __forceinline__ void put16(void* out, int64_t at, int count, const fl
 // a wave at a time.  MFMA row 16 (i / 4) + 4 j + i % 4 of the wave's 64 is row i
 // of product j, so that a lane ends with 16 consecutive columns of its token.
 // The sums start from the base's values, which are loaded a turn ahead.  BIG:
-// more than 32 ranks, 64 at a time.
-template <int DT, int OT, int TT, bool SLOT, bool BIG>
+// more than 32 ranks, 64 at a time.  DIRECT: each workgroup computes h itself, the
+// whole of A[s] x, so that a few tokens take one launch.
+template <int DT, int OT, int TT, bool SLOT, bool BIG, bool DIRECT>
 __global__ __launch_bounds__(kThreads, BIG ? 2 : 3) void lora_up_kernel(LoraUpArgs p) {
   typedef typename Elem<DT>::type T;
   typedef typename Elem<OT>::type O;
@@ -353,6 +354,7 @@ __global__ __launch_bounds__(kThreads, BIG ? 2 : 3) void lora_up_kernel(LoraUpAr
   constexpr int kBase = 16 / Piece<OT>::kN;     // of 16 columns
   __shared__ TokenList list;
   __shared__ __align__(16) Ranked<DT, TOK, kPass> hs;
+  __shared__ f32x4_t red[DIRECT ? kWaves : 1][2][kWave];
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   const int i = lane % 16, q = lane / 16;
   const int64_t first = SLOT ? 0 : (int64_t)blockIdx.x * TOK;
@@ -419,6 +421,39 @@ __global__ __launch_bounds__(kThreads, BIG ? 2 : 3) void lora_up_kernel(LoraUpAr
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) hs.put(t, r + e, narrow, h[e]);
+      }
+    };
+    // the same from x: every wave a share of K, added in wave order
+    auto stage_x = [&](auto rt_c) {
+      constexpr int RT = decltype(rt_c)::value;
+      f32x4_t acc[RT][1];
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) acc[rt][0] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+      if (s >= 0) {
+        const T* xr[1] = {static_cast<const T*>(p.x) + token((in >> i) & 1 ? i : 0) * p.ld_x};
+        const T* ar[RT];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          const int r = 16 * rt + i;
+          ar[rt] = static_cast<const T*>(p.a) + ((int64_t)s * p.rank + (r < p.rank ? r : p.rank - 1)) * p.k;
+        }
+        down_products<DT, RT, 1>(ar, xr, 0, p.k, wave, q, acc);
+      }
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) red[wave][rt][lane] = acc[rt][0];
+      __syncthreads();
+      if (wave < RT) {
+        f32x4_t v = red[0][wave % 2][lane];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) v += red[w][wave % 2][lane];
+        const float c = s >= 0 && p.scale ? p.scale[s] : 1.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = 16 * wave + 4 * q + e;
+          const bool live = r < p.rank && (in >> i) & 1;
+          if (live && p.h_out && blockIdx.y == 0) p.h_out[token(i) * p.rank + r] = v[e];
+          hs.put(i, r, narrow, live ? c * v[e] : 0.0f);
+        }
       }
     };
     auto load_b = [&](int adapter, int64_t n0, int j, int r0, RankPiece<DT> (&b)[kPieces]) {
@@ -489,7 +524,9 @@ __global__ __launch_bounds__(kThreads, BIG ? 2 : 3) void lora_up_kernel(LoraUpAr
     fetch(w0 + wave * kWave, raw);
     if (once) {
       __syncthreads();
-      stage(0);
+      if constexpr (!DIRECT) stage(0);
+      else if (narrow) stage_x(std::integral_constant<int, 1>{});
+      else stage_x(std::integral_constant<int, 2>{});
       __syncthreads();
     }
     for (int64_t turn = w0; turn < n_end; turn += kThreads) {
@@ -1019,12 +1056,14 @@ void down_dt(const LoraDownArgs& a, int group, dim3 grid, hipStream_t s) {
 template <int DT, int OT>
 void up_out(const LoraUpArgs& a, int group, dim3 grid, hipStream_t s) {
   const bool big = a.rank > 32;
-  if (group == 1)
-    big ? lora_up_kernel<DT, OT, 1, true, true><<<grid, kThreads, 0, s>>>(a)
-        : lora_up_kernel<DT, OT, 1, true, false><<<grid, kThreads, 0, s>>>(a);
+  if (a.x)
+    lora_up_kernel<DT, OT, 1, true, false, true><<<grid, kThreads, 0, s>>>(a);
+  else if (group == 1)
+    big ? lora_up_kernel<DT, OT, 1, true, true, false><<<grid, kThreads, 0, s>>>(a)
+        : lora_up_kernel<DT, OT, 1, true, false, false><<<grid, kThreads, 0, s>>>(a);
   else
-    big ? lora_up_kernel<DT, OT, 2, false, true><<<grid, kThreads, 0, s>>>(a)
-        : lora_up_kernel<DT, OT, 2, false, false><<<grid, kThreads, 0, s>>>(a);
+    big ? lora_up_kernel<DT, OT, 2, false, true, false><<<grid, kThreads, 0, s>>>(a)
+        : lora_up_kernel<DT, OT, 2, false, false, false><<<grid, kThreads, 0, s>>>(a);
 }
 
 template <int DT>
@@ -1070,6 +1109,14 @@ int32_t lora_chunk(int dtype, int64_t tokens, int64_t k, int64_t n, int32_t rank
   const int64_t want = ((rank > 32 ? 512 : 768) + tiles - 1) / tiles;
   const int64_t c = ((tokens + want - 1) / want + 63) / 64 * 64;
   return (int32_t)(c < 64 ? 64 : c);
+}
+
+// Whether the up products may compute h themselves: up to 32 ranks of 160 KB in
+// all, and 16 MB read by the call's workgroups.
+bool lora_direct(int dtype, int64_t tokens, int64_t k, int64_t n, int32_t rank) {
+  const int64_t bytes = (int64_t)rank * k * (dtype == 0 ? 4 : 2);
+  return tokens <= kWindow && rank <= 32 && bytes <= (160 << 10) &&
+         bytes * tokens * ((n + 255) / 256) <= (16 << 20);
 }
 
 hipError_t launch_lora_down(LoraDownArgs a, hipStream_t s) {
