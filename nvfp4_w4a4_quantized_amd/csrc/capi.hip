@@ -941,7 +941,7 @@ size_t lora_forward_workspace_size(int64_t tokens, int64_t k, int32_t rank) {
       rank > kMaxRank)
     return 0;
   Carver c(nullptr);
-  c.take<float>((size_t)(lora_shares(tokens, k, rank) * tokens * rank));
+  c.take<float>((size_t)(lora_shares(tokens, k) * tokens * rank));
   return c.used;
 }
 
@@ -966,7 +966,7 @@ int lora_forward(const void* x, int dtype, int64_t tokens, int64_t k, int64_t ld
       launch_lora_down(lora_down(x, dtype, tokens, k, ld_x, ids, a, adapters, rank, shares), s) !=
           hipSuccess)
     return NVFP4_HIP_ERROR;
-  LoraUpArgs u = lora_up(shares, lora_shares(tokens, k, rank), tokens, n, ids, b, dtype, scale, adapters,
+  LoraUpArgs u = lora_up(shares, lora_shares(tokens, k), tokens, n, ids, b, dtype, scale, adapters,
                          rank, base, out_dtype, ld_base, out, out_dtype);
   u.h_out = h;
   if (direct) { u.x = x; u.a = a; u.k = k; u.ld_x = ld_x; }
@@ -982,7 +982,7 @@ struct LoraMatvecLayout {
 static LoraMatvecLayout carve_lora_matvec(void* ws, int64_t tokens, int64_t n, int64_t k, int32_t rank) {
   Carver c(ws);
   LoraMatvecLayout L;
-  L.shares = c.take<float>((size_t)(lora_shares(tokens, k, rank) * tokens * rank));
+  L.shares = c.take<float>((size_t)(lora_shares(tokens, k) * tokens * rank));
   L.y = c.take<float>((size_t)(tokens * n));
   L.bytes = c.used;
   return L;
@@ -1020,7 +1020,7 @@ int nvfp4_lora_matvec(const void* x, int x_dtype, int64_t tokens, int64_t ld_x,
   MatvecArgs m = matvec_args(x, x_dtype, ld_x, tokens, w, 1, n, k);
   m.out = L.y; m.out_dtype = 0;
   if (launch_matvec(m, s) != hipSuccess) return NVFP4_HIP_ERROR;
-  LoraUpArgs u = lora_up(L.shares, lora_shares(tokens, k, rank), tokens, n, ids, b, x_dtype, scale,
+  LoraUpArgs u = lora_up(L.shares, lora_shares(tokens, k), tokens, n, ids, b, x_dtype, scale,
                          adapters, rank, L.y, 0, n, out, out_dtype);
   if (direct) { u.x = x; u.a = a; u.k = k; u.ld_x = ld_x; }
   return hip_status(launch_lora_up(u, s));
@@ -1043,7 +1043,7 @@ static LoraBackwardLayout carve_lora_backward(void* ws, int dtype, int64_t T, in
   const size_t e = dtype_size(dtype), wide = (size_t)rank * (size_t)(k + n);
   L.at = c.take<char>(e * S * rank * k);
   L.bt = c.take<char>(e * S * rank * n);
-  const int sk = lora_shares(T, k, rank), sn = lora_shares(T, n, rank);
+  const int sk = lora_shares(T, k), sn = lora_shares(T, n);
   L.shares = c.take<float>((size_t)((sk > sn ? sk : sn) * T * rank));
   L.g = c.take<float>((size_t)(T * rank));
   L.h = c.take<float>((size_t)(T * rank));
@@ -1085,7 +1085,7 @@ int lora_backward(const void* dy, int dtype, int64_t tokens, int64_t n, int64_t 
   if (!h) {
     e = launch_lora_down(lora_down(x, dtype, tokens, k, ld_x, ids, a, adapters, rank, L.shares), s);
     if (e == hipSuccess)
-      e = launch_lora_join_shares(L.shares, lora_shares(tokens, k, rank), tokens * rank, L.h, s);
+      e = launch_lora_join_shares(L.shares, lora_shares(tokens, k), tokens * rank, L.h, s);
   }
   LoraPrepareArgs pr{};
   pr.sort.ids = ids; pr.sort.tokens = tokens; pr.sort.adapters = adapters; pr.sort.chunk = L.chunk;
@@ -1096,7 +1096,7 @@ int lora_backward(const void* dy, int dtype, int64_t tokens, int64_t n, int64_t 
   if (e == hipSuccess)
     e = launch_lora_down(lora_down(dy, dtype, tokens, n, ld_dy, ids, L.bt, adapters, rank, L.shares), s);
   if (e == hipSuccess) {
-    LoraUpArgs u = lora_up(L.shares, lora_shares(tokens, n, rank), tokens, k, ids, L.at, dtype, scale,
+    LoraUpArgs u = lora_up(L.shares, lora_shares(tokens, n), tokens, k, ids, L.at, dtype, scale,
                            adapters, rank, base, dtype, ld_base, dx, dtype);
     u.h_out = L.g; u.h_scaled = 1;
     e = launch_lora_up(u, s);

@@ -262,7 +262,7 @@ struct LoraDownArgs {
   const void* x; int dtype; int64_t tokens, k, ld_x;   // the long rows
   const int32_t* ids; int32_t adapters, rank;
   const void* a;              // [adapters, rank, k]
-  float* h;                   // [lora_shares(tokens, k, rank), tokens, rank]
+  float* h;                   // [lora_shares(tokens, k), tokens, rank]
   int64_t share;              // (the launcher's)
 };
 struct LoraUpArgs {
@@ -299,7 +299,7 @@ struct LoraGradArgs {
   float* parts;               // [max_entries, rank * (k + n)]
 };
 bool lora_direct(int dtype, int64_t tokens, int64_t k, int64_t n, int32_t rank);
-int lora_shares(int64_t tokens, int64_t k, int32_t rank);
+int lora_shares(int64_t tokens, int64_t k);
 int32_t lora_chunk(int dtype, int64_t tokens, int64_t k, int64_t n, int32_t rank);
 hipError_t launch_lora_down(LoraDownArgs a, hipStream_t s);
 hipError_t launch_lora_up(LoraUpArgs a, hipStream_t s);

@@ -40,6 +40,7 @@ constexpr int kWindow = 256;    // most tokens that workgroups per token look th
 constexpr int kWaves = 4;
 constexpr int kThreads = kWaves * kWave;
 constexpr int kRanks = 64;      // ranks of one pass
+constexpr int kMostShares = 8;  // of K
 
 // ---- the tokens of one adapter ------------------------------------------
 
@@ -300,58 +301,52 @@ struct RankPiece {
       for (int e = 0; e < kN; ++e) v[e] = r + e < end ? row[r + e] : (typename Elem<DT>::type)0;
     }
   }
+  // end a multiple of kN: zeros from there on
+  __device__ __forceinline__ void load_whole(const typename Elem<DT>::type* row, int r, int end) {
+    const bool in = r < end;
+    __builtin_memcpy(v, row + (in ? r : 0), sizeof(v));
+    uint32_t w[sizeof(v) / 4];
+    __builtin_memcpy(w, v, sizeof(v));
+#pragma unroll
+    for (uint32_t& x : w) x = in ? x : 0u;
+    __builtin_memcpy(v, w, sizeof(v));
+  }
 };
 
-// Values of 16 columns from `at` on, `count` of them inside.
-template <int DT>
-__device__ __forceinline__ void get16(const void* base, int64_t at, int count, float (&v)[16]) {
+// N values from `at` on, `left` of them inside (zeros behind).
+template <int DT, int N>
+__device__ __forceinline__ void get_some(const void* from, int64_t at, int64_t left, float (&v)[N]) {
   typedef typename Elem<DT>::type T;
-  const T* b = static_cast<const T*>(base) + at;
-  if (count >= 16) {
-#pragma unroll
-    for (int c = 0; c < 16; c += Piece<DT>::kN) {
-      Piece<DT> p;
-      p.load(b + c);
-#pragma unroll
-      for (int e = 0; e < Piece<DT>::kN; ++e) v[c + e] = p.get(e);
-    }
+  const T* b = static_cast<const T*>(from) + at;
+  T x[N];
+  if (left >= N) {
+    __builtin_memcpy(x, b, sizeof(x));
   } else {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) v[e] = e < count ? Elem<DT>::to_float(b[e]) : 0.0f;
+    for (int e = 0; e < N; ++e) x[e] = e < left ? b[e] : (T)0;
   }
-}
-
-template <int DT>
-__device__ __forceinline__ void put16(void* out, int64_t at, int count, const float (&v)[16]) {
-  typename Elem<DT>::type* o = static_cast<typename Elem<DT>::type*>(out) + at;
-  if (count >= 16) {
 #pragma unroll
-    for (int c = 0; c < 16; c += Piece<DT>::kN) {
-      Piece<DT> w;
-#pragma unroll
-      for (int e = 0; e < Piece<DT>::kN; ++e) w.set(e, v[c + e]);
-      w.store(o + c);
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 16; ++e)
-      if (e < count) o[e] = Elem<DT>::from_float(v[e]);
-  }
+  for (int e = 0; e < N; ++e) v[e] = Elem<DT>::to_float(x[e]);
 }
 
 // Grid: x = tokens (SLOT) or groups of 16 TT tokens, y = p.wide columns each, 64
-// a wave at a time.  MFMA row 16 (i / 4) + 4 j + i % 4 of the wave's 64 is row i
-// of product j, so that a lane ends with 16 consecutive columns of its token.
+// a wave at a time.  Which of the wave's 64 columns is row i of product j is chosen
+// so that a lane ends with 16-byte pieces of its token, and a load or store covers
+// 64 consecutive bytes of every token (32 bytes a lane, in two halves of 16 each,
+// cost 4096 x 5120 29 us instead of MEASURED).
 // The sums start from the base's values, which are loaded a turn ahead.  BIG:
-// more than 32 ranks, 64 at a time.  DIRECT: each workgroup computes h itself, the
+// more than 32 ranks, 64 at a time.  WHOLE: whole pieces everywhere and the kind of
+// base known, so that no branch stands around a load (the compiler waits for every
+// load in flight where its paths join).  DIRECT: each workgroup computes h itself, the
 // whole of A[s] x, so that a few tokens take one launch.
-template <int DT, int OT, int TT, bool SLOT, bool BIG, bool DIRECT>
+enum { kAny = 0, kNoBase = 1, kSameBase = 2, kWideBase = 3 };    // kWideBase: binary32
+template <int DT, int OT, int TT, bool SLOT, bool BIG, bool DIRECT, int WHOLE>
 __global__ __launch_bounds__(kThreads, BIG ? 2 : 3) void lora_up_kernel(LoraUpArgs p) {
   typedef typename Elem<DT>::type T;
   typedef typename Elem<OT>::type O;
   constexpr int TOK = 16 * TT;
   constexpr int kPass = BIG ? kRanks : 32, kPieces = kPass / (DT == 1 ? 32 : 16);
-  constexpr int kBase = 16 / Piece<OT>::kN;     // of 16 columns
+  constexpr int kN = Piece<OT>::kN, kBase = 16 / kN;     // columns of a piece, pieces of a lane
   __shared__ TokenList list;
   __shared__ __align__(16) Ranked<DT, TOK, kPass> hs;
   __shared__ f32x4_t red[DIRECT ? kWaves : 1][2][kWave];
@@ -373,54 +368,59 @@ __global__ __launch_bounds__(kThreads, BIG ? 2 : 3) void lora_up_kernel(LoraUpAr
     auto token = [&](int at) -> int64_t { return SLOT ? list.at[g0 + at] : first + at; };
 
     // c h of the group's tokens, ranks r0 and on: four of a token's ranks a
-    // thread, eight shares of them in flight, added in order
-    auto stage = [&](int r0) {
+    // thread, its shares in flight together and added in order
+    auto fetch_h = [&](int v, int r0, int padded, float (&h)[kMostShares][4]) {
+      const int t = v / (padded / 4), r = 4 * (v % (padded / 4));
       const int ranks = p.rank - r0 < kPass ? p.rank - r0 : kPass;
-      const int padded = DT == 1 ? (narrow ? 16 : (ranks + 31) / 32 * 32) : (ranks + 15) / 16 * 16;
+      const bool live = t < TOK && r < ranks && (SLOT ? g0 + t < m : first + t < p.tokens);
+      const float* from = p.h + (live ? token(t) * p.rank + r0 + r : 0);
       const int64_t step = p.tokens * p.rank;
-      const bool dense = p.rank % 4 == 0;
-      for (int v = threadIdx.x; v < TOK * padded / 4; v += kThreads) {
-        const int t = v / (padded / 4), r = 4 * (v % (padded / 4));
-        float h[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if ((in >> t) & 1 && r < ranks) {
-          const int64_t tok = token(t), at = tok * p.rank + r0 + r;
-          const int a = SLOT ? s : key_of(p.ids[tok], p.adapters);
-          if (a >= 0) {
-            const float c = p.scale ? p.scale[a] : 1.0f;
-            if (dense) {
-              __builtin_memcpy(h, p.h + at, 16);
-              for (int w = 1; w < p.shares; w += 8) {
-                float more[8][4];
+      if (WHOLE != kAny || p.rank % 4 == 0) {
 #pragma unroll
-                for (int u = 0; u < 8; ++u)
-                  __builtin_memcpy(more[u], p.h + at + (w + u < p.shares ? w + u : 0) * step, 16);
+        for (int w = 0; w < kMostShares; ++w) __builtin_memcpy(h[w], from + (w < p.shares ? w * step : 0), 16);
+      } else {
 #pragma unroll
-                for (int u = 0; u < 8; ++u)
+        for (int w = 0; w < kMostShares; ++w)
 #pragma unroll
-                  for (int e = 0; e < 4; ++e) h[e] = w + u < p.shares ? h[e] + more[u][e] : h[e];
-              }
-            } else {
-              for (int w = 0; w < p.shares; ++w)
+          for (int e = 0; e < 4; ++e) h[w][e] = w < p.shares && live && r + e < ranks ? from[w * step + e] : 0.0f;
+      }
+    };
+    auto put_h = [&](int v, int r0, int padded, const float (&h)[kMostShares][4]) {
+      const int t = v / (padded / 4), r = 4 * (v % (padded / 4));
+      const int ranks = p.rank - r0 < kPass ? p.rank - r0 : kPass;
+      const bool live = t < TOK && r < ranks && (in >> (t & 63)) & 1;
+      const int a = SLOT ? s : __shfl(key, t & 63);
+      const float c = a >= 0 && p.scale ? p.scale[a] : 1.0f;
+      float f[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  if (r + e < ranks) h[e] = w == 0 ? p.h[at + e] : h[e] + p.h[at + e + w * step];
-            }
-            if (p.h_out && blockIdx.y == 0 && !p.h_scaled) {
+      for (int e = 0; e < 4; ++e) {
+        f[e] = h[0][e];
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (r + e < ranks) p.h_out[at + e] = h[e];
-            }
+        for (int w = 1; w < kMostShares; ++w) f[e] = w < p.shares ? f[e] + h[w][e] : f[e];
+        if (!live || a < 0) f[e] = 0.0f;
+      }
+      if (live && p.h_out && blockIdx.y == 0) {
+        float* to = p.h_out + token(t) * p.rank + r0 + r;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) h[e] *= c;
-          }
-          if (p.h_out && blockIdx.y == 0 && (p.h_scaled || a < 0)) {
+        for (int e = 0; e < 4; ++e)
+          if (r + e < ranks) to[e] = p.h_scaled ? c * f[e] : f[e];
+      }
+      if (t < TOK) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (r + e < ranks) p.h_out[at + e] = h[e];
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) hs.put(t, r + e, narrow, h[e]);
+        for (int e = 0; e < 4; ++e) hs.put(t, r + e, narrow, c * f[e]);
+      }
+    };
+    auto padded_ranks = [&](int r0) -> int {
+      const int ranks = p.rank - r0 < kPass ? p.rank - r0 : kPass;
+      return DT == 1 ? (narrow ? 16 : (ranks + 31) / 32 * 32) : (ranks + 15) / 16 * 16;
+    };
+    auto stage = [&](int r0) {
+      const int padded = padded_ranks(r0);
+      // (every thread takes every turn: put_h exchanges values in the wave)
+      for (int v = threadIdx.x; v - (int)threadIdx.x < TOK * padded / 4; v += kThreads) {
+        float h[kMostShares][4];
+        fetch_h(v, r0, padded, h);
+        put_h(v, r0, padded, h);
       }
     };
     // the same from x: every wave a share of K, added in wave order
@@ -457,18 +457,19 @@ __global__ __launch_bounds__(kThreads, BIG ? 2 : 3) void lora_up_kernel(LoraUpAr
       }
     };
     auto load_b = [&](int adapter, int64_t n0, int j, int r0, RankPiece<DT> (&b)[kPieces]) {
-      const int64_t n = n0 + 16 * (i / 4) + 4 * j + i % 4;
+      const int64_t n = n0 + (kN == 8 ? 32 * (j / 2) + 8 * (i / 4) + 4 * (j % 2) + i % 4 : 16 * j + i);
       const T* row = static_cast<const T*>(p.b) + ((int64_t)adapter * p.n + (n < p.n ? n : p.n - 1)) * p.rank;
 #pragma unroll
       for (int k = 0; k < kPieces; ++k) {
         const int r = r0 + (DT == 1 ? (narrow ? 8 * (q % 2) : 32 * k + 8 * q) : 16 * k + 4 * q);
-        if ((DT == 1 ? 32 : 16) * k < p.rank - r0) b[k].load(row, r, p.rank);
+        if constexpr (WHOLE != kAny) b[k].load_whole(row, r, p.rank);
+        else if ((DT == 1 ? 32 : 16) * k < p.rank - r0) b[k].load(row, r, p.rank);
       }
     };
-    // acc[j][t] += B h for the columns of j in [J0, J1)
-    auto multiply = [&](const RankPiece<DT> (&b)[4][kPieces], int r0, auto J0, auto J1, f32x4_t (&acc)[4][TT]) {
+    // acc[j][t] += B h for the products [J, J + JN)
+    auto products = [&](const RankPiece<DT>* b, int r0, auto jn_c, f32x4_t (*acc)[TT]) {
+      constexpr int JN = decltype(jn_c)::value;
       const int ranks = p.rank - r0 < kPass ? p.rank - r0 : kPass;
-      constexpr int j0 = decltype(J0)::value, j1 = decltype(J1)::value;
       if constexpr (DT == 1) {
         const int steps = narrow ? 2 : (ranks + 31) / 32 * 3;
 #pragma unroll
@@ -478,9 +479,9 @@ __global__ __launch_bounds__(kThreads, BIG ? 2 : 3) void lora_up_kernel(LoraUpAr
           for (int t = 0; t < TT; ++t) {
             const bf16x8_t h = *reinterpret_cast<const bf16x8_t*>(hs.part + Ranked<DT, TOK, kPass>::at(st, 16 * t + i, 8 * q));
 #pragma unroll
-            for (int j = j0; j < j1; ++j) {
+            for (int j = 0; j < JN; ++j) {
               bf16x8_t u;
-              __builtin_memcpy(&u, b[j][st / 3].v, 16);
+              __builtin_memcpy(&u, b[j * kPieces + st / 3].v, 16);
               acc[j][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u, h, acc[j][t], 0, 0, 0);
             }
           }
@@ -493,71 +494,85 @@ __global__ __launch_bounds__(kThreads, BIG ? 2 : 3) void lora_up_kernel(LoraUpAr
           for (int t = 0; t < TT; ++t) {
             const f32x4_t h = *reinterpret_cast<const f32x4_t*>(hs.row + (16 * t + i) * Ranked<DT, TOK, kPass>::kLd + 16 * rb + 4 * q);
 #pragma unroll
-            for (int j = j0; j < j1; ++j)
+            for (int j = 0; j < JN; ++j)
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                acc[j][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(Elem<DT>::to_float(b[j][rb].v[e]), h[e], acc[j][t], 0, 0, 0);
+                acc[j][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(Elem<DT>::to_float(b[j * kPieces + rb].v[e]), h[e], acc[j][t], 0, 0, 0);
           }
         }
       }
     };
-    using C0 = std::integral_constant<int, 0>;
-    using C4 = std::integral_constant<int, 4>;
-    // the lane's columns from n on, and its tokens' base there
-    auto columns = [&](int64_t n0) -> int {
-      const int64_t left = n_end - n0 - 16 * q;
-      return left < 16 ? (int)left : 16;
-    };
-    const bool same = p.base && p.base_dtype == OT;
+    // the lane's piece c, and the tokens' base there
+    auto column = [&](int64_t n0, int c) -> int64_t { return n0 + 64 / kBase * c + kN * q; };
+    const bool same = WHOLE != kAny ? WHOLE == kSameBase : p.base && p.base_dtype == OT;
     auto fetch = [&](int64_t n0, Piece<OT> (&raw)[TT][kBase]) {
-      const int count = columns(n0);
+      if (WHOLE != kAny && n0 >= n_end) n0 = w0;      // (a wave without columns: not used)
 #pragma unroll
       for (int t = 0; t < TT; ++t) {
-        if (!same || count < 16) continue;
-        const O* b = static_cast<const O*>(p.base) + token((in >> (16 * t + i)) & 1 ? 16 * t + i : 0) * p.ld_base + n0 + 16 * q;
+        const O* b = static_cast<const O*>(p.base) + token((in >> (16 * t + i)) & 1 ? 16 * t + i : 0) * p.ld_base;
 #pragma unroll
-        for (int c = 0; c < kBase; ++c) raw[t][c].load(b + c * Piece<OT>::kN);
+        for (int c = 0; c < kBase; ++c)
+          if (same && (WHOLE != kAny || column(n0, c) + kN <= n_end)) raw[t][c].load(b + column(n0, c));
       }
     };
+    // what the first turn needs is in flight together: h (all of a thread's, where
+    // the ranks fit one pass of up to 32), then the adapter's rows, then the base
     Piece<OT> raw[TT][kBase];
+    RankPiece<DT> b[4][kPieces];
     const bool once = !BIG || p.rank <= kPass;
+    float mine[kMostShares][4];
+    const int padded = padded_ranks(0);
+    if constexpr (!BIG && !DIRECT) fetch_h(threadIdx.x, 0, padded, mine);
+    uint64_t todo = in;
+    int a = SLOT ? s : __shfl(key, __builtin_ctzll(todo));
+    auto load_all = [&](int64_t n0) {
+      if (a >= 0) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) load_b(a, n0, j, 0, b[j]);
+      }
+    };
+    load_all(w0 + wave * kWave);
     fetch(w0 + wave * kWave, raw);
     if (once) {
       __syncthreads();
-      if constexpr (!DIRECT) stage(0);
+      if constexpr (BIG) stage(0);
+      else if constexpr (!DIRECT) put_h(threadIdx.x, 0, padded, mine);
       else if (narrow) stage_x(std::integral_constant<int, 1>{});
       else stage_x(std::integral_constant<int, 2>{});
       __syncthreads();
     }
     for (int64_t turn = w0; turn < n_end; turn += kThreads) {
-      const int64_t n0 = turn + wave * kWave, n = n0 + 16 * q;
-      const int count = columns(n0);
+      const int64_t n0 = turn + wave * kWave;
       f32x4_t acc[4][TT];
-      uint64_t todo = in;
-      int a = SLOT ? s : __shfl(key, __builtin_ctzll(todo));
-      RankPiece<DT> b[4][kPieces];
-      if (a >= 0) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) load_b(a, n0, j, 0, b[j]);
+      if (WHOLE != kAny && !BIG && n0 >= n_end) break;      // (a turn of BIG has barriers)
+      if (turn != w0) {
+        todo = in;
+        a = SLOT ? s : __shfl(key, __builtin_ctzll(todo));
+        load_all(n0);
       }
 #pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        float v[16];
-        if (same && count >= 16) {
+      for (int t = 0; t < TT; ++t)
 #pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = raw[t][e / Piece<OT>::kN].get(e % Piece<OT>::kN);
-        } else {
+        for (int c = 0; c < kBase; ++c) {
+          const int64_t left = WHOLE != kAny ? kN : n_end - column(n0, c);
+          float v[kN];
+          if (same && left >= kN) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = 0.0f;
-          const int64_t tok = token((in >> (16 * t + i)) & 1 ? 16 * t + i : 0);
-          if (same && count > 0) get16<OT>(p.base, tok * p.ld_base + n, count, v);
-          else if (p.base && count > 0) get16<0>(p.base, tok * p.ld_base + n, count, v);
+            for (int e = 0; e < kN; ++e) v[e] = raw[t][c].get(e);
+          } else {
+#pragma unroll
+            for (int e = 0; e < kN; ++e) v[e] = 0.0f;
+            const int64_t at = token((in >> (16 * t + i)) & 1 ? 16 * t + i : 0) * p.ld_base + column(n0, c);
+            if constexpr (WHOLE == kAny) {
+              if (same && left > 0) get_some<OT, kN>(p.base, at, left, v);
+              else if (p.base && left > 0) get_some<0, kN>(p.base, at, left, v);
+            } else if constexpr (WHOLE == kWideBase) {
+              get_some<0, kN>(p.base, at, kN, v);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < kN; ++e) acc[kN / 4 * c + e / 4][t][e % 4] = v[e];
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[j][t][e] = v[4 * j + e];
-      }
       if (turn + kThreads < n_end) fetch(n0 + kThreads, raw);
       for (;;) {
         const uint64_t mask = SLOT ? in : __ballot(key == a);
@@ -574,40 +589,38 @@ __global__ __launch_bounds__(kThreads, BIG ? 2 : 3) void lora_up_kernel(LoraUpAr
             for (int j = 0; j < 4; ++j) load_b(a, n0, j, r0, b[j]);
           }
           if (mask == in) {
-            multiply(b, r0, C0{}, C4{}, acc);
-          } else {
+            products(&b[0][0], r0, std::integral_constant<int, 4>{}, acc);
+            continue;
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
             // only its own tokens take an adapter's results: another's infinity
             // or NaN times their zeros would not be zero
-            f32x4_t now[4][TT];
+            f32x4_t now[1][TT];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int t = 0; t < TT; ++t) now[0][t] = acc[j][t];
+            products(b[j], r0, std::integral_constant<int, 1>{}, now);
 #pragma unroll
-              for (int t = 0; t < TT; ++t) now[j][t] = acc[j][t];
-            multiply(b, r0, C0{}, C4{}, now);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-              for (int t = 0; t < TT; ++t)
-                if ((mask >> (16 * t + i)) & 1) acc[j][t] = now[j][t];
+            for (int t = 0; t < TT; ++t)
+              if ((mask >> (16 * t + i)) & 1) acc[j][t] = now[0][t];
           }
         }
         if (todo == 0) break;
         a = __shfl(key, __builtin_ctzll(todo));
-        if (a >= 0) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) load_b(a, n0, j, 0, b[j]);
-        }
+        load_all(n0);
       }
-      if (count > 0) {
 #pragma unroll
-        for (int t = 0; t < TT; ++t) {
-          if (!((in >> (16 * t + i)) & 1)) continue;
-          float v[16];
+      for (int t = 0; t < TT; ++t) {
+        if (!((in >> (16 * t + i)) & 1)) continue;
+        O* const o = static_cast<O*>(p.out) + token(16 * t + i) * p.n;
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+        for (int c = 0; c < kBase; ++c) {
+          const int64_t n = column(n0, c), left = WHOLE != kAny ? kN : n_end - n;
+          Piece<OT> w;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[4 * j + e] = acc[j][t][e];
-          put16<OT>(p.out, token(16 * t + i) * p.n + n, count, v);
+          for (int e = 0; e < kN; ++e) w.set(e, acc[kN / 4 * c + e / 4][t][e % 4]);
+          if (left >= kN) w.store(o + n);
+          else if (left > 0) w.store_part(o + n, (int)left);
         }
       }
     }
@@ -1053,17 +1066,29 @@ void down_dt(const LoraDownArgs& a, int group, dim3 grid, hipStream_t s) {
   else down_rt<DT, 4>(a, group, grid, s);
 }
 
-template <int DT, int OT>
-void up_out(const LoraUpArgs& a, int group, dim3 grid, hipStream_t s) {
+template <int DT, int OT, int WHOLE>
+void up_kind(const LoraUpArgs& a, int group, dim3 grid, hipStream_t s) {
   const bool big = a.rank > 32;
   if (a.x)
-    lora_up_kernel<DT, OT, 1, true, false, true><<<grid, kThreads, 0, s>>>(a);
+    lora_up_kernel<DT, OT, 1, true, false, true, WHOLE><<<grid, kThreads, 0, s>>>(a);
   else if (group == 1)
-    big ? lora_up_kernel<DT, OT, 1, true, true, false><<<grid, kThreads, 0, s>>>(a)
-        : lora_up_kernel<DT, OT, 1, true, false, false><<<grid, kThreads, 0, s>>>(a);
+    big ? lora_up_kernel<DT, OT, 1, true, true, false, WHOLE><<<grid, kThreads, 0, s>>>(a)
+        : lora_up_kernel<DT, OT, 1, true, false, false, WHOLE><<<grid, kThreads, 0, s>>>(a);
   else
-    big ? lora_up_kernel<DT, OT, 2, false, true, false><<<grid, kThreads, 0, s>>>(a)
-        : lora_up_kernel<DT, OT, 2, false, false, false><<<grid, kThreads, 0, s>>>(a);
+    big ? lora_up_kernel<DT, OT, 2, false, true, false, WHOLE><<<grid, kThreads, 0, s>>>(a)
+        : lora_up_kernel<DT, OT, 2, false, false, false, WHOLE><<<grid, kThreads, 0, s>>>(a);
+}
+
+template <int DT, int OT>
+void up_out(const LoraUpArgs& a, int group, dim3 grid, hipStream_t s) {
+  if constexpr (DT == OT) {
+    if (a.n % (a.rank > 32 ? kThreads : kWave) == 0 && a.rank % (DT == 1 ? 8 : 4) == 0) {
+      if (!a.base) return up_kind<DT, OT, kNoBase>(a, group, grid, s);
+      if (a.base_dtype == OT) return up_kind<DT, OT, kSameBase>(a, group, grid, s);
+      return up_kind<DT, OT, kWideBase>(a, group, grid, s);
+    }
+  }
+  up_kind<DT, OT, kAny>(a, group, grid, s);
 }
 
 template <int DT>
@@ -1081,12 +1106,12 @@ void grad_dt(const LoraGradArgs& a, dim3 grid, hipStream_t s) {
 }
 
 // Tokens of a workgroup of the down products (1: the slots of up to kWindow): as
-// many as leave two workgroups a CU, so that the adapter is read least often, but
-// more than 16 where its rows are long ones of many ranks.
-int down_group(int64_t tokens, int32_t rank) {
+// many as leave two workgroups a CU with up to sixteen shares of K, so that the
+// adapter is read least often (rank 16, 8192 x 5120: 64 tokens 21.4 us, 32 23.3, 16
+// 28.0; rank 64, 32768 x 5120: 96, 159, 222; 1003 x 1999 15.0, 10.3, 10.1).
+int down_group(int64_t tokens) {
   if (tokens <= kWindow) return 1;
-  if (tokens >= 64 * 512) return 64;
-  return tokens >= 32 * 512 || rank > 32 ? 32 : 16;
+  return tokens >= 2048 ? 64 : (tokens >= 1024 ? 32 : 16);
 }
 int up_group(int64_t tokens) { return tokens <= kWindow ? 1 : 32; }
 int64_t groups(int64_t tokens, int group) { return (tokens + group - 1) / group; }
@@ -1095,11 +1120,11 @@ int64_t groups(int64_t tokens, int group) { return (tokens + group - 1) / group;
 
 // Shares of K: as many as bring the launch to two workgroups a CU, of no less
 // than one 128-byte piece a wave.
-int lora_shares(int64_t tokens, int64_t k, int32_t rank) {
-  const int64_t blocks = groups(tokens, down_group(tokens, rank)), most = (k + 255) / 256;
+int lora_shares(int64_t tokens, int64_t k) {
+  const int64_t blocks = groups(tokens, down_group(tokens)), most = (k + 255) / 256;
   int64_t w = blocks > 0 ? (512 + blocks - 1) / blocks : 1;
   w = w < most ? w : most;
-  return (int)(w < 1 ? 1 : (w > 16 ? 16 : w));
+  return (int)(w < 1 ? 1 : (w > kMostShares ? kMostShares : w));
 }
 
 // Tokens of a chunk of the gradients: enough chunks for three workgroups a CU.
@@ -1121,7 +1146,7 @@ bool lora_direct(int dtype, int64_t tokens, int64_t k, int64_t n, int32_t rank) 
 
 hipError_t launch_lora_down(LoraDownArgs a, hipStream_t s) {
   if (a.tokens == 0) return hipSuccess;
-  const int shares = lora_shares(a.tokens, a.k, a.rank), group = down_group(a.tokens, a.rank);
+  const int shares = lora_shares(a.tokens, a.k), group = down_group(a.tokens);
   a.share = ((a.k + shares - 1) / shares + 255) / 256 * 256;
   const dim3 grid((unsigned)groups(a.tokens, group), shares, (a.rank + kRanks - 1) / kRanks);
   if (a.dtype == 0) down_dt<0>(a, group, grid, s);
