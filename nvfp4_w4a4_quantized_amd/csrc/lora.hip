@@ -619,7 +619,7 @@ __global__ __launch_bounds__(kThreads, BIG ? 2 : 3) void lora_up_kernel(LoraUpAr
           Piece<OT> w;
 #pragma unroll
           for (int e = 0; e < kN; ++e) w.set(e, acc[kN / 4 * c + e / 4][t][e % 4]);
-          if (left >= kN) w.store(o + n);
+          if (left >= kN) __builtin_memcpy(o + n, w.v, 16);
           else if (left > 0) w.store_part(o + n, (int)left);
         }
       }
