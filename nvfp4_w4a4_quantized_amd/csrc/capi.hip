@@ -1047,7 +1047,7 @@ static LoraBackwardLayout carve_lora_backward(void* ws, int dtype, int64_t T, in
   L.shares = c.take<float>((size_t)((sk > sn ? sk : sn) * T * rank));
   L.g = c.take<float>((size_t)(T * rank));
   L.h = c.take<float>((size_t)(T * rank));
-  L.rows = c.take<int32_t>((size_t)T);
+  L.rows = c.take<int32_t>((size_t)T + kRowsBehind);
   L.chunk = lora_chunk(dtype, T, k, n, rank);
   L.max_entries = (int32_t)(T / L.chunk) + S;
   L.entries = c.take<int4>((size_t)L.max_entries);

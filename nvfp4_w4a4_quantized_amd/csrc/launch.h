@@ -258,6 +258,7 @@ hipError_t launch_decode_combine(const float* y_rows, const int32_t* idx, int64_
 
 // ---- lora.hip ----
 constexpr int kMaxAdapters = 1024;
+constexpr int kRowsBehind = 192;   // rows that the gradients' read-ahead may look at
 struct LoraDownArgs {
   const void* x; int dtype; int64_t tokens, k, ld_x;   // the long rows
   const int32_t* ids; int32_t adapters, rank;
@@ -281,7 +282,7 @@ struct LoraUpArgs {
 };
 struct LoraSortArgs {
   const int32_t* ids; int64_t tokens; int32_t adapters, chunk, max_entries;
-  int32_t* rows;              // [tokens]
+  int32_t* rows;              // [tokens + kRowsBehind]: zeros behind the last routed token
   int4* entries;              // [max_entries]
   int32_t* chunk0;            // [adapters + 1]
 };

@@ -737,11 +737,13 @@ __device__ __forceinline__ void lora_sort(const LoraSortArgs& p, int32_t* place,
       p.entries[before[1] + c] = make_int4(s, r0, r1, chunks);
     }
     if (s == S - 1) {
+      sums[2][0] = before[0] + count;       // all routed tokens
       p.chunk0[S] = before[1] + chunks;
       for (int c = before[1] + chunks; c < p.max_entries; ++c) p.entries[c] = make_int4(-1, 0, 0, 0);
     }
   }
   __syncthreads();
+  for (int r = sums[2][0] + threadIdx.x; r < tokens + kRowsBehind; r += kSortWaves * kWave) p.rows[r] = 0;
   walk_keys(p, t0, t1, [&](int t, int k) {
     each(k, [&](int key, uint64_t mask) {
       if (k == key) p.rows[at + bits_below(mask)] = t;
@@ -770,7 +772,7 @@ __global__ __launch_bounds__(kSortWaves * kWave) void lora_prepare_kernel(LoraPr
   union Shared {
     struct {
       int32_t place[kSortWaves * kMaxAdapters];
-      int32_t sums[2][kSortWaves];
+      int32_t sums[3][kSortWaves];
     } sort;
     T tile[64][65];
   };
@@ -878,18 +880,19 @@ __global__ __launch_bounds__(kThreads) void lora_grad_kernel(LoraGradArgs p) {
 // The binary32 form above is bound by its matrix instructions from rank 32 on
 // (rank 64: 512 us for 470 MB).
 template <int RT>
-__global__ __launch_bounds__(512, 4) void lora_grad16_kernel(LoraGradArgs p) {
-  constexpr int R = 16 * RT, W = 8, C = 4;    // waves, columns of a lane
+__global__ __launch_bounds__(RT == 4 ? 256 : 512, RT == 4 ? 3 : 4) void lora_grad16_kernel(LoraGradArgs p) {
+  constexpr int R = 16 * RT, W = RT == 4 ? 4 : 8, C = 4;    // waves, columns of a lane
   // [part][rank][32 tokens], 16-byte chunk c of row r at c ^ (r / 4) % 4
   __shared__ __align__(16) uint16_t parts[2][3 * R * 32];
   const int4 e = p.entries[blockIdx.y];
   if (e.x < 0) return;
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   const int i = lane % 16, q = lane / 16, z0 = blockIdx.z * kRanks;
-  const int tiles_a = (int)((p.k + 511) / 512);
+  constexpr int kCols = 16 * C * W;
+  const int tiles_a = (int)((p.k + kCols - 1) / kCols);
   const bool down = (int)blockIdx.x < tiles_a;       // dA (g, x), else dB (c h, dy)
   const int64_t width = down ? p.k : p.n, ld = down ? p.ld_x : p.ld_dy;
-  const int64_t c0 = (int64_t)(down ? blockIdx.x : blockIdx.x - tiles_a) * 512 + 16 * C * wave + C * i;
+  const int64_t c0 = (int64_t)(down ? blockIdx.x : blockIdx.x - tiles_a) * kCols + 16 * C * wave + C * i;
   const uint16_t* const rows = static_cast<const uint16_t*>(down ? p.x : p.dy);
   const float* const values = down ? p.g : p.h;
   const float c = down || !p.scale ? 1.0f : p.scale[e.x];
@@ -901,19 +904,14 @@ __global__ __launch_bounds__(512, 4) void lora_grad16_kernel(LoraGradArgs p) {
     for (int j = 0; j < C; ++j) acc[rt][j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
 
   // Tokens of the 32 from the chunk's row t on: the lane's eight, whose columns it
-  // reads, and the one whose values the thread spreads (rows past the last: it).
+  // reads, and the one whose values the thread spreads.  (Rows past the chunk's are
+  // another adapter's or the zeros behind the last: valid tokens, not used.)
   struct Tokens {
     int x[8], v;
   };
   auto tokens = [&](int t, Tokens& k) {
-    const int r = t + 8 * q, rv = t + (int)threadIdx.x / (2 * W);
-    if (r + 8 <= e.z) {
-      __builtin_memcpy(k.x, p.rows + r, 32);
-    } else {
-#pragma unroll
-      for (int u = 0; u < 8; ++u) k.x[u] = p.rows[r + u < e.z ? r + u : e.z - 1];
-    }
-    k.v = p.rows[rv < e.z ? rv : e.z - 1];
+    __builtin_memcpy(k.x, p.rows + t + 8 * q, 32);
+    k.v = p.rows[t + (int)threadIdx.x / (2 * W)];
   };
   struct Columns {
     uint16_t v[C];
@@ -931,13 +929,14 @@ __global__ __launch_bounds__(512, 4) void lora_grad16_kernel(LoraGradArgs p) {
     }
   };
   constexpr int kMine = R / (2 * W);      // ranks of a thread
-  auto gather = [&](int t, const Tokens& k, float (&v)[kMine]) {
+  auto gather = [&](int t, int token, float (&v)[kMine]) {
     const bool in = t + (int)threadIdx.x / (2 * W) < e.z;
-    const float* from = values + (int64_t)k.v * p.rank + z0;
+    const float* from = values + (int64_t)token * p.rank + z0;
 #pragma unroll
     for (int m = 0; m < kMine; ++m) {
       const int rank = threadIdx.x % (2 * W) + 2 * W * m;
-      v[m] = in && z0 + rank < p.rank ? c * from[rank] : 0.0f;
+      const float f = from[z0 + rank < p.rank ? rank : 0];
+      v[m] = in && z0 + rank < p.rank ? c * f : 0.0f;
     }
   };
   auto spread = [&](uint16_t* to, const float (&v)[kMine]) {
@@ -951,22 +950,14 @@ __global__ __launch_bounds__(512, 4) void lora_grad16_kernel(LoraGradArgs p) {
       for (int k = 0; k < 3; ++k) to[(k * R + r) * 32 + 8 * ((t / 8) ^ ((r >> 2) & 3)) + t % 8] = b[k];
     }
   };
-  Columns x[8];
-  Tokens next;
+  // The columns are read two turns ahead, the tokens three, the values one.
+  Columns x0[8], x1[8];
+  Tokens now, next;
   float v[kMine];
-  const int start = e.y;
-  if (start < e.z) {
-    tokens(start, next);
-    gather(start, next, v);
-    fetch(next, x);
-    tokens(start + 32 < e.z ? start + 32 : start, next);
-    spread(parts[0], v);
-  }
-  int at = 0;
-  for (int t = start; t < e.z; t += 32, at ^= 1) {
+  int v1 = 0, at = 0;
+  auto turn = [&](int t, Columns (&x)[8]) {
     __syncthreads();
-    const bool more = t + 32 < e.z;
-    if (more) gather(t + 32, next, v);
+    gather(t + 32, v1, v);
     // column b of the lane's: a dword of two tokens from words b / 2 of both
     bf16x8_t col[C];
 #pragma unroll
@@ -978,16 +969,15 @@ __global__ __launch_bounds__(512, 4) void lora_grad16_kernel(LoraGradArgs p) {
         __builtin_memcpy(&lo, x[2 * u].v + b / 2 * 2, 4);
         __builtin_memcpy(&hi, x[2 * u + 1].v + b / 2 * 2, 4);
         w[u] = __builtin_amdgcn_perm(hi, lo, b % 2 ? 0x07060302u : 0x05040100u);
-        // (rows past the chunk's last are that row again: no infinity times zero)
+        // (rows past the chunk's are zeros: no infinity times zero)
         const int r = t + 8 * q + 2 * u;
         w[u] = r + 1 < e.z ? w[u] : (r < e.z ? w[u] & 0xFFFFu : 0u);
       }
       __builtin_memcpy(&col[b], w, 16);
     }
-    if (more) {
-      fetch(next, x);
-      tokens(t + 64 < e.z ? t + 64 : t, next);
-    }
+    fetch(next, x);
+    v1 = next.v;
+    tokens(t + 96, next);
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
@@ -997,7 +987,22 @@ __global__ __launch_bounds__(512, 4) void lora_grad16_kernel(LoraGradArgs p) {
 #pragma unroll
         for (int b = 0; b < C; ++b) acc[rt][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, col[b], acc[rt][b], 0, 0, 0);
       }
-    if (more) spread(parts[at ^ 1], v);
+    at ^= 1;
+    spread(parts[at], v);
+  };
+  if (e.y < e.z) {
+    tokens(e.y, now);
+    tokens(e.y + 32, next);
+    fetch(now, x0);
+    gather(e.y, now.v, v);
+    v1 = next.v;
+    fetch(next, x1);
+    tokens(e.y + 64, next);
+    spread(parts[0], v);
+    for (int t = e.y; t < e.z; t += 64) {
+      turn(t, x0);
+      if (t + 32 < e.z) turn(t + 32, x1);
+    }
   }
   const int64_t wide = (int64_t)p.rank * (p.k + p.n);
   float* out = e.w > 1 ? p.parts + blockIdx.y * wide + (down ? 0 : p.rank * p.k)
@@ -1129,9 +1134,9 @@ int lora_shares(int64_t tokens, int64_t k) {
 
 // Tokens of a chunk of the gradients: enough chunks for three workgroups a CU.
 int32_t lora_chunk(int dtype, int64_t tokens, int64_t k, int64_t n, int32_t rank) {
-  const int64_t each = dtype == 1 ? 512 : 128, tiles = (k + each - 1) / each + (n + each - 1) / each;
+  const int64_t each = dtype == 1 ? (rank > 32 ? 256 : 512) : 128, tiles = (k + each - 1) / each + (n + each - 1) / each;
   // (each chunk's sums of more than 32 ranks are as long to write as 600 tokens' rows)
-  const int64_t want = ((rank > 32 ? 512 : 768) + tiles - 1) / tiles;
+  const int64_t want = (768 + tiles - 1) / tiles;
   const int64_t c = ((tokens + want - 1) / want + 63) / 64 * 64;
   return (int32_t)(c < 64 ? 64 : c);
 }
@@ -1186,14 +1191,14 @@ hipError_t launch_lora_join_shares(const float* in, int shares, int64_t elements
 
 hipError_t launch_lora_grad(const LoraGradArgs& a, int32_t max_entries, const int32_t* chunk0,
                             hipStream_t s) {
-  const int64_t each = a.dtype == 1 ? 512 : 128;
+  const int64_t each = a.dtype == 1 ? (a.rank > 32 ? 256 : 512) : 128;
   const unsigned tiles = (unsigned)((a.k + each - 1) / each + (a.n + each - 1) / each);
   const dim3 grid(tiles, (unsigned)max_entries, (a.rank + kRanks - 1) / kRanks);
   if (a.dtype == 0) grad_dt<0>(a, grid, s);
   else if (a.dtype == 2) grad_dt<2>(a, grid, s);
   else if (a.rank <= 16) lora_grad16_kernel<1><<<grid, 512, 0, s>>>(a);
   else if (a.rank <= 32) lora_grad16_kernel<2><<<grid, 512, 0, s>>>(a);
-  else lora_grad16_kernel<4><<<grid, 512, 0, s>>>(a);
+  else lora_grad16_kernel<4><<<grid, 256, 0, s>>>(a);
   if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
   if (max_entries > a.adapters) {      // some adapter may have several chunks
     const int64_t wide = a.rank * (a.k + a.n);
