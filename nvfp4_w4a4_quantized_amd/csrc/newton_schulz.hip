@@ -7,11 +7,13 @@
 // times a power of two that brings its largest possible element near the top of
 // the range, and a X is taken from both.  The products run on the matrix cores
 // in binary16 with binary32 sums:
-//   - 16-bit "fast" products take hi alone.  What they lose, 2^-12 relative to P
-//     X, is lost where P X is as large as the result; the small singular values,
-//     which the iteration multiplies by a per step, keep the 22 bits of a X.
-//     Against binary64 the result of 768 x 2048 gradients is 1e-3 off (bf16's own
-//     rounding: 1.7e-3; bf16 products: 2e-2).
+//   - 16-bit "fast" products take hi alone, of X and of P + a I, and a lo is added
+//     to them: the small singular values, which the iteration multiplies by a per
+//     step, keep X's 22 bits.  (Taking a hi from memory instead of the products
+//     reads X once more: an update of 128 matrices of 2048 x 768 takes 524 us
+//     instead of 502.)  Against
+//     binary64 the result of 768 x 2048 gradients is 1e-3 off (bf16's own rounding:
+//     1.7e-3; X in 11 bits: 3e-3 to 5e-2; bf16 products: 2e-2).
 //   - "exact" products take hi hi + hi lo + lo hi: 1.8e-6 off, as binary32.
 // A gradient far below eps keeps its digits: X is multiplied by a further 2^k0,
 // k0 = floor(-log2 |X0|), which shrinks by the iteration's growth every step.
@@ -21,6 +23,13 @@
 // Gram product, A, P, X of the tall update) or K-major (X of the tall Gram
 // product and of the wide update) and go from memory straight into a four-slot
 // LDS ring; K-major tiles are read with the transposing LDS loads.
+//
+// Bound, for many matrices: 128 of 2048 x 768 (1.6 TFLOP) take 4.5 ms.  A and P run
+// at 0.8 and 0.5 PFLOP/s counted without the mirrored half (matrix cores 51 % busy
+// at the 1.9 GHz that the clock falls to), the update of X is memory bound (2.3 GB a
+// step past the second-level cache, 4.4 TB/s).  Overlapping LDS reads with products
+// by half stages changed them by 1 to 4 %.  One matrix leaves CUs idle: 5120 x 2048
+// has 136 tiles of A for 256 CUs.
 #include <type_traits>
 
 #include "elem.h"
@@ -73,8 +82,10 @@ __global__ __launch_bounds__(256) void ns_start_kernel(NsSource g, const double*
                                                        _Float16* hi, _Float16* lo, int32_t* k0_out) {
   typedef typename Elem<DT>::type T;
   const int64_t e = blockIdx.y;
+  const int lane = threadIdx.x % kWave;
   double sum = 0.0;
-  for (int i = 0; i < parts; ++i) sum += part[e * parts + i];
+  for (int i = lane; i < parts; i += kWave) sum += part[e * parts + i];
+  for (int d = 32; d > 0; d /= 2) sum += __shfl_xor(sum, d);
   const double norm = sqrt(sum), below = norm + eps;
   // (a zero matrix stays zero whatever eps is; a norm that is no number gives NaN)
   int k0 = 0;
@@ -86,16 +97,31 @@ __global__ __launch_bounds__(256) void ns_start_kernel(NsSource g, const double*
   if (r >= g.rows) return;
   const T* row = static_cast<const T*>(g.g) + e * g.ld_batch + r * g.ld_row;
   const int64_t at = (e * g.rows + r) * ld;
-  for (int64_t c = (int64_t)(threadIdx.x % kWave) * 8; c < ld; c += kWave * 8) {
+  auto put = [&](int64_t c, const float (&x)[8]) {
     half8_t h, l;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const double v = c + i < g.cols ? f * (double)Elem<DT>::to_float(row[c + i]) : 0.0;
+      const double v = f * (double)x[i];
       h[i] = (_Float16)(float)v;
       l[i] = (_Float16)(float)(v - (double)h[i]);
     }
     *reinterpret_cast<half8_t*>(hi + at + c) = h;
     *reinterpret_cast<half8_t*>(lo + at + c) = l;
+  };
+  int64_t c = (int64_t)lane * 8;
+  for (; c + 8 <= g.cols; c += kWave * 8) {
+    T v[8];
+    __builtin_memcpy(v, row + c, sizeof(v));
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = Elem<DT>::to_float(v[i]);
+    put(c, x);
+  }
+  for (; c < ld; c += kWave * 8) {
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = c + i < g.cols ? Elem<DT>::to_float(row[c + i]) : 0.0f;
+    put(c, x);
   }
 }
 
@@ -156,12 +182,13 @@ __device__ __forceinline__ void put8(void* out, int64_t at, int64_t count, const
   }
 }
 
-// A workgroup's TM x TN tile, 2 x 2 waves that take every stage (KG = 1), or two
-// such groups that take half of each stage's k and add their sums in LDS.
+// A workgroup's TM x TN tile: 2 x TN / 64 waves that take every stage (KG = 1), or
+// two such groups that take half of each stage's k and add their sums in LDS.
 template <int TM_, int TN_, int KG_, int RING_>
 struct Tile {
-  static constexpr int TM = TM_, TN = TN_, KG = KG_, RING = RING_, BK = 32 * KG_, NW = 4 * KG_;
+  static constexpr int TM = TM_, TN = TN_, KG = KG_, RING = RING_, BK = 32 * KG_, NW = TN_ / 32 * KG_;
 };
+using Huge = Tile<256, 256, 1, 4>;
 using Wide = Tile<256, 128, 1, 3>;     // 72 KiB of LDS: two workgroups a CU
 using Deep = Tile<128, 128, 2, 4>;     // 128 KiB: one, with twice the waves on a tile
 
@@ -170,7 +197,7 @@ using Deep = Tile<128, 128, 2, 4>;     // 128 KiB: one, with twice the waves on 
 template <typename S, bool AM, bool BMAJ, int EPI, bool EXACT>
 __global__ __launch_bounds__(64 * S::NW, 2) void ns_gemm_kernel(NsGemmArgs p) {
   constexpr int TM = S::TM, TN = S::TN, KG = S::KG, RING = S::RING, BK = S::BK, NW = S::NW;
-  constexpr int IB = TM / 64, JB = TN / 64;       // a wave's blocks of 32 x 32
+  constexpr int IB = TM / 64, JB = 2, WN = TN / 64;       // a wave's blocks of 32 x 32; waves along N
   constexpr int A_BYTES = TM * BK * 2, B_BYTES = TN * BK * 2;
   constexpr int QA = A_BYTES / 1024 / NW, QB = B_BYTES / 1024 / NW;   // load instructions per wave
   // one array per slot, so that the compiler sees that a load into one slot
@@ -271,56 +298,68 @@ __global__ __launch_bounds__(64 * S::NW, 2) void ns_gemm_kernel(NsGemmArgs p) {
     for (int j = 0; j < JB; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
-  const int group = wave / 4;
-  const int rm = (wave % 2) * (TM / 2), rn = (wave / 2 % 2) * (TN / 2);   // the wave's first row and column
-  auto multiply = [&](auto u) {
+  const int group = KG == 2 ? wave / 4 : 0;
+  const int rm = (wave % 2) * (TM / 2), rn = (wave / 2 % WN) * 64;   // the wave's first row and column
+  // the fragments of half a stage (of the group's k): 16 k
+  struct Half {
+    half8_t a[IB], b[JB];
+  };
+  auto read = [&](auto u, int kk, Half& f) {
     const _Float16* la = reinterpret_cast<const _Float16*>(slot(u));
     const _Float16* lb = reinterpret_cast<const _Float16*>(slot(u) + A_BYTES);
-    half8_t fa[2][IB], fb[2][JB];
+    const int k = 32 * group + 16 * kk;
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      const int k = 32 * group + 16 * kk;
+    for (int j = 0; j < JB; ++j) f.b[j] = fragment<TN, BK, BMAJ>(lb, rn + j * 32, k, lane);
 #pragma unroll
-      for (int j = 0; j < JB; ++j) fb[kk][j] = fragment<TN, BK, BMAJ>(lb, rn + j * 32, k, lane);
-#pragma unroll
-      for (int i = 0; i < IB; ++i) fa[kk][i] = fragment<TM, BK, AM>(la, rm + i * 32, k, lane);
-    }
+    for (int i = 0; i < IB; ++i) f.a[i] = fragment<TM, BK, AM>(la, rm + i * 32, k, lane);
     __builtin_amdgcn_sched_barrier(0);
+  };
+  auto multiply = [&](const Half& f) {
     __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk)
+    for (int i = 0; i < IB; ++i)
 #pragma unroll
-      for (int i = 0; i < IB; ++i)
-#pragma unroll
-        for (int j = 0; j < JB; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fb[kk][j], fa[kk][i], acc[i][j], 0, 0, 0);
+      for (int j = 0; j < JB; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.b[j], f.a[i], acc[i][j], 0, 0, 0);
     __builtin_amdgcn_s_setprio(0);
+    __builtin_amdgcn_sched_barrier(0);
   };
 
-  // Stages st + 1 .. st + RING - 1 are in flight while stage st is multiplied.
-  // Before a turn's barrier a wave waits for its own loads of stage st (leaving
-  // those of the later stages outstanding) and for its LDS reads of stage st - 1,
-  // which the products may still be waiting for: behind the barrier every
-  // wave's part of stage st has landed, and the slot of stage st - 1 is free for
-  // stage st + RING - 1.
+  // A half is multiplied while the next one is read from LDS, and RING stages are
+  // in LDS or on their way.  Between a stage's halves a wave waits for its own loads
+  // of the next stage (leaving those of the later ones outstanding) and for its LDS
+  // reads of this one, which the products may still be waiting for: behind the
+  // barrier every wave's part of the next stage has landed, and this stage's slot is
+  // free for the one RING further on.  Stages past the last are zeros.
   constexpr int WAIT = (RING - 2) * (QA + QB);
   constexpr int WAIT_IMM = (WAIT & 15) | ((WAIT >> 4) << 14) | (7 << 4);       // vmcnt(WAIT) lgkmcnt(0)
+  constexpr int WAIT0 = WAIT + QA + QB;
+  constexpr int WAIT0_IMM = (WAIT0 & 15) | ((WAIT0 >> 4) << 14) | (7 << 4);
   using C0 = std::integral_constant<int, 0>;
   using C1 = std::integral_constant<int, 1>;
   using C2 = std::integral_constant<int, 2>;
   using C3 = std::integral_constant<int, 3>;
+  Half f0, f1;
   auto turn = [&](auto u, int st) {
-    using Next = std::integral_constant<int, (decltype(u)::value + RING - 1) % RING>;
+    using Next = std::integral_constant<int, (decltype(u)::value + 1) % RING>;
+    read(u, 1, f1);
+    multiply(f0);
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
     __builtin_amdgcn_s_waitcnt(WAIT_IMM);
     __builtin_amdgcn_s_barrier();
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
-    load(Next{}, st + RING - 1);
-    multiply(u);
+    load(u, st + RING);
+    read(Next{}, 0, f0);
+    multiply(f1);
   };
   load(C0{}, 0);
   load(C1{}, 1);
-  if constexpr (RING == 4) load(C2{}, 2);
+  load(C2{}, 2);
+  if constexpr (RING == 4) load(C3{}, 3);
+  __builtin_amdgcn_s_waitcnt(WAIT0_IMM);
+  __builtin_amdgcn_s_barrier();
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  read(C0{}, 0, f0);
   int st = 0;
   for (; st + RING <= nst; st += RING) {
     turn(C0{}, st);
@@ -368,21 +407,23 @@ __global__ __launch_bounds__(64 * S::NW, 2) void ns_gemm_kernel(NsGemmArgs p) {
   // chunk c of row r at c ^ r % 16), so that memory is read and written in
   // 128-byte rows, and in 64-byte ones of the mirrored tile.
   float* const tile = reinterpret_cast<float*>(
-      KG == 2 ? (wave / 4 == 0 ? S2 : S3) + (wave % 4) * 8192 : (wave < 2 ? S0 : S1) + (wave % 2) * 8192);
+      KG == 2 ? (wave / 4 == 0 ? S2 : S3) + (wave % 4) * 8192
+              : WN == 4 ? (wave < 4 ? S0 : S1) + (wave % 4) * 8192 : (wave < 2 ? S0 : S1) + (wave % 2) * 8192);
   const int h = lane >> 5, l32 = lane & 31, lr = lane / 8, lc = lane % 8;
   const int k0 = p.k0[e], kj = k0 - p.drop > 0 ? k0 - p.drop : 0;
   const int kn = kj - p.growth > 0 ? kj - p.growth : 0;
   const float f = EPI == kGram ? ldexpf(p.f, -2 * kj) : p.f;
   const float up = EPI == kApply ? ldexpf(1.0f, kn - kj) : (EPI == kLast ? ldexpf(p.up, -kj) : 1.0f);
   // Eight values of Y from (row, col) on, and the eight results f acc + g Y there.
-  constexpr bool kLow = EXACT || EPI == kApply || EPI == kLast;    // Y has a lower part
+  constexpr bool kLow = EXACT || EPI == kApply || EPI == kLast;    // Y's lower part is taken,
+  constexpr bool kHigh = EXACT || EPI == kPoly;                    // and its upper one
   struct Given {
     half8_t hi, lo;
   };
   auto given = [&](int64_t row, int64_t col) -> Given {
     Given y;
     const int64_t at = e * p.y.stride + row * p.y.ld + col;
-    y.hi = *reinterpret_cast<const half8_t*>(p.y.hi + at);
+    if constexpr (kHigh) y.hi = *reinterpret_cast<const half8_t*>(p.y.hi + at);
     if constexpr (kLow) y.lo = *reinterpret_cast<const half8_t*>(p.y.lo + at);
     return y;
   };
@@ -392,7 +433,9 @@ __global__ __launch_bounds__(64 * S::NW, 2) void ns_gemm_kernel(NsGemmArgs p) {
       v[c] *= f;
       if constexpr (EPI != kGram) {
         if constexpr (kLow) v[c] = fmaf(p.g, (float)y.lo[c], v[c]);
-        v[c] = up * (v[c] + p.g * (float)y.hi[c]);
+        if constexpr (kHigh) v[c] += p.g * (float)y.hi[c];
+        if constexpr (EPI == kPoly && !EXACT) v[c] += row == col + c ? p.up : 0.0f;
+        v[c] *= up;
       }
     }
     if constexpr (EPI == kLast) {
@@ -491,11 +534,15 @@ hipError_t one_product(int epi, bool tall, const NsGemmArgs& a, hipStream_t s) {
 }
 
 hipError_t product(int epi, bool tall, const NsGemmArgs& a, hipStream_t s) {
-  // Wide where it has a tile for every CU.  Deep / Wide, microseconds a launch:
-  // 44 Gram tiles of 5120 x 2048 46 / 76, 80 (exact) of four 1000 x 2047 61 / 92;
-  // 256 update tiles of the latter 71 / 61, 320 of the former 71 / 65; 128
-  // matrices of 2048 x 768: A 242 / 214, P 139 / 142, X 682 / 562.
-  if (a.batch * tiles_of<Wide>(epi == kGram || epi == kPoly, a.m, a.n) >= 256)
+  // Huge where it has two tiles for every CU, else Wide where it has one: larger
+  // tiles read each operand less often, smaller ones leave fewer CUs idle.
+  // Microseconds a launch, Deep / Wide / Huge: A of 5120 x 2048 46 / 76 / 113, its
+  // X 71 / 65 / 63; A (exact) of four 1000 x 2047 61 / 92 / 139, their X 71 / 61 /
+  // 83; 128 of 2048 x 768: A 242 / 211 / 207, P 139 / 139 / 125, X 682 / 558 / 524.
+  const bool sym = epi == kGram || epi == kPoly;
+  if (a.batch * tiles_of<Huge>(sym, a.m, a.n) >= 512)
+    return a.exact ? one_product<Huge, true>(epi, tall, a, s) : one_product<Huge, false>(epi, tall, a, s);
+  if (a.batch * tiles_of<Wide>(sym, a.m, a.n) >= 256)
     return a.exact ? one_product<Wide, true>(epi, tall, a, s) : one_product<Wide, false>(epi, tall, a, s);
   return a.exact ? one_product<Deep, true>(epi, tall, a, s) : one_product<Deep, false>(epi, tall, a, s);
 }
@@ -533,7 +580,7 @@ bool ns_bounds(int steps, float a, float b, float c, NsScales* out) {
     if (i + 1 < steps) top = fmax(top, u);
   }
   const double l = top * top;
-  const double v = fmax(fabs(b) * l + fabs(c) * l * l, 1e-3);
+  const double v = fmax(fabs(a) + fabs(b) * l + fabs(c) * l * l, 1e-3);    // of P + a I
   if (!(v <= 8192.0)) return false;
   auto scale = [](double most) { return exp2(floor(log2(32768.0 / most))); };
   out->x = (float)scale(top);
@@ -556,8 +603,8 @@ int64_t ns_batch(int64_t batch, int64_t rows, int64_t cols) {
 }
 
 int ns_norm_parts(int64_t batch, int64_t rows) {
-  int64_t p = 1024 / batch;
-  p = p < 1 ? 1 : (p > 64 ? 64 : p);
+  int64_t p = 2048 / batch;
+  p = p < 1 ? 1 : (p > 1024 ? 1024 : p);
   return (int)(p < rows ? p : rows);
 }
 
@@ -604,6 +651,7 @@ hipError_t launch_newton_schulz(const NsArgs& a, hipStream_t s) {
       g.c_hi = a.sq[2]; g.c_lo = a.sq[3];
       g.f = a.c * a.scales.p / (a.scales.a * a.scales.a);
       g.g = a.b * a.scales.p / a.scales.a;
+      g.up = a.a * a.scales.p;
       st = product(kPoly, tall, g, s);
       if (st != hipSuccess) break;
       // X
