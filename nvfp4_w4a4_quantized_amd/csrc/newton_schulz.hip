@@ -5,16 +5,16 @@
 //
 // Arithmetic.  X is kept as two binary16 parts (hi, and lo the rest: 22 bits)
 // times a power of two that brings its largest possible element near the top of
-// the range, and a X is taken from both.  The products run on the matrix cores
-// in binary16 with binary32 sums:
+// the range.  The products run on the matrix cores in binary16 with binary32 sums:
 //   - 16-bit "fast" products take hi alone, of X and of P + a I, and a lo is added
 //     to them: the small singular values, which the iteration multiplies by a per
 //     step, keep X's 22 bits.  (Taking a hi from memory instead of the products
 //     reads X once more: an update of 128 matrices of 2048 x 768 takes 524 us
-//     instead of 502.)  Against
-//     binary64 the result of 768 x 2048 gradients is 1e-3 off (bf16's own rounding:
-//     1.7e-3; X in 11 bits: 3e-3 to 5e-2; bf16 products: 2e-2).
-//   - "exact" products take hi hi + hi lo + lo hi: 1.8e-6 off, as binary32.
+//     instead of 502.)  Against binary64 the result of 768 x 2048 gradients is
+//     1e-3 off (bf16's own rounding: 1.7e-3; X in 11 bits: 3e-3 to 5e-2; bf16
+//     products: 2e-2).
+//   - "exact" products take hi hi + hi lo + lo hi, and a X from both parts: 1.9e-6
+//     off (four 1000 x 2047), binary32 throughout 3.2e-6.
 // A gradient far below eps keeps its digits: X is multiplied by a further 2^k0,
 // k0 = floor(-log2 |X0|), which shrinks by the iteration's growth every step.
 //
@@ -40,7 +40,6 @@ namespace nvfp4 {
 
 namespace {
 
-typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
 typedef short short4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) short4_t lds_short4_t;
 
@@ -182,33 +181,34 @@ __device__ __forceinline__ void put8(void* out, int64_t at, int64_t count, const
   }
 }
 
-// A workgroup's TM x TN tile: 2 x TN / 64 waves that take every stage (KG = 1), or
-// two such groups that take half of each stage's k and add their sums in LDS.
+// A workgroup's TM x TN tile: 2 x TN / 64 waves that take every stage of 32 k (KG =
+// 1), or two such groups that take half of each stage of 64 and add their sums in LDS.
 template <int TM_, int TN_, int KG_, int RING_>
 struct Tile {
   static constexpr int TM = TM_, TN = TN_, KG = KG_, RING = RING_, BK = 32 * KG_, NW = TN_ / 32 * KG_;
 };
-using Huge = Tile<256, 256, 1, 4>;
-using Wide = Tile<256, 128, 1, 3>;     // 72 KiB of LDS: two workgroups a CU
-using Deep = Tile<128, 128, 2, 4>;     // 128 KiB: one, with twice the waves on a tile
+using Huge = Tile<256, 256, 1, 4>;     // 128 KiB of LDS, eight waves
+using Wide = Tile<256, 128, 1, 3>;     // 72 KiB: two workgroups of four waves a CU
+using Deep = Tile<128, 128, 2, 4>;     // 128 KiB, eight waves
 
 // C = A B over k with the epilogue EPI; AM, BMAJ: the operand is K-major;
 // EXACT: products of both parts, and A and P have two.
 template <typename S, bool AM, bool BMAJ, int EPI, bool EXACT>
 __global__ __launch_bounds__(64 * S::NW, 2) void ns_gemm_kernel(NsGemmArgs p) {
-  constexpr int TM = S::TM, TN = S::TN, KG = S::KG, RING = S::RING, BK = S::BK, NW = S::NW;
+  constexpr int TM = S::TM, TN = S::TN, KG = S::KG, NW = S::NW;
+  // exact stages hold both parts of 32 k
+  constexpr int PARTS = EXACT ? 2 : 1, BK = EXACT ? 32 : S::BK, RING = EXACT && TM == 256 ? 2 : S::RING;
   constexpr int IB = TM / 64, JB = 2, WN = TN / 64;       // a wave's blocks of 32 x 32; waves along N
   constexpr int A_BYTES = TM * BK * 2, B_BYTES = TN * BK * 2;
   constexpr int QA = A_BYTES / 1024 / NW, QB = B_BYTES / 1024 / NW;   // load instructions per wave
   // one array per slot, so that the compiler sees that a load into one slot
   // does not write the slot being read
-  constexpr int SLOT = A_BYTES + B_BYTES;
+  constexpr int SLOT = PARTS * (A_BYTES + B_BYTES);
   __shared__ __align__(16) uint8_t S0[SLOT];
   __shared__ __align__(16) uint8_t S1[SLOT];
-  __shared__ __align__(16) uint8_t S2[SLOT];
+  __shared__ __align__(16) uint8_t S2[RING >= 3 ? SLOT : 16];
   __shared__ __align__(16) uint8_t S3[RING == 4 ? SLOT : 16];
   constexpr bool SYM = EPI == kGram || EPI == kPoly;
-  constexpr int kParts = EXACT ? 3 : 1;
   const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
 
   // consecutive tiles of a matrix on one XCD (workgroups go round the eight)
@@ -234,7 +234,7 @@ __global__ __launch_bounds__(64 * S::NW, 2) void ns_gemm_kernel(NsGemmArgs p) {
   const __amdgpu_buffer_rsrc_t bhi = buffer_rsrc(p.b.hi + e * p.b.stride, p.b.bytes);
   const __amdgpu_buffer_rsrc_t alo = buffer_rsrc(p.a.lo + e * p.a.stride, p.a.bytes);
   const __amdgpu_buffer_rsrc_t blo = buffer_rsrc(p.b.lo + e * p.b.stride, p.b.bytes);
-  const int steps = (int)((p.k + BK - 1) / BK), nst = steps * kParts;
+  const int nst = (int)((p.k + BK - 1) / BK);
 
   // A lane's offsets of stage 0.  Rows past the matrix lie past its resource
   // and read zeros; columns past ld are masked.
@@ -268,27 +268,25 @@ __global__ __launch_bounds__(64 * S::NW, 2) void ns_gemm_kernel(NsGemmArgs p) {
     else if constexpr (U == 2) return S2;
     else return S3;
   };
-  // stage st: step st / kParts of k, and of the parts hi hi, hi lo, lo hi the
-  // (st % kParts)-th; stages past the last read zeros
-  int part = 0;
+  // stage st of both operands (and both parts); stages past the last read zeros
   uint32_t sa = 0, sb = 0;
   auto load = [&](auto u, int st) {
-    uint8_t* s = slot(u);
     const bool live = st < nst;
-    const __amdgpu_buffer_rsrc_t ra = EXACT && part == 2 ? alo : ahi, rb = EXACT && part == 1 ? blo : bhi;
 #pragma unroll
-    for (int q = 0; q < QA; ++q)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void_t*)(s + (wave + NW * q) * 1024), 16,
-                                               (int)(live ? ao[q] + sa : kNone), 0, 0, 0);
+    for (int part = 0; part < PARTS; ++part) {
+      uint8_t* s = slot(u) + part * (A_BYTES + B_BYTES);
 #pragma unroll
-    for (int q = 0; q < QB; ++q)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void_t*)(s + A_BYTES + (wave + NW * q) * 1024), 16,
-                                               (int)(live ? bo[q] + sb : kNone), 0, 0, 0);
-    if (++part == kParts) {
-      part = 0;
-      sa += astep;
-      sb += bstep;
+      for (int q = 0; q < QA; ++q)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(part == 0 ? ahi : alo, (lds_void_t*)(s + (wave + NW * q) * 1024),
+                                                 16, (int)(live ? ao[q] + sa : kNone), 0, 0, 0);
+#pragma unroll
+      for (int q = 0; q < QB; ++q)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(part == 0 ? bhi : blo,
+                                                 (lds_void_t*)(s + A_BYTES + (wave + NW * q) * 1024), 16,
+                                                 (int)(live ? bo[q] + sb : kNone), 0, 0, 0);
     }
+    sa += astep;
+    sb += bstep;
   };
 
   float16_t acc[IB][JB];
@@ -300,76 +298,103 @@ __global__ __launch_bounds__(64 * S::NW, 2) void ns_gemm_kernel(NsGemmArgs p) {
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
   const int group = KG == 2 ? wave / 4 : 0;
   const int rm = (wave % 2) * (TM / 2), rn = (wave / 2 % WN) * 64;   // the wave's first row and column
-  // the fragments of half a stage (of the group's k): 16 k
+  // The fragments of 16 k of a part.
   struct Half {
     half8_t a[IB], b[JB];
   };
-  auto read = [&](auto u, int kk, Half& f) {
-    const _Float16* la = reinterpret_cast<const _Float16*>(slot(u));
-    const _Float16* lb = reinterpret_cast<const _Float16*>(slot(u) + A_BYTES);
-    const int k = 32 * group + 16 * kk;
+  auto read = [&](auto u, int part, int k, Half& f) {
+    const uint8_t* from = slot(u) + part * (A_BYTES + B_BYTES);
+    const _Float16* la = reinterpret_cast<const _Float16*>(from);
+    const _Float16* lb = reinterpret_cast<const _Float16*>(from + A_BYTES);
 #pragma unroll
     for (int j = 0; j < JB; ++j) f.b[j] = fragment<TN, BK, BMAJ>(lb, rn + j * 32, k, lane);
 #pragma unroll
     for (int i = 0; i < IB; ++i) f.a[i] = fragment<TM, BK, AM>(la, rm + i * 32, k, lane);
     __builtin_amdgcn_sched_barrier(0);
   };
-  auto multiply = [&](const Half& f) {
+  auto multiply = [&](const half8_t (&a)[IB], const half8_t (&b)[JB]) {
     __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int i = 0; i < IB; ++i)
 #pragma unroll
       for (int j = 0; j < JB; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.b[j], f.a[i], acc[i][j], 0, 0, 0);
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(b[j], a[i], acc[i][j], 0, 0, 0);
     __builtin_amdgcn_s_setprio(0);
     __builtin_amdgcn_sched_barrier(0);
   };
 
-  // A half is multiplied while the next one is read from LDS, and RING stages are
-  // in LDS or on their way.  Between a stage's halves a wave waits for its own loads
-  // of the next stage (leaving those of the later ones outstanding) and for its LDS
-  // reads of this one, which the products may still be waiting for: behind the
+  // 16 k are multiplied while the next ones are read from LDS, and RING stages are
+  // in LDS or on their way.  Before a stage's last products a wave waits for its own
+  // loads of the next stage (leaving those of the later ones outstanding) and for its
+  // LDS reads of this one, which the products may still be waiting for: behind the
   // barrier every wave's part of the next stage has landed, and this stage's slot is
   // free for the one RING further on.  Stages past the last are zeros.
-  constexpr int WAIT = (RING - 2) * (QA + QB);
+  constexpr int LOADS = PARTS * (QA + QB), WAIT = (RING - 2) * LOADS, WAIT0 = (RING - 1) * LOADS;
   constexpr int WAIT_IMM = (WAIT & 15) | ((WAIT >> 4) << 14) | (7 << 4);       // vmcnt(WAIT) lgkmcnt(0)
-  constexpr int WAIT0 = WAIT + QA + QB;
   constexpr int WAIT0_IMM = (WAIT0 & 15) | ((WAIT0 >> 4) << 14) | (7 << 4);
+  static_assert(WAIT0 < 64, "vmcnt range");
   using C0 = std::integral_constant<int, 0>;
   using C1 = std::integral_constant<int, 1>;
   using C2 = std::integral_constant<int, 2>;
   using C3 = std::integral_constant<int, 3>;
-  Half f0, f1;
-  auto turn = [&](auto u, int st) {
+  constexpr int HALVES = BK / 16 / KG;            // a group's, of a stage
+  const int kg = 16 * HALVES * group;             // its first k
+  Half f0, f1, low;
+  // the next stage's first fragments, behind the barrier
+  auto change = [&](auto u, int st, Half& f) {
     using Next = std::integral_constant<int, (decltype(u)::value + 1) % RING>;
-    read(u, 1, f1);
-    multiply(f0);
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
     __builtin_amdgcn_s_waitcnt(WAIT_IMM);
     __builtin_amdgcn_s_barrier();
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
     load(u, st + RING);
-    read(Next{}, 0, f0);
-    multiply(f1);
+    read(Next{}, 0, kg, f);
+  };
+  auto turn = [&](auto u, int st) {
+    if constexpr (!EXACT) {
+      read(u, 0, kg + 16, f1);
+      multiply(f0.a, f0.b);
+      change(u, st, f0);
+      multiply(f1.a, f1.b);
+    } else if constexpr (HALVES == 2) {
+      read(u, 1, kg, low);
+      multiply(f0.a, f0.b);
+      read(u, 0, kg + 16, f1);
+      multiply(f0.a, low.b);
+      multiply(low.a, f0.b);
+      read(u, 1, kg + 16, low);
+      multiply(f1.a, f1.b);
+      change(u, st, f0);
+      multiply(f1.a, low.b);
+      multiply(low.a, f1.b);
+    } else {                                      // (the ring is even: f0 and f1 in turn)
+      Half& now = decltype(u)::value % 2 == 0 ? f0 : f1;
+      read(u, 1, kg, low);
+      multiply(now.a, now.b);
+      change(u, st, decltype(u)::value % 2 == 0 ? f1 : f0);
+      multiply(now.a, low.b);
+      multiply(low.a, now.b);
+    }
   };
   load(C0{}, 0);
   load(C1{}, 1);
-  load(C2{}, 2);
+  if constexpr (RING >= 3) load(C2{}, 2);
   if constexpr (RING == 4) load(C3{}, 3);
   __builtin_amdgcn_s_waitcnt(WAIT0_IMM);
   __builtin_amdgcn_s_barrier();
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
-  read(C0{}, 0, f0);
+  read(C0{}, 0, kg, f0);
   int st = 0;
   for (; st + RING <= nst; st += RING) {
     turn(C0{}, st);
     turn(C1{}, st + 1);
-    turn(C2{}, st + 2);
+    if constexpr (RING >= 3) turn(C2{}, st + 2);
     if constexpr (RING == 4) turn(C3{}, st + 3);
   }
   if (st < nst) turn(C0{}, st);
-  if (st + 1 < nst) turn(C1{}, st + 1);
-  if (RING == 4 && st + 2 < nst) turn(C2{}, st + 2);
+  if (RING >= 3 && st + 1 < nst) turn(C1{}, st + 1);
+  if constexpr (RING == 4)
+    if (st + 2 < nst) turn(C2{}, st + 2);
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
   __builtin_amdgcn_s_waitcnt(7 << 4);      // no load into LDS outlives the loop, no read is left
   __builtin_amdgcn_s_barrier();
@@ -537,14 +562,18 @@ hipError_t product(int epi, bool tall, const NsGemmArgs& a, hipStream_t s) {
   // Huge where it has two tiles for every CU, else Wide where it has one: larger
   // tiles read each operand less often, smaller ones leave fewer CUs idle.
   // Microseconds a launch, Deep / Wide / Huge: A of 5120 x 2048 46 / 76 / 113, its
-  // X 71 / 65 / 63; A (exact) of four 1000 x 2047 61 / 92 / 139, their X 71 / 61 /
-  // 83; 128 of 2048 x 768: A 242 / 211 / 207, P 139 / 139 / 125, X 682 / 558 / 524.
+  // X 71 / 65 / 63; 128 of 2048 x 768: A 242 / 211 / 207, P 139 / 139 / 125, X
+  // 682 / 558 / 524.  Exact stages hold twice as much, so that Wide would run alone
+  // on a CU: Huge where it has a tile for every CU.  A call of four 1000 x 2047 735
+  // (Deep) / 1339 us, of sixteen 1536 x 2048 5391 / 4925, of 128 2048 x 768 10617 /
+  // 9480 (in turn over three stages of one part each: 775, 5165, 9980).
   const bool sym = epi == kGram || epi == kPoly;
-  if (a.batch * tiles_of<Huge>(sym, a.m, a.n) >= 512)
-    return a.exact ? one_product<Huge, true>(epi, tall, a, s) : one_product<Huge, false>(epi, tall, a, s);
-  if (a.batch * tiles_of<Wide>(sym, a.m, a.n) >= 256)
-    return a.exact ? one_product<Wide, true>(epi, tall, a, s) : one_product<Wide, false>(epi, tall, a, s);
-  return a.exact ? one_product<Deep, true>(epi, tall, a, s) : one_product<Deep, false>(epi, tall, a, s);
+  if (a.exact)
+    return a.batch * tiles_of<Huge>(sym, a.m, a.n) >= 256 ? one_product<Huge, true>(epi, tall, a, s)
+                                                          : one_product<Deep, true>(epi, tall, a, s);
+  if (a.batch * tiles_of<Huge>(sym, a.m, a.n) >= 512) return one_product<Huge, false>(epi, tall, a, s);
+  if (a.batch * tiles_of<Wide>(sym, a.m, a.n) >= 256) return one_product<Wide, false>(epi, tall, a, s);
+  return one_product<Deep, false>(epi, tall, a, s);
 }
 
 int64_t pad64(int64_t v) { return (v + 63) / 64 * 64; }
