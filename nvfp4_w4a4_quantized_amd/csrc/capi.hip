@@ -1030,7 +1030,7 @@ struct LoraBackwardLayout {
   void* at; void* bt;         // A and B transposed: [S, K, R], [S, R, N]
   float* shares;              // of g, then (without the forward's h) of h
   float* g; float* h;         // [tokens, rank]
-  int32_t* rows; int4* entries; int32_t* chunk0;
+  int32_t* rows; int4* entries; int32_t* part0;
   float* parts;
   int32_t chunk, max_entries;
   size_t bytes;
@@ -1051,8 +1051,9 @@ static LoraBackwardLayout carve_lora_backward(void* ws, int dtype, int64_t T, in
   L.chunk = lora_chunk(dtype, T, k, n, rank);
   L.max_entries = (int32_t)(T / L.chunk) + S;
   L.entries = c.take<int4>((size_t)L.max_entries);
-  L.chunk0 = c.take<int32_t>((size_t)S + 1);
-  L.parts = c.take<float>(L.max_entries > S ? L.max_entries * wide : 0);
+  L.part0 = c.take<int32_t>((size_t)S + 1);
+  // an adapter of more than a chunk's tokens has at most twice their quotient of chunks
+  L.parts = c.take<float>((size_t)(2 * T / L.chunk) * wide);
   L.bytes = c.used;
   return L;
 }
@@ -1090,7 +1091,7 @@ int lora_backward(const void* dy, int dtype, int64_t tokens, int64_t n, int64_t 
   LoraPrepareArgs pr{};
   pr.sort.ids = ids; pr.sort.tokens = tokens; pr.sort.adapters = adapters; pr.sort.chunk = L.chunk;
   pr.sort.max_entries = L.max_entries; pr.sort.rows = L.rows; pr.sort.entries = L.entries;
-  pr.sort.chunk0 = L.chunk0;
+  pr.sort.part0 = L.part0;
   pr.a = a; pr.b = b; pr.dtype = dtype; pr.k = k; pr.n = n; pr.rank = rank; pr.at = L.at; pr.bt = L.bt;
   if (e == hipSuccess) e = launch_lora_prepare(pr, s);
   if (e == hipSuccess)
@@ -1105,7 +1106,7 @@ int lora_backward(const void* dy, int dtype, int64_t tokens, int64_t n, int64_t 
   gr.x = x; gr.dy = dy; gr.dtype = dtype; gr.k = k; gr.n = n; gr.ld_x = ld_x; gr.ld_dy = ld_dy;
   gr.g = L.g; gr.h = h ? h : L.h; gr.scale = scale; gr.adapters = adapters; gr.rank = rank;
   gr.rows = L.rows; gr.entries = L.entries; gr.da = da; gr.db = db; gr.parts = L.parts;
-  if (e == hipSuccess) e = launch_lora_grad(gr, L.max_entries, L.chunk0, s);
+  if (e == hipSuccess) e = launch_lora_grad(gr, L.max_entries, L.part0, s);
   return hip_status(e);
 }
 

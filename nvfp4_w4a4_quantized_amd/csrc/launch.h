@@ -284,7 +284,7 @@ struct LoraSortArgs {
   const int32_t* ids; int64_t tokens; int32_t adapters, chunk, max_entries;
   int32_t* rows;              // [tokens + kRowsBehind]: zeros behind the last routed token
   int4* entries;              // [max_entries]
-  int32_t* chunk0;            // [adapters + 1]
+  int32_t* part0;             // [adapters + 1]
 };
 struct LoraPrepareArgs {
   LoraSortArgs sort;
@@ -297,7 +297,7 @@ struct LoraGradArgs {
   const float* scale; int32_t adapters, rank;
   const int32_t* rows; const int4* entries;
   float* da; float* db;       // [adapters, rank, k], [adapters, n, rank]
-  float* parts;               // [max_entries, rank * (k + n)]
+  float* parts;               // [2 tokens / chunk, rank * (k + n)]: of adapters with several chunks
 };
 bool lora_direct(int dtype, int64_t tokens, int64_t k, int64_t n, int32_t rank);
 int lora_shares(int64_t tokens, int64_t k);
@@ -307,7 +307,7 @@ hipError_t launch_lora_up(LoraUpArgs a, hipStream_t s);
 hipError_t launch_lora_prepare(const LoraPrepareArgs& a, hipStream_t s);
 hipError_t launch_lora_join_shares(const float* in, int shares, int64_t elements, float* out,
                                    hipStream_t s);
-hipError_t launch_lora_grad(const LoraGradArgs& a, int32_t max_entries, const int32_t* chunk0,
+hipError_t launch_lora_grad(const LoraGradArgs& a, int32_t max_entries, const int32_t* part0,
                             hipStream_t s);
 
 // ---- newton_schulz.hip ----

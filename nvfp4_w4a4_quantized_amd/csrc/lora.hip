@@ -644,9 +644,9 @@ __global__ __launch_bounds__(256) void lora_join_shares_kernel(const float* in, 
 //
 // The sort: tokens in adapter order (ascending inside an adapter) and the chunks
 // that the gradients are summed in, by sixteen waves with a consecutive share of
-// the tokens each.  entry = {adapter, first row, end row, number of its adapter's
-// chunks}; every adapter has one chunk at least, unused entries have adapter -1.
-// chunk0[s] is adapter s's first chunk.
+// the tokens each.  entry = {adapter, first row, end row, 1 + the chunk's part, or 0
+// where its adapter has no other chunk}; every adapter has one chunk at least, unused
+// entries have adapter -1.  Adapter s's parts are part0[s] to part0[s + 1].
 constexpr int kSortWaves = 16, kAhead = 16;
 
 // Calls f(first token, key) for every 64 tokens of [t0, t1), kAhead loads in flight.
@@ -712,9 +712,10 @@ __device__ __forceinline__ void lora_sort(const LoraSortArgs& p, int32_t* place,
       count += c;
     }
   const int chunks = s < S ? (count > p.chunk ? (count + p.chunk - 1) / p.chunk : 1) : 0;
-  int v[2] = {count, chunks}, before[2];
+  const int parts = chunks > 1 ? chunks : 0;
+  int v[3] = {count, chunks, parts}, before[3];
 #pragma unroll
-  for (int a = 0; a < 2; ++a) {
+  for (int a = 0; a < 3; ++a) {
     int x = v[a];
     for (int d = 1; d < kWave; d *= 2) {
       const int y = __shfl_up(x, d);
@@ -724,26 +725,25 @@ __device__ __forceinline__ void lora_sort(const LoraSortArgs& p, int32_t* place,
     before[a] = x - v[a];
   }
   __syncthreads();
-  for (int w = 0; w < wave; ++w) {
-    before[0] += sums[0][w];
-    before[1] += sums[1][w];
-  }
+  for (int w = 0; w < wave; ++w)
+#pragma unroll
+    for (int a = 0; a < 3; ++a) before[a] += sums[a][w];
   if (s < S) {
     for (int w = 0; w < kSortWaves; ++w) place[w * S + s] += before[0];
-    p.chunk0[s] = before[1];
+    p.part0[s] = before[2];
     for (int c = 0; c < chunks; ++c) {
       const int r0 = before[0] + c * p.chunk;
       const int r1 = r0 + p.chunk < before[0] + count ? r0 + p.chunk : before[0] + count;
-      p.entries[before[1] + c] = make_int4(s, r0, r1, chunks);
+      p.entries[before[1] + c] = make_int4(s, r0, r1, parts > 0 ? 1 + before[2] + c : 0);
     }
     if (s == S - 1) {
-      sums[2][0] = before[0] + count;       // all routed tokens
-      p.chunk0[S] = before[1] + chunks;
+      sums[3][0] = before[0] + count;       // all routed tokens
+      p.part0[S] = before[2] + parts;
       for (int c = before[1] + chunks; c < p.max_entries; ++c) p.entries[c] = make_int4(-1, 0, 0, 0);
     }
   }
   __syncthreads();
-  for (int r = sums[2][0] + threadIdx.x; r < tokens + kRowsBehind; r += kSortWaves * kWave) p.rows[r] = 0;
+  for (int r = sums[3][0] + threadIdx.x; r < tokens + kRowsBehind; r += kSortWaves * kWave) p.rows[r] = 0;
   walk_keys(p, t0, t1, [&](int t, int k) {
     each(k, [&](int key, uint64_t mask) {
       if (k == key) p.rows[at + bits_below(mask)] = t;
@@ -772,7 +772,7 @@ __global__ __launch_bounds__(kSortWaves * kWave) void lora_prepare_kernel(LoraPr
   union Shared {
     struct {
       int32_t place[kSortWaves * kMaxAdapters];
-      int32_t sums[3][kSortWaves];
+      int32_t sums[4][kSortWaves];
     } sort;
     T tile[64][65];
   };
@@ -848,7 +848,7 @@ __global__ __launch_bounds__(kThreads) void lora_grad_kernel(LoraGradArgs p) {
       }
   }
   const int64_t wide = (int64_t)p.rank * (p.k + p.n);
-  float* out = e.w > 1 ? p.parts + blockIdx.y * wide + (down ? 0 : p.rank * p.k)
+  float* out = e.w > 0 ? p.parts + (e.w - 1) * wide + (down ? 0 : p.rank * p.k)
                        : (down ? p.da + (int64_t)e.x * p.rank * p.k : p.db + (int64_t)e.x * p.rank * p.n);
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
@@ -1005,7 +1005,7 @@ __global__ __launch_bounds__(RT == 4 ? 256 : 512, RT == 4 ? 3 : 4) void lora_gra
     }
   }
   const int64_t wide = (int64_t)p.rank * (p.k + p.n);
-  float* out = e.w > 1 ? p.parts + blockIdx.y * wide + (down ? 0 : p.rank * p.k)
+  float* out = e.w > 0 ? p.parts + (e.w - 1) * wide + (down ? 0 : p.rank * p.k)
                        : (down ? p.da + (int64_t)e.x * p.rank * p.k : p.db + (int64_t)e.x * p.rank * p.n);
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
@@ -1044,9 +1044,9 @@ __global__ __launch_bounds__(RT == 4 ? 256 : 512, RT == 4 ? 3 : 4) void lora_gra
 }
 
 // The gradients of adapters of several chunks: the parts added in chunk order.
-__global__ __launch_bounds__(256) void lora_join_parts_kernel(LoraGradArgs p, const int32_t* chunk0) {
-  const int s = blockIdx.y, c0 = chunk0[s], c1 = chunk0[s + 1];
-  if (c1 - c0 < 2) return;
+__global__ __launch_bounds__(256) void lora_join_parts_kernel(LoraGradArgs p, const int32_t* part0) {
+  const int s = blockIdx.y, c0 = part0[s], c1 = part0[s + 1];
+  if (c1 == c0) return;
   const int64_t na = p.rank * p.k, wide = na + p.rank * p.n;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= wide) return;
@@ -1189,7 +1189,7 @@ hipError_t launch_lora_join_shares(const float* in, int shares, int64_t elements
   return hipGetLastError();
 }
 
-hipError_t launch_lora_grad(const LoraGradArgs& a, int32_t max_entries, const int32_t* chunk0,
+hipError_t launch_lora_grad(const LoraGradArgs& a, int32_t max_entries, const int32_t* part0,
                             hipStream_t s) {
   const int64_t each = a.dtype == 1 ? (a.rank > 32 ? 256 : 512) : 128;
   const unsigned tiles = (unsigned)((a.k + each - 1) / each + (a.n + each - 1) / each);
@@ -1202,7 +1202,7 @@ hipError_t launch_lora_grad(const LoraGradArgs& a, int32_t max_entries, const in
   if (hipGetLastError() != hipSuccess) return hipErrorLaunchFailure;
   if (max_entries > a.adapters) {      // some adapter may have several chunks
     const int64_t wide = a.rank * (a.k + a.n);
-    lora_join_parts_kernel<<<dim3((unsigned)((wide + 255) / 256), (unsigned)a.adapters), 256, 0, s>>>(a, chunk0);
+    lora_join_parts_kernel<<<dim3((unsigned)((wide + 255) / 256), (unsigned)a.adapters), 256, 0, s>>>(a, part0);
   }
   return hipGetLastError();
 }

@@ -44,7 +44,10 @@ SHAPES = [
     (256, 72, 40, 8, 1, "one"), (255, 4100, 31, 4, 300, "random"), (257, 264, 520, 16, 4, "runs"),
     (300, 777, 511, 24, 6, "wild"), (512, 64, 96, 64, 2, "random"), (700, 130, 258, 100, 3, "runs"),
     (333, 96, 64, 256, 2, "runs"), (40, 96, 65, 256, 4, "random"), (1030, 48, 56, 5, 9, "none"),
-    (1500, 320, 192, 12, 1, "one"), (2100, 40, 24, 2, 1000, "random")]
+    (1500, 320, 192, 12, 1, "one"), (2100, 40, 24, 2, 1000, "random"),
+    # several chunks of every adapter, of some; whole pieces and 32 ranks, 64, 128
+    (3000, 24, 40, 6, 20, "random"), (900, 64, 128, 32, 9, "runs"), (2050, 128, 256, 64, 5, "runs"),
+    (600, 256, 512, 128, 3, "runs")]
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
@@ -144,6 +147,29 @@ def test_infinities_and_nan_stay_with_their_token(T, dtype):
     assert bool(torch.isnan(da[0]).all()) and bool(torch.isnan(db[0, 11]).all())
     assert bool(torch.isfinite(da[1:]).all()) and bool(torch.isfinite(db[1:]).all())
     assert not bool(da[3].any()) and not bool(db[3].any())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rank", [8, 48])
+@pytest.mark.parametrize("T", [12, 400])
+def test_a_broken_adapter_reaches_its_own_tokens_alone(T, rank, dtype):
+    """An adapter full of NaN and infinities beside others, token by token."""
+    from nvfp4_w4a4_quantized_amd import ops
+    K, N, S = 72, 128, 3
+    c = make(T, K, N, rank, S, "random", dtype, 7)
+    c["ids"] = (torch.arange(T) % 4 - 1).to(torch.int32)
+    x, a, b, ids, base, dy = cuda(c, "x", "a", "b", "ids", "base", "dy")
+    want, h = ops.lora_forward(x, a, b, ids, base=base, return_h=True)
+    back = ops.lora_backward(dy, x, a, b, ids, h=h)
+    a[1], b[1] = float("nan"), INF
+    own = (ids == 1)
+    y, h2 = ops.lora_forward(x, a, b, ids, base=base, return_h=True)
+    assert torch.equal(y[~own], want[~own]) and torch.equal(h2[~own], h[~own])
+    assert not bool(torch.isfinite(y[own]).any())
+    dx, da, db = ops.lora_backward(dy, x, a, b, ids, h=h)
+    assert torch.equal(dx[~own], back[0][~own]) and not bool(torch.isfinite(dx[own]).any())
+    for s in (0, 2):
+        assert torch.equal(da[s], back[1][s]) and torch.equal(db[s], back[2][s])
 
 
 def spread(t, left, right):
