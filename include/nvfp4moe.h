@@ -684,7 +684,7 @@ int moe_expert_decode(const void* x, int x_dtype, int64_t tokens, int64_t hidden
  * Limits (NVFP4_UNSUPPORTED beyond): rank <= 256; adapters <= 1024; tokens <=
  * 2^24; n, k <= 2^18; nvfp4_lora_matvec: tokens <= 65536 and nvfp4_matvec's.
  * A batch is read fastest when the tokens of a request lie together: beyond 256
- * tokens, 64 consecutive ones are multiplied adapter by adapter.
+ * tokens, up to 64 consecutive ones are multiplied adapter by adapter.
  * ---------------------------------------------------------------------- */
 size_t lora_forward_workspace_size(int64_t tokens, int64_t k, int32_t rank);
 int lora_forward(const void* x, int dtype, int64_t tokens, int64_t k, int64_t ld_x,

@@ -12,10 +12,10 @@
 //
 // Tokens of one adapter are multiplied together.  Few tokens (up to kWindow):
 // a workgroup per token looks its adapter's tokens up and the first of them
-// does the work of all.  Many: a workgroup takes 64 consecutive tokens and does
-// one adapter after the other, each keeping the results of its own tokens, so a
-// batch whose requests lie together reads each token's row once and an adapter
-// once per 64 tokens.
+// does the work of all.  Many: a workgroup takes consecutive tokens (16 to 64 down,
+// 32 up) and does one adapter after the other, each keeping the results of its own
+// tokens, so a batch whose requests lie together reads each token's row once and
+// an adapter once per workgroup.
 //
 // Arithmetic: down multiplies in the type of x by MFMA 16x16x32 (binary32:
 // 16x16x4) into binary32; h and g stay binary32.  What they enter are binary32
@@ -24,6 +24,14 @@
 // values.  Sums over K that several workgroups share are joined in workgroup
 // order, sums over tokens in token order per chunk: results do not depend on
 // timing.
+//
+// Bound: the long rows' bytes.  Measured (bf16): down 8192 x 5120 of rank 16 21 us
+// (3.9 TB/s), 32768 x 5120 of rank 64 95 us (3.5 TB/s); up 4096 x 5120 with a base 27
+// us (3.1 TB/s), 8192 x 2048 22 us (3.0), 32768 x 2048 of rank 64 83 us (3.4);
+// gradients of 8192 tokens of rank 16 37 us (3.2 TB/s), of 32768 of rank 64 216 us
+// (2.2 TB/s: vector instructions issue 26 % of the time, matrix cores 17 %, LDS bank
+// conflicts 9 %; none is at its limit).  One token's 64 KB of A and 160 KB of B take
+// 7 us, most of it latency.
 #include <type_traits>
 
 #include "elem.h"
@@ -333,7 +341,7 @@ __device__ __forceinline__ void get_some(const void* from, int64_t at, int64_t l
 // a wave at a time.  Which of the wave's 64 columns is row i of product j is chosen
 // so that a lane ends with 16-byte pieces of its token, and a load or store covers
 // 64 consecutive bytes of every token (32 bytes a lane, in two halves of 16 each,
-// cost 4096 x 5120 29 us instead of MEASURED).
+// cost 4096 x 5120 29.6 us instead of 27.4).
 // The sums start from the base's values, which are loaded a turn ahead.  BIG:
 // more than 32 ranks, 64 at a time.  WHOLE: whole pieces everywhere and the kind of
 // base known, so that no branch stands around a load (the compiler waits for every
@@ -874,9 +882,11 @@ __global__ __launch_bounds__(kThreads) void lora_grad_kernel(LoraGradArgs p) {
 
 // The same for bf16 rows on MFMA 16x16x32: the g or c h of 32 tokens go through
 // LDS as their three bf16 parts, token by token of a rank, and the rows' values
-// are brought from eight tokens' registers into a column's by byte permutes.  Four
-// waves of 128 columns, or (64 ranks, whose sums take the registers) eight of 64.
-// Grid: x = 512 columns of x, then of dy.
+// are brought from eight tokens' registers into a column's by byte permutes.  A wave
+// takes 64 columns, a workgroup eight waves (four waves of 128 columns: 74 us instead
+// of 35 for 8192 tokens of rank 16), or with 64 ranks four waves (222 us for 32768
+// tokens, eight 230 to 239, with longer chunks; columns read two turns ahead instead
+// of one 213).  Grid: x = 512 (256) columns of x, then of dy.
 // The binary32 form above is bound by its matrix instructions from rank 32 on
 // (rank 64: 512 us for 470 MB).
 template <int RT>
@@ -1111,7 +1121,7 @@ void grad_dt(const LoraGradArgs& a, dim3 grid, hipStream_t s) {
 }
 
 // Tokens of a workgroup of the down products (1: the slots of up to kWindow): as
-// many as leave two workgroups a CU with up to sixteen shares of K, so that the
+// many as the batch can spare with up to kMostShares shares of K, so that the
 // adapter is read least often (rank 16, 8192 x 5120: 64 tokens 21.4 us, 32 23.3, 16
 // 28.0; rank 64, 32768 x 5120: 96, 159, 222; 1003 x 1999 15.0, 10.3, 10.1).
 int down_group(int64_t tokens) {
@@ -1135,14 +1145,15 @@ int lora_shares(int64_t tokens, int64_t k) {
 // Tokens of a chunk of the gradients: enough chunks for three workgroups a CU.
 int32_t lora_chunk(int dtype, int64_t tokens, int64_t k, int64_t n, int32_t rank) {
   const int64_t each = dtype == 1 ? (rank > 32 ? 256 : 512) : 128, tiles = (k + each - 1) / each + (n + each - 1) / each;
-  // (each chunk's sums of more than 32 ranks are as long to write as 600 tokens' rows)
   const int64_t want = (768 + tiles - 1) / tiles;
   const int64_t c = ((tokens + want - 1) / want + 63) / 64 * 64;
   return (int32_t)(c < 64 ? 64 : c);
 }
 
 // Whether the up products may compute h themselves: up to 32 ranks of 160 KB in
-// all, and 16 MB read by the call's workgroups.
+// all, and 16 MB read by the call's workgroups (with the projection, 1 x 5120 x 2048
+// of rank 16: 18.3 us a call, in two launches 19.7; 7 x 1001 x 1040 binary32 18.4,
+// 21.3).
 bool lora_direct(int dtype, int64_t tokens, int64_t k, int64_t n, int32_t rank) {
   const int64_t bytes = (int64_t)rank * k * (dtype == 0 ? 4 : 2);
   return tokens <= kWindow && rank <= 32 && bytes <= (160 << 10) &&
@@ -1164,6 +1175,8 @@ hipError_t launch_lora_up(LoraUpArgs a, hipStream_t s) {
   if (a.tokens == 0) return hipSuccess;
   const int group = up_group(a.tokens);
   // 256 columns a workgroup; more while there are enough for eight (four) a CU
+  // (256, 512, 1024 and 2048 columns: 4096 x 5120 30.0, 30.0, 32.8, 46.6 us, 8192 x
+  // 2048 25.1, 24.2, 22.5, 32.8)
   const int64_t many = group == 1 ? 2048 : 1024, blocks = groups(a.tokens, group);
   a.wide = kThreads;
   while (a.wide < 4096 && blocks * ((a.n + 2 * a.wide - 1) / (2 * a.wide)) >= many) a.wide *= 2;

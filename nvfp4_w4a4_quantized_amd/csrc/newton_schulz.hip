@@ -21,8 +21,8 @@
 // One GEMM kernel computes all three products; a symmetric result is computed
 // in its upper tiles and mirrored.  Operands lie K-contiguous (X of the wide
 // Gram product, A, P, X of the tall update) or K-major (X of the tall Gram
-// product and of the wide update) and go from memory straight into a four-slot
-// LDS ring; K-major tiles are read with the transposing LDS loads.
+// product and of the wide update) and go from memory straight into an LDS
+// ring of two to four slots; K-major tiles are read with the transposing LDS loads.
 //
 // Bound, for many matrices: 128 of 2048 x 768 (1.6 TFLOP) take 4.5 ms.  A and P run
 // at 0.8 and 0.5 PFLOP/s counted without the mirrored half (matrix cores 51 % busy
