@@ -682,7 +682,11 @@ int moe_expert_decode(const void* x, int x_dtype, int64_t tokens, int64_t hidden
  *   workspace  *_workspace_size() bytes, 16-byte aligned; every word read is
  *              written before by the same call
  * Limits (NVFP4_UNSUPPORTED beyond): rank <= 256; adapters <= 1024; tokens <=
- * 2^24; n, k <= 2^18; nvfp4_lora_matvec: tokens <= 65536 and nvfp4_matvec's.
+ * 2^24; n, k <= 2^18; nvfp4_lora_matvec: tokens <= 65536 and nvfp4_matvec's;
+ * lora_backward: tokens * rank < 2^32, and adapters * ceil(rank / 64) * (ceil(k /
+ * 64) + ceil(n / 64)) < 2^22 - 1.
+ * Outputs and the workspace overlap nothing else, but for base as said above: the
+ * inputs are read again while and after outputs are written.
  * A batch is read fastest when the tokens of a request lie together: beyond 256
  * tokens, up to 64 consecutive ones are multiplied adapter by adapter.
  * ---------------------------------------------------------------------- */
@@ -723,7 +727,8 @@ int nvfp4_lora_matvec(const void* x, int x_dtype, int64_t tokens, int64_t ld_x,
  * bits may differ between calls with other numbers of matrices.
  *   g          [batch, rows, cols], dtype code; rows ld_row apart, matrices
  *              ld_batch apart (elements)
- *   out        dense [batch, rows, cols], out_dtype; may be g itself
+ *   out        dense [batch, rows, cols], out_dtype; may be g itself (dense and of
+ *              that type), and may not overlap it otherwise
  *   a, b, c    the quintic's coefficients, the same every step.  Singular values
  *              start in [0, 1]; coefficients that let them grow past 8, or b A + c
  *              A A past 8192, are NVFP4_UNSUPPORTED.

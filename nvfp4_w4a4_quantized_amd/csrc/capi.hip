@@ -1058,11 +1058,18 @@ static LoraBackwardLayout carve_lora_backward(void* ws, int dtype, int64_t T, in
   return L;
 }
 
+// A launch takes fewer than 2^32 threads: one per value of h where it is computed
+// again, and 1024 per 64 x 64 tile of A and B, which the transposes take, and the sort.
+static bool lora_backward_fits(int64_t tokens, int64_t k, int64_t n, int32_t adapters, int32_t rank) {
+  const int64_t tiles = (int64_t)adapters * ((rank + 63) / 64) * ((k + 63) / 64 + (n + 63) / 64);
+  return tokens * rank < (1LL << 32) && tiles < (1 << 22) - 1;
+}
+
 size_t lora_backward_workspace_size(int dtype, int64_t tokens, int64_t k, int64_t n,
                                     int32_t adapters, int32_t rank) {
   if (!valid_dtype(dtype) || tokens < 0 || tokens > kMaxLoraTokens || k < 1 || n < 1 ||
       k > kMaxLoraWidth || n > kMaxLoraWidth || adapters < 1 || adapters > kMaxAdapters || rank < 1 ||
-      rank > kMaxRank)
+      rank > kMaxRank || !lora_backward_fits(tokens, k, n, adapters, rank))
     return 0;
   return carve_lora_backward(nullptr, dtype, tokens, k, n, adapters, rank).bytes;
 }
@@ -1074,6 +1081,7 @@ int lora_backward(const void* dy, int dtype, int64_t tokens, int64_t n, int64_t 
                   void* workspace, size_t workspace_bytes, void* stream) {
   const int st = lora_status(dtype, tokens, k, n, ids, a, b, scale, adapters, rank);
   if (st != NVFP4_OK) return st;
+  if (!lora_backward_fits(tokens, k, n, adapters, rank)) return NVFP4_UNSUPPORTED;
   if (!rows_ok(dy, tokens, n, ld_dy, dtype) || !rows_ok(x, tokens, k, ld_x, dtype) ||
       (base && !rows_ok(base, tokens, k, ld_base, dtype)) || !rows_ok(dx, tokens, k, k, dtype) ||
       !da || !db || !aligned(da, 4) || !aligned(db, 4) || !aligned(h, 4) || !workspace ||

@@ -887,7 +887,7 @@ def lora_forward(x, a, b, ids, scale=None, base=None, out_dtype=None, out=None,
     x[t]) with s = ids[t].  x [T, K], a [S, R, K], b [S, N, R] of one type
     (float32, bf16 or fp16), ids int32 [T] (outside [0, S): no adapter), scale
     float32 [S], base [T, N] in the output's type (the projection's output; `out`
-    may be base itself).  Returns y [T, N] in out_dtype (x's by default), with
+    may be base itself, but overlap nothing else).  Returns y [T, N] in out_dtype (x's by default), with
     return_h also h = a[s] x[t] float32 [T, R], lora_backward's argument."""
     ld = _need_rows(x, "x")
     T, K = x.shape
@@ -906,7 +906,7 @@ def lora_forward(x, a, b, ids, scale=None, base=None, out_dtype=None, out=None,
 def lora_backward(dy, x, a, b, ids, scale=None, h=None, base=None, out=None, workspace=None):
     """Gradients of lora_forward from dy [T, N] (x's type): dx [T, K] (x's type)
     = base[t] + a[s]^T g[t] with g[t] = scale[s] b[s]^T dy[t] (base: the rest of
-    x's gradient; `out` may be base itself), da float32 [S, R, K] and db float32
+    x's gradient; `out` may be base itself, but overlap nothing else), da float32 [S, R, K] and db float32
     [S, N, R].  h: the forward's (None: computed again).  Returns (dx, da, db)."""
     ld_dy = _need_rows(dy, "dy")
     T, N = dy.shape
@@ -965,7 +965,8 @@ def newton_schulz(g, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315), eps
     batch [E, rows, cols] of them (float32, bf16 or fp16; the last dimension
     dense): X = g / (|g|_F + eps), then `steps` times X = a X + (b A + c A A) X
     with A = X X^T (from the other side where rows > cols), times scale.
-    Returns g's shape in out_dtype (g's by default; `out` may be g itself).
+    Returns g's shape in out_dtype (g's by default; `out` may be g itself if that
+    is dense and of the same type, and may not overlap it otherwise).
     bf16 results take faster products, below bf16's own rounding."""
     if not isinstance(g, torch.Tensor):
         raise TypeError("g must be a torch.Tensor")

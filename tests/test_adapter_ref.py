@@ -70,6 +70,21 @@ def test_backward_refusals(L):  # noqa: F811
     assert L.lora_backward_workspace_size(3, 4, 48, 40, 3, 8) == 0
 
 
+def test_backward_refuses_more_threads_than_a_launch_takes(L):  # noqa: F811
+    """2^32 threads: tokens * rank (h computed again), and the tiles of 64 x 64 that
+    A and B are transposed in, 1024 threads each and one more for the sort."""
+    good = [F, 1, 4, 40, 40, F, 48, 48, F, F, F, None, 3, 8, None, None, 48, F, F, F, F, 1 << 30, None]
+    many = change(change(good, 2, 1 << 24), 13, 256)
+    assert L.lora_backward(*many) == UNSUPPORTED
+    assert L.lora_backward_workspace_size(1, 1 << 24, 48, 40, 3, 256) == 0
+    assert L.lora_backward(*change(many, 13, 255)) == WS_SMALL
+    # 1024 adapters of 4 x (512 + 512) tiles, 2^22 in all; 4 x (512 + 511) are taken
+    for k, n, want in ((1 << 15, 1 << 15, UNSUPPORTED), (1 << 15, (1 << 15) - 64, WS_SMALL)):
+        wide = [F, 1, 4, n, n, F, k, k, F, F, F, None, 1024, 256, None, None, k, F, F, F, F, 1 << 30, None]
+        assert L.lora_backward(*wide) == want, (k, n)
+        assert (L.lora_backward_workspace_size(1, 4, k, n, 1024, 256) == 0) == (want == UNSUPPORTED)
+
+
 def test_matvec_refusals(L):  # noqa: F811
     w = Weights(0x1000, 0x1000, 0x1000, 0)
     # x, dtype, T, ld, w, n, k, ids, a, b, scale, S, rank, out_dtype, out, ws, bytes, s
