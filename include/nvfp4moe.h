@@ -667,7 +667,9 @@ int moe_expert_decode(const void* x, int x_dtype, int64_t tokens, int64_t hidden
  * reproducible.  The order of the sums goes by the call's sizes: a row's last
  * bits may differ between calls with other numbers of tokens.  16-bit inputs
  * below 2^-126 (bf16) may count as zero.  Infinities and NaN of a token stay in
- * its own rows and, on the way back, its adapter's gradients.
+ * its own rows and, on the way back, its adapter's gradients; an infinity gives
+ * what the formula's products and sums give (beside bf16 rows and adapters, values
+ * of h and g below 2^-94 may count as zero there).
  *   x, dy      [tokens, ld], dtype code; a [adapters, rank, k] and b [adapters,
  *              n, rank] dense, of the same type (adapters of a smaller rank hold
  *              zeros in the rest)

@@ -20,8 +20,7 @@
 // Arithmetic: down multiplies in the type of x by MFMA 16x16x32 (binary32:
 // 16x16x4) into binary32; h and g stay binary32.  What they enter are binary32
 // products: of bf16 B, A, x and dy with the three bf16 parts of the binary32
-// value, an exact sum (MFMA 16x16x32), else MFMA 16x16x4 of the exactly widened
-// values.  Sums over K that several workgroups share are joined in workgroup
+// value (MFMA 16x16x32), else MFMA 16x16x4 of the exactly widened values.  Sums over K that several workgroups share are joined in workgroup
 // order, sums over tokens in token order per chunk: results do not depend on
 // timing.
 //
@@ -251,21 +250,27 @@ __global__ __launch_bounds__(kThreads) void lora_down_kernel(LoraDownArgs p) {
 
 // The three bf16 parts of a binary32 value: the upper half of its bits, of what
 // is left of it, and the rest.  The lower parts of an infinity are the largest
-// finite value's: they add to it with its sign.
-__device__ __forceinline__ void bf16_parts(float v, uint16_t (&part)[3]) {
+// finite value's: they add to it with its sign.  A lower part that is zero holds
+// 2^-32 of the value instead, and so does the returned fourth one, which stands
+// where the operands repeat beside nothing: an infinity of the other operand times
+// each part has the sign of its product with the value (NaN if that is zero).  The
+// parts' sum is the value to 2^-30 of it, far below the binary32 sums that it enters.
+__device__ __forceinline__ uint16_t bf16_parts(float v, uint16_t (&part)[3]) {
   part[0] = (uint16_t)(__float_as_uint(v) >> 16);
   v = __builtin_amdgcn_fmed3f(v, -__FLT_MAX__, __FLT_MAX__);
+  const float least = v * 0x1p-32f;
 #pragma unroll
   for (int i = 1; i < 3; ++i) {
     v -= __uint_as_float(__float_as_uint(v) & 0xFFFF0000u);
-    part[i] = (uint16_t)(__float_as_uint(v) >> 16);
+    part[i] = (uint16_t)(__float_as_uint(v == 0.0f ? least : v) >> 16);
   }
+  return (uint16_t)(__float_as_uint(least) >> 16);
 }
 
 // c h of up to TOK tokens and PASS ranks, as the products' operand.  bf16: a step
 // is 32 k of one MFMA, tokens' rows of 64 bytes (16-byte chunk k of row t at
 // k ^ (t / 4) % 4).  Up to 16 ranks take two steps, the first two parts beside
-// each other and the third beside zeros; more take three, a part each, per 32
+// each other and the third beside the fourth; more take three, a part each, per 32
 // ranks.  Else: rows of binary32.
 template <int DT, int TOK, int PASS>
 struct Ranked {
@@ -280,12 +285,12 @@ struct Ranked {
   __device__ __forceinline__ void put(int t, int r, bool narrow, float v) {
     if constexpr (DT == 1) {
       uint16_t b[3];
-      bf16_parts(v, b);
+      const uint16_t least = bf16_parts(v, b);
       if (narrow) {
         part[at(0, t, r)] = b[0];
         part[at(0, t, 16 + r)] = b[1];
         part[at(1, t, r)] = b[2];
-        part[at(1, t, 16 + r)] = 0;
+        part[at(1, t, 16 + r)] = least;
       } else {
 #pragma unroll
         for (int i = 0; i < 3; ++i) part[at(r / 32 * 3 + i, t, r % 32)] = b[i];
