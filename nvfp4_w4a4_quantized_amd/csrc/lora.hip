@@ -419,8 +419,9 @@ __global__ __launch_bounds__(kThreads, BIG ? 2 : 3) void lora_up_kernel(LoraUpAr
           if (r + e < ranks) to[e] = p.h_scaled ? c * f[e] : f[e];
       }
       if (t < TOK) {
+        // (ranks past the last stay zero whatever the scale is)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) hs.put(t, r + e, narrow, c * f[e]);
+        for (int e = 0; e < 4; ++e) hs.put(t, r + e, narrow, live && a >= 0 && r + e < ranks ? c * f[e] : 0.0f);
       }
     };
     auto padded_ranks = [&](int r0) -> int {

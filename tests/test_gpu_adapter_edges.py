@@ -84,3 +84,27 @@ def test_infinities_on_the_way_back(T, rank, dtype):
     same(got[0], dx, (N + rank + 24) * A.ULP * dxm, "dx")
     same(got[1], da, (N + T + 40) * A.ULP * dam, "da")
     same(got[2], db, (T + 24) * A.ULP * dbm, "db")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rank", [5, 20, 40, 100])
+@pytest.mark.parametrize("T", [4, 200, 300])
+def test_an_infinite_scale(T, rank, dtype):
+    """With positive values every product of it is one infinity, whatever the rank
+    is padded to."""
+    from nvfp4_w4a4_quantized_amd import ops
+    K, N, S = 40, 88, 2
+    c = positive(make(T, K, N, rank, S, "random", dtype, 14), "x", "a", "b", "dy")
+    c["ids"] = (torch.arange(T) % 3).to(torch.int32)
+    c["scale"] = torch.tensor([INF, -2.0])
+    x, a, b, ids, base, dy, scale = cuda(c, "x", "a", "b", "ids", "base", "dy", "scale")
+    y, ym, h, _ = A.forward(c["x"], c["a"], c["b"], c["ids"], c["scale"], c["base"])
+    say("infinite scale", T, rank, dtype)
+    same(ops.lora_forward(x, a, b, ids, scale=scale, base=base), y, (K + rank + 24) * A.ULP * ym, "y")
+    (dx, dxm), (da, dam), (db, dbm) = A.backward(c["dy"], c["x"], c["a"], c["b"], c["ids"], c["scale"],
+                                                 h.float(), None)
+    assert bool((dx[0] == INF).all()) and bool((da[0] == INF).all()) and bool((db[0] == INF).all())
+    got = ops.lora_backward(dy, x, a, b, ids, scale=scale, h=h.float().cuda())
+    same(got[0], dx, (N + rank + 24) * A.ULP * dxm, "dx")
+    same(got[1], da, (N + T + 40) * A.ULP * dam, "da")
+    same(got[2], db, (T + 24) * A.ULP * dbm, "db")
