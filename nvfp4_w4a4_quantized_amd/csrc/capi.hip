@@ -1130,7 +1130,7 @@ struct NsLayout {
   size_t bytes;
 };
 
-static NsLayout carve_ns(void* ws, int64_t batch, int64_t rows, int64_t cols, bool exact) {
+static NsLayout carve_ns(void* ws, int64_t batch, int64_t rows, int64_t cols) {
   Carver c(ws);
   NsLayout L{};
   const int64_t m = ns_batch(batch, rows, cols), n = rows < cols ? rows : cols;
@@ -1139,8 +1139,7 @@ static NsLayout carve_ns(void* ws, int64_t batch, int64_t rows, int64_t cols, bo
   L.norms = c.take<double>((size_t)(m * ns_norm_parts(m, rows)));
   L.k0 = c.take<int32_t>((size_t)m);
   for (int i = 0; i < 4; ++i) L.x[i] = c.take<_Float16>(xs);
-  for (int i = 0; i < 4; ++i)
-    if (exact || i % 2 == 0) L.sq[i] = c.take<_Float16>(ns);
+  for (int i = 0; i < 4; ++i) L.sq[i] = c.take<_Float16>(ns);
   L.bytes = c.used;
   if (n <= 64) {              // (whichever of the two the coefficients choose)
     Carver d(ws);
@@ -1160,7 +1159,7 @@ static int ns_status(int64_t batch, int64_t rows, int64_t cols, int out_dtype) {
 
 size_t newton_schulz_workspace_size(int64_t batch, int64_t rows, int64_t cols, int out_dtype) {
   if (ns_status(batch, rows, cols, out_dtype) != NVFP4_OK || batch == 0) return 0;
-  return carve_ns(nullptr, batch, rows, cols, out_dtype != 1).bytes;
+  return carve_ns(nullptr, batch, rows, cols).bytes;
 }
 
 int newton_schulz(const void* g, int dtype, int64_t batch, int64_t rows, int64_t cols,
@@ -1180,12 +1179,12 @@ int newton_schulz(const void* g, int dtype, int64_t batch, int64_t rows, int64_t
   NsArgs n{};
   if (steps > kMaxSteps || !ns_bounds(steps, a, b, c, &n.scales)) return NVFP4_UNSUPPORTED;
   if (batch == 0) return NVFP4_OK;
-  const bool exact = out_dtype != 1;
-  const NsLayout L = carve_ns(workspace, batch, rows, cols, exact);
+  const NsLayout L = carve_ns(workspace, batch, rows, cols);
   if (workspace_bytes < L.bytes) return NVFP4_WORKSPACE_TOO_SMALL;
   n.src.g = g; n.src.dtype = dtype; n.src.rows = rows; n.src.cols = cols;
   n.src.ld_row = ld_row; n.src.ld_batch = ld_batch; n.batch = batch;
-  n.steps = steps; n.a = a; n.b = b; n.c = c; n.eps = eps; n.out_scale = scale; n.exact = exact;
+  n.steps = steps; n.a = a; n.b = b; n.c = c; n.eps = eps; n.out_scale = scale;
+  n.exact = out_dtype != 1 || !n.scales.fast;
   n.out = out; n.out_dtype = out_dtype; n.norms = L.norms; n.k0 = L.k0;
   for (int i = 0; i < 4; ++i) {
     n.x[i] = L.x[i];

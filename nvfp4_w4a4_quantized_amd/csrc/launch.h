@@ -317,6 +317,7 @@ struct NsSource {
 struct NsScales {             // powers of two that X, A and P are kept times
   float x, a, p;
   int growth;                 // bits that a small X may grow by per step
+  bool fast;                  // products of the upper parts are enough for bf16
 };
 struct NsMatrix {             // a batch of matrices in two binary16 parts
   const _Float16* hi; const _Float16* lo;
