@@ -734,7 +734,8 @@ int nvfp4_lora_matvec(const void* x, int x_dtype, int64_t tokens, int64_t ld_x,
  *              that type), and may not overlap it otherwise
  *   a, b, c    the quintic's coefficients, the same every step.  Singular values
  *              start in [0, 1]; coefficients that let them grow past 8, or b A + c
- *              A A past 8192, are NVFP4_UNSUPPORTED.
+ *              A A past 8192, are NVFP4_UNSUPPORTED, and so is an |a| whose power
+ *              to the steps is below 2^-8 (but for matrices computed in binary64).
  *   workspace  newton_schulz_workspace_size() bytes (at most about 4 GiB, or one
  *              matrix's), 16-byte aligned; every word read is written before by
  *              the same call

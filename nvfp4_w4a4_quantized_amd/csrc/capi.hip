@@ -1178,6 +1178,8 @@ int newton_schulz(const void* g, int dtype, int64_t batch, int64_t rows, int64_t
     return NVFP4_INVALID_ARGUMENT;
   NsArgs n{};
   if (steps > kMaxSteps || !ns_bounds(steps, a, b, c, &n.scales)) return NVFP4_UNSUPPORTED;
+  const bool small = ns_is_small(rows, cols, steps, a, b, c);
+  if (!small && !ns_keeps_small(steps, a)) return NVFP4_UNSUPPORTED;
   if (batch == 0) return NVFP4_OK;
   const NsLayout L = carve_ns(workspace, batch, rows, cols);
   if (workspace_bytes < L.bytes) return NVFP4_WORKSPACE_TOO_SMALL;
@@ -1191,7 +1193,7 @@ int newton_schulz(const void* g, int dtype, int64_t batch, int64_t rows, int64_t
     n.sq[i] = L.sq[i];
   }
   n.small_parts = L.parts; n.small_q = L.q;
-  if (ns_is_small(rows, cols, steps, a, b, c))
+  if (small)
     return hip_status(launch_newton_schulz_small(n, static_cast<hipStream_t>(stream)));
   return hip_status(launch_newton_schulz(n, static_cast<hipStream_t>(stream)));
 }

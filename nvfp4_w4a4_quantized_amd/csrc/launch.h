@@ -346,6 +346,7 @@ struct NsArgs {
   double* small_parts; double* small_q;   // of a short side alone
 };
 bool ns_bounds(int steps, float a, float b, float c, NsScales* out);
+bool ns_keeps_small(int steps, float a);
 int64_t ns_batch(int64_t batch, int64_t rows, int64_t cols);
 int ns_norm_parts(int64_t batch, int64_t rows);
 hipError_t launch_newton_schulz(const NsArgs& a, hipStream_t s);

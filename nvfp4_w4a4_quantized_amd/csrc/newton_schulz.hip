@@ -640,6 +640,12 @@ bool ns_bounds(int steps, float a, float b, float c, NsScales* out) {
   return true;
 }
 
+// Whether X's two parts hold the digits of what a multiplies: an X of 16384 x 16384 starts
+// with elements of 2^-14, 2^1 as they are kept, and the lower part is rounded to 2^-24.
+// 2^-8 of them, where that is 2e-6 in the mean, is as far as a may take them (0.5 in 20
+// steps: 256 x 384 1e-4 off, in 8 steps 4e-8).
+bool ns_keeps_small(int steps, float a) { return steps * log2(fmin(fabs((double)a), 1.0)) >= -8.0; }
+
 // Matrices that are taken together: as many as fit 4 GiB of workspace (128 of
 // 2048 x 768 together take 5.2 ms; 62 at a time 5.7, 16, whose X would stay in
 // the last-level cache, 5.7: their launches do not fill the last round of CUs).
