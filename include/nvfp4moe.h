@@ -721,13 +721,14 @@ int nvfp4_lora_matvec(const void* x, int x_dtype, int64_t tokens, int64_t ld_x,
  *   out = scale * X
  * The norm is binary64.  X is kept to 22 bits.  float32 and fp16 results take
  * products of all 22 bits, summed in binary32 (errors as of a binary32
- * computation).  bf16 results take products of the upper 11 bits where their error,
- * by the coefficients and the steps, stays near bf16's own rounding (the usual
- * coefficients 3.4445, -4.775, 2.0315: up to five steps, 2e-3 of the result's norm
- * with the rounding), else those of all 22.  Matrices with a side of at most 64 are
- * computed in binary64 (unless a^(2 steps) > 2^26).  A zero matrix gives zeros; one that holds an infinity or NaN gives NaN throughout, and no other
- * matrix is touched by it.  Results are bitwise reproducible; a matrix's last
- * bits may differ between calls with other numbers of matrices.
+ * computation).  bf16 results take products of the upper 11 bits in as many of the
+ * last steps as keep their error, by the coefficients, near bf16's own rounding (five of
+ * the usual 3.4445, -4.775, 2.0315: 2e-3 to 3e-3 of the result's norm with the rounding),
+ * and those of all 22 before.  Matrices with a side of at most 64 are computed in
+ * binary64 (unless a^(2 steps) > 2^26).  A zero matrix gives zeros; one that holds an infinity or
+ * NaN gives NaN throughout, and no other matrix is touched by it.  Results are bitwise
+ * reproducible; a matrix's last bits may differ between calls with other numbers of
+ * matrices.
  *   g          [batch, rows, cols], dtype code; rows ld_row apart, matrices
  *              ld_batch apart (elements)
  *   out        dense [batch, rows, cols], out_dtype; may be g itself (dense and of

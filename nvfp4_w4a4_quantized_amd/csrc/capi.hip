@@ -1121,7 +1121,6 @@ int lora_backward(const void* dy, int dtype, int64_t tokens, int64_t n, int64_t 
 // ---- the orthogonalised update ----
 
 constexpr int64_t kMaxSide = 16384, kMaxMatrices = 1 << 20;
-constexpr int kMaxSteps = 64;
 
 struct NsLayout {
   double* norms; int32_t* k0;
@@ -1177,7 +1176,7 @@ int newton_schulz(const void* g, int dtype, int64_t batch, int64_t rows, int64_t
   if (!aligned(g, dtype_size(dtype)) || !aligned(out, dtype_size(out_dtype)) || !aligned(workspace, 16))
     return NVFP4_INVALID_ARGUMENT;
   NsArgs n{};
-  if (steps > kMaxSteps || !ns_bounds(steps, a, b, c, &n.scales)) return NVFP4_UNSUPPORTED;
+  if (steps > kMaxNsSteps || !ns_bounds(steps, a, b, c, &n.scales)) return NVFP4_UNSUPPORTED;
   const bool small = ns_is_small(rows, cols, steps, a, b, c);
   if (!small && !ns_keeps_small(steps, a)) return NVFP4_UNSUPPORTED;
   if (batch == 0) return NVFP4_OK;
@@ -1186,7 +1185,7 @@ int newton_schulz(const void* g, int dtype, int64_t batch, int64_t rows, int64_t
   n.src.g = g; n.src.dtype = dtype; n.src.rows = rows; n.src.cols = cols;
   n.src.ld_row = ld_row; n.src.ld_batch = ld_batch; n.batch = batch;
   n.steps = steps; n.a = a; n.b = b; n.c = c; n.eps = eps; n.out_scale = scale;
-  n.exact = out_dtype != 1 || !n.scales.fast;
+  n.exact = out_dtype != 1 ? steps : steps - n.scales.fast;
   n.out = out; n.out_dtype = out_dtype; n.norms = L.norms; n.k0 = L.k0;
   for (int i = 0; i < 4; ++i) {
     n.x[i] = L.x[i];

@@ -311,13 +311,14 @@ hipError_t launch_lora_grad(const LoraGradArgs& a, int32_t max_entries, const in
                             hipStream_t s);
 
 // ---- newton_schulz.hip ----
+constexpr int kMaxNsSteps = 64;
 struct NsSource {
   const void* g; int dtype; int64_t rows, cols, ld_row, ld_batch;
 };
 struct NsScales {             // powers of two that X, A and P are kept times
   float x, a, p;
   int growth;                 // bits that a small X may grow by per step
-  bool fast;                  // products of the upper parts are enough for bf16
+  int fast;                   // last steps that a bf16 result may take products of the upper parts in
 };
 struct NsMatrix {             // a batch of matrices in two binary16 parts
   const _Float16* hi; const _Float16* lo;
@@ -337,7 +338,7 @@ struct NsGemmArgs {
 struct NsArgs {
   NsSource src; int64_t batch;
   int steps; float a, b, c; double eps; float out_scale;
-  int exact;                  // products of both parts
+  int exact;                  // first steps, whose products take both parts
   NsScales scales;
   void* out; int out_dtype;
   double* norms; int32_t* k0;

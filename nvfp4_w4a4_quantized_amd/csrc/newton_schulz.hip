@@ -6,8 +6,8 @@
 // Arithmetic.  X is kept as two binary16 parts (hi, and lo the rest: 22 bits)
 // times a power of two that brings its largest possible element near the top of
 // the range.  The products run on the matrix cores in binary16 with binary32 sums:
-//   - 16-bit "fast" products, of bf16 results where the coefficients and the number
-//     of steps let them (ns_bounds), take hi alone, of X and of P + a I, and a lo is added
+//   - 16-bit "fast" products, of bf16 results in as many of the last steps as the
+//     coefficients let them (ns_bounds), take hi alone, of X and of P + a I, and a lo is added
 //     to them: the small singular values, which the iteration multiplies by a per
 //     step, keep X's 22 bits.  (Taking a hi from memory instead of the products
 //     reads X once more: an update of 128 matrices of 2048 x 768 takes 524 us
@@ -587,15 +587,17 @@ int64_t pad64(int64_t v) { return (v + 63) / 64 * 64; }
 // is kept, of |b A + c A A|, and the bits that a small one grows by per step.
 // false: the coefficients let X leave the range that binary16 holds.
 //
-// fast: whether products of 11 bits stay near bf16's own rounding, 1.7e-3 in the mean.
-// Such a rounding is 2e-4 off in the mean; a step makes it of P and of X in P X, and of
-// A in P, 2e-4 sqrt(2 |P|^2 + (1.7 |b A + 2 c A A|)^2) with both at their largest, and the
-// steps' errors, which turn the singular vectors, add up as their squares.  The usual
-// coefficients: 2.3e-3 for five steps (measured 1.2e-3 to 1.6e-3), 2.5e-3 for six,
-// 8.4e-3 for 64 (7e-3 to 3.5e-2).  A step that takes a singular value below half of itself
-// would raise what was made before.
+// fast: how many steps, the last ones, products of 11 bits may take so that the result
+// stays near bf16's own rounding, 1.7e-3 in the mean.  Such a rounding is 2e-4 off in the
+// mean; a step makes it of P and of X in P X, and of A in P, 2e-4 sqrt(2 |P|^2 + (1.7 |b A +
+// 2 c A A|)^2) with both at their largest, and the steps' errors, which turn the singular
+// vectors, add up as their squares.  The usual coefficients: 2.3e-3 for five steps (measured
+// 1.2e-3 to 1.6e-3 for five in all, up to 2.3e-3 for the last of more), 8.4e-3 for 64 (7e-3
+// to 3.5e-2).  A step that takes a singular value below half of itself would raise what was
+// made before: none then.  5120 x 2048: five steps 0.63 ms, six 0.87, ten 1.89 (all exact
+// from six on: 1.70 and 2.80).
 bool ns_bounds(int steps, float a, float b, float c, NsScales* out) {
-  double u = 1.0, top = 1.0, off = 0.0, least = 1e30;
+  double u = 1.0, top = 1.0, least = 1e30, off[kMaxNsSteps];
   auto f = [&](double x) { return fabs(x * (a + x * x * ((double)b + (double)c * x * x))); };
   for (int i = 0; i < steps; ++i) {
     // the largest |b y + c y y| and |b y + 2 c y y| on [0, u^2], and the least factor of a
@@ -607,7 +609,7 @@ bool ns_bounds(int steps, float a, float b, float c, NsScales* out) {
       most_a = fmax(most_a, fabs(b * y + 2.0 * c * y * y));
       least = fmin(least, (a > 0.0f ? 1.0 : -1.0) * (a + b * y + c * y * y));
     }
-    off += 2.0 * most_p * most_p + 2.89 * most_a * most_a;
+    off[i] = 2.0 * most_p * most_p + 2.89 * most_a * most_a;
     // the extrema of a x + b x^3 + c x^5 on [0, u]: its end and the roots of
     // a + 3 b y + 5 c y^2, y = x^2
     double best = f(u);
@@ -634,7 +636,10 @@ bool ns_bounds(int steps, float a, float b, float c, NsScales* out) {
   out->x = (float)scale(top);
   out->a = (float)scale(l);
   out->p = (float)scale(v);
-  out->fast = least >= 0.5 && 2e-4 * sqrt(off) <= 2.4e-3;
+  out->fast = 0;
+  double sum = 0.0;
+  while (least >= 0.5 && out->fast < steps && 2e-4 * sqrt(sum += off[steps - 1 - out->fast]) <= 2.4e-3)
+    ++out->fast;
   const double grow = fabs(a) + fabs(b) + fabs(c);
   out->growth = grow <= 1.0 ? 0 : (int)ceil(log2(grow));
   return true;
@@ -693,7 +698,7 @@ hipError_t launch_newton_schulz(const NsArgs& a, hipStream_t s) {
       const NsMatrix A = {a.sq[0], a.sq[1], ns, ldn, (uint32_t)(ns * 2)};
       const NsMatrix P = {a.sq[2], a.sq[3], ns, ldn, (uint32_t)(ns * 2)};
       NsGemmArgs g{};
-      g.batch = m; g.exact = a.exact; g.k0 = a.k0; g.growth = a.scales.growth;
+      g.batch = m; g.exact = i < a.exact; g.k0 = a.k0; g.growth = a.scales.growth;
       g.drop = i * a.scales.growth;
       // A
       g.a = g.b = X; g.m = g.n = n; g.k = tall ? src.rows : src.cols;

@@ -967,8 +967,8 @@ def newton_schulz(g, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315), eps
     with A = X X^T (from the other side where rows > cols), times scale.
     Returns g's shape in out_dtype (g's by default; `out` may be g itself if that
     is dense and of the same type, and may not overlap it otherwise).
-    bf16 results take faster products where these stay near bf16's own rounding (the
-    usual coefficients: up to five steps)."""
+    bf16 results take faster products in the last steps, as many as stay near bf16's
+    own rounding (the usual coefficients: five)."""
     if not isinstance(g, torch.Tensor):
         raise TypeError("g must be a torch.Tensor")
     if not g.is_cuda:
