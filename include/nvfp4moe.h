@@ -690,7 +690,9 @@ int moe_expert_decode(const void* x, int x_dtype, int64_t tokens, int64_t hidden
  * Outputs and the workspace overlap nothing else, but for base as said above: the
  * inputs are read again while and after outputs are written.
  * A batch is read fastest when the tokens of a request lie together: beyond 256
- * tokens, up to 64 consecutive ones are multiplied adapter by adapter.
+ * tokens, up to 64 consecutive ones are multiplied adapter by adapter.  Up to 256
+ * tokens in all, an adapter's are multiplied 16 at a time, one after the other: 64
+ * and more of one adapter take longer than a batch of 257 tokens.
  * ---------------------------------------------------------------------- */
 size_t lora_forward_workspace_size(int64_t tokens, int64_t k, int32_t rank);
 int lora_forward(const void* x, int dtype, int64_t tokens, int64_t k, int64_t ld_x,
@@ -725,10 +727,10 @@ int nvfp4_lora_matvec(const void* x, int x_dtype, int64_t tokens, int64_t ld_x,
  * last steps as keep their error, by the coefficients, near bf16's own rounding (five of
  * the usual 3.4445, -4.775, 2.0315: 2e-3 to 3e-3 of the result's norm with the rounding),
  * and those of all 22 before.  Matrices with a side of at most 64 are computed in
- * binary64 (unless a^(2 steps) > 2^26).  A zero matrix gives zeros; one that holds an infinity or
- * NaN gives NaN throughout, and no other matrix is touched by it.  Results are bitwise
- * reproducible; a matrix's last bits may differ between calls with other numbers of
- * matrices.
+ * binary64 (unless a^(2 steps) > 2^26).  A zero matrix gives zeros; one that holds an
+ * infinity or NaN gives NaN throughout, and no other matrix is touched by it.  Results
+ * are bitwise reproducible; a matrix's last bits may differ between calls with other
+ * numbers of matrices.
  *   g          [batch, rows, cols], dtype code; rows ld_row apart, matrices
  *              ld_batch apart (elements)
  *   out        dense [batch, rows, cols], out_dtype; may be g itself (dense and of

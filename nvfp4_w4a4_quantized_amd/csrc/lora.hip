@@ -12,7 +12,9 @@
 //
 // Tokens of one adapter are multiplied together.  Few tokens (up to kWindow):
 // a workgroup per token looks its adapter's tokens up and the first of them
-// does the work of all.  Many: a workgroup takes consecutive tokens (16 to 64 down,
+// does the work of all, 16 at a time (which costs many tokens of few adapters
+// dear: 2048 -> 5120 of rank 16, one adapter, 64 tokens 23 us, 256 tokens 156, 257
+// tokens 14).  Many: a workgroup takes consecutive tokens (16 to 64 down,
 // 32 up) and does one adapter after the other, each keeping the results of its own
 // tokens, so a batch whose requests lie together reads each token's row once and
 // an adapter once per workgroup.
@@ -346,7 +348,9 @@ __device__ __forceinline__ void get_some(const void* from, int64_t at, int64_t l
 // a wave at a time.  Which of the wave's 64 columns is row i of product j is chosen
 // so that a lane ends with 16-byte pieces of its token, and a load or store covers
 // 64 consecutive bytes of every token (32 bytes a lane, in two halves of 16 each,
-// cost 4096 x 5120 29.6 us instead of 27.4).
+// cost 4096 x 5120 29.6 us instead of 27.4).  Beyond kWindow tokens the three waves a SIMD
+// leave registers in scratch, 8 to 154 of them, in every form of fp16, of binary32 with a
+// base or any width, and of bf16 into binary32 of any width.
 // The sums start from the base's values, which are loaded a turn ahead.  BIG:
 // more than 32 ranks, 64 at a time.  WHOLE: whole pieces everywhere and the kind of
 // base known, so that no branch stands around a load (the compiler waits for every
@@ -894,7 +898,7 @@ __global__ __launch_bounds__(kThreads) void lora_grad_kernel(LoraGradArgs p) {
 // tokens, eight 230 to 239, with longer chunks; columns read two turns ahead instead
 // of one 213).  Grid: x = 512 (256) columns of x, then of dy.
 // The binary32 form above is bound by its matrix instructions from rank 32 on
-// (rank 64: 512 us for 470 MB).
+// (rank 64: 512 us for 470 MB).  Ranks 17 to 64 leave 5 and 10 registers in scratch.
 template <int RT>
 __global__ __launch_bounds__(RT == 4 ? 256 : 512, RT == 4 ? 3 : 4) void lora_grad16_kernel(LoraGradArgs p) {
   constexpr int R = 16 * RT, W = RT == 4 ? 4 : 8, C = 4;    // waves, columns of a lane
@@ -1181,8 +1185,9 @@ hipError_t launch_lora_up(LoraUpArgs a, hipStream_t s) {
   if (a.tokens == 0) return hipSuccess;
   const int group = up_group(a.tokens);
   // 256 columns a workgroup; more while there are enough for eight (four) a CU
-  // (256, 512, 1024 and 2048 columns: 4096 x 5120 30.0, 30.0, 32.8, 46.6 us, 8192 x
-  // 2048 25.1, 24.2, 22.5, 32.8)
+  // (256, 512, 1024 and 2048 columns: 4096 x 5120 28.6, 26.6, 30.4, 42.7 us, 8192 x
+  // 2048 24.0, 22.7, 22.4, 33.8).  Up to kWindow tokens the workgroups of an adapter's
+  // other tokens are counted with it and have nothing to do.
   const int64_t many = group == 1 ? 2048 : 1024, blocks = groups(a.tokens, group);
   a.wide = kThreads;
   while (a.wide < 4096 && blocks * ((a.n + 2 * a.wide - 1) / (2 * a.wide)) >= many) a.wide *= 2;

@@ -562,11 +562,12 @@ hipError_t one_product(int epi, bool tall, const NsGemmArgs& a, hipStream_t s) {
 hipError_t product(int epi, bool tall, const NsGemmArgs& a, hipStream_t s) {
   // Huge where it has two tiles for every CU, else Wide where it has one: larger
   // tiles read each operand less often, smaller ones leave fewer CUs idle.
-  // Microseconds a launch, Deep / Wide / Huge: A of 5120 x 2048 46 / 76 / 113, its
-  // X 71 / 65 / 63; 128 of 2048 x 768: A 242 / 211 / 207, P 139 / 139 / 125, X
-  // 682 / 558 / 524.  Exact stages hold twice as much, so that Wide would run alone
-  // on a CU: Huge where it has a tile for every CU.  A call of four 1000 x 2047 735
-  // (Deep) / 1339 us, of sixteen 1536 x 2048 5391 / 4925, of 128 2048 x 768 10617 /
+  // Microseconds a launch, Deep / Wide / Huge: A of 5120 x 2048 46 / 76 / 113; 128 of
+  // 2048 x 768: A 242 / 211 / 207, P 139 / 139 / 125, X 682 / 558 / 524.  (X of 5120 x
+  // 2048, 160 tiles of Huge and 320 of Wide: the call takes 575 with Huge and 632 with
+  // Wide, which the rule gives it.)  Exact stages hold twice as much, so that Wide would
+  // run alone on a CU: Huge where it has a tile for every CU.  A call of four 1000 x 2047
+  // 735 (Deep) / 1339 us, of sixteen 1536 x 2048 5391 / 4925, of 128 2048 x 768 10617 /
   // 9480 (in turn over three stages of one part each: 775, 5165, 9980).
   const bool sym = epi == kGram || epi == kPoly;
   if (a.exact)
@@ -652,8 +653,8 @@ bool ns_bounds(int steps, float a, float b, float c, NsScales* out) {
 bool ns_keeps_small(int steps, float a) { return steps * log2(fmin(fabs((double)a), 1.0)) >= -8.0; }
 
 // Matrices that are taken together: as many as fit 4 GiB of workspace (128 of
-// 2048 x 768 together take 5.2 ms; 62 at a time 5.7, 16, whose X would stay in
-// the last-level cache, 5.7: their launches do not fill the last round of CUs).
+// 2048 x 768 together take 4.5 ms; 62 at a time 4.9, 16, whose X would stay in
+// the last-level cache, 5.3: their launches do not fill the last round of CUs).
 int64_t ns_batch(int64_t batch, int64_t rows, int64_t cols) {
   const int64_t n = rows < cols ? rows : cols;
   const int64_t one = 8 * rows * pad64(cols) + 8 * n * pad64(n);
